@@ -35,6 +35,9 @@ OUT_BF16 = 0
 OUT_F32 = 1
 AMAX_MAX = 0
 AMAX_MOST_RECENT = 1
+KV_E4M3 = 0
+KV_E5M2 = 1
+KV_BF16 = 2
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -77,6 +80,20 @@ class AdamWHparams(ctypes.Structure):
                                               "weight_decay", "bias_correction1", "bias_correction2")]
 
 
+class _PagedKV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                *[(f"{t}_{n}_stride", ctypes.c_int64) for t in "kv" for n in ("page", "head", "row")],
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("format", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class _PagedBatch(ctypes.Structure):
+    _fields_ = [("q_offsets", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("page_table_ld", ctypes.c_int64), ("seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32),
+                ("max_new", ctypes.c_int32)]
+
+
 _I64, _I32, _VP, _INT = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int
 _SIGS = {
     "fp8_abi_version": (_INT, []),
@@ -108,6 +125,11 @@ _SIGS = {
                                       _I64, _VP]),
     "fp8_wgrad_recompute_error": (_INT, [_I64, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _VP, _VP]),
     "fp8_adamw_step_fp8_states": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, ctypes.POINTER(AdamWHparams), _VP]),
+    "fp8_rope_append_kv": (_INT, [ctypes.POINTER(_PagedKV), ctypes.POINTER(_PagedBatch), _I64, _VP, _I64, _I32, _VP,
+                                  _I64, _VP, _I64, _VP, _I64, _I32, _I32, _VP, _I64, _VP]),
+    "fp8_paged_attention_workspace_bytes": (ctypes.c_size_t, []),
+    "fp8_paged_attention": (_INT, [ctypes.POINTER(_PagedKV), ctypes.POINTER(_PagedBatch), _I64, _VP, _I64, _I32,
+                                   ctypes.c_float, _VP, _I64, _VP, _VP, _VP]),
     "fp8_moe_route_pad": (_INT, [_VP, _I64, _INT, _INT, _INT, _I64, _VP, _VP, _VP, _VP, _VP, _VP,
                                  _VP, _VP]),
     "fp8_moe_gather": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP, _INT, _I64, _VP, _VP, _VP]),
@@ -499,6 +521,136 @@ def adamw_step_fp8_states(param, grad, m, m_scales, v, v_scales, hparams: AdamWH
             _buf(v_scales, "v_scales", _F32, n // 128))
     _check("fp8_adamw_step_fp8_states", L.fp8_adamw_step_fp8_states(*args, n, ctypes.byref(hparams),
                                                                     _stream(stream)))
+
+
+# ------------------------------------------------------------------ paged key / value cache
+
+class PagedKV:
+    """One layer's paged cache: ``k`` and ``v`` [num_pages, heads, page_size, head_dim], any strides
+    with contiguous elements (a [num_pages, page_size, heads, head_dim] pool is passed as
+    ``pool.transpose(1, 2)``).  BF16, or FP8 codes with device scales [1] (None = 1): torch's float8
+    types name their format, ``torch.uint8`` codes take ``fmt`` (KV_E4M3 or KV_E5M2).  Checked and
+    marshalled once; keeps the tensors alive."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, fmt=KV_E4M3):
+        kinds = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.float8_e5m2: KV_E5M2, torch.uint8: fmt}
+        st = _PagedKV()
+        for name, t, scale in (("k", k, k_scale), ("v", v, v_scale)):
+            _on_device(t, name, tuple(kinds))
+            if t.dim() != 4:
+                raise ValueError(f"{name}: expected [num_pages][heads][page_size][head_dim], got {tuple(t.shape)}")
+            if t.stride(3) != 1:
+                raise ValueError(f"{name}: elements of a row must be contiguous (stride {t.stride(3)})")
+            setattr(st, name, t.data_ptr())
+            for i, n in enumerate(("page", "head", "row")):   # a dimension of one is never stepped over
+                step = t.stride(i) if t.shape[i] > 1 else t.shape[3]
+                setattr(st, f"{name}_{n}_stride", step)
+            setattr(st, f"{name}_scale", _buf(scale, f"{name}_scale", _F32, 1, True))
+        if v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError(f"v: {tuple(v.shape)} {v.dtype}, expected {tuple(k.shape)} {k.dtype} like k")
+        if kinds[k.dtype] not in (KV_E4M3, KV_E5M2, KV_BF16) or (k.dtype == torch.uint8 and fmt == KV_BF16):
+            raise ValueError("fmt: expected KV_E4M3 or KV_E5M2 for byte codes")
+        if k.dtype == torch.bfloat16 and (k_scale is not None or v_scale is not None):
+            raise ValueError("k_scale, v_scale: a BF16 cache has no scales")
+        st.format = kinds[k.dtype]
+        st.num_pages, st.heads, st.page_size, st.head_dim = k.shape
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.head_dim, self.device = k.shape[1], k.shape[3], k.device
+        self._ref = ctypes.byref(st)
+
+
+class PagedBatch:
+    """The sequences of a call: ``q_offsets`` [seqs + 1], ``kv_lens`` [seqs] (new tokens included),
+    ``page_table`` [seqs, pages_per_seq], int32 on the device and read there by every call, so a serving
+    loop updates them in place; ``max_new`` bounds the new tokens of a sequence."""
+
+    def __init__(self, q_offsets, kv_lens, page_table, max_new):
+        pt, seqs, width, ld = _mat(page_table, "page_table", _I32)
+        st = _PagedBatch(_buf(q_offsets, "q_offsets", _I32, seqs + 1), _buf(kv_lens, "kv_lens", _I32, seqs), pt, ld,
+                         seqs, width, int(max_new))
+        self.q_offsets, self.kv_lens, self.page_table, self.max_new = q_offsets, kv_lens, page_table, int(max_new)
+        self.device = page_table.device
+        self._ref = ctypes.byref(st)
+
+
+def _paged(cache, batch):
+    if not isinstance(cache, PagedKV) or not isinstance(batch, PagedBatch):
+        raise TypeError("cache, batch: expected a PagedKV and a PagedBatch")
+    if cache.device != batch.device or cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"cache on {cache.device}, batch on {batch.device}: both must be on the current device")
+    return cache._ref, batch._ref
+
+
+def _heads(t, name, tokens, heads, dim):
+    """(pointer, row stride) of a [tokens, heads, dim] BF16 tensor whose heads lie side by side."""
+    _on_device(t, name, _BF16)
+    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads) or \
+            (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{'tokens' if tokens is None else tokens}]"
+                         f"[{'heads' if heads is None else heads}][{dim}]")
+    sT, sH, sE = t.stride()
+    if t.numel() and (sE != 1 or (t.shape[1] > 1 and sH != dim)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
+    return t.data_ptr(), (sT if t.shape[0] > 1 else t.shape[1] * dim)
+
+
+def rope_append_kv(cache, batch, k, v, rope=None, q=None, q_out=None, interleaved=False, stream=None):
+    """Appends ``k`` and ``v`` [tokens, heads, head_dim] to the cache at their sequences' positions, ``k``
+    rotated by the table ``rope`` [positions, rot_dim] (cosines, then sines; None: no rotation); ``q``
+    [tokens, q_heads, head_dim] is rotated into ``q_out`` (may be ``q``)."""
+    L = lib()
+    refs = _paged(cache, batch)
+    D = cache.head_dim
+    pk, ldk = _heads(k, "k", None, cache.heads, D)
+    T = k.shape[0]
+    pv, ldv = _heads(v, "v", T, cache.heads, D)
+    if (q is None) != (q_out is None):
+        raise ValueError("q, q_out: give both or neither")
+    pq = pqo = None
+    ldq = ldqo = H = 0
+    if q is not None:
+        pq, ldq = _heads(q, "q", T, None, D)
+        H = q.shape[1]
+        pqo, ldqo = _heads(q_out, "q_out", T, H, D)
+    pr, n, rot = None, 0, 0
+    if rope is not None:
+        n, rot = _shape(rope, "rope", 2)
+        pr = _buf(rope, "rope", _F32, n * rot)
+    _check("fp8_rope_append_kv", L.fp8_rope_append_kv(*refs, T, pq, ldq, H, pk, ldk, pv, ldv, pr, n, rot,
+                                                      int(interleaved), pqo, ldqo, _stream(stream)))
+
+
+def new_attention_workspace(device="cuda") -> torch.Tensor:
+    """A zeroed workspace of paged_attention (the same for every batch; the library leaves its
+    counters zeroed)."""
+    n = (int(lib().fp8_paged_attention_workspace_bytes()) + 15) // 16 * 16
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_attention(cache, batch, q, out, workspace, lse=None, scale=None, stream=None):
+    """``out`` [tokens, q_heads, head_dim] <- attention of the new tokens' queries ``q`` over the cache
+    (their keys already appended); ``lse`` [tokens, q_heads] FP32 optional; ``scale`` defaults to
+    head_dim ** -0.5."""
+    L = lib()
+    refs = _paged(cache, batch)
+    D = cache.head_dim
+    pq, ldq = _heads(q, "q", None, None, D)
+    T, H = q.shape[:2]
+    po, ldo = _heads(out, "out", T, H, D)
+    pl = _buf(lse, "lse", _F32, T * H, True)
+    ws = _buf(workspace, "workspace", (torch.uint8,), _attention_workspace())
+    _check("fp8_paged_attention", L.fp8_paged_attention(*refs, T, pq, ldq, H, D ** -0.5 if scale is None else scale,
+                                                        po, ldo, pl, ws, _stream(stream)))
+
+
+_ws_bytes = {}
+
+
+def _attention_workspace():
+    dev = torch.cuda.current_device()
+    if dev not in _ws_bytes:
+        _ws_bytes[dev] = int(lib().fp8_paged_attention_workspace_bytes())
+    return _ws_bytes[dev]
 
 
 # ------------------------------------------------------------------ MoE glue

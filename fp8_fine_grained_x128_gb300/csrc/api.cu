@@ -420,6 +420,89 @@ FP8FG_API int fp8_adamw_step_fp8_states(float *param, const void *grad, uint8_t 
     return launch_adamw_fp8(param, grad, m, m_scales, v, v_scales, n, *hparams, S(stream));
 }
 
+// The cache and batch descriptors of the paged entry points.
+static int paged_checks(const fp8_paged_kv_t *c, const fp8_paged_batch_t *b, int64_t tokens)
+{
+    if (!c || !b) return FP8_ERR_INVALID_ARG;
+    if (c->format < FP8_KV_E4M3 || c->format > FP8_KV_BF16) return FP8_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->heads < 1 || c->heads > 65535) return FP8_ERR_INVALID_ARG;
+    if (c->format == FP8_KV_BF16 && (c->k_scale || c->v_scale)) return FP8_ERR_INVALID_ARG;
+    if (b->seqs < 0 || b->seqs > 65536 || b->max_new < 0 || b->pages_per_seq < 0) return FP8_ERR_INVALID_ARG;
+    if (tokens < 0 || tokens >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128) return FP8_ERR_UNSUPPORTED;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 && c->page_size != 256)
+        return FP8_ERR_UNSUPPORTED;
+    if ((int64_t)b->pages_per_seq * c->page_size >= (int64_t)1 << 31 || b->page_table_ld < b->pages_per_seq)
+        return FP8_ERR_SHAPE;
+    if (tokens == 0 || b->seqs == 0) return FP8_OK;
+    if (!c->k || !c->v || !b->q_offsets || !b->kv_lens) return FP8_ERR_INVALID_ARG;
+    if (b->pages_per_seq > 0 && !b->page_table) return FP8_ERR_INVALID_ARG;
+    const int64_t esz = c->format == FP8_KV_BF16 ? 2 : 1;
+    const int64_t strides[6] = {c->k_page_stride, c->k_head_stride, c->k_row_stride,
+                                c->v_page_stride, c->v_head_stride, c->v_row_stride};
+    for (int64_t s : strides) {
+        if (s <= 0 || s >= (int64_t)1 << 39) return FP8_ERR_SHAPE;
+        if ((s * esz) % 16 != 0) return FP8_ERR_ALIGNMENT;
+    }
+    if (c->k_row_stride < c->head_dim || c->v_row_stride < c->head_dim) return FP8_ERR_SHAPE;
+    return aligned16(c->k) && aligned16(c->v) ? FP8_OK : FP8_ERR_ALIGNMENT;
+}
+
+// A [tokens][ld] BF16 operand of `heads` heads of d elements.
+static int paged_rows_check(const void *p, int64_t ld, int64_t heads, int64_t d)
+{
+    if (!p) return FP8_ERR_INVALID_ARG;
+    if (ld < heads * d) return FP8_ERR_SHAPE;
+    return aligned16(p) && ld % 8 == 0 ? FP8_OK : FP8_ERR_ALIGNMENT;
+}
+
+FP8FG_API int fp8_rope_append_kv(const fp8_paged_kv_t *cache, const fp8_paged_batch_t *batch, int64_t tokens,
+                                 const void *q, int64_t q_ld, int32_t q_heads, const void *k, int64_t k_ld,
+                                 const void *v, int64_t v_ld, const float *rope, int64_t rope_len, int32_t rot_dim,
+                                 int32_t interleaved, void *q_out, int64_t q_out_ld, void *stream)
+{
+    int rc = paged_checks(cache, batch, tokens);
+    if (rc != FP8_OK) return rc;
+    if (q_heads < 0 || q_heads > 65535 || rope_len < 0 || (interleaved != 0 && interleaved != 1))
+        return FP8_ERR_INVALID_ARG;
+    if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 != 0) return FP8_ERR_SHAPE;
+    if (tokens == 0 || batch->seqs == 0) return FP8_OK;
+    const int d = cache->head_dim;
+    if (q_heads > 0 && ((rc = paged_rows_check(q, q_ld, q_heads, d)) != FP8_OK ||
+                        (rc = paged_rows_check(q_out, q_out_ld, q_heads, d)) != FP8_OK))
+        return rc;
+    if ((rc = paged_rows_check(k, k_ld, cache->heads, d)) != FP8_OK ||
+        (rc = paged_rows_check(v, v_ld, cache->heads, d)) != FP8_OK)
+        return rc;
+    if (rot_dim > 0 && !rope) return FP8_ERR_INVALID_ARG;
+    if (rope && !aligned16(rope)) return FP8_ERR_ALIGNMENT;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_rope_append_kv(*cache, *batch, tokens, q, q_ld, q_heads, k, k_ld, v, v_ld, rope, rope_len, rot_dim,
+                                 interleaved, q_out, q_out_ld, st, S(stream));
+}
+
+FP8FG_API size_t fp8_paged_attention_workspace_bytes(void) { return paged_attention_workspace_bytes(); }
+
+FP8FG_API int fp8_paged_attention(const fp8_paged_kv_t *cache, const fp8_paged_batch_t *batch, int64_t tokens,
+                                  const void *q, int64_t q_ld, int32_t q_heads, float softmax_scale, void *out,
+                                  int64_t out_ld, float *lse, void *workspace, void *stream)
+{
+    int rc = paged_checks(cache, batch, tokens);
+    if (rc != FP8_OK) return rc;
+    if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0) return FP8_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.0f) || softmax_scale > 3.0e38f) return FP8_ERR_INVALID_ARG;
+    if (tokens * q_heads >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
+    if (tokens == 0 || batch->seqs == 0) return FP8_OK;
+    if ((rc = paged_rows_check(q, q_ld, q_heads, cache->head_dim)) != FP8_OK ||
+        (rc = paged_rows_check(out, out_ld, q_heads, cache->head_dim)) != FP8_OK)
+        return rc;
+    if (!workspace) return FP8_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return FP8_ERR_ALIGNMENT;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_paged_attention(*cache, *batch, tokens, q, q_ld, q_heads, softmax_scale, out, out_ld, lse,
+                                  workspace, st, S(stream));
+}
+
 FP8FG_API int fp8_moe_route_pad(const float *logits, int64_t T, int E, int topk, int align, int64_t M_capacity,
                                 int32_t *topk_idx, float *topk_prob, int32_t *counts, int32_t *group_offsets,
                                 int32_t *row_token, float *row_prob, uint8_t *row_is_pad, void *stream)

@@ -69,6 +69,18 @@ int launch_wgrad_recompute_error(int64_t M, int64_t N, int64_t K, const void *dY
 int launch_adamw_fp8(float *p, const void *g, uint8_t *qm, float *sm, uint8_t *qv, float *sv, int64_t n,
                      const fp8_adamw_hparams_t &h, cudaStream_t st);
 
+// paged_append.cu
+int launch_rope_append_kv(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, int64_t tokens, const void *q,
+                          int64_t q_ld, int q_heads, const void *k, int64_t k_ld, const void *v, int64_t v_ld,
+                          const float *rope, int64_t rope_len, int rot_dim, int interleaved, void *q_out,
+                          int64_t q_out_ld, int *status, cudaStream_t st);
+
+// paged_attn.cu
+size_t paged_attention_workspace_bytes();
+int launch_paged_attention(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, int64_t tokens, const void *q,
+                           int64_t q_ld, int q_heads, float scale, void *out, int64_t out_ld, float *lse, void *ws,
+                           int *status, cudaStream_t st);
+
 // moe.cu
 int launch_moe_route_pad(const float *logits, int64_t T, int E, int topk, int align, int64_t Mcap,
                          int32_t *topk_idx, float *topk_prob, int32_t *counts, int32_t *offsets, int32_t *row_token,

@@ -420,6 +420,104 @@ FP8FG_API int fp8_adamw_step_fp8_states(float *param, const void *grad, uint8_t 
                                         uint8_t *v, float *v_scales, int64_t n,
                                         const fp8_adamw_hparams_t *hparams, void *stream);
 
+/* ------------------------------------------------ paged key / value cache
+ *
+ * The rollout side of [FP8-RL]: "KV cache compression" keeps a layer's keys
+ * and values in FP8 with per-tensor scales (fp8_quant_pertensor_current
+ * calibrates them).  The cache is a pool of pages of page_size tokens each; a
+ * page table gives every sequence's pages in order, so sequences grow without
+ * moving.  The pages fix neither the paging nor its layout: both are this
+ * library's own. */
+
+typedef enum { FP8_KV_E4M3 = 0, FP8_KV_E5M2 = 1, FP8_KV_BF16 = 2 } fp8_kv_format_t;
+
+/* One layer's cache.  Row r of page p, head h starts at element
+ * p * page_stride + h * head_stride + r * row_stride of k (v) and holds
+ * head_dim contiguous elements: any order of pages, heads and rows, and K and
+ * V interleaved in one allocation, are strides.
+ *   k, v: 16-byte aligned; every stride a positive multiple of 16 bytes.
+ *   k_scale, v_scale: DEVICE float[1]; an element stands for code * scale.
+ *   NULL = 1.  Must be NULL for FP8_KV_BF16.
+ *   page_size: 16, 32, 64, 128 or 256.  head_dim: 64 or 128.  heads >= 1. */
+typedef struct {
+    void *k, *v;
+    int64_t k_page_stride, k_head_stride, k_row_stride;
+    int64_t v_page_stride, v_head_stride, v_row_stride;
+    const float *k_scale, *v_scale;
+    int32_t format, num_pages, page_size, heads, head_dim;
+} fp8_paged_kv_t;
+
+/* The sequences of one call.  Sequence b's new tokens are rows
+ * [q_offsets[b], q_offsets[b+1]) of q, k and v; kv_lens[b] counts its tokens
+ * in the cache INCLUDING the new ones, so new token i stands at position
+ * kv_lens[b] - (q_offsets[b+1] - q_offsets[b]) + i.  Its token at position p
+ * is row p % page_size of page page_table[b * page_table_ld + p / page_size].
+ *   q_offsets: DEVICE int32[seqs + 1], non-decreasing.  Rows outside
+ *   [q_offsets[0], q_offsets[seqs]) belong to no sequence: not read, and
+ *   their outputs not written.
+ *   kv_lens: DEVICE int32[seqs], 0 .. pages_per_seq * page_size (< 2^31).
+ *   page_table: DEVICE int32, entries of the pages in use in [0, num_pages).
+ *   max_new: an upper bound on the new tokens of any sequence.
+ * These arrays are read on the device (a captured graph replays with what
+ * they then hold) and checked there: a value outside its range records
+ * FP8_ERR_INVALID_ARG, nothing outside the buffers is read or written, and
+ * the outputs of that sequence are unspecified.  0 <= seqs <= 65536. */
+typedef struct {
+    const int32_t *q_offsets, *kv_lens, *page_table;
+    int64_t page_table_ld;
+    int32_t seqs, pages_per_seq, max_new;
+} fp8_paged_batch_t;
+
+/* Appends the new tokens' keys and values to the cache, rotating queries and
+ * keys by their positions on the way.  With c, s = the FP32 table's row for
+ * the token's position (rope [rope_len][rot_dim]: cosines in columns
+ * [0, rot_dim/2), sines after them), every pair (x1, x2) of the first rot_dim
+ * elements of a head becomes (x1 c - x2 s, x2 c + x1 s) in FP32:
+ *   interleaved = 0: pairs (i, i + rot_dim/2);  1: pairs (2i, 2i + 1);
+ * the other elements pass unchanged.  q_out gets the rotated queries rounded
+ * to BF16; the cache gets the rotated keys and the values rounded once, to
+ * BF16 or to RNE_satfinite(x / scale) (IEEE binary32 division).
+ *   q [tokens][q_ld] (q_heads heads of head_dim side by side; NULL with
+ *   q_heads = 0: keys and values only), k, v [tokens][k_ld / v_ld]
+ *   (cache->heads heads): BF16, typically column ranges of one projection.
+ *   q_out [tokens][q_out_ld] BF16; may be q itself.
+ *   rot_dim: a multiple of 16, 0 (no rotation, rope NULL) .. head_dim.
+ *   All pointers 16-byte aligned, leading dimensions multiples of 8.
+ * A position outside the table or the page table records
+ * FP8_ERR_INVALID_ARG and that token is not written.  A key or value that is
+ * Inf or NaN records FP8_ERR_NONFINITE (what the cache then holds for that
+ * token is unspecified).  Two new tokens must not share a cache row. */
+FP8FG_API int fp8_rope_append_kv(const fp8_paged_kv_t *cache, const fp8_paged_batch_t *batch, int64_t tokens,
+                                 const void *q, int64_t q_ld, int32_t q_heads, const void *k, int64_t k_ld,
+                                 const void *v, int64_t v_ld, const float *rope, int64_t rope_len,
+                                 int32_t rot_dim, int32_t interleaved, void *q_out, int64_t q_out_ld,
+                                 void *stream);
+
+/* Bytes of the caller-owned workspace of fp8_paged_attention on the current
+ * device (the same for every batch).  Zero it once before the first use;
+ * every call that completes leaves its counters zeroed again. */
+FP8FG_API size_t fp8_paged_attention_workspace_bytes(void);
+
+/* Attention of the new tokens over the cache (their own keys and values
+ * already appended).  For the token at position p and query head h, which
+ * reads cache head h / (q_heads / heads):
+ *   x_j = softmax_scale * (q . k_j),  j = 0 .. p
+ *   out = sum_j exp(x_j) v_j / sum_j exp(x_j),   lse = log sum_j exp(x_j)
+ * with k_j, v_j the values the cache stands for.  Scores, the running maximum
+ * and sum and the output's sum are FP32; the probabilities are rounded to 16
+ * bits for the product with the values.  A token at a negative position (more
+ * new tokens than kv_lens counts) sees no key: out = 0, lse = -inf.
+ *   q, out [tokens][q_ld / out_ld] BF16 (q_heads heads of head_dim);
+ *   lse (optional) [tokens][q_heads] FP32.  q_heads a multiple of heads.
+ * Cache rows at positions >= kv_lens[b] may hold anything.  A key or value
+ * below it that is Inf or NaN makes the outputs of that sequence's tokens
+ * unspecified.
+ * workspace: fp8_paged_attention_workspace_bytes() bytes, 16-byte aligned;
+ * calls sharing one must not overlap on the GPU. */
+FP8FG_API int fp8_paged_attention(const fp8_paged_kv_t *cache, const fp8_paged_batch_t *batch, int64_t tokens,
+                                  const void *q, int64_t q_ld, int32_t q_heads, float softmax_scale, void *out,
+                                  int64_t out_ld, float *lse, void *workspace, void *stream);
+
 /* -------------------------------------------------------------- MoE glue */
 
 /* Router + padded routing map ([Ling] "FP8 padding routing map").
