@@ -432,7 +432,7 @@ static int paged_checks(const fp8_paged_kv_t *c, const fp8_paged_batch_t *b, int
     if (c->head_dim != 64 && c->head_dim != 128) return FP8_ERR_UNSUPPORTED;
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 && c->page_size != 256)
         return FP8_ERR_UNSUPPORTED;
-    if ((int64_t)b->pages_per_seq * c->page_size >= (int64_t)1 << 31 || b->page_table_ld < b->pages_per_seq)
+    if ((int64_t)b->pages_per_seq * c->page_size > ((int64_t)1 << 31) - 1024 || b->page_table_ld < b->pages_per_seq)
         return FP8_ERR_SHAPE;
     if (tokens == 0 || b->seqs == 0) return FP8_OK;
     if (!c->k || !c->v || !b->q_offsets || !b->kv_lens) return FP8_ERR_INVALID_ARG;

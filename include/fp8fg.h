@@ -455,7 +455,7 @@ typedef struct {
  *   q_offsets: DEVICE int32[seqs + 1], non-decreasing.  Rows outside
  *   [q_offsets[0], q_offsets[seqs]) belong to no sequence: not read, and
  *   their outputs not written.
- *   kv_lens: DEVICE int32[seqs], 0 .. pages_per_seq * page_size (< 2^31).
+ *   kv_lens: DEVICE int32[seqs], 0 .. pages_per_seq * page_size (<= 2^31 - 1024).
  *   page_table: DEVICE int32, entries of the pages in use in [0, num_pages).
  *   max_new: an upper bound on the new tokens of any sequence.
  * These arrays are read on the device (a captured graph replays with what
