@@ -857,6 +857,21 @@ bool make_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, u
                CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_pages(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, uint64_t inner, uint64_t page_size,
+                    uint64_t heads, uint64_t pages, uint64_t row_bytes, uint64_t head_bytes, uint64_t page_bytes,
+                    uint32_t box_inner, uint32_t box_rows, bool swizzle)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {inner, page_size, heads, pages};
+    cuuint64_t strides[3] = {row_bytes, head_bytes, page_bytes};
+    cuuint32_t box[4] = {box_inner, box_rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, dtype, 4, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2-D map over an FP8 (byte) matrix [rows][inner], box 128 (K) x box_rows,
 // 128-byte swizzle (the layout the MMA descriptors expect).
 static bool make_map(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t rows, uint32_t box_rows)

@@ -19,4 +19,106 @@ __device__ __forceinline__ int seq_of_token(const int32_t *__restrict__ offsets,
     return n - 1;
 }
 
+struct AttnArgs {
+    fp8_paged_kv_t c;
+    fp8_paged_batch_t b;
+    int64_t tokens, q_ld, out_ld;
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    float scale;   // softmax scale
+    int q_heads, group;
+    int *few_count;      // workspace: one counter a CTA of k_attn_few,
+    void *few_parts;     // its parts of broken pairs,
+    void *many_joins;    // k_attn_many's records of broken units
+    float *many_parts;   // and their parts
+    int *status;
+};
+
+// Up to kFewRows rows (new tokens x group) of a sequence go to k_attn_few, more
+// to k_attn_many.
+constexpr int kFewRows = 16;
+
+// The maximum in use may lag behind the true one by 2^kLazy before the sums
+// are rescaled: no result depends on it but through roundings.
+constexpr float kLazy = 8.0f;
+// With a BF16 cache P is rounded to BF16 (unit roundoff 2^-8), and a row's error
+// averages out over its keys; a row that sees fewer than kFineKeys gets P as the
+// sum of two BF16 terms (an error of 2^-17) and a second product with V.
+constexpr int kFineKeys = 256;
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+// Sequence b: its first row of q, its rows (new tokens x group; 0: none, or not
+// to be read) and its length.  false: a value outside its range.
+__device__ __forceinline__ bool seq_lengths(const AttnArgs &g, int b, int &first, int &rows, int &len)
+{
+    first = g.b.q_offsets[b];
+    const int64_t n = (int64_t)g.b.q_offsets[b + 1] - first;
+    len = g.b.kv_lens[b];
+    rows = 0;
+    if (n == 0) return true;
+    if (first < 0 || n < 0 || first + n > g.tokens || n > g.b.max_new) return false;
+    rows = (int)n * g.group;
+    if (len < 0 || len > (int64_t)g.b.pages_per_seq * g.c.page_size) {
+        len = 0;
+        return false;
+    }
+    return true;
+}
+
+// Two FP8 codes (the low 16 bits of w) as FP16, exactly.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp8x2_f16(uint32_t w)
+{
+    uint32_t h;
+    const uint16_t c = (uint16_t)w;
+    if (FMT == FP8_KV_E4M3)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    else
+        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(c));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+// Inclusive sum over the CTA's threads; `total` = the last thread's.
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *warp_sums, int64_t &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    total = 0;
+    int64_t before = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i < warp) before += warp_sums[i];
+        total += warp_sums[i];
+    }
+    return v + before;
+}
+
+// paged_few.cu, paged_many.cu
+size_t few_parts_bytes();
+int few_grid();
+int run_few(const AttnArgs &g, cudaStream_t st);
+size_t many_joins_bytes();
+size_t many_parts_bytes();
+int run_many(const AttnArgs &g, cudaStream_t st);
+
 }  // namespace fp8fg

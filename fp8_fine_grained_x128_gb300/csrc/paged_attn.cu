@@ -1,640 +1,27 @@
 // paged_attn.cu -- attention of a chunk of new tokens over a paged key/value
-// cache (sm_103a).
+// cache: the choice of kernel and the workspace.
 //
 // Softmax over the keys in one pass with a running maximum and sum (Milakov
 // and Gimelshein, "Online normalizer calculation for softmax", 2018): scores
 // are kept as log2 values x, a part of the keys is summed up as m = max x,
 // l = sum 2^(x - m), o = sum 2^(x - m) v, and parts join by rescaling to the
-// larger m.
-#include <algorithm>
-
+// larger m.  A sequence whose rows (new tokens x query heads of a group) fit
+// one 16-row operand is bound by the cache's bytes and goes to k_attn_few
+// (mma.sync); the others go to k_attn_many (tcgen05, 256 rows a unit).  Each
+// kernel reads the lengths on the device and leaves the other's sequences
+// alone; a batch that can hold only short ones launches k_attn_few alone.
 #include "kernels.h"
 #include "paged.cuh"
 
 namespace fp8fg {
 
-struct AttnArgs {
-    fp8_paged_kv_t c;
-    fp8_paged_batch_t b;
-    int64_t tokens, q_ld, out_ld;
-    const uint16_t *q;
-    uint16_t *out;
-    float *lse;
-    float scale;   // softmax scale
-    int q_heads, group;
-    void *few_parts;
-    int *few_count;
-    int *status;
-};
+// Workspace: k_attn_few's counters and parts, then k_attn_many's.
+static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// ------------------------------------------------------------ few rows: split over the keys
-//
-// Up to 16 rows (new tokens x query heads of a group) share one cache head.
-// Bound: HBM bandwidth, every key and value read once.  All (sequence, head)
-// pairs' 64-key tiles stand in one line that is cut into equal runs, one per
-// CTA, so ragged batches and a single long cache balance alike; a CTA's run
-// covers whole pairs, which it finishes alone, and at most two broken ones,
-// whose partial maxima, sums and outputs go to the workspace.  The last CTA
-// to arrive at a broken pair joins its parts in order (the result does not
-// depend on who is last).
-//
-// A warp takes 16 keys of each tile and never waits for another warp: its
-// copies (cp.async, zero-filled past the sequence's end) go through its own
-// ring.  S = Q K^T and O += P V run on m16n8k16 mma.sync; its rate is far
-// from binding here (the rows are padded to 16 and the copies still take
-// longer).  The contraction order over head_dim is free, so a lane reads 16
-// contiguous bytes of a key as operand registers, and Q is laid out to match.
-// FP8 codes become FP16 exactly (one conversion per two codes); Q is scaled
-// by a power of two per row to fit FP16, and P by 2^6.
-
-constexpr int kFewThreads = 128;
-constexpr int kFewTile = 64;      // keys of a tile: 4 warps x 16
-constexpr int kFewRows = 16;
-constexpr float kLazy = 8.0f;     // the maximum in use may lag by 2^8 before sums are rescaled
-
-template <int D, int FMT>
-struct Few {
-    static constexpr int kEsz = FMT == FP8_KV_BF16 ? 2 : 1;
-    static constexpr int kRowB = D * kEsz;
-    static constexpr int kCh = kRowB / 16;                      // 16-byte chunks of a row
-    static constexpr int kStage = 2 * 16 * kRowB;               // a warp's K and V of 16 keys
-    static constexpr int kStages = kStage >= 8192 ? 2 : 4;
-    static constexpr int kRing = 4 * kStages * kStage;
-    static constexpr int kORow = D + 8;                         // floats of a merge row (bank spread)
-    static constexpr int kMerge = 4 * kFewRows * kORow * 4;
-    static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
-    static constexpr float kOff = FMT == FP8_KV_BF16 ? 0.0f : 6.0f;   // P is kept as 2^kOff p
-};
-
-// The CTA-wide line of tiles: sequence b contributes heads * few_tiles(b).
-__device__ __forceinline__ bool seq_lengths(const AttnArgs &g, int b, int &first, int &rows, int &len)
+size_t paged_attention_workspace_bytes()
 {
-    first = g.b.q_offsets[b];
-    const int64_t n = (int64_t)g.b.q_offsets[b + 1] - first;
-    len = g.b.kv_lens[b];
-    rows = 0;
-    if (n == 0) return true;
-    if (first < 0 || n < 0 || first + n > g.tokens || n > g.b.max_new) return false;
-    rows = (int)n * g.group;
-    if (len < 0 || len > (int64_t)g.b.pages_per_seq * g.c.page_size) {
-        len = 0;
-        return false;
-    }
-    return true;
-}
-
-__device__ __forceinline__ int few_tiles(const AttnArgs &g, int b)
-{
-    if (b >= g.b.seqs) return 0;
-    int first, rows, len;
-    if (!seq_lengths(g, b, first, rows, len)) set_status(g.status, FP8_ERR_INVALID_ARG);
-    if (rows < 1 || rows > kFewRows) return 0;
-    return max(1, (len + kFewTile - 1) / kFewTile);
-}
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <int FMT>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    if (FMT == FP8_KV_BF16)
-        mma_bf16(c, a, b0, b1);
-    else
-        mma_f16(c, a, b0, b1);
-}
-
-// Two FP8 codes (the low 16 bits of w) as FP16, exactly.
-template <int FMT>
-__device__ __forceinline__ uint32_t fp8x2_f16(uint32_t w)
-{
-    uint32_t h;
-    const uint16_t c = (uint16_t)w;
-    if (FMT == FP8_KV_E4M3)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-    else
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(c));
-    return h;
-}
-
-__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4])
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
-}
-
-// 16-byte copy; bytes 0: zero fill, nothing read.
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Where chunk c of row r lies in a ring block: the chunk index is exchanged
-// so that a warp's reads meet every bank once (64-byte FP8 value rows: twice).
-template <int CH, bool V8>
-__device__ __forceinline__ uint32_t few_at(int r, int c)
-{
-    if (CH == 4) return (uint32_t)(r * 64 + ((V8 ? c ^ ((r >> 1) & 3) : c) << 4));
-    const int x = V8 ? r & 7 : ((r & 1) << 2) | ((r >> 1) & 3);
-    return (uint32_t)(r * CH * 16 + ((c ^ x) << 4));
-}
-
-// Inclusive sum over the CTA's threads; `total` = the last thread's.
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *warp_sums, int64_t &total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    total = 0;
-    int64_t before = 0;
-    for (int i = 0; i < nw; ++i) {
-        if (i < warp) before += warp_sums[i];
-        total += warp_sums[i];
-    }
-    return v + before;
-}
-
-struct FewPart {   // a broken pair's part in the workspace
-    float m[kFewRows], l[kFewRows];
-    float o[kFewRows * 128];
-};
-
-template <int D, int FMT>
-__global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
-{
-    using C = Few<D, FMT>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_sums[4], s_start[2];
-    __shared__ float s_m[4][kFewRows], s_l[4][kFewRows];
-    __shared__ int s_last;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int gr = lane >> 2, t4 = lane & 3;
-
-    // this CTA's run [s, s_end) of the line of tiles, and the pair it starts in
-    int64_t total = 0, sum, ctas, s, s_end;
-    int b = 0;
-    int64_t before = 0;   // tiles of the sequences before b
-    for (int b0 = 0; b0 < g.b.seqs; b0 += kFewThreads) {
-        cta_scan((int64_t)few_tiles(g, b0 + tid) * g.c.heads, s_sums, sum);
-        total += sum;
-    }
-    if (total == 0) return;
-    ctas = min((int64_t)gridDim.x, total);
-    if (blockIdx.x >= ctas) return;
-    s = blockIdx.x * total / ctas;
-    s_end = (blockIdx.x + 1) * total / ctas;
-    for (int b0 = 0; b0 < g.b.seqs; b0 += kFewThreads) {
-        const int64_t n = (int64_t)few_tiles(g, b0 + tid) * g.c.heads;
-        const int64_t incl = cta_scan(n, s_sums, sum);
-        if (s < before + sum) {
-            if (s >= before + incl - n && s < before + incl) {
-                s_start[0] = b0 + tid;
-                s_start[1] = before + incl - n;
-            }
-            __syncthreads();
-            b = (int)s_start[0];
-            before = s_start[1];
-            break;
-        }
-        before += sum;
-    }
-
-    const float ks = g.c.k_scale ? *g.c.k_scale : 1.0f, vs = g.c.v_scale ? *g.c.v_scale : 1.0f;
-    const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
-    float *merge = reinterpret_cast<float *>(smem);
-    const uint8_t *kbase = static_cast<const uint8_t *>(g.c.k), *vbase = static_cast<const uint8_t *>(g.c.v);
-
-    while (s < s_end) {
-        int first, rows, len;
-        seq_lengths(g, b, first, rows, len);
-        const int nt = few_tiles(g, b);
-        if ((int64_t)nt * g.c.heads <= s - before) {   // the next sequence with tiles
-            before += (int64_t)nt * g.c.heads;
-            ++b;
-            continue;
-        }
-        const int h = (int)((s - before) / nt), tile0 = (int)(s - before - (int64_t)h * nt);
-        const int tile1 = (int)min((int64_t)nt, tile0 + (s_end - s));
-        const int new_tokens = rows / g.group;
-        const int32_t *table = g.b.page_table + b * g.b.page_table_ld;
-
-        // copies of tile i's 16 keys of this warp into ring slot i
-        int pages = 0, pbase = tile0 - 32;
-        auto issue = [&](int i) {
-            if (i < tile1) {
-                if (i - pbase >= 32) {
-                    pbase = i;
-                    const int key = (i + lane) * kFewTile + warp * 16;
-                    pages = (i + lane < tile1 && key < len) ? table[key / g.c.page_size] : 0;
-                    if (pages < 0 || pages >= g.c.num_pages) {
-                        set_status(g.status, FP8_ERR_INVALID_ARG);
-                        pages = -1;
-                    }
-                }
-                const int key0 = i * kFewTile + warp * 16;
-                const int64_t page = __shfl_sync(0xffffffffu, pages, i - pbase);
-                if (key0 < len && page >= 0) {
-                    const int rip = key0 & (g.c.page_size - 1);
-                    const uint8_t *kp = kbase + C::kEsz * (page * g.c.k_page_stride + h * g.c.k_head_stride + rip * g.c.k_row_stride);
-                    const uint8_t *vp = vbase + C::kEsz * (page * g.c.v_page_stride + h * g.c.v_head_stride + rip * g.c.v_row_stride);
-                    const uint32_t dst = ring + ((i - tile0) % C::kStages) * C::kStage;
-#pragma unroll
-                    for (int e = 0; e < 16 * C::kCh / 32; ++e) {
-                        const int r = (e * 32 + lane) / C::kCh, c = (e * 32 + lane) % C::kCh;
-                        const uint32_t n = key0 + r < len ? 16u : 0u;
-                        cp_async16z(dst + few_at<C::kCh, false>(r, c), kp + C::kEsz * r * g.c.k_row_stride + c * 16, n);
-                        cp_async16z(dst + C::kStage / 2 + few_at<C::kCh, FMT != FP8_KV_BF16>(r, c),
-                                    vp + C::kEsz * r * g.c.v_row_stride + c * 16, n);
-                    }
-                }
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < C::kStages; ++i) issue(tile0 + i);
-
-        // Q as the A operand of D / 16 contraction steps; rows gr and gr + 8
-        uint32_t qa[D / 16][4];
-        float mul[2];
-        int pos[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int row = gr + 8 * u;
-            const int tok = row / g.group;
-            pos[u] = row < rows ? len - new_tokens + tok : -1;
-            uint4 v[D / 32];
-            const uint16_t *qp = g.q + (int64_t)(first + tok) * g.q_ld + (int64_t)(h * g.group + row % g.group) * D;
-            // BF16: chunk t4 + 4c of 8 values; FP8: 16 values, two chunks side by side
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const int d = FMT == FP8_KV_BF16 ? 8 * (t4 + 4 * c) : 16 * (t4 + 4 * (c / 2)) + 8 * (c % 2);
-                v[c] = row < rows ? *reinterpret_cast<const uint4 *>(qp + d) : make_uint4(0, 0, 0, 0);
-            }
-            mul[u] = g.scale * 1.44269504f * ks;
-            float up = 1.0f;
-            if (FMT != FP8_KV_BF16) {   // a power of two that brings the row's largest value into [2^14, 2^15)
-                uint32_t m = 0;
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) m = max(m, absmax8(v[c]));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const int e = min(max((int)(m >> 7), 15), 254) - 127;   // exponent of the largest value
-                up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                mul[u] *= __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-            }
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)   // word i: step 2c + i / 2, register u + 2 (i % 2)
-                    qa[2 * c + i / 2][u + 2 * (i % 2)] =
-                        FMT == FP8_KV_BF16 ? w[i] : f16x2_rn(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
-            }
-        }
-
-        float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-
-        for (int i = tile0; i < tile1; ++i) {
-            cp_async_wait<C::kStages - 1>();
-            __syncwarp();
-            const int key0 = i * kFewTile + warp * 16;
-            const uint32_t kb = ring + ((i - tile0) % C::kStages) * C::kStage, vb = kb + C::kStage / 2;
-            if (key0 < len) {   // (a page out of range left the slot as it was: unspecified outputs)
-                float x[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < C::kCh / 4; ++c) {
-                        const uint4 w = lds128(kb + few_at<C::kCh, false>(n * 8 + gr, t4 + 4 * c));
-                        if (FMT == FP8_KV_BF16) {
-                            mma16<FMT>(x[n], qa[2 * c], w.x, w.y);
-                            mma16<FMT>(x[n], qa[2 * c + 1], w.z, w.w);
-                        } else {
-                            mma16<FMT>(x[n], qa[4 * c], fp8x2_f16<FMT>(w.x), fp8x2_f16<FMT>(w.x >> 16));
-                            mma16<FMT>(x[n], qa[4 * c + 1], fp8x2_f16<FMT>(w.y), fp8x2_f16<FMT>(w.y >> 16));
-                            mma16<FMT>(x[n], qa[4 * c + 2], fp8x2_f16<FMT>(w.z), fp8x2_f16<FMT>(w.z >> 16));
-                            mma16<FMT>(x[n], qa[4 * c + 3], fp8x2_f16<FMT>(w.w), fp8x2_f16<FMT>(w.w >> 16));
-                        }
-                    }
-                }
-                // log2 scores; keys a row does not see: -inf
-                uint32_t pa[4];
-                bool grow = false;
-                float up[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float v[4] = {x[0][2 * u], x[0][2 * u + 1], x[1][2 * u], x[1][2 * u + 1]};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + (e / 2) * 8 + 2 * t4 + (e & 1);
-                        v[e] = key <= pos[u] ? v[e] * mul[u] : -INFINITY;
-                    }
-                    float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    up[u] = 1.0f;
-                    if (mx > m[u] + kLazy || (m[u] == -INFINITY && mx > -INFINITY)) {
-                        up[u] = ex2_approx_ftz(m[u] - mx);
-                        m[u] = mx;
-                        grow = true;
-                    }
-                    const float base = m[u] == -INFINITY ? 0.0f : m[u] - C::kOff;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = ex2_approx_ftz(v[e] - base);
-                    l[u] = l[u] * up[u] + ((v[0] + v[1]) + (v[2] + v[3]));
-                    pa[u] = FMT == FP8_KV_BF16 ? bf16x2_rn(v[0], v[1]) : f16x2_rn(v[0], v[1]);
-                    pa[u + 2] = FMT == FP8_KV_BF16 ? bf16x2_rn(v[2], v[3]) : f16x2_rn(v[2], v[3]);
-                }
-                if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        o[j][0] *= up[0];
-                        o[j][1] *= up[0];
-                        o[j][2] *= up[1];
-                        o[j][3] *= up[1];
-                    }
-                }
-                if (FMT == FP8_KV_BF16) {
-#pragma unroll
-                    for (int j = 0; j < D / 8; j += 2) {
-                        uint32_t w[4];
-                        ldsm_x4_t(vb + few_at<C::kCh, false>(lane & 15, j + (lane >> 4)), w);
-                        mma16<FMT>(o[j], pa, w[0], w[1]);
-                        mma16<FMT>(o[j + 1], pa, w[2], w[3]);
-                    }
-                } else if (D == 128) {   // column n of product j is head element 16 n + j
-                    uint4 r[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        r[e] = lds128(vb + few_at<C::kCh, true>(2 * t4 + (e & 1) + 8 * (e >> 1), gr));
-                    const uint32_t w[4][4] = {{r[0].x, r[0].y, r[0].z, r[0].w}, {r[1].x, r[1].y, r[1].z, r[1].w},
-                                              {r[2].x, r[2].y, r[2].z, r[2].w}, {r[3].x, r[3].y, r[3].z, r[3].w}};
-#pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) {
-                        const uint32_t a0 = __byte_perm(w[0][i4], w[1][i4], 0x5140), a1 = __byte_perm(w[0][i4], w[1][i4], 0x7362);
-                        const uint32_t b0 = __byte_perm(w[2][i4], w[3][i4], 0x5140), b1 = __byte_perm(w[2][i4], w[3][i4], 0x7362);
-                        mma16<FMT>(o[4 * i4], pa, fp8x2_f16<FMT>(a0), fp8x2_f16<FMT>(b0));
-                        mma16<FMT>(o[4 * i4 + 1], pa, fp8x2_f16<FMT>(a0 >> 16), fp8x2_f16<FMT>(b0 >> 16));
-                        mma16<FMT>(o[4 * i4 + 2], pa, fp8x2_f16<FMT>(a1), fp8x2_f16<FMT>(b1));
-                        mma16<FMT>(o[4 * i4 + 3], pa, fp8x2_f16<FMT>(a1 >> 16), fp8x2_f16<FMT>(b1 >> 16));
-                    }
-                } else {                 // column n of product j is head element 8 n + j
-                    uint2 r[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        r[e] = lds64(vb + few_at<C::kCh, true>(2 * t4 + (e & 1) + 8 * (e >> 1), gr >> 1) + 8 * (gr & 1));
-                    const uint32_t w[4][2] = {{r[0].x, r[0].y}, {r[1].x, r[1].y}, {r[2].x, r[2].y}, {r[3].x, r[3].y}};
-#pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        const uint32_t a0 = __byte_perm(w[0][i2], w[1][i2], 0x5140), a1 = __byte_perm(w[0][i2], w[1][i2], 0x7362);
-                        const uint32_t b0 = __byte_perm(w[2][i2], w[3][i2], 0x5140), b1 = __byte_perm(w[2][i2], w[3][i2], 0x7362);
-                        mma16<FMT>(o[4 * i2], pa, fp8x2_f16<FMT>(a0), fp8x2_f16<FMT>(b0));
-                        mma16<FMT>(o[4 * i2 + 1], pa, fp8x2_f16<FMT>(a0 >> 16), fp8x2_f16<FMT>(b0 >> 16));
-                        mma16<FMT>(o[4 * i2 + 2], pa, fp8x2_f16<FMT>(a1), fp8x2_f16<FMT>(b1));
-                        mma16<FMT>(o[4 * i2 + 3], pa, fp8x2_f16<FMT>(a1 >> 16), fp8x2_f16<FMT>(b1 >> 16));
-                    }
-                }
-            }
-            __syncwarp();   // all lanes have read the slot before it is filled again
-            issue(i + C::kStages);
-        }
-        cp_async_wait<0>();
-        __syncthreads();    // the ring becomes the merge buffer
-
-        // the four warps' parts of the run joined
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
-            l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
-            if (t4 == 0) {
-                s_m[warp][gr + 8 * u] = m[u];
-                s_l[warp][gr + 8 * u] = l[u];
-            }
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                if (gr + 8 * u >= rows) continue;
-                float *p = merge + (warp * kFewRows + gr + 8 * u) * C::kORow;
-                if (FMT == FP8_KV_BF16)
-                    *reinterpret_cast<float2 *>(p + 8 * j + 2 * t4) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
-                else {
-                    p[(D / 8) * (2 * t4) + j] = o[j][2 * u];
-                    p[(D / 8) * (2 * t4 + 1) + j] = o[j][2 * u + 1];
-                }
-            }
-        }
-        __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == nt;
-        const int64_t pair0 = before + (int64_t)h * nt;   // the pair's place in the line
-        FewPart *part = static_cast<FewPart *>(g.few_parts) + 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
-        auto write_row = [&](int row, int d, float4 v, float mr, float lr) {
-            const float inv = lr > 0.0f ? vs / lr : 0.0f;
-            const int64_t tok = first + row / g.group;
-            const int head = h * g.group + row % g.group;
-            const int64_t at = tok * g.out_ld + (int64_t)head * D + d;
-            if (dbg_span(at, 4, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status))
-                *reinterpret_cast<uint2 *>(g.out + at) = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
-            if (g.lse && d == 0)
-                g.lse[tok * g.q_heads + head] = lr > 0.0f ? (mr - C::kOff + log2f(lr)) * 0.693147181f : -INFINITY;
-        };
-        for (int e = tid; e < rows * (D / 4); e += kFewThreads) {
-            const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-            const float mr = fmaxf(fmaxf(s_m[0][row], s_m[1][row]), fmaxf(s_m[2][row], s_m[3][row]));
-            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float lr = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(s_m[w][row] - mr);
-                const float4 v = *reinterpret_cast<const float4 *>(merge + (w * kFewRows + row) * C::kORow + d);
-                a.x += f * v.x;
-                a.y += f * v.y;
-                a.z += f * v.z;
-                a.w += f * v.w;
-                lr += f * s_l[w][row];
-            }
-            if (whole) {
-                write_row(row, d, a, mr, lr);
-            } else {
-                *reinterpret_cast<float4 *>(part->o + row * D + d) = a;
-                if (d == 0) {
-                    part->m[row] = mr;
-                    part->l[row] = lr;
-                }
-            }
-        }
-        if (!whole) {
-            // CTA c's run starts at floor(c total / ctas): c holds tile p iff c = ceil((p + 1) ctas / total) - 1
-            const int64_t c0 = ((pair0 + 1) * ctas + total - 1) / total - 1;
-            const int64_t c1 = ((pair0 + nt) * ctas + total - 1) / total - 1;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(&g.few_count[c0], 1) == (int)(c1 - c0);
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                const FewPart *parts = static_cast<const FewPart *>(g.few_parts);
-                for (int e = tid; e < rows * (D / 4); e += kFewThreads) {
-                    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-                    float mr = -INFINITY, lr = 0.0f;
-                    for (int64_t c = c0; c <= c1; ++c) mr = fmaxf(mr, __ldcg(&parts[2 * c + (c == c0)].m[row]));
-                    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const FewPart &q = parts[2 * c + (c == c0)];
-                        const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&q.m[row]) - mr);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(q.o + row * D + d));
-                        a.x += f * v.x;
-                        a.y += f * v.y;
-                        a.z += f * v.z;
-                        a.w += f * v.w;
-                        lr += f * __ldcg(&q.l[row]);
-                    }
-                    write_row(row, d, a, mr, lr);
-                }
-                if (tid == 0) g.few_count[c0] = 0;
-            }
-        }
-        __syncthreads();    // the merge buffer becomes the ring again
-        s += tile1 - tile0;
-    }
-}
-
-// ------------------------------------------------------------ more rows
-
-
-template <int FMT>
-__device__ __forceinline__ float kv_value(const void *base, int64_t i)
-{
-    if (FMT == FP8_KV_BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t *>(base)[i] << 16);
-    uint32_t h;
-    const uint16_t w = static_cast<const uint8_t *>(base)[i];
-    if (FMT == FP8_KV_E4M3)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(w));
-    else
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(w));
-    float f;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 %0, a;\n\t}" : "=f"(f) : "r"(h));
-    return f;
-}
-
-template <int D, int FMT>
-__global__ void __launch_bounds__(128) k_attn_rows(AttnArgs g)
-{
-    constexpr int kE = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = ((int64_t)blockIdx.x * 128 + threadIdx.x) >> 5;
-    const int64_t t = w / g.q_heads;
-    if (t >= g.tokens) return;
-    const int h = (int)(w - t * g.q_heads), hk = h / g.group;
-    const int seq = seq_of_token(g.b.q_offsets, g.b.seqs, t, lane);
-    if (seq < 0 || seq >= g.b.seqs) return;
-    int first, rows, len;
-    seq_lengths(g, seq, first, rows, len);
-    if (rows <= kFewRows) return;
-    const int64_t pos = len - rows / g.group + t - first;
-    const float ks = g.c.k_scale ? *g.c.k_scale : 1.0f, vs = g.c.v_scale ? *g.c.v_scale : 1.0f;
-    float q[kE], o[kE] = {}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e)
-        q[e] = __uint_as_float((uint32_t)g.q[t * g.q_ld + (int64_t)h * D + lane + 32 * e] << 16);
-    for (int64_t j = 0; j <= pos && j < len; ++j) {
-        const int page = g.b.page_table[seq * g.b.page_table_ld + j / g.c.page_size];
-        if (page < 0 || page >= g.c.num_pages) {
-            if (lane == 0) set_status(g.status, FP8_ERR_INVALID_ARG);
-            return;
-        }
-        const int64_t r = j % g.c.page_size;
-        const int64_t ka = page * g.c.k_page_stride + hk * g.c.k_head_stride + r * g.c.k_row_stride;
-        const int64_t va = page * g.c.v_page_stride + hk * g.c.v_head_stride + r * g.c.v_row_stride;
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) s += q[e] * kv_value<FMT>(g.c.k, ka + lane + 32 * e);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= g.scale * ks;
-        const float mn = fmaxf(m, s), a = expf(m - mn), p = expf(s - mn);
-        l = l * a + p;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] = o[e] * a + p * kv_value<FMT>(g.c.v, va + lane + 32 * e);
-        m = mn;
-    }
-    const float inv = l > 0.0f ? vs / l : 0.0f;
-    const int64_t at = t * g.out_ld + (int64_t)h * D;
-    if (dbg_span(at, D, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status)) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) g.out[at + lane + 32 * e] = (uint16_t)bf16x2_rn(o[e] * inv, 0.0f);
-    }
-    if (g.lse && lane == 0) g.lse[t * g.q_heads + h] = l > 0.0f ? m + logf(l) : -INFINITY;
-}
-
-// Workspace: counters, then the parts of broken pairs.
-constexpr size_t kCountBytes = 4096;   // one counter a CTA
-
-static int few_grid() { return std::min(3 * sm_count(), (int)(kCountBytes / sizeof(int))); }
-
-size_t paged_attention_workspace_bytes() { return kCountBytes + (size_t)few_grid() * 2 * sizeof(FewPart); }
-
-template <int D, int FMT>
-static int run_attn(const AttnArgs &g, cudaStream_t st)
-{
-    static bool attr_done[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (!attr_done[dev & 63]) {
-        if (cudaFuncSetAttribute(k_attn_few<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D, FMT>::kBytes) !=
-            cudaSuccess)
-            return FP8_ERR_CUDA;
-        attr_done[dev & 63] = true;
-    }
-    k_attn_few<D, FMT><<<few_grid(), kFewThreads, Few<D, FMT>::kBytes, st>>>(g);
-    if ((int64_t)g.b.max_new * g.group > kFewRows) {
-        const int64_t blocks = (g.tokens * g.q_heads + 3) / 4;
-        k_attn_rows<D, FMT><<<(unsigned)blocks, 128, 0, st>>>(g);
-    }
-    return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    return align256((size_t)few_grid() * sizeof(int)) + align256(few_parts_bytes()) + align256(many_joins_bytes()) +
+           many_parts_bytes();
 }
 
 int launch_paged_attention(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, int64_t tokens, const void *q,
@@ -654,16 +41,17 @@ int launch_paged_attention(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, 
     g.out_ld = out_ld;
     g.lse = lse;
     g.status = status;
-    g.few_count = static_cast<int *>(ws);
-    g.few_parts = static_cast<uint8_t *>(ws) + kCountBytes;
-    if (c.head_dim == 128) {
-        if (c.format == FP8_KV_BF16) return run_attn<128, FP8_KV_BF16>(g, st);
-        if (c.format == FP8_KV_E5M2) return run_attn<128, FP8_KV_E5M2>(g, st);
-        return run_attn<128, FP8_KV_E4M3>(g, st);
-    }
-    if (c.format == FP8_KV_BF16) return run_attn<64, FP8_KV_BF16>(g, st);
-    if (c.format == FP8_KV_E5M2) return run_attn<64, FP8_KV_E5M2>(g, st);
-    return run_attn<64, FP8_KV_E4M3>(g, st);
+    uint8_t *p = static_cast<uint8_t *>(ws);
+    g.few_count = reinterpret_cast<int *>(p);
+    p += align256((size_t)few_grid() * sizeof(int));
+    g.few_parts = p;
+    p += align256(few_parts_bytes());
+    g.many_joins = p;
+    p += align256(many_joins_bytes());
+    g.many_parts = reinterpret_cast<float *>(p);
+    const int rc = run_few(g, st);
+    if (rc != FP8_OK || (int64_t)b.max_new * g.group <= kFewRows) return rc;
+    return run_many(g, st);
 }
 
 }  // namespace fp8fg

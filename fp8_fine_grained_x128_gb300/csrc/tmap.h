@@ -14,6 +14,13 @@ namespace fp8fg {
 bool make_map_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, uint64_t inner, uint64_t rows,
                  uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapL2promotion l2);
 
+// Tensor map over a paged cache: rows of `inner` elements, page_size of them a
+// page and head, at byte strides row / head / page; boxes of box_inner x
+// box_rows elements of one page and head.  swizzle: 128-byte, else none.
+bool make_map_pages(CUtensorMap *map, CUtensorMapDataType dtype, const void *ptr, uint64_t inner, uint64_t page_size,
+                    uint64_t heads, uint64_t pages, uint64_t row_bytes, uint64_t head_bytes, uint64_t page_bytes,
+                    uint32_t box_inner, uint32_t box_rows, bool swizzle);
+
 // Raster band of a persistent GEMM over (M / 128) x (N / bn) tiles whose A
 // operand holds a_bytes (K bytes per row) and B b_bytes, for
 // tile_coords_raster: keep the smaller operand resident in L2 when it fits
