@@ -113,6 +113,37 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *warp_sums, int64
     return v + before;
 }
 
+// Bounded wait on an mbarrier phase for roles that hand over many times a
+// microsecond: the clock is read only after 256 polls (reading it at once, as
+// mbar_wait_bounded does, put about 1 us on every wait that had to wait).
+__device__ __forceinline__ bool wait_slow(uint32_t addr, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait_a(addr, parity)) return true;
+        if ((i & 255u) != 0u) continue;
+        if (*abort_flag) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitTimeoutNs) {
+            if (!*abort_flag) {
+                *abort_flag = 1;
+                set_status(status, FP8_ERR_TIMEOUT);
+            }
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool thread_wait(uint32_t addr, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    return mbar_try_wait_a(addr, parity) || wait_slow(addr, parity, abort_flag, status);
+}
+// The same for a whole warp, which stays converged.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    return __all_sync(0xffffffffu, thread_wait(smem_u32(bar), parity, abort_flag, status));
+}
+
 // paged_few.cu, paged_many.cu
 size_t few_parts_bytes();
 int few_grid();

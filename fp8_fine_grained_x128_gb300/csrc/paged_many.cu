@@ -16,10 +16,11 @@
 // and k_attn_join adds them up in order.
 //
 // Warps: 0-3 and 4-7 the softmax of the two halves, 8 TMA, 9 MMA, 10 walks the
-// run and hands its segments to the others ahead of time; with an FP8 cache
-// 12-15 turn the code tiles into FP16 operand tiles (exactly), and Q is
+// run and hands its segments to the others ahead of time, 11 sees that a tile's
+// operands have landed; with an FP8 cache 12-15 turn the code tiles into FP16 operand tiles (exactly), and Q is
 // scaled per row by a power of two to fit FP16, P by 2^6.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged.cuh"
@@ -29,7 +30,7 @@ namespace fp8fg {
 
 constexpr int kUnitRows = 256;
 constexpr int kTile = 128;            // keys of a tile
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kWalkWarp = 10, kConvWarp0 = 12;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kWalkWarp = 10, kGateWarp = 11, kConvWarp0 = 12;
 constexpr int kSegs = 4;              // segments handed over ahead
 constexpr int kSub = 128 * 128;       // bytes of 128 rows x 64 16-bit elements, 128-byte swizzle
 
@@ -45,7 +46,7 @@ struct Many {
     static constexpr int kKV = kQ + 2 * kTileB;
     static constexpr int kRaw = kKV + kStages * kTileB;
     static constexpr int kBar = kRaw + kRawStages * kRawB;
-    static constexpr int kBars = 2 * kStages + 2 * kRawStages + 2 * 4 + 2 * kSegs + 1;
+    static constexpr int kBars = 2 * kStages + 2 * kRawStages + 10 + 2 * kSegs + 1;
     static constexpr int kBytes = 1024 + kBar + kBars * 8;
     static constexpr float kOff = kFp8 ? 6.0f : 0.0f;      // P is kept as 2^kOff p
     // register split of the warpgroups (the launch has 128 a thread with an FP8 cache, 168 with a BF16 one)
@@ -119,6 +120,22 @@ __device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t 
         : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// The largest of three.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // 4-D tiled bulk tensor load (columns, row in page, head, page).
 __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap *map, uint64_t *bar, int x, int y,
@@ -263,8 +280,8 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
     uint64_t *raw_empty = raw_full + C::kRawStages;
     uint64_t *q_full = raw_empty + C::kRawStages;                    // per half
     uint64_t *s_full = q_full + 2;
-    uint64_t *p_ready = s_full + 2;
-    uint64_t *o_full = p_ready + 2;
+    uint64_t *p_ready = s_full + 2;   // per half and 64 keys
+    uint64_t *o_full = p_ready + 4;
     uint64_t *seg_full = o_full + 2;
     uint64_t *seg_empty = seg_full + kSegs;
     uint64_t *mma_done = seg_empty + kSegs;
@@ -274,7 +291,8 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
     __shared__ int64_t s_total[C::kThreads / 32];
     volatile int *abort_flag = &abort_word;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the shuffle tells the compiler that the role, and what follows from it, is the same in a whole warp)
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr int kWarps = C::kThreads / 32;
 
     // the line's length
@@ -286,22 +304,23 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
     if (lane == 0) s_total[warp] = total;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&full[i], C::kFp8 ? 128 : 1);
+            mbar_init(&full[i], C::kFp8 ? 4 : 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < C::kRawStages; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 128);
+            mbar_init(&raw_empty[i], 4);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(&q_full[x], 128);
+            mbar_init(&q_full[x], 4);
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_ready[x], 128);
+            mbar_init(&p_ready[2 * x], 4 + 1);   // and the gate
+            mbar_init(&p_ready[2 * x + 1], 4);
             mbar_init(&o_full[x], 1);
         }
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(&seg_full[i], 1);
-            mbar_init(&seg_empty[i], 8 + 2 + (C::kFp8 ? 4 : 0));   // the warps that read it
+            mbar_init(&seg_empty[i], 8 + 3 + (C::kFp8 ? 4 : 0));   // the warps that read it
         }
         mbar_init(mma_done, 1);
         abort_word = 0;
@@ -327,7 +346,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
 
     // the n-th segment of the run, by a whole warp; false: the end, or an abort
     auto next_segment = [&](uint32_t n, Segment &q) {
-        if (!warp_wait_or_abort(&seg_full[n % kSegs], (n / kSegs) & 1, abort_flag, g.status)) return false;
+        if (!warp_wait(&seg_full[n % kSegs], (n / kSegs) & 1, abort_flag, g.status)) return false;
         q = segs[n % kSegs];
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[n % kSegs]);
@@ -378,93 +397,120 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                 for (int c = 0; c < D / 8; ++c)
                     *reinterpret_cast<uint4 *>(qs + (c / 8) * kSub + (((c & 7) ^ (r & 7)) << 4)) = v[c];
                 fence_proxy_async_smem();
-                mbar_arrive(&q_full[x]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[x]);
             }
             const int pos_min = __shfl_sync(0xffffffffu, pos, 0);   // rows' positions do not decrease
             const bool fine = !C::kFp8 && fine_unit(q, g.group);
             float m = -INFINITY, l = 0.0f;
             for (int j = tile0; j < tile1; ++j, ++it) {
-                if (!warp_wait_or_abort(&s_full[x], it & 1, abort_flag, g.status)) { ok = false; break; }
+                if (!warp_wait(&s_full[x], it & 1, abort_flag, g.status)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[4][32];
+                uint64_t sum[2];
+                float up = 1.0f;
+                const bool masked = j * kTile + kTile - 1 > pos_min;   // keys past the row's position
+                auto load = [&] {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tc_ld_32x32b_x32(tS + 32 * c, s[c]);
-                tc_wait_ld();
-                if (j * kTile + kTile - 1 > pos_min) {   // keys past the row's position
-                    const int lim = pos - j * kTile;
+                    for (int c = 0; c < 4; ++c) tc_ld_32x32b_x32(tS + 32 * c, s[c]);
+                    tc_wait_ld();
+                    if (masked) {
+                        const int lim = pos - j * kTile;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i > lim) s[c][i] = 0xFF800000u;   // -inf
+                    }
+                };
+                auto row_max = [&] {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i > lim) s[c][i] = 0xFF800000u;   // -inf
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])));
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                const bool grow = mt > m && (m == -INFINITY || (mt - m) * mul > kLazy);
-                const float up = grow ? ex2_approx_ftz((m - mt) * mul) : 1.0f;
-                if (grow) m = mt;
-                const float base = m == -INFINITY ? 0.0f : C::kOff - m * mul;
-                const uint64_t mul2 = f2_pack(mul, mul), base2 = f2_pack(base, base);
-                uint64_t sum[2] = {0, 0};
-                auto exp2_pair = [&](int c, int i, float &a, float &b) {
-                    f2_unpack(f2_fma_bits(s[c][i], s[c][i + 1], mul2, base2), a, b);
-                    a = ex2_approx_ftz(a);
-                    b = ex2_approx_ftz(b);
-                    sum[(i >> 1) & 1] = f2_fma(f2_pack(a, b), f2_pack(1.0f, 1.0f), sum[(i >> 1) & 1]);
+                        for (int i = 0; i < 32; i += 2)
+                            mx[c] = max3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+                    return max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                 };
-                if (fine) {   // P in two terms, the second in the upper half of S's columns
+                // P of 64 keys with the maximum m in use, packed into s[hf]
+                auto exps = [&](auto two_terms, int hf) {
+                    constexpr bool FINE = decltype(two_terms)::value;
+                    const float base = m == -INFINITY ? 0.0f : C::kOff - m * mul;
+                    const uint64_t mul2 = f2_pack(mul, mul), base2 = f2_pack(base, base);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
                         uint32_t lo[16];
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             float a, b;
-                            exp2_pair(c, i, a, b);
-                            const uint32_t hi = bf16x2_rn(a, b);
-                            lo[i / 2] = bf16x2_rn(a - bf16_lo(hi), b - bf16_hi(hi));
-                            s[c][i / 2] = hi;
+                            f2_unpack(f2_fma_bits(s[c][i], s[c][i + 1], mul2, base2), a, b);
+                            a = ex2_approx_ftz(a);
+                            b = ex2_approx_ftz(b);
+                            sum[(i >> 1) & 1] = f2_fma(f2_pack(a, b), f2_pack(1.0f, 1.0f), sum[(i >> 1) & 1]);
+                            const uint32_t hi = C::kFp8 ? f16x2_rn(a, b) : bf16x2_rn(a, b);
+                            if (FINE) lo[i / 2] = bf16x2_rn(a - bf16_lo(hi), b - bf16_hi(hi));
+                            s[hf][(c & 1) * 16 + i / 2] = hi;
                         }
-                        tc_st_32x32b_x16(tS + 16 * c, s[c]);
-                        tc_st_32x32b_x16(tS + 64 + 16 * c, lo);
+                        // the second term of P, in the upper half of S's columns
+                        if (FINE) tc_st_32x32b_x16(tS + 64 + 16 * c, lo);
                     }
+                };
+                auto store = [&](int hf) {
+                    tc_st_32x32b_x32(tS + 32 * hf, s[hf]);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[2 * x + hf]);
+                };
+                load();
+                // After the first tile the maximum rarely grows by 2^kLazy: the first half's P is taken
+                // with the one in use while the new one is found, and again in that rare case.
+                const bool guess = !fine && j > tile0;
+                float mt;
+                sum[0] = sum[1] = 0;
+                if (guess) {
+                    mt = row_max();
+                    exps(std::false_type(), 0);
                 } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a, b;
-                            exp2_pair(c, i, a, b);
-                            s[c / 2][(c & 1) * 16 + i / 2] = C::kFp8 ? f16x2_rn(a, b) : bf16x2_rn(a, b);
-                        }
-                    tc_st_32x32b_x32(tS, s[0]);
-                    tc_st_32x32b_x32(tS + 32, s[1]);
+                    mt = row_max();
                 }
-                // the products so far are complete (S of this tile was issued after them): rescale them
-                if (__any_sync(0xffffffffu, grow) && j > tile0) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tc_ld_32x32b_x32(tO + 32 * c, o);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * up);
-                        tc_st_32x32b_x32(tO + 32 * c, o);
+                const bool grow = mt > m && (m == -INFINITY || (mt - m) * mul > kLazy);
+                if (!guess || __any_sync(0xffffffffu, grow)) {
+                    if (guess) load();   // S is still there
+                    if (grow) {
+                        up = ex2_approx_ftz((m - mt) * mul);
+                        m = mt;
                     }
+                    // the products so far are complete (S of this tile was issued after them): rescale them
+                    if (j > tile0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tc_ld_32x32b_x16(tO + 16 * c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * up);
+                            tc_st_32x32b_x16(tO + 16 * c, o);
+                        }
+                    }
+                    sum[0] = sum[1] = 0;
+                    if (!C::kFp8 && fine)
+                        exps(std::true_type(), 0);
+                    else
+                        exps(std::false_type(), 0);
                 }
-                tc_wait_st();
-                tc_fence_before();
-                mbar_arrive(&p_ready[x]);
+                store(0);
+                if (!C::kFp8 && fine)
+                    exps(std::true_type(), 1);
+                else
+                    exps(std::false_type(), 1);
+                store(1);
                 float a, b, c, d;
                 f2_unpack(sum[0], a, b);
                 f2_unpack(sum[1], c, d);
                 l = l * up + ((a + b) + (c + d));
             }
-            if (!ok || !warp_wait_or_abort(&o_full[x], un & 1, abort_flag, g.status)) break;
+            if (!ok || !warp_wait(&o_full[x], un & 1, abort_flag, g.status)) break;
             ++un;
             tc_fence_after();
             const float inv = l > 0.0f ? vs / l : 0.0f;
@@ -531,7 +577,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         const int slot = it % kRing;
-                        if (!warp_wait_or_abort(&rempty[slot], ((it / kRing) & 1) ^ 1, abort_flag, g.status)) { ok = false; break; }
+                        if (!warp_wait(&rempty[slot], ((it / kRing) & 1) ^ 1, abort_flag, g.status)) { ok = false; break; }
                         ++it;
                         if (lane == 0)   // a page out of range reads as zeros and still counts its bytes
                             mbar_arrive_expect_tx(&rfull[slot], boxes * box_rows * D * (C::kFp8 ? 1 : 2));
@@ -559,6 +605,9 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             __syncwarp();
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------- MMA issuer
+            // The whole warp walks along and one elected lane issues: the operands stay in
+            // uniform registers.  (One lane alone in a branch took about 70 cycles to issue
+            // an MMA of 64, so that no MMA was queued while it waited on a barrier.)
             constexpr uint32_t id_qk = idesc_16(!C::kFp8, false, 128, kTile);
             constexpr uint32_t id_pv = idesc_16(!C::kFp8, true, 128, D);
             const uint32_t sq = smem_u32(smem + C::kQ), skv = smem_u32(smem + C::kKV);
@@ -566,77 +615,115 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             uint32_t done[2] = {0, 0};   // P tiles of each half
             uint32_t un[2] = {0, 0};     // units of each half
             bool ok = true;
-            auto qk = [&](int x, int slot) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * kSub + (k % 4) * 32;
-                    tc_mma_16_ss(tmem + x * 128, desc_lo(sq + x * C::kTileB + off, 16),
-                                 desc_lo(skv + slot * C::kTileB + off, 16), id_qk, k > 0);
-                }
-                tc_commit(&s_full[x]);
-            };
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                ok = ok && warp_wait_or_abort(bar, parity, abort_flag, g.status);
-                tc_fence_after();
+                ok = ok && warp_wait(bar, parity, abort_flag, g.status);
                 return ok;
             };
+            auto wait_tile = [&](uint32_t i) { return wait(&full[i % C::kStages], (i / C::kStages) & 1); };
+            auto qk = [&](int x, int slot) {
+                const uint32_t qa = desc_lo(sq + x * C::kTileB, 16), kb = desc_lo(skv + slot * C::kTileB, 16);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * kSub + (k % 4) * 32) >> 4;
+                        tc_mma_16_ss(tmem + x * 128, qa + off, kb + off, id_qk, k > 0);
+                    }
+                    tc_commit(&s_full[x]);
+                }
+                __syncwarp();
+            };
             Segment q;
-            for (uint32_t n = 0; ok && next_segment(n, q); ++n) {
+            for (uint32_t n = 0; ok; ++n) {
+                if (!wait(&seg_full[n % kSegs], (n / kSegs) & 1)) break;
+                q = segs[n % kSegs];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&seg_empty[n % kSegs]);
+                if (q.tile1 == 0) break;
                 const int tile0 = q.tile0, tile1 = q.tile1, halves = q.rows > 128 ? 2 : 1;
                 const int terms = !C::kFp8 && fine_unit(q, g.group) ? 2 : 1;   // of P
-                if (!wait(&full[it % C::kStages], (it / C::kStages) & 1)) break;
+                if (!wait_tile(it)) break;
                 for (int x = 0; x < halves && ok; ++x) {
                     if (!wait(&q_full[x], un[x] & 1)) break;
                     ++un[x];
-                    if (lane == 0) qk(x, it % C::kStages);
+                    qk(x, it % C::kStages);
                 }
                 if (!ok) break;
-                if (lane == 0) tc_commit(&empty[it % C::kStages]);
+                if (elect_one()) tc_commit(&empty[it % C::kStages]);
                 ++it;
                 for (int j = tile0; j < tile1; ++j) {
                     const int vslot = it % C::kStages, kslot = (it + 1) % C::kStages;
                     const bool more = j + 1 < tile1;
-                    if (!wait(&full[vslot], (it / C::kStages) & 1)) break;
-                    if (!C::kFp8 && (j + 1) * kTile > q.len) {
-                        // rows past the sequence's end may hold anything, and 0 x NaN is NaN: zero them
-                        for (int i = max(0, q.len - j * kTile) * 8 + lane; i < kTile * 8; i += 32)
-#pragma unroll
-                            for (int sub = 0; sub < D / 64; ++sub)
-                                *reinterpret_cast<uint4 *>(smem + C::kKV + vslot * C::kTileB + sub * kSub + i * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (more && !wait(&full[kslot], ((it + 1) / C::kStages) & 1)) break;
                     for (int x = 0; x < halves; ++x) {
-                        if (!wait(&p_ready[x], done[x] & 1)) break;
-                        ++done[x];
-                        if (lane == 0) {
-                            for (int e = 0; e < terms; ++e)
 #pragma unroll
-                                for (int k = 0; k < kTile / 16; ++k)
-                                    tc_mma_16_ts(tmem + 256 + x * D, tmem + x * 128 + 64 * e + 8 * k,
-                                                 desc_lo(skv + vslot * C::kTileB + k * 2048, kSub), id_pv,
-                                                 j > tile0 || k > 0 || e > 0);
-                            if (more)
-                                qk(x, kslot);
-                            else
-                                tc_commit(&o_full[x]);
+                        for (int hf = 0; hf < 2; ++hf) {
+                            if (!wait(&p_ready[2 * x + hf], done[x] & 1)) break;
+                            tc_fence_after();
+                            const uint32_t vb = desc_lo(skv + vslot * C::kTileB, kSub);
+                            if (elect_one()) {
+                                for (int e = 0; e < terms; ++e)
+#pragma unroll
+                                    for (int k = hf * kTile / 32; k < (hf + 1) * kTile / 32; ++k)
+                                        tc_mma_16_ts(tmem + 256 + x * D, tmem + x * 128 + 64 * e + 8 * k, vb + k * 128,
+                                                     id_pv, j > tile0 || k > 0 || e > 0);
+                            }
+                            __syncwarp();
                         }
+                        if (!ok) break;
+                        ++done[x];
+                        if (more)
+                            qk(x, kslot);
+                        else if (elect_one())
+                            tc_commit(&o_full[x]);
                     }
                     if (!ok) break;
-                    if (lane == 0) {
+                    if (elect_one()) {
                         tc_commit(&empty[vslot]);
                         if (more) tc_commit(&empty[kslot]);
                     }
+                    __syncwarp();
                     it += more ? 2 : 1;
                 }
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_commit(mma_done);
                 mbar_wait_bounded(mma_done, 0, nullptr);
             }
             __syncwarp();
+        } else if (warp == kGateWarp) {
+            // ---------------------------------------------- gate: the operands of P V and the next Q K^T
+            // Arrives on a tile's first p_ready once its values and the next tile's keys have landed,
+            // so that the MMA warp has one barrier to wait on (each wait costs it about 100 cycles).
+            // Value rows past the sequence's end may hold anything, and 0 x NaN is NaN: they are
+            // zeroed here (the FP8 form's are when the codes are converted).
+            uint32_t it = 0, done[2] = {0, 0};
+            bool ok = true;
+            auto tile = [&](uint32_t i) { return warp_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, g.status); };
+            Segment q;
+            for (uint32_t n = 0; ok && next_segment(n, q); ++n) {
+                const int halves = q.rows > 128 ? 2 : 1;
+                ++it;   // the segment's first keys: the MMA warp waits for those itself
+                for (int j = q.tile0; j < q.tile1; ++j) {
+                    const bool more = j + 1 < q.tile1;
+                    if (!(ok = tile(it))) break;
+                    if (!C::kFp8 && (j + 1) * kTile > q.len) {
+                        uint8_t *v = smem + C::kKV + (it % C::kStages) * C::kTileB;
+                        for (int c = max(0, q.len - j * kTile) * 8 + lane; c < kTile * 8; c += 32)
+#pragma unroll
+                            for (int sub = 0; sub < D / 64; ++sub)
+                                *reinterpret_cast<uint4 *>(v + sub * kSub + c * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (more && !(ok = tile(it + 1))) break;
+                    it += more ? 2 : 1;
+                    for (int x = 0; x < halves; ++x) {   // the last tile's phase first: one arrival each
+                        if (done[x] > 0 && !(ok = warp_wait(&p_ready[2 * x], (done[x] - 1) & 1, abort_flag, g.status))) break;
+                        ++done[x];
+                        if (lane == 0) mbar_arrive(&p_ready[2 * x]);
+                    }
+                    if (!ok) break;
+                }
+            }
         } else if (warp == kWalkWarp) {
             // ---------------------------------------------- the run, segment by segment
             Walk w;
@@ -645,7 +732,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             w.seek(g, 0, 0);
             ManyJoin j{};
             for (uint32_t n = 0;; ++n) {
-                if (!warp_wait_or_abort(&seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag, g.status)) break;
+                if (!warp_wait(&seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag, g.status)) break;
                 const bool more = w.valid();
                 Segment q{};
                 if (more) q = w.segment();
@@ -679,17 +766,20 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             for (int j2 = 2 * tile0; j2 < 2 * tile1; ++j2, ++it) {
                 const int keys = min(kTile, max(0, q.len - (j2 >> 1) * kTile));
                 const int raw = it % C::kRawStages, slot = it % C::kStages;
-                if (!warp_wait_or_abort(&raw_full[raw], (it / C::kRawStages) & 1, abort_flag, g.status) ||
-                    !warp_wait_or_abort(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort_flag, g.status)) {
+                if (!warp_wait(&raw_full[raw], (it / C::kRawStages) & 1, abort_flag, g.status) ||
+                    !warp_wait(&empty[slot], ((it / C::kStages) & 1) ^ 1, abort_flag, g.status)) {
                     ok = false;
                     break;
                 }
                 const uint32_t src = smem_u32(smem + C::kRaw + raw * C::kRawB) + t * 16;
                 uint8_t *dst = smem + C::kKV + slot * C::kTileB + (c / 4) * kSub;
+                uint4 codes[kChunks];
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) codes[i] = lds128(src + i * 2048);
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     const int r = r0 + i * (128 / kChunks);
-                    uint4 v = lds128(src + i * 2048);
+                    uint4 v = codes[i];
                     if (r >= keys) v = make_uint4(0, 0, 0, 0);   // past the sequence's end
                     const uint4 lo = make_uint4(fp8x2_f16<FMT>(v.x), fp8x2_f16<FMT>(v.x >> 16), fp8x2_f16<FMT>(v.y),
                                                 fp8x2_f16<FMT>(v.y >> 16));
@@ -702,8 +792,11 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                     *reinterpret_cast<uint4 *>(dst + r * 128 + ((c1 ^ (r & 7)) << 4)) = odd ? lo : hi;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&raw_empty[raw]);
-                mbar_arrive(&full[slot]);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&raw_empty[raw]);
+                    mbar_arrive(&full[slot]);
+                }
             }
         }
     }
