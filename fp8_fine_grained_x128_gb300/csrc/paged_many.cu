@@ -31,6 +31,7 @@ namespace fp8fg {
 constexpr int kUnitRows = 256;
 constexpr int kTile = 128;            // keys of a tile
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kWalkWarp = 10, kGateWarp = 11, kConvWarp0 = 12;
+constexpr int kUnitCost = 2;          // a unit's own time (Q, first scores, output) in tiles' times
 constexpr int kSegs = 4;              // segments handed over ahead
 constexpr int kSub = 128 * 128;       // bytes of 128 rows x 64 16-bit elements, 128-byte swizzle
 
@@ -50,7 +51,7 @@ struct Many {
     static constexpr int kBytes = 1024 + kBar + kBars * 8;
     static constexpr float kOff = kFp8 ? 6.0f : 0.0f;      // P is kept as 2^kOff p
     // register split of the warpgroups (the launch has 128 a thread with an FP8 cache, 168 with a BF16 one)
-    static constexpr int kSoftRegs = kFp8 ? 176 : 208, kMmaRegs = kFp8 ? 72 : 88, kConvRegs = kFp8 ? 88 : 0;
+    static constexpr int kSoftRegs = kFp8 ? 176 : 216, kMmaRegs = 72, kConvRegs = kFp8 ? 88 : 0;
     static constexpr int kLaunchRegs = 128 * (2 * kSoftRegs + kMmaRegs + kConvRegs);
     static_assert(kLaunchRegs <= kThreads * (kFp8 ? 128 : 168), "register split above what the block is launched with");
 };
@@ -168,11 +169,12 @@ struct Segment {
 __device__ __forceinline__ bool fine_unit(const Segment &q, int group) { return q.pos0 + q.row0 / group < kFineKeys; }
 
 // The walk of one warp over its CTA's run of the line.  The line: sequence by
-// sequence, in each head by head, in each unit by unit, in each tile by tile.
-// Every member is the same in all lanes.
+// sequence, in each head by head, in each unit by unit, in each kUnitCost
+// places for the unit and one for every tile, so that equal runs take equal
+// times.  Every member is the same in all lanes.
 struct Walk {
     int64_t s, s_end;        // the run still to do
-    int64_t unit0;           // the line's place of the current unit's first tile
+    int64_t unit0;           // the line's place where the current unit begins
     int64_t seq_end;         // and of the sequence's end
     int b, first, rows, len, pos0;   // pos0: position of the sequence's first new token
     int head, unit, nt;      // nt: tiles of the unit
@@ -182,9 +184,10 @@ struct Walk {
         const int last = (min(rows, (u + 1) * kUnitRows) - 1) / g.group;
         return max(1, (max(0, pos0 + last + 1) + kTile - 1) / kTile);
     }
+    __device__ __forceinline__ int cost_of(const AttnArgs &g, int u) const { return kUnitCost + tiles_of(g, u); }
     __device__ __forceinline__ int units() const { return (rows + kUnitRows - 1) / kUnitRows; }
 
-    // the sequence's tiles of one head (a sum over its units, lanes side by side)
+    // the sequence's places of one head (a sum over its units, lanes side by side)
     __device__ __forceinline__ int64_t load(const AttnArgs &g, int seq)
     {
         b = seq;
@@ -193,7 +196,7 @@ struct Walk {
         if (rows <= kFewRows) return 0;
         pos0 = len - rows / g.group;
         int64_t n = 0;
-        for (int u = threadIdx.x & 31; u < units(); u += 32) n += tiles_of(g, u);
+        for (int u = threadIdx.x & 31; u < units(); u += 32) n += cost_of(g, u);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
         return n;
@@ -215,7 +218,7 @@ struct Walk {
         unit0 = before + head * per_head;
         for (unit = 0;;) {   // 32 units a step
             const int u = unit + (int)(threadIdx.x & 31);
-            const int n = u < units() ? tiles_of(g, u) : 0;
+            const int n = u < units() ? cost_of(g, u) : 0;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -238,8 +241,8 @@ struct Walk {
     __device__ __forceinline__ Segment segment() const
     {
         Segment q;
-        q.tile0 = (int)(s - unit0);
-        q.tile1 = (int)min((int64_t)nt, s_end - unit0);
+        q.tile0 = (int)max((int64_t)0, s - unit0 - kUnitCost);
+        q.tile1 = (int)min((int64_t)nt, s_end - unit0 - kUnitCost);   // <= tile0: none of its tiles in this run
         q.whole = q.tile0 == 0 && q.tile1 == nt;
         q.seq = b;
         q.first = first;
@@ -252,7 +255,7 @@ struct Walk {
     }
     __device__ __forceinline__ void next(const AttnArgs &g)
     {
-        unit0 += nt;
+        unit0 += kUnitCost + nt;
         s = unit0;
         if (s >= s_end) return;
         if (s >= seq_end) {
@@ -362,47 +365,61 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
         const float ks = g.c.k_scale ? *g.c.k_scale : 1.0f, vs = g.c.v_scale ? *g.c.v_scale : 1.0f;
         uint32_t it = 0, un = 0;
         bool ok = true;
-        Segment q;
-        for (uint32_t n = 0; ok && next_segment(n, q); ++n) {
-            const int tile0 = q.tile0, tile1 = q.tile1;
-            if (x * 128 >= q.rows) continue;
-            const int lrow = x * 128 + r;                       // row of the unit
-            const int row = q.row0 + min(lrow, q.rows - 1);
-            const int tok = row / g.group, head = q.head * g.group + row % g.group;
-            const int pos = q.pos0 + tok;
+        uint32_t nseg = 0;
+        auto next_active = [&](Segment &q) {   // the next segment with rows of this half
+            while (next_segment(nseg++, q))
+                if (x * 128 < q.rows) return true;
+            return false;
+        };
+        auto row_of = [&](const Segment &q) { return q.row0 + min(x * 128 + r, q.rows - 1); };
+        auto q_row = [&](const Segment &q) {   // its token and query head
+            const int row = row_of(q);
+            return make_int2(q.first + row / g.group, q.head * g.group + row % g.group);
+        };
+        // The row of Q into the swizzled operand tile; returns the factor from the product to log2 scores.
+        auto load_q = [&](const Segment &q) {
+            const int2 at = q_row(q);
             float mul = fmaxf(g.scale * kLog2e * ks, 1.17549435e-38f);
-            // the row of Q into the swizzled operand tile
-            {
-                const uint4 *qp = reinterpret_cast<const uint4 *>(g.q + (int64_t)(q.first + tok) * g.q_ld + (int64_t)head * D);
-                uint4 v[D / 8];
+            const uint4 *qp = reinterpret_cast<const uint4 *>(g.q + (int64_t)at.x * g.q_ld + (int64_t)at.y * D);
+            uint4 v[D / 8];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = qp[c];
-                if (C::kFp8) {   // a power of two that brings the row's largest value into [2^14, 2^15)
-                    uint32_t m = 0;
+            for (int c = 0; c < D / 8; ++c) v[c] = qp[c];
+            if (C::kFp8) {   // a power of two that brings the row's largest value into [2^14, 2^15)
+                uint32_t m = 0;
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) m = max(m, absmax8(v[c]));
-                    const int e = min(max((int)(m >> 7), 15), 254) - 127;
-                    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                    mul = fmaxf(mul * __uint_as_float((uint32_t)(127 - 14 + e) << 23), 1.17549435e-38f);
+                for (int c = 0; c < D / 8; ++c) m = max(m, absmax8(v[c]));
+                const int e = min(max((int)(m >> 7), 15), 254) - 127;
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                mul = fmaxf(mul * __uint_as_float((uint32_t)(127 - 14 + e) << 23), 1.17549435e-38f);
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        uint32_t h[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+                for (int c = 0; c < D / 8; ++c) {
+                    uint32_t h[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) h[i] = f16x2_rn(bf16_lo(h[i]) * up, bf16_hi(h[i]) * up);
-                        v[c] = make_uint4(h[0], h[1], h[2], h[3]);
-                    }
+                    for (int i = 0; i < 4; ++i) h[i] = f16x2_rn(bf16_lo(h[i]) * up, bf16_hi(h[i]) * up);
+                    v[c] = make_uint4(h[0], h[1], h[2], h[3]);
                 }
-                uint8_t *qs = smem + C::kQ + x * C::kTileB + r * 128;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4 *>(qs + (c / 8) * kSub + (((c & 7) ^ (r & 7)) << 4)) = v[c];
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[x]);
             }
-            const int pos_min = __shfl_sync(0xffffffffu, pos, 0);   // rows' positions do not decrease
+            uint8_t *qs = smem + C::kQ + x * C::kTileB + r * 128;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4 *>(qs + (c / 8) * kSub + (((c & 7) ^ (r & 7)) << 4)) = v[c];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[x]);
+            return mul;
+        };
+        Segment q;
+        bool have = next_active(q);
+        float mul = have ? load_q(q) : 0.0f;
+        while (have) {
+            const int tile0 = q.tile0, tile1 = q.tile1;
+            const int pos = q.pos0 + row_of(q) / g.group;
             const bool fine = !C::kFp8 && fine_unit(q, g.group);
+            const int pos_min = __shfl_sync(0xffffffffu, pos, 0);   // rows' positions do not decrease
             float m = -INFINITY, l = 0.0f;
+            // (one loop with a branch on the number of P's terms inside was 15% slower)
+            auto tiles = [&](auto two_terms) {
+            constexpr bool FINE = decltype(two_terms)::value;
             for (int j = tile0; j < tile1; ++j, ++it) {
                 if (!warp_wait(&s_full[x], it & 1, abort_flag, g.status)) { ok = false; break; }
                 tc_fence_after();
@@ -433,8 +450,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                     return max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                 };
                 // P of 64 keys with the maximum m in use, packed into s[hf]
-                auto exps = [&](auto two_terms, int hf) {
-                    constexpr bool FINE = decltype(two_terms)::value;
+                auto exps = [&](int hf) {
                     const float base = m == -INFINITY ? 0.0f : C::kOff - m * mul;
                     const uint64_t mul2 = f2_pack(mul, mul), base2 = f2_pack(base, base);
 #pragma unroll
@@ -464,13 +480,14 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                 };
                 load();
                 // After the first tile the maximum rarely grows by 2^kLazy: the first half's P is taken
-                // with the one in use while the new one is found, and again in that rare case.
-                const bool guess = !fine && j > tile0;
+                // with the one in use while the new one is found, and again in that rare case.  (Not with
+                // an FP8 cache, whose converting warps leave this one fewer registers: 702 against 738 us.)
+                const bool guess = !FINE && !C::kFp8 && j > tile0;
                 float mt;
                 sum[0] = sum[1] = 0;
                 if (guess) {
                     mt = row_max();
-                    exps(std::false_type(), 0);
+                    exps(0);
                 } else {
                     mt = row_max();
                 }
@@ -494,28 +511,35 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                         }
                     }
                     sum[0] = sum[1] = 0;
-                    if (!C::kFp8 && fine)
-                        exps(std::true_type(), 0);
-                    else
-                        exps(std::false_type(), 0);
+                    exps(0);
                 }
                 store(0);
-                if (!C::kFp8 && fine)
-                    exps(std::true_type(), 1);
-                else
-                    exps(std::false_type(), 1);
+                exps(1);
                 store(1);
                 float a, b, c, d;
                 f2_unpack(sum[0], a, b);
                 f2_unpack(sum[1], c, d);
                 l = l * up + ((a + b) + (c + d));
             }
-            if (!ok || !warp_wait(&o_full[x], un & 1, abort_flag, g.status)) break;
+            };
+            if (fine)
+                tiles(std::integral_constant<bool, !C::kFp8>());
+            else
+                tiles(std::false_type());
+            if (!ok) break;
+            // every product with this Q is complete (the last S was): the next one replaces it, and its
+            // first scores are under way while this segment ends
+            Segment next;
+            const bool more = next_active(next);
+            const float next_mul = more ? load_q(next) : 0.0f;
+            if (!warp_wait(&o_full[x], un & 1, abort_flag, g.status)) break;
             ++un;
             tc_fence_after();
             const float inv = l > 0.0f ? vs / l : 0.0f;
             float *part = g.many_parts + (int64_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * kPartFloats;
-            const int64_t at = (int64_t)(q.first + tok) * g.out_ld + (int64_t)head * D;
+            const int lrow = x * 128 + r;
+            const int2 th = q_row(q);
+            const int64_t at = (int64_t)th.x * g.out_ld + (int64_t)th.y * D;
             const bool mine = lrow < q.rows, whole = q.whole != 0;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -541,11 +565,14 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                 }
             }
             if (mine && whole && g.lse)
-                g.lse[(int64_t)(q.first + tok) * g.q_heads + head] = l > 0.0f ? (m * mul - C::kOff + log2f(l)) * kLn2 : -INFINITY;
+                g.lse[(int64_t)th.x * g.q_heads + th.y] = l > 0.0f ? (m * mul - C::kOff + log2f(l)) * kLn2 : -INFINITY;
             if (mine && !whole) {
                 part[kUnitRows * 128 + lrow] = m == -INFINITY ? -INFINITY : m * mul;
                 part[kUnitRows * 128 + kUnitRows + lrow] = l;
             }
+            q = next;
+            mul = next_mul;
+            have = more;
         }
     } else if (warp < kConvWarp0) {
         regs_dec<C::kMmaRegs>();
@@ -733,9 +760,14 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             ManyJoin j{};
             for (uint32_t n = 0;; ++n) {
                 if (!warp_wait(&seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag, g.status)) break;
-                const bool more = w.valid();
                 Segment q{};
-                if (more) q = w.segment();
+                while (w.valid()) {
+                    q = w.segment();
+                    if (q.tile1 > q.tile0) break;
+                    w.next(g);
+                }
+                const bool more = w.valid();
+                if (!more) q.tile1 = 0;
                 if (lane == 0) {
                     segs[n % kSegs] = q;
                     mbar_arrive(&seg_full[n % kSegs]);
@@ -743,7 +775,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                 if (!more) break;
                 if (!q.whole && q.tile0 == 0) {
                     j.rows = q.rows;
-                    j.last = (int)(((w.unit0 + w.nt) * ctas + total - 1) / total - 1);
+                    j.last = (int)(((w.unit0 + kUnitCost + w.nt) * ctas + total - 1) / total - 1);
                     j.row0 = q.row0;
                     j.head = q.head;
                     j.first = q.first;
