@@ -31,7 +31,7 @@ namespace fp8fg {
 constexpr int kUnitRows = 256;
 constexpr int kTile = 128;            // keys of a tile
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kWalkWarp = 10, kGateWarp = 11, kConvWarp0 = 12;
-constexpr int kUnitCost = 2;          // a unit's own time (Q, first scores, output) in tiles' times
+constexpr int kUnitCost = 4;          // a unit's own time (Q, first scores, output) in tiles' times
 constexpr int kSegs = 4;              // segments handed over ahead
 constexpr int kSub = 128 * 128;       // bytes of 128 rows x 64 16-bit elements, 128-byte swizzle
 
@@ -376,33 +376,45 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             const int row = row_of(q);
             return make_int2(q.first + row / g.group, q.head * g.group + row % g.group);
         };
-        // The row of Q into the swizzled operand tile; returns the factor from the product to log2 scores.
+        // The warp's 32 rows of Q into the swizzled operand tile, D / 8 lanes side by side on a row (a row
+        // a lane met 32 lines an instruction: 3000 cycles); returns the factor from the lane's row's
+        // products to log2 scores.
         auto load_q = [&](const Segment &q) {
+            constexpr int kLanes = D / 8, kRows = 32 / kLanes;   // lanes of a row, rows an instruction
             const int2 at = q_row(q);
+            const int64_t off = (int64_t)at.x * g.q_ld + (int64_t)at.y * D;
             float mul = fmaxf(g.scale * kLog2e * ks, 1.17549435e-38f);
-            const uint4 *qp = reinterpret_cast<const uint4 *>(g.q + (int64_t)at.x * g.q_ld + (int64_t)at.y * D);
             uint4 v[D / 8];
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) v[c] = qp[c];
-            if (C::kFp8) {   // a power of two that brings the row's largest value into [2^14, 2^15)
-                uint32_t m = 0;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) m = max(m, absmax8(v[c]));
-                const int e = min(max((int)(m >> 7), 15), 254) - 127;
-                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-                mul = fmaxf(mul * __uint_as_float((uint32_t)(127 - 14 + e) << 23), 1.17549435e-38f);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint32_t h[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = f16x2_rn(bf16_lo(h[i]) * up, bf16_hi(h[i]) * up);
-                    v[c] = make_uint4(h[0], h[1], h[2], h[3]);
-                }
+            for (int i = 0; i < D / 8; ++i) {
+                const int64_t o = __shfl_sync(0xffffffffu, off, i * kRows + lane / kLanes);
+                v[i] = *reinterpret_cast<const uint4 *>(g.q + o + 8 * (lane % kLanes));
             }
-            uint8_t *qs = smem + C::kQ + x * C::kTileB + r * 128;
+            if (C::kFp8) {   // a power of two that brings each row's largest value into [2^14, 2^15)
+                int mine = 0;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4 *>(qs + (c / 8) * kSub + (((c & 7) ^ (r & 7)) << 4)) = v[c];
+                for (int i = 0; i < D / 8; ++i) {
+                    uint32_t m = absmax8(v[i]);
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const int e = min(max((int)(m >> 7), 15), 254) - 127;
+                    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                    uint32_t h[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = f16x2_rn(bf16_lo(h[k]) * up, bf16_hi(h[k]) * up);
+                    v[i] = make_uint4(h[0], h[1], h[2], h[3]);
+                    const int of_row = __shfl_sync(0xffffffffu, e, (lane % kRows) * kLanes);   // row i * kRows + lane % kRows
+                    if (lane / kRows == i) mine = of_row;
+                }
+                mul = fmaxf(mul * __uint_as_float((uint32_t)(127 - 14 + mine) << 23), 1.17549435e-38f);
+            }
+            const int c = lane % kLanes;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const int row = (warp & 3) * 32 + i * kRows + lane / kLanes;
+                *reinterpret_cast<uint4 *>(smem + C::kQ + x * C::kTileB + (c / 8) * kSub + row * 128 +
+                                           (((c & 7) ^ (row & 7)) << 4)) = v[i];
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[x]);
@@ -536,39 +548,75 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             ++un;
             tc_fence_after();
             const float inv = l > 0.0f ? vs / l : 0.0f;
-            float *part = g.many_parts + (int64_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * kPartFloats;
             const int lrow = x * 128 + r;
-            const int2 th = q_row(q);
-            const int64_t at = (int64_t)th.x * g.out_ld + (int64_t)th.y * D;
-            const bool mine = lrow < q.rows, whole = q.whole != 0;
+            const bool mine = lrow < q.rows;
+            if (q.whole) {
+                const int2 th = q_row(q);
+                const int64_t off = mine ? (int64_t)th.x * g.out_ld + (int64_t)th.y * D : -1;
+                // 16 rows x 64 columns a load: a lane holds columns 8j + 2 (lane % 4) + {0, 1} of rows lane / 4
+                // and 8 more; four lanes turn their 4 x 4 words so that each stores 16 bytes of one row
+                const int t4 = lane & 3;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tc_ld_32x32b_x32(tO + 32 * c, o);
-                tc_wait_ld();
-                if (!mine) continue;
-                if (whole) {
-                    if (!dbg_span(at + 32 * c, 32, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status)) continue;
+                for (int lh = 0; lh < 2; ++lh) {
+                    int64_t o2[2];
+                    float inv2[2];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[i + e]) * inv;
-                        *reinterpret_cast<uint4 *>(g.out + at + 32 * c + i) = make_uint4(
-                            bf16x2_rn(f[0], f[1]), bf16x2_rn(f[2], f[3]), bf16x2_rn(f[4], f[5]), bf16x2_rn(f[6], f[7]));
+                    for (int u = 0; u < 2; ++u) {
+                        const int from = 16 * lh + 8 * u + (lane >> 2);
+                        o2[u] = __shfl_sync(0xffffffffu, off, from);
+                        inv2[u] = __shfl_sync(0xffffffffu, inv, from);
                     }
-                } else {
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+                        uint32_t o[32];
+                        tc_ld_16x256b_x8(tO + ((uint32_t)(16 * lh) << 16) + 64 * h, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = bf16x2_rn(__uint_as_float(o[4 * (4 * e + k) + 2 * u]) * inv2[u],
+                                                     __uint_as_float(o[4 * (4 * e + k) + 2 * u + 1]) * inv2[u]);
+#pragma unroll
+                                for (int k = 0; k < 4; k += 2) {
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, (t4 & 1) ? w[k] : w[k + 1], 1);
+                                    w[k] = (t4 & 1) ? got : w[k];
+                                    w[k + 1] = (t4 & 1) ? w[k + 1] : got;
+                                }
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, (t4 & 2) ? w[k] : w[k + 2], 2);
+                                    w[k] = (t4 & 2) ? got : w[k];
+                                    w[k + 2] = (t4 & 2) ? w[k + 2] : got;
+                                }
+                                const int64_t at = o2[u] + 64 * h + 32 * e + 8 * t4;
+                                if (o2[u] >= 0 && dbg_span(at, 8, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status))
+                                    *reinterpret_cast<uint4 *>(g.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                    }
+                }
+                if (mine && g.lse)
+                    g.lse[(int64_t)th.x * g.q_heads + th.y] = l > 0.0f ? (m * mul - C::kOff + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                float *part = g.many_parts + (int64_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * kPartFloats;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tc_ld_32x32b_x32(tO + 32 * c, o);
+                    tc_wait_ld();
+                    if (!mine) continue;
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
                         reinterpret_cast<uint4 *>(part)[(8 * c + i / 4) * kUnitRows + lrow] =
                             make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
-            }
-            if (mine && whole && g.lse)
-                g.lse[(int64_t)th.x * g.q_heads + th.y] = l > 0.0f ? (m * mul - C::kOff + log2f(l)) * kLn2 : -INFINITY;
-            if (mine && !whole) {
-                part[kUnitRows * 128 + lrow] = m == -INFINITY ? -INFINITY : m * mul;
-                part[kUnitRows * 128 + kUnitRows + lrow] = l;
+                if (mine) {
+                    part[kUnitRows * 128 + lrow] = m == -INFINITY ? -INFINITY : m * mul;
+                    part[kUnitRows * 128 + kUnitRows + lrow] = l;
+                }
             }
             q = next;
             mul = next_mul;
