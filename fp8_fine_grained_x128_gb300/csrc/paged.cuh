@@ -42,10 +42,12 @@ constexpr int kFewRows = 16;
 // The maximum in use may lag behind the true one by 2^kLazy before the sums
 // are rescaled: no result depends on it but through roundings.
 constexpr float kLazy = 8.0f;
-// With a BF16 cache P is rounded to BF16 (unit roundoff 2^-8), and a row's error
-// averages out over its keys; a row that sees fewer than kFineKeys gets P as the
-// sum of two BF16 terms (an error of 2^-17) and a second product with V.
-constexpr int kFineKeys = 256;
+// With a BF16 cache P is rounded to BF16 (unit roundoff 2^-8).  A row's error
+// averages out over the keys that carry its weight, so where there may be few of
+// them more is done: below kFineKeys keys P is the sum of two BF16 terms (an error
+// of 2^-17, and a second product with V); below kExactKeys the maximum in use does
+// not lag, so that the key that carries most has p = 1, which is exact.
+constexpr int kFineKeys = 128, kExactKeys = 2048;
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 // Sequence b: its first row of q, its rows (new tokens x group; 0: none, or not

@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
         }
 
         const bool fine = len - new_tokens < kFineKeys;
+        const float lazy = FMT == FP8_KV_BF16 && len < kExactKeys ? 0.0f : kLazy;
         float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     up[u] = 1.0f;
-                    if (mx > m[u] + kLazy || (m[u] == -INFINITY && mx > -INFINITY)) {
+                    if (mx > m[u] + lazy) {
                         up[u] = ex2_approx_ftz(m[u] - mx);
                         m[u] = mx;
                         grow = true;

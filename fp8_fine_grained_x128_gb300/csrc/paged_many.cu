@@ -42,7 +42,7 @@ struct Many {
     static constexpr int kTileB = (D / 64) * kSub;         // an operand tile
     static constexpr int kStages = D == 64 ? 6 : kFp8 ? 4 : 5;
     static constexpr int kRawB = kFp8 ? kTile * D : 0;     // a tile of codes
-    static constexpr int kRawStages = kFp8 ? (D == 64 ? 4 : 2) : 0;
+    static constexpr int kRawStages = kFp8 ? (D == 64 ? 4 : 2) : 1;   // (BF16: an unused pair of barriers)
     static constexpr int kQ = 0;
     static constexpr int kKV = kQ + 2 * kTileB;
     static constexpr int kRaw = kKV + kStages * kTileB;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
 {
     using C = Many<D, FMT>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBar);   // operand tiles
     uint64_t *empty = full + C::kStages;
     uint64_t *raw_full = empty + C::kStages;                         // code tiles
@@ -345,7 +345,9 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    // (uniform in the compiler's eyes, like everything the MMA warp's operands come from: operands that are
+    // not took the issue 64 cycles an MMA instead of 33, and the kernel a tenth to a quarter longer)
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
     // the n-th segment of the run, by a whole warp; false: the end, or an abort
     auto next_segment = [&](uint32_t n, Segment &q) {
@@ -428,6 +430,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             const int pos = q.pos0 + row_of(q) / g.group;
             const bool fine = !C::kFp8 && fine_unit(q, g.group);
             const int pos_min = __shfl_sync(0xffffffffu, pos, 0);   // rows' positions do not decrease
+            const float lazy = !C::kFp8 && pos_min < kExactKeys ? 0.0f : kLazy;
             float m = -INFINITY, l = 0.0f;
             // (one loop with a branch on the number of P's terms inside was 15% slower)
             auto tiles = [&](auto two_terms) {
@@ -491,27 +494,15 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&p_ready[2 * x + hf]);
                 };
                 load();
-                // After the first tile the maximum rarely grows by 2^kLazy: the first half's P is taken
-                // with the one in use while the new one is found, and again in that rare case.  (Not with
-                // an FP8 cache, whose converting warps leave this one fewer registers: 702 against 738 us.)
-                const bool guess = !FINE && !C::kFp8 && j > tile0;
-                float mt;
-                sum[0] = sum[1] = 0;
-                if (guess) {
-                    mt = row_max();
-                    exps(0);
-                } else {
-                    mt = row_max();
-                }
-                const bool grow = mt > m && (m == -INFINITY || (mt - m) * mul > kLazy);
-                if (!guess || __any_sync(0xffffffffu, grow)) {
-                    if (guess) load();   // S is still there
+                const float mt = row_max();
+                const bool grow = mt > m && (m == -INFINITY || (mt - m) * mul > lazy);
+                if (__any_sync(0xffffffffu, grow)) {
                     if (grow) {
                         up = ex2_approx_ftz((m - mt) * mul);
                         m = mt;
                     }
                     // the products so far are complete (S of this tile was issued after them): rescale them
-                    if (j > tile0 && __any_sync(0xffffffffu, grow)) {
+                    if (j > tile0) {
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
@@ -522,9 +513,9 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                             tc_st_32x32b_x16(tO + 16 * c, o);
                         }
                     }
-                    sum[0] = sum[1] = 0;
-                    exps(0);
                 }
+                sum[0] = sum[1] = 0;
+                exps(0);
                 store(0);
                 exps(1);
                 store(1);
@@ -770,13 +761,15 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             // so that the MMA warp has one barrier to wait on (each wait costs it about 100 cycles).
             // Value rows past the sequence's end may hold anything, and 0 x NaN is NaN: they are
             // zeroed here (the FP8 form's are when the codes are converted).
+            // It sees every place of the ring in turn, so that no phase of a slot is mistaken for another.
             uint32_t it = 0, done[2] = {0, 0};
             bool ok = true;
             auto tile = [&](uint32_t i) { return warp_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, g.status); };
             Segment q;
             for (uint32_t n = 0; ok && next_segment(n, q); ++n) {
                 const int halves = q.rows > 128 ? 2 : 1;
-                ++it;   // the segment's first keys: the MMA warp waits for those itself
+                if (!(ok = tile(it))) break;   // the segment's first keys (the MMA warp waits for those itself)
+                ++it;
                 for (int j = q.tile0; j < q.tile1; ++j) {
                     const bool more = j + 1 < q.tile1;
                     if (!(ok = tile(it))) break;
