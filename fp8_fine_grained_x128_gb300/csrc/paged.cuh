@@ -35,9 +35,10 @@ struct AttnArgs {
     int *status;
 };
 
-// Up to kFewRows rows (new tokens x group) of a sequence go to k_attn_few, more
-// to k_attn_many.
-constexpr int kFewRows = 16;
+// A batch whose sequences have at most kFewMost rows (new tokens x group) goes to
+// k_attn_few as a whole; in others the sequences of up to kFewRows do, and the
+// rest to k_attn_many.
+constexpr int kFewRows = 16, kFewMost = 64;
 
 // The maximum in use may lag behind the true one by 2^kLazy before the sums
 // are rescaled: no result depends on it but through roundings.
@@ -149,7 +150,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // paged_few.cu, paged_many.cu
 size_t few_parts_bytes();
 int few_grid();
-int run_few(const AttnArgs &g, cudaStream_t st);
+int run_few(const AttnArgs &g, int rows, cudaStream_t st);   // sequences of up to `rows` (<= kFewMost) rows
 size_t many_joins_bytes();
 size_t many_parts_bytes();
 int run_many(const AttnArgs &g, cudaStream_t st);

@@ -49,9 +49,10 @@ int launch_paged_attention(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, 
     g.many_joins = p;
     p += align256(many_joins_bytes());
     g.many_parts = reinterpret_cast<float *>(p);
-    const int rc = run_few(g, st);
-    if (rc != FP8_OK || (int64_t)b.max_new * g.group <= kFewRows) return rc;
-    return run_many(g, st);
+    const int64_t rows = (int64_t)b.max_new * g.group;
+    if (rows <= kFewMost) return run_few(g, (int)rows, st);
+    const int rc = run_few(g, kFewRows, st);
+    return rc != FP8_OK ? rc : run_many(g, st);
 }
 
 }  // namespace fp8fg

@@ -25,30 +25,39 @@
 
 namespace fp8fg {
 
-constexpr int kFewThreads = 128;
-constexpr int kFewTile = 64;      // keys of a tile: 4 warps x 16
-
-template <int D, int FMT>
+// MG groups of 16 rows, each to KS warps that take 16 keys each of a KS x 16-key
+// tile; the MG warps that share 16 keys share their ring.  One group: three
+// CTAs of four warps per SM; two and four groups: one CTA of twelve, whose
+// registers (168 a thread) fill the SM.
+template <int D, int FMT, int MG>
 struct Few {
     static constexpr int kEsz = FMT == FP8_KV_BF16 ? 2 : 1;
+    static constexpr int kSlices = MG == 1 ? 4 : 12 / MG;
+    static constexpr int kThreads = 32 * MG * kSlices;
+    static constexpr int kCtas = MG == 1 ? 3 : 1;               // per SM
+    static constexpr int kTile = 16 * kSlices;                  // keys
+    static constexpr int kRows = 16 * MG;
     static constexpr int kRowB = D * kEsz;
     static constexpr int kCh = kRowB / 16;                      // 16-byte chunks of a row
-    static constexpr int kStage = 2 * 16 * kRowB;               // a warp's K and V of 16 keys
-    static constexpr int kStages = kStage >= 8192 ? 2 : 4;
-    static constexpr int kRing = 4 * kStages * kStage;
+    static constexpr int kStage = 2 * 16 * kRowB;               // K and V of 16 keys
+    static constexpr int kFit = (MG == 1 ? 64 : 192) * 1024 / (kSlices * kStage);
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr int kRing = kSlices * kStages * kStage;
     static constexpr int kORow = D + 8;                         // floats of a merge row (bank spread)
-    static constexpr int kMerge = 4 * kFewRows * kORow * 4;
+    static constexpr int kMerge = kSlices * kRows * kORow * 4;
     static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
     static constexpr float kOff = FMT == FP8_KV_BF16 ? 0.0f : 6.0f;   // P is kept as 2^kOff p
 };
 
+// Tiles of sequence b (0: not one of this kernel's).
+template <class C>
 __device__ __forceinline__ int few_tiles(const AttnArgs &g, int b)
 {
     if (b >= g.b.seqs) return 0;
     int first, rows, len;
     if (!seq_lengths(g, b, first, rows, len)) set_status(g.status, FP8_ERR_INVALID_ARG);
-    if (rows < 1 || rows > kFewRows) return 0;
-    return max(1, (len + kFewTile - 1) / kFewTile);
+    if (rows < 1 || rows > C::kRows) return 0;
+    return max(1, (len + C::kTile - 1) / C::kTile);
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -107,28 +116,31 @@ __device__ __forceinline__ uint32_t few_at(int r, int c)
     return (uint32_t)(r * CH * 16 + ((c ^ x) << 4));
 }
 
+template <int ROWS>
 struct FewPart {   // a broken pair's part in the workspace
-    float m[kFewRows], l[kFewRows];
-    float o[kFewRows * 128];
+    float m[ROWS], l[ROWS];
+    float o[ROWS * 128];
 };
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
+template <int D, int FMT, int MG>
+__global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kCtas) k_attn_few(AttnArgs g)
 {
-    using C = Few<D, FMT>;
+    using C = Few<D, FMT, MG>;
+    constexpr int kThreads = C::kThreads, kSlices = C::kSlices;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_sums[4], s_start[2];
-    __shared__ float s_m[4][kFewRows], s_l[4][kFewRows];
+    __shared__ int64_t s_sums[kThreads / 32], s_start[2];
+    __shared__ float s_m[kSlices][C::kRows], s_l[kSlices][C::kRows];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gr = lane >> 2, t4 = lane & 3;
+    const int slice = warp / MG, mrow = 16 * (warp % MG);   // this warp's keys of a tile and first row
 
     // this CTA's run [s, s_end) of the line of tiles, and the pair it starts in
     int64_t total = 0, sum, ctas, s, s_end;
     int b = 0;
     int64_t before = 0;   // tiles of the sequences before b
-    for (int b0 = 0; b0 < g.b.seqs; b0 += kFewThreads) {
-        cta_scan((int64_t)few_tiles(g, b0 + tid) * g.c.heads, s_sums, sum);
+    for (int b0 = 0; b0 < g.b.seqs; b0 += kThreads) {
+        cta_scan((int64_t)few_tiles<C>(g, b0 + tid) * g.c.heads, s_sums, sum);
         total += sum;
     }
     if (total == 0) return;
@@ -136,8 +148,8 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
     if (blockIdx.x >= ctas) return;
     s = blockIdx.x * total / ctas;
     s_end = (blockIdx.x + 1) * total / ctas;
-    for (int b0 = 0; b0 < g.b.seqs; b0 += kFewThreads) {
-        const int64_t n = (int64_t)few_tiles(g, b0 + tid) * g.c.heads;
+    for (int b0 = 0; b0 < g.b.seqs; b0 += kThreads) {
+        const int64_t n = (int64_t)few_tiles<C>(g, b0 + tid) * g.c.heads;
         const int64_t incl = cta_scan(n, s_sums, sum);
         if (s < before + sum) {
             if (s >= before + incl - n && s < before + incl) {
@@ -153,14 +165,14 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
     }
 
     const float ks = g.c.k_scale ? *g.c.k_scale : 1.0f, vs = g.c.v_scale ? *g.c.v_scale : 1.0f;
-    const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
+    const uint32_t ring = smem_u32(smem) + slice * (C::kStages * C::kStage);
     float *merge = reinterpret_cast<float *>(smem);
     const uint8_t *kbase = static_cast<const uint8_t *>(g.c.k), *vbase = static_cast<const uint8_t *>(g.c.v);
 
     while (s < s_end && b < g.b.seqs) {   // (b ends the walk only if the lengths changed meanwhile)
         int first, rows, len;
         seq_lengths(g, b, first, rows, len);
-        const int nt = few_tiles(g, b);
+        const int nt = few_tiles<C>(g, b);
         if ((int64_t)nt * g.c.heads <= s - before) {   // the next sequence with tiles
             before += (int64_t)nt * g.c.heads;
             ++b;
@@ -171,40 +183,44 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
         const int new_tokens = rows / g.group;
         const int32_t *table = g.b.page_table + b * g.b.page_table_ld;
 
-        // copies of tile i's 16 keys of this warp into ring slot i
+        // copies of tile i's 16 keys of this slice into its ring, spread over its warps
         int pages = 0, pbase = tile0 - 32;
         auto issue = [&](int i) {
             if (i < tile1) {
                 if (i - pbase >= 32) {
                     pbase = i;
-                    const int key = (i + lane) * kFewTile + warp * 16;
+                    const int key = (i + lane) * C::kTile + slice * 16;
                     pages = (i + lane < tile1 && key < len) ? table[key / g.c.page_size] : 0;
                     if (pages < 0 || pages >= g.c.num_pages) {
                         set_status(g.status, FP8_ERR_INVALID_ARG);
                         pages = -1;
                     }
                 }
-                const int key0 = i * kFewTile + warp * 16;
+                const int key0 = i * C::kTile + slice * 16;
                 const int64_t page = __shfl_sync(0xffffffffu, pages, i - pbase);
                 if (key0 < len && page >= 0) {
                     const int rip = key0 & (g.c.page_size - 1);
                     const uint8_t *kp = kbase + C::kEsz * (page * g.c.k_page_stride + h * g.c.k_head_stride + rip * g.c.k_row_stride);
                     const uint8_t *vp = vbase + C::kEsz * (page * g.c.v_page_stride + h * g.c.v_head_stride + rip * g.c.v_row_stride);
                     const uint32_t dst = ring + ((i - tile0) % C::kStages) * C::kStage;
+                    constexpr int kHalf = 16 * C::kCh / 32;   // of a warp's copies: keys, then values
 #pragma unroll
-                    for (int e = 0; e < 16 * C::kCh / 32; ++e) {
-                        const int r = (e * 32 + lane) / C::kCh, c = (e * 32 + lane) % C::kCh;
+                    for (int e0 = 0; e0 < 2 * kHalf / MG; ++e0) {
+                        const int e = MG == 1 ? e0 : e0 * MG + warp % MG, v = e >= kHalf;
+                        const int i32 = (e - v * kHalf) * 32 + lane, r = i32 / C::kCh, c = i32 % C::kCh;
                         const uint32_t n = key0 + r < len ? 16u : 0u;
-                        cp_async16z(dst + few_at<C::kCh, false>(r, c), kp + C::kEsz * r * g.c.k_row_stride + c * 16, n);
-                        cp_async16z(dst + C::kStage / 2 + few_at<C::kCh, FMT != FP8_KV_BF16>(r, c),
-                                    vp + C::kEsz * r * g.c.v_row_stride + c * 16, n);
+                        if (!v)
+                            cp_async16z(dst + few_at<C::kCh, false>(r, c), kp + C::kEsz * r * g.c.k_row_stride + c * 16, n);
+                        else
+                            cp_async16z(dst + C::kStage / 2 + few_at<C::kCh, FMT != FP8_KV_BF16>(r, c),
+                                        vp + C::kEsz * r * g.c.v_row_stride + c * 16, n);
                     }
                 }
             }
             cp_async_commit();
         };
 #pragma unroll
-        for (int i = 0; i < C::kStages; ++i) issue(tile0 + i);
+        for (int i = 0; i < (MG == 1 ? C::kStages : C::kStages - 1); ++i) issue(tile0 + i);
 
         // Q as the A operand of D / 16 contraction steps; rows gr and gr + 8
         uint32_t qa[D / 16][4];
@@ -212,7 +228,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
         int pos[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int row = gr + 8 * u;
+            const int row = mrow + gr + 8 * u;
             const int tok = row / g.group;
             pos[u] = row < rows ? len - new_tokens + tok : -1;
             uint4 v[D / 32];
@@ -252,11 +268,17 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
 
         for (int i = tile0; i < tile1; ++i) {
-            cp_async_wait<C::kStages - 1>();
-            __syncwarp();
-            const int key0 = i * kFewTile + warp * 16;
+            if (MG == 1) {
+                cp_async_wait<C::kStages - 1>();
+                __syncwarp();
+            } else {   // tile i has landed for the slice's warps, and they are done with tile i - 1: its slot is free
+                cp_async_wait<C::kStages - 2>();
+                named_bar_sync(1 + slice, 32 * MG);
+                issue(i + C::kStages - 1);
+            }
+            const int key0 = i * C::kTile + slice * 16;
             const uint32_t kb = ring + ((i - tile0) % C::kStages) * C::kStage, vb = kb + C::kStage / 2;
-            if (key0 < len) {   // (a page out of range left the slot as it was: unspecified outputs)
+            if (key0 < len && mrow < rows) {   // (a page out of range left the slot as it was: unspecified outputs)
                 float x[2][4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
@@ -361,25 +383,27 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
                     }
                 }
             }
-            __syncwarp();   // all lanes have read the slot before it is filled again
-            issue(i + C::kStages);
+            if (MG == 1) {
+                __syncwarp();   // all lanes have read the slot before it is filled again
+                issue(i + C::kStages);
+            }
         }
         cp_async_wait<0>();
         __syncthreads();    // the ring becomes the merge buffer
 
-        // the four warps' parts of the run joined
+        // the slices' parts of the run joined
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
             l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
             if (t4 == 0) {
-                s_m[warp][gr + 8 * u] = m[u];
-                s_l[warp][gr + 8 * u] = l[u];
+                s_m[slice][mrow + gr + 8 * u] = m[u];
+                s_l[slice][mrow + gr + 8 * u] = l[u];
             }
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
-                if (gr + 8 * u >= rows) continue;
-                float *p = merge + (warp * kFewRows + gr + 8 * u) * C::kORow;
+                if (mrow + gr + 8 * u >= rows) continue;
+                float *p = merge + (slice * C::kRows + mrow + gr + 8 * u) * C::kORow;
                 if (FMT == FP8_KV_BF16)
                     *reinterpret_cast<float2 *>(p + 8 * j + 2 * t4) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
                 else {
@@ -391,7 +415,8 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == nt;
         const int64_t pair0 = before + (int64_t)h * nt;   // the pair's place in the line
-        FewPart *part = static_cast<FewPart *>(g.few_parts) + 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
+        using Part = FewPart<C::kRows>;
+        Part *part = static_cast<Part *>(g.few_parts) + 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
         auto write_row = [&](int row, int d, float4 v, float mr, float lr) {
             const float inv = lr > 0.0f ? vs / lr : 0.0f;
             const int64_t tok = first + row / g.group;
@@ -402,15 +427,17 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
             if (g.lse && d == 0)
                 g.lse[tok * g.q_heads + head] = lr > 0.0f ? (mr - C::kOff + log2f(lr)) * kLn2 : -INFINITY;
         };
-        for (int e = tid; e < rows * (D / 4); e += kFewThreads) {
+        for (int e = tid; e < rows * (D / 4); e += kThreads) {
             const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-            const float mr = fmaxf(fmaxf(s_m[0][row], s_m[1][row]), fmaxf(s_m[2][row], s_m[3][row]));
+            float mr = s_m[0][row];
+#pragma unroll
+            for (int w = 1; w < kSlices; ++w) mr = fmaxf(mr, s_m[w][row]);
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float lr = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < kSlices; ++w) {
                 const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(s_m[w][row] - mr);
-                const float4 v = *reinterpret_cast<const float4 *>(merge + (w * kFewRows + row) * C::kORow + d);
+                const float4 v = *reinterpret_cast<const float4 *>(merge + (w * C::kRows + row) * C::kORow + d);
                 a.x += f * v.x;
                 a.y += f * v.y;
                 a.z += f * v.z;
@@ -437,15 +464,15 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                const FewPart *parts = static_cast<const FewPart *>(g.few_parts);
-                for (int e = tid; e < rows * (D / 4); e += kFewThreads) {
+                const Part *parts = static_cast<const Part *>(g.few_parts);
+                for (int e = tid; e < rows * (D / 4); e += kThreads) {
                     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
                     float mr = -INFINITY, lr = 0.0f;
                     for (int64_t c = c0; c <= c1; ++c) mr = fmaxf(mr, __ldcg(&parts[2 * c + (c == c0)].m[row]));
                     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
                     for (int64_t c = c0; c <= c1; ++c) {
-                        const FewPart &q = parts[2 * c + (c == c0)];
+                        const Part &q = parts[2 * c + (c == c0)];
                         const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&q.m[row]) - mr);
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(q.o + row * D + d));
                         a.x += f * v.x;
@@ -466,34 +493,47 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_attn_few(AttnArgs g)
 
 int few_grid() { return 3 * sm_count(); }
 
-size_t few_parts_bytes() { return (size_t)few_grid() * 2 * sizeof(FewPart); }
+size_t few_parts_bytes()
+{
+    return (size_t)sm_count() * 2 * std::max(3 * sizeof(FewPart<16>), std::max(sizeof(FewPart<32>), sizeof(FewPart<64>)));
+}
 
-template <int D, int FMT>
+template <int D, int FMT, int MG>
 static int launch_few(const AttnArgs &g, cudaStream_t st)
 {
+    using C = Few<D, FMT, MG>;
+    static_assert(C::kCtas * C::kBytes <= 224 * 1024 && C::kStages >= 2, "the rings do not fit the SM");
     static bool attr_done[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!attr_done[dev & 63]) {
-        if (cudaFuncSetAttribute(k_attn_few<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D, FMT>::kBytes) !=
+        if (cudaFuncSetAttribute(k_attn_few<D, FMT, MG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes) !=
             cudaSuccess)
             return FP8_ERR_CUDA;
         attr_done[dev & 63] = true;
     }
-    k_attn_few<D, FMT><<<few_grid(), kFewThreads, Few<D, FMT>::kBytes, st>>>(g);
+    k_attn_few<D, FMT, MG><<<C::kCtas * sm_count(), C::kThreads, C::kBytes, st>>>(g);
     return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
-int run_few(const AttnArgs &g, cudaStream_t st)
+template <int D, int FMT>
+static int launch_few_rows(const AttnArgs &g, int rows, cudaStream_t st)
+{
+    if (rows <= 16) return launch_few<D, FMT, 1>(g, st);
+    if (rows <= 32) return launch_few<D, FMT, 2>(g, st);
+    return launch_few<D, FMT, 4>(g, st);
+}
+
+int run_few(const AttnArgs &g, int rows, cudaStream_t st)
 {
     if (g.c.head_dim == 128) {
-        if (g.c.format == FP8_KV_BF16) return launch_few<128, FP8_KV_BF16>(g, st);
-        if (g.c.format == FP8_KV_E5M2) return launch_few<128, FP8_KV_E5M2>(g, st);
-        return launch_few<128, FP8_KV_E4M3>(g, st);
+        if (g.c.format == FP8_KV_BF16) return launch_few_rows<128, FP8_KV_BF16>(g, rows, st);
+        if (g.c.format == FP8_KV_E5M2) return launch_few_rows<128, FP8_KV_E5M2>(g, rows, st);
+        return launch_few_rows<128, FP8_KV_E4M3>(g, rows, st);
     }
-    if (g.c.format == FP8_KV_BF16) return launch_few<64, FP8_KV_BF16>(g, st);
-    if (g.c.format == FP8_KV_E5M2) return launch_few<64, FP8_KV_E5M2>(g, st);
-    return launch_few<64, FP8_KV_E4M3>(g, st);
+    if (g.c.format == FP8_KV_BF16) return launch_few_rows<64, FP8_KV_BF16>(g, rows, st);
+    if (g.c.format == FP8_KV_E5M2) return launch_few_rows<64, FP8_KV_E5M2>(g, rows, st);
+    return launch_few_rows<64, FP8_KV_E4M3>(g, rows, st);
 }
 
 }  // namespace fp8fg
