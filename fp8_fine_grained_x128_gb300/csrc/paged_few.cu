@@ -25,22 +25,24 @@
 
 namespace fp8fg {
 
-// MG groups of 16 rows, each to KS warps that take 16 keys each of a KS x 16-key
-// tile; the MG warps that share 16 keys share their ring.  One group: three
-// CTAs of four warps per SM; two and four groups: one CTA of twelve, whose
-// registers (168 a thread) fill the SM.
+constexpr int kFewThreads = 128, kFewCtas = 3;
+
+// MG groups of 16 rows (1, 2 or 4) and 4 / MG slices of 16 keys: a warp has one
+// group and one slice, and the MG warps of a slice share its ring.  Three CTAs
+// of four warps per SM (168 registers a thread fill it): while one starts or
+// ends a pair, the others' copies go on.  (One CTA of twelve warps left the
+// memory idle meanwhile: 84 against 60 us for 32 sequences x 5 tokens.)
 template <int D, int FMT, int MG>
 struct Few {
     static constexpr int kEsz = FMT == FP8_KV_BF16 ? 2 : 1;
-    static constexpr int kSlices = MG == 1 ? 4 : 12 / MG;
-    static constexpr int kThreads = 32 * MG * kSlices;
-    static constexpr int kCtas = MG == 1 ? 3 : 1;               // per SM
+    static constexpr int kSlices = 4 / MG;
     static constexpr int kTile = 16 * kSlices;                  // keys
     static constexpr int kRows = 16 * MG;
+    static constexpr int kPairCost = 2 * MG;                    // a pair's own time (start, join) in tiles' times
     static constexpr int kRowB = D * kEsz;
     static constexpr int kCh = kRowB / 16;                      // 16-byte chunks of a row
     static constexpr int kStage = 2 * 16 * kRowB;               // K and V of 16 keys
-    static constexpr int kFit = (MG == 1 ? 64 : 192) * 1024 / (kSlices * kStage);
+    static constexpr int kFit = 64 * 1024 / (kSlices * kStage);
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kRing = kSlices * kStages * kStage;
     static constexpr int kORow = D + 8;                         // floats of a merge row (bank spread)
@@ -49,7 +51,8 @@ struct Few {
     static constexpr float kOff = FMT == FP8_KV_BF16 ? 0.0f : 6.0f;   // P is kept as 2^kOff p
 };
 
-// Tiles of sequence b (0: not one of this kernel's).
+// Tiles of a pair of sequence b (0: not one of this kernel's), and its places in
+// the line: kPairCost for the pair, then its tiles.
 template <class C>
 __device__ __forceinline__ int few_tiles(const AttnArgs &g, int b)
 {
@@ -58,6 +61,13 @@ __device__ __forceinline__ int few_tiles(const AttnArgs &g, int b)
     if (!seq_lengths(g, b, first, rows, len)) set_status(g.status, FP8_ERR_INVALID_ARG);
     if (rows < 1 || rows > C::kRows) return 0;
     return max(1, (len + C::kTile - 1) / C::kTile);
+}
+
+template <class C>
+__device__ __forceinline__ int64_t few_places(const AttnArgs &g, int b)
+{
+    const int nt = few_tiles<C>(g, b);
+    return nt > 0 ? (int64_t)(C::kPairCost + nt) * g.c.heads : 0;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -123,10 +133,10 @@ struct FewPart {   // a broken pair's part in the workspace
 };
 
 template <int D, int FMT, int MG>
-__global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kCtas) k_attn_few(AttnArgs g)
+__global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
 {
     using C = Few<D, FMT, MG>;
-    constexpr int kThreads = C::kThreads, kSlices = C::kSlices;
+    constexpr int kThreads = kFewThreads, kSlices = C::kSlices;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sums[kThreads / 32], s_start[2];
     __shared__ float s_m[kSlices][C::kRows], s_l[kSlices][C::kRows];
@@ -135,12 +145,13 @@ __global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kC
     const int gr = lane >> 2, t4 = lane & 3;
     const int slice = warp / MG, mrow = 16 * (warp % MG);   // this warp's keys of a tile and first row
 
-    // this CTA's run [s, s_end) of the line of tiles, and the pair it starts in
-    int64_t total = 0, sum, ctas, s, s_end;
+    // this CTA's run [s, s_end) of the line of tiles, and the sequence it starts in
+    int64_t total = 0, sum, ctas, s, s_end, n, incl;
     int b = 0;
-    int64_t before = 0;   // tiles of the sequences before b
+    int64_t before = 0;   // places of the sequences before b
     for (int b0 = 0; b0 < g.b.seqs; b0 += kThreads) {
-        cta_scan((int64_t)few_tiles<C>(g, b0 + tid) * g.c.heads, s_sums, sum);
+        n = few_places<C>(g, b0 + tid);
+        incl = cta_scan(n, s_sums, sum);
         total += sum;
     }
     if (total == 0) return;
@@ -149,8 +160,10 @@ __global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kC
     s = blockIdx.x * total / ctas;
     s_end = (blockIdx.x + 1) * total / ctas;
     for (int b0 = 0; b0 < g.b.seqs; b0 += kThreads) {
-        const int64_t n = (int64_t)few_tiles<C>(g, b0 + tid) * g.c.heads;
-        const int64_t incl = cta_scan(n, s_sums, sum);
+        if (g.b.seqs > kThreads) {   // (else the sums are still here)
+            n = few_places<C>(g, b0 + tid);
+            incl = cta_scan(n, s_sums, sum);
+        }
         if (s < before + sum) {
             if (s >= before + incl - n && s < before + incl) {
                 s_start[0] = b0 + tid;
@@ -169,28 +182,52 @@ __global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kC
     float *merge = reinterpret_cast<float *>(smem);
     const uint8_t *kbase = static_cast<const uint8_t *>(g.c.k), *vbase = static_cast<const uint8_t *>(g.c.v);
 
+    int pages = 0, pbase = 0, pages_of = -1;
     while (s < s_end && b < g.b.seqs) {   // (b ends the walk only if the lengths changed meanwhile)
         int first, rows, len;
         seq_lengths(g, b, first, rows, len);
         const int nt = few_tiles<C>(g, b);
-        if ((int64_t)nt * g.c.heads <= s - before) {   // the next sequence with tiles
-            before += (int64_t)nt * g.c.heads;
+        const int64_t seq_end = before + (nt > 0 ? (int64_t)(C::kPairCost + nt) * g.c.heads : 0);
+        if (seq_end <= s) {   // the next sequence with tiles
+            before = seq_end;
             ++b;
+            pages_of = -1;
             continue;
         }
-        const int h = (int)((s - before) / nt), tile0 = (int)(s - before - (int64_t)h * nt);
-        const int tile1 = (int)min((int64_t)nt, tile0 + (s_end - s));
+        const int h = (int)((s - before) / (C::kPairCost + nt));
+        const int64_t pair0 = before + (int64_t)h * (C::kPairCost + nt) + C::kPairCost;   // the place of its first tile
+        const int tile0 = (int)max((int64_t)0, s - pair0), tile1 = (int)min((int64_t)nt, s_end - pair0);
+        s = min(s_end, pair0 + nt);
+        if (tile1 <= tile0) continue;   // a run that ends before the pair's tiles
         const int new_tokens = rows / g.group;
         const int32_t *table = g.b.page_table + b * g.b.page_table_ld;
 
+        // this lane's chunks of Q rows gr and gr + 8: on their way before the copies
+        uint4 qv[2][D / 32];
+        int pos[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int row = mrow + gr + 8 * u, tok = row / g.group;
+            pos[u] = row < rows ? len - new_tokens + tok : -1;
+            const uint16_t *qp = g.q + (int64_t)(first + tok) * g.q_ld + (int64_t)(h * g.group + row % g.group) * D;
+            // BF16: chunk t4 + 4c of 8 values; FP8: 16 values, two chunks side by side
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                const int d = FMT == FP8_KV_BF16 ? 8 * (t4 + 4 * c) : 16 * (t4 + 4 * (c / 2)) + 8 * (c % 2);
+                qv[u][c] = row < rows ? *reinterpret_cast<const uint4 *>(qp + d) : make_uint4(0, 0, 0, 0);
+            }
+        }
+
         // copies of tile i's 16 keys of this slice into its ring, spread over its warps
-        int pages = 0, pbase = tile0 - 32;
+        // (the pages of 32 tiles at a time, a tile a lane; those at hand serve a sequence's next head too)
+        if (pages_of != b || tile0 < pbase || tile0 >= pbase + 32) pbase = tile0 - 32;
+        pages_of = b;
         auto issue = [&](int i) {
             if (i < tile1) {
                 if (i - pbase >= 32) {
                     pbase = i;
                     const int key = (i + lane) * C::kTile + slice * 16;
-                    pages = (i + lane < tile1 && key < len) ? table[key / g.c.page_size] : 0;
+                    pages = (i + lane < nt && key < len) ? table[key / g.c.page_size] : 0;
                     if (pages < 0 || pages >= g.c.num_pages) {
                         set_status(g.status, FP8_ERR_INVALID_ARG);
                         pages = -1;
@@ -225,20 +262,9 @@ __global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kC
         // Q as the A operand of D / 16 contraction steps; rows gr and gr + 8
         uint32_t qa[D / 16][4];
         float mul[2];
-        int pos[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int row = mrow + gr + 8 * u;
-            const int tok = row / g.group;
-            pos[u] = row < rows ? len - new_tokens + tok : -1;
-            uint4 v[D / 32];
-            const uint16_t *qp = g.q + (int64_t)(first + tok) * g.q_ld + (int64_t)(h * g.group + row % g.group) * D;
-            // BF16: chunk t4 + 4c of 8 values; FP8: 16 values, two chunks side by side
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const int d = FMT == FP8_KV_BF16 ? 8 * (t4 + 4 * c) : 16 * (t4 + 4 * (c / 2)) + 8 * (c % 2);
-                v[c] = row < rows ? *reinterpret_cast<const uint4 *>(qp + d) : make_uint4(0, 0, 0, 0);
-            }
+            const uint4 (&v)[D / 32] = qv[u];
             mul[u] = g.scale * kLog2e * ks;
             float up = 1.0f;
             if (FMT != FP8_KV_BF16) {   // a power of two that brings the row's largest value into [2^14, 2^15)
@@ -414,7 +440,6 @@ __global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kC
         }
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == nt;
-        const int64_t pair0 = before + (int64_t)h * nt;   // the pair's place in the line
         using Part = FewPart<C::kRows>;
         Part *part = static_cast<Part *>(g.few_parts) + 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
         auto write_row = [&](int row, int d, float4 v, float mr, float lr) {
@@ -458,12 +483,14 @@ __global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kC
             // CTA c's run starts at floor(c total / ctas): c holds tile p iff c = ceil((p + 1) ctas / total) - 1
             const int64_t c0 = ((pair0 + 1) * ctas + total - 1) / total - 1;
             const int64_t c1 = ((pair0 + nt) * ctas + total - 1) / total - 1;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(&g.few_count[c0], 1) == (int)(c1 - c0);
+            __syncthreads();   // the CTA's stores, then one thread's fence for them all
+            if (tid == 0) {
+                __threadfence();
+                s_last = atomicAdd(&g.few_count[c0], 1) == (int)(c1 - c0);
+                __threadfence();
+            }
             __syncthreads();
             if (s_last) {
-                __threadfence();
                 const Part *parts = static_cast<const Part *>(g.few_parts);
                 for (int e = tid; e < rows * (D / 4); e += kThreads) {
                     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
@@ -487,22 +514,18 @@ __global__ void __launch_bounds__(Few<D, FMT, MG>::kThreads, Few<D, FMT, MG>::kC
             }
         }
         __syncthreads();    // the merge buffer becomes the ring again
-        s += tile1 - tile0;
     }
 }
 
-int few_grid() { return 3 * sm_count(); }
+int few_grid() { return kFewCtas * sm_count(); }
 
-size_t few_parts_bytes()
-{
-    return (size_t)sm_count() * 2 * std::max(3 * sizeof(FewPart<16>), std::max(sizeof(FewPart<32>), sizeof(FewPart<64>)));
-}
+size_t few_parts_bytes() { return (size_t)few_grid() * 2 * sizeof(FewPart<kFewMost>); }
 
 template <int D, int FMT, int MG>
 static int launch_few(const AttnArgs &g, cudaStream_t st)
 {
     using C = Few<D, FMT, MG>;
-    static_assert(C::kCtas * C::kBytes <= 224 * 1024 && C::kStages >= 2, "the rings do not fit the SM");
+    static_assert(kFewCtas * C::kBytes <= 224 * 1024 && C::kStages >= 2, "the rings do not fit the SM");
     static bool attr_done[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -512,7 +535,7 @@ static int launch_few(const AttnArgs &g, cudaStream_t st)
             return FP8_ERR_CUDA;
         attr_done[dev & 63] = true;
     }
-    k_attn_few<D, FMT, MG><<<C::kCtas * sm_count(), C::kThreads, C::kBytes, st>>>(g);
+    k_attn_few<D, FMT, MG><<<few_grid(), kFewThreads, C::kBytes, st>>>(g);
     return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
 }
 
