@@ -170,7 +170,12 @@ _I32 = (torch.int32,)
 _OUT = (torch.bfloat16, torch.float32)
 
 
+_cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _on_device(t, name, dtypes):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.get_device() == _cuda_device():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.device.type != "cuda":
@@ -228,8 +233,13 @@ def _gran_scales(gran, rows, cols):
     return 1
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
     if stream is None:
+        if _raw_stream is not None:   # without the Stream object: 0.1 instead of 3 us a call
+            return _raw_stream(_cuda_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -555,7 +565,7 @@ class PagedKV:
         st.format = kinds[k.dtype]
         st.num_pages, st.heads, st.page_size, st.head_dim = k.shape
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.heads, self.head_dim, self.device = k.shape[1], k.shape[3], k.device
+        self.heads, self.head_dim, self.device, self._device = k.shape[1], k.shape[3], k.device, k.get_device()
         self._ref = ctypes.byref(st)
 
 
@@ -569,29 +579,31 @@ class PagedBatch:
         st = _PagedBatch(_buf(q_offsets, "q_offsets", _I32, seqs + 1), _buf(kv_lens, "kv_lens", _I32, seqs), pt, ld,
                          seqs, width, int(max_new))
         self.q_offsets, self.kv_lens, self.page_table, self.max_new = q_offsets, kv_lens, page_table, int(max_new)
-        self.device = page_table.device
+        self.device, self._device = page_table.device, page_table.get_device()
         self._ref = ctypes.byref(st)
 
 
 def _paged(cache, batch):
     if not isinstance(cache, PagedKV) or not isinstance(batch, PagedBatch):
         raise TypeError("cache, batch: expected a PagedKV and a PagedBatch")
-    if cache.device != batch.device or cache.device.index != torch.cuda.current_device():
+    if not cache._device == batch._device == _cuda_device():
         raise ValueError(f"cache on {cache.device}, batch on {batch.device}: both must be on the current device")
     return cache._ref, batch._ref
 
 
 def _heads(t, name, tokens, heads, dim):
-    """(pointer, row stride) of a [tokens, heads, dim] BF16 tensor whose heads lie side by side."""
+    """(pointer, row stride, tokens, heads) of a [tokens, heads, dim] BF16 tensor whose heads lie side by side."""
     _on_device(t, name, _BF16)
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads) or \
-            (tokens is not None and t.shape[0] != tokens):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{'tokens' if tokens is None else tokens}]"
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads) or \
+            (tokens is not None and shape[0] != tokens):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{'tokens' if tokens is None else tokens}]"
                          f"[{'heads' if heads is None else heads}][{dim}]")
+    T, H, _ = shape
     sT, sH, sE = t.stride()
-    if t.numel() and (sE != 1 or (t.shape[1] > 1 and sH != dim)):
+    if (sE != 1 or (sH != dim and H > 1)) and t.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous (strides {t.stride()})")
-    return t.data_ptr(), (sT if t.shape[0] > 1 else t.shape[1] * dim)
+    return t.data_ptr(), (sT if T > 1 else H * dim), T, H
 
 
 def rope_append_kv(cache, batch, k, v, rope=None, q=None, q_out=None, interleaved=False, stream=None):
@@ -601,17 +613,15 @@ def rope_append_kv(cache, batch, k, v, rope=None, q=None, q_out=None, interleave
     L = lib()
     refs = _paged(cache, batch)
     D = cache.head_dim
-    pk, ldk = _heads(k, "k", None, cache.heads, D)
-    T = k.shape[0]
-    pv, ldv = _heads(v, "v", T, cache.heads, D)
+    pk, ldk, T, _ = _heads(k, "k", None, cache.heads, D)
+    pv, ldv, _, _ = _heads(v, "v", T, cache.heads, D)
     if (q is None) != (q_out is None):
         raise ValueError("q, q_out: give both or neither")
     pq = pqo = None
     ldq = ldqo = H = 0
     if q is not None:
-        pq, ldq = _heads(q, "q", T, None, D)
-        H = q.shape[1]
-        pqo, ldqo = _heads(q_out, "q_out", T, H, D)
+        pq, ldq, _, H = _heads(q, "q", T, None, D)
+        pqo, ldqo, _, _ = _heads(q_out, "q_out", T, H, D)
     pr, n, rot = None, 0, 0
     if rope is not None:
         n, rot = _shape(rope, "rope", 2)
@@ -634,9 +644,8 @@ def paged_attention(cache, batch, q, out, workspace, lse=None, scale=None, strea
     L = lib()
     refs = _paged(cache, batch)
     D = cache.head_dim
-    pq, ldq = _heads(q, "q", None, None, D)
-    T, H = q.shape[:2]
-    po, ldo = _heads(out, "out", T, H, D)
+    pq, ldq, T, H = _heads(q, "q", None, None, D)
+    po, ldo, _, _ = _heads(out, "out", T, H, D)
     pl = _buf(lse, "lse", _F32, T * H, True)
     ws = _buf(workspace, "workspace", (torch.uint8,), _attention_workspace())
     _check("fp8_paged_attention", L.fp8_paged_attention(*refs, T, pq, ldq, H, D ** -0.5 if scale is None else scale,
@@ -647,7 +656,7 @@ _ws_bytes = {}
 
 
 def _attention_workspace():
-    dev = torch.cuda.current_device()
+    dev = _cuda_device()
     if dev not in _ws_bytes:
         _ws_bytes[dev] = int(lib().fp8_paged_attention_workspace_bytes())
     return _ws_bytes[dev]
