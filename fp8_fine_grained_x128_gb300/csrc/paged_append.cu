@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
 {
     constexpr int kLanes = D / 16;             // lanes of a head row
     constexpr int kSlots = 32 / kLanes;        // head rows side by side in a warp
+    dependents_launch();
+    dependency_wait();
     const int lane = threadIdx.x & 31;
     const int64_t w = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
     const int64_t t = w / g.parts;
@@ -223,11 +225,8 @@ static int run_append(AppendArgs &g, int interleaved, cudaStream_t st)
     g.parts = (g.q_heads + 2 * g.c.heads + per_warp - 1) / per_warp;
     const int64_t warps = g.tokens * g.parts, blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (blocks >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
-    if (interleaved)
-        k_rope_append<D, FMT, true><<<(unsigned)blocks, kAppendThreads, 0, st>>>(g);
-    else
-        k_rope_append<D, FMT, false><<<(unsigned)blocks, kAppendThreads, 0, st>>>(g);
-    return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    return launch_dependent(interleaved ? k_rope_append<D, FMT, true> : k_rope_append<D, FMT, false>, dim3((unsigned)blocks),
+                            kAppendThreads, 0, st, g);
 }
 
 int launch_rope_append_kv(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, int64_t tokens, const void *q,

@@ -145,6 +145,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
     const int gr = lane >> 2, t4 = lane & 3;
     const int slice = warp / MG, mrow = 16 * (warp % MG);   // this warp's keys of a tile and first row
 
+    dependents_launch();
+    dependency_wait();
     // this CTA's run [s, s_end) of the line of tiles, and the sequence it starts in
     int64_t total = 0, sum, ctas, s, s_end, n, incl;
     int b = 0;
@@ -157,8 +159,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
     if (total == 0) return;
     ctas = min((int64_t)gridDim.x, total);
     if (blockIdx.x >= ctas) return;
-    s = blockIdx.x * total / ctas;
-    s_end = (blockIdx.x + 1) * total / ctas;
+    s = div_short(blockIdx.x * total, ctas);
+    s_end = div_short((blockIdx.x + 1) * total, ctas);
     for (int b0 = 0; b0 < g.b.seqs; b0 += kThreads) {
         if (g.b.seqs > kThreads) {   // (else the sums are still here)
             n = few_places<C>(g, b0 + tid);
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
             pages_of = -1;
             continue;
         }
-        const int h = (int)((s - before) / (C::kPairCost + nt));
+        const int h = (int)div_short(s - before, C::kPairCost + nt);
         const int64_t pair0 = before + (int64_t)h * (C::kPairCost + nt) + C::kPairCost;   // the place of its first tile
         const int tile0 = (int)max((int64_t)0, s - pair0), tile1 = (int)min((int64_t)nt, s_end - pair0);
         s = min(s_end, pair0 + nt);
@@ -481,8 +483,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
         }
         if (!whole) {
             // CTA c's run starts at floor(c total / ctas): c holds tile p iff c = ceil((p + 1) ctas / total) - 1
-            const int64_t c0 = ((pair0 + 1) * ctas + total - 1) / total - 1;
-            const int64_t c1 = ((pair0 + nt) * ctas + total - 1) / total - 1;
+            const int64_t c0 = div_short((pair0 + 1) * ctas + total - 1, total) - 1;
+            const int64_t c1 = div_short((pair0 + nt) * ctas + total - 1, total) - 1;
             __syncthreads();   // the CTA's stores, then one thread's fence for them all
             if (tid == 0) {
                 __threadfence();
@@ -535,8 +537,7 @@ static int launch_few(const AttnArgs &g, cudaStream_t st)
             return FP8_ERR_CUDA;
         attr_done[dev & 63] = true;
     }
-    k_attn_few<D, FMT, MG><<<few_grid(), kFewThreads, C::kBytes, st>>>(g);
-    return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    return launch_dependent(k_attn_few<D, FMT, MG>, dim3(few_grid()), kFewThreads, C::kBytes, st, g);
 }
 
 template <int D, int FMT>

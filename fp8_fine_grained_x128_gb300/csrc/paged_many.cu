@@ -298,6 +298,8 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     constexpr int kWarps = C::kThreads / 32;
 
+    dependents_launch();
+    dependency_wait();
     // the line's length
     int64_t total = 0;
     for (int b = warp; b < g.b.seqs; b += kWarps) {
@@ -888,6 +890,8 @@ constexpr int kJoinSlices = 8;
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_join(AttnArgs g, float off)
 {
+    dependents_launch();
+    dependency_wait();
     const ManyJoin j = static_cast<const ManyJoin *>(g.many_joins)[blockIdx.x];
     if (j.rows == 0) return;
     const int c0 = blockIdx.x;
@@ -950,10 +954,9 @@ static int launch_many(const AttnArgs &g, cudaStream_t st)
         !make_map_pages(&mV, type, g.c.v, D, g.c.page_size, g.c.heads, g.c.num_pages, g.c.v_row_stride * esz,
                         g.c.v_head_stride * esz, g.c.v_page_stride * esz, C::kFp8 ? D : 64, box_rows, !C::kFp8))
         return FP8_ERR_CUDA;
-    k_attn_many<D, FMT><<<sm_count(), C::kThreads, C::kBytes, st>>>(mK, mV, g, box_rows);
-    if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
-    k_attn_join<D><<<dim3(sm_count(), kJoinSlices), 256, 0, st>>>(g, C::kOff);
-    return cudaGetLastError() == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    const int rc = launch_dependent(k_attn_many<D, FMT>, dim3(sm_count()), C::kThreads, C::kBytes, st, mK, mV, g, box_rows);
+    if (rc != FP8_OK) return rc;
+    return launch_dependent(k_attn_join<D>, dim3(sm_count(), kJoinSlices), 256, 0, st, g, C::kOff);
 }
 
 int run_many(const AttnArgs &g, cudaStream_t st)
