@@ -39,15 +39,7 @@ struct Vec16 {   // two chunks of 8 BF16
     uint4 a, b;
 };
 
-__device__ __forceinline__ bool has_nonfinite8(uint4 v)
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
-    return bad;
-}
+__device__ __forceinline__ bool has_nonfinite16(const Vec16 &v) { return max(absmax8(v.a), absmax8(v.b)) >= 0x7F80u; }
 
 __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8])
 {
@@ -128,7 +120,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
     int row[kAppendRows];
 #pragma unroll
     for (int i = 0; i < kAppendRows; ++i) {
-        const int r = (part * kAppendRows + i) * kSlots + slot;
+        const int r = (i * g.parts + part) * kSlots + slot;   // (every warp has its share of the keys and values)
         row[i] = r < rows ? r : -1;
         if (r >= rows) continue;
         const uint16_t *p = r < g.q_heads                ? g.q + t * g.q_ld + (int64_t)r * D
@@ -182,7 +174,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
         float a[8], b[8];
         unpack8(x[i].a, a);
         unpack8(x[i].b, b);
-        if (!is_q && (has_nonfinite8(x[i].a) || has_nonfinite8(x[i].b))) set_status(g.status, FP8_ERR_NONFINITE);
+        if (!is_q && has_nonfinite16(x[i])) set_status(g.status, FP8_ERR_NONFINITE);
         if (turn && !is_v) {
             if (INTERLEAVED) {
 #pragma unroll
