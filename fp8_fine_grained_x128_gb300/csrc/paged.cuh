@@ -69,17 +69,15 @@ __device__ __forceinline__ bool seq_lengths(const AttnArgs &g, int b, int &first
     return true;
 }
 
-// Two FP8 codes (the low 16 bits of w) as FP16, exactly.
+// The four FP8 codes of w as two pairs of FP16 values, exactly.
 template <int FMT>
-__device__ __forceinline__ uint32_t fp8x2_f16(uint32_t w)
+__device__ __forceinline__ void fp8x4_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t h;
-    const uint16_t c = (uint16_t)w;
     if (FMT == FP8_KV_E4M3)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-    else
-        asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(c));
-    return h;
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+    else   // an E5M2 code is an FP16 number's upper byte
+        lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);
 }
 
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi)

@@ -91,6 +91,23 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
         mma_f16(c, a, b0, b1);
 }
 
+// Four products of P with FP8 values: a and b hold the codes of two keys each (bytes 2i and 2i + 1:
+// column i of the first two, of the last two products).
+template <int FMT>
+__device__ __forceinline__ void pv4(float (&o0)[4], float (&o1)[4], float (&o2)[4], float (&o3)[4], const uint32_t (&p)[4],
+                                    uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1)
+{
+    uint32_t al, ah, bl, bh;
+    fp8x4_f16<FMT>(a0, al, ah);
+    fp8x4_f16<FMT>(b0, bl, bh);
+    mma16<FMT>(o0, p, al, bl);
+    mma16<FMT>(o1, p, ah, bh);
+    fp8x4_f16<FMT>(a1, al, ah);
+    fp8x4_f16<FMT>(b1, bl, bh);
+    mma16<FMT>(o2, p, al, bl);
+    mma16<FMT>(o3, p, ah, bh);
+}
+
 __device__ __forceinline__ uint2 lds64(uint32_t addr)
 {
     uint2 v;
@@ -289,7 +306,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
             }
         }
 
-        const bool fine = len - new_tokens < kFineKeys;
+        const bool fine = len - new_tokens < kFineKeys, two = rows > mrow + 8;
         const float lazy = FMT == FP8_KV_BF16 && len < kExactKeys ? 0.0f : kLazy;
         float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -318,10 +335,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
                             mma16<FMT>(x[n], qa[2 * c], w.x, w.y);
                             mma16<FMT>(x[n], qa[2 * c + 1], w.z, w.w);
                         } else {
-                            mma16<FMT>(x[n], qa[4 * c], fp8x2_f16<FMT>(w.x), fp8x2_f16<FMT>(w.x >> 16));
-                            mma16<FMT>(x[n], qa[4 * c + 1], fp8x2_f16<FMT>(w.y), fp8x2_f16<FMT>(w.y >> 16));
-                            mma16<FMT>(x[n], qa[4 * c + 2], fp8x2_f16<FMT>(w.z), fp8x2_f16<FMT>(w.z >> 16));
-                            mma16<FMT>(x[n], qa[4 * c + 3], fp8x2_f16<FMT>(w.w), fp8x2_f16<FMT>(w.w >> 16));
+                            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t b0, b1;
+                                fp8x4_f16<FMT>(v[e], b0, b1);
+                                mma16<FMT>(x[n], qa[4 * c + e], b0, b1);
+                            }
                         }
                     }
                 }
@@ -331,11 +351,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
                 float up[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
+                    if (u == 1 && !two) {   // rows 8 to 15 of the group: none
+                        pa[1] = pa[3] = pl[1] = pl[3] = 0;
+                        up[1] = 1.0f;
+                        continue;
+                    }
                     float v[4] = {x[0][2 * u], x[0][2 * u + 1], x[1][2 * u], x[1][2 * u + 1]};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + (e / 2) * 8 + 2 * t4 + (e & 1);
-                        v[e] = key <= pos[u] ? v[e] * mul[u] : -INFINITY;
+                    for (int e = 0; e < 4; ++e) v[e] *= mul[u];
+                    if (key0 + 15 > len - new_tokens) {   // some row may not see some of the keys
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + (e / 2) * 8 + 2 * t4 + (e & 1) > pos[u]) v[e] = -INFINITY;
                     }
                     float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -389,10 +416,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
                     for (int i4 = 0; i4 < 4; ++i4) {
                         const uint32_t a0 = __byte_perm(w[0][i4], w[1][i4], 0x5140), a1 = __byte_perm(w[0][i4], w[1][i4], 0x7362);
                         const uint32_t b0 = __byte_perm(w[2][i4], w[3][i4], 0x5140), b1 = __byte_perm(w[2][i4], w[3][i4], 0x7362);
-                        mma16<FMT>(o[4 * i4], pa, fp8x2_f16<FMT>(a0), fp8x2_f16<FMT>(b0));
-                        mma16<FMT>(o[4 * i4 + 1], pa, fp8x2_f16<FMT>(a0 >> 16), fp8x2_f16<FMT>(b0 >> 16));
-                        mma16<FMT>(o[4 * i4 + 2], pa, fp8x2_f16<FMT>(a1), fp8x2_f16<FMT>(b1));
-                        mma16<FMT>(o[4 * i4 + 3], pa, fp8x2_f16<FMT>(a1 >> 16), fp8x2_f16<FMT>(b1 >> 16));
+                        pv4<FMT>(o[4 * i4], o[4 * i4 + 1], o[4 * i4 + 2], o[4 * i4 + 3], pa, a0, a1, b0, b1);
                     }
                 } else {                 // column n of product j is head element 8 n + j
                     uint2 r[4];
@@ -404,10 +428,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
                     for (int i2 = 0; i2 < 2; ++i2) {
                         const uint32_t a0 = __byte_perm(w[0][i2], w[1][i2], 0x5140), a1 = __byte_perm(w[0][i2], w[1][i2], 0x7362);
                         const uint32_t b0 = __byte_perm(w[2][i2], w[3][i2], 0x5140), b1 = __byte_perm(w[2][i2], w[3][i2], 0x7362);
-                        mma16<FMT>(o[4 * i2], pa, fp8x2_f16<FMT>(a0), fp8x2_f16<FMT>(b0));
-                        mma16<FMT>(o[4 * i2 + 1], pa, fp8x2_f16<FMT>(a0 >> 16), fp8x2_f16<FMT>(b0 >> 16));
-                        mma16<FMT>(o[4 * i2 + 2], pa, fp8x2_f16<FMT>(a1), fp8x2_f16<FMT>(b1));
-                        mma16<FMT>(o[4 * i2 + 3], pa, fp8x2_f16<FMT>(a1 >> 16), fp8x2_f16<FMT>(b1 >> 16));
+                        pv4<FMT>(o[4 * i2], o[4 * i2 + 1], o[4 * i2 + 2], o[4 * i2 + 3], pa, a0, a1, b0, b1);
                     }
                 }
             }

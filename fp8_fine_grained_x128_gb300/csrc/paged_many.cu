@@ -856,10 +856,11 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                     const int r = r0 + i * (128 / kChunks);
                     uint4 v = codes[i];
                     if (r >= keys) v = make_uint4(0, 0, 0, 0);   // past the sequence's end
-                    const uint4 lo = make_uint4(fp8x2_f16<FMT>(v.x), fp8x2_f16<FMT>(v.x >> 16), fp8x2_f16<FMT>(v.y),
-                                                fp8x2_f16<FMT>(v.y >> 16));
-                    const uint4 hi = make_uint4(fp8x2_f16<FMT>(v.z), fp8x2_f16<FMT>(v.z >> 16), fp8x2_f16<FMT>(v.w),
-                                                fp8x2_f16<FMT>(v.w >> 16));
+                    uint4 lo, hi;
+                    fp8x4_f16<FMT>(v.x, lo.x, lo.y);
+                    fp8x4_f16<FMT>(v.y, lo.z, lo.w);
+                    fp8x4_f16<FMT>(v.z, hi.x, hi.y);
+                    fp8x4_f16<FMT>(v.w, hi.z, hi.w);
                     // the two halves of the row's 128-byte lines in opposite order: no bank met twice
                     const int odd = (c >> 2) & 1;
                     const int c0 = 2 * (c & 3) + odd, c1 = c0 ^ 1;
