@@ -444,7 +444,8 @@ static int paged_checks(const fp8_paged_kv_t *c, const fp8_paged_batch_t *b, int
         if (s <= 0 || s >= (int64_t)1 << 39) return FP8_ERR_SHAPE;
         if ((s * esz) % 16 != 0) return FP8_ERR_ALIGNMENT;
     }
-    if (c->k_row_stride < c->head_dim || c->v_row_stride < c->head_dim) return FP8_ERR_SHAPE;
+    for (int64_t s : {c->k_row_stride, c->v_row_stride})
+        if (s < c->head_dim || s >= (int64_t)1 << 22) return FP8_ERR_SHAPE;
     return aligned16(c->k) && aligned16(c->v) ? FP8_OK : FP8_ERR_ALIGNMENT;
 }
 

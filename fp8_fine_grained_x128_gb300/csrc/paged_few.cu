@@ -7,8 +7,8 @@
 // CTA, so ragged batches and a single long cache balance alike; a CTA's run
 // covers whole pairs, which it finishes alone, and at most two broken ones,
 // whose partial maxima, sums and outputs go to the workspace.  The last CTA
-// to arrive at a broken pair joins its parts in order (the result does not
-// depend on who is last).
+// to announce its part of a broken pair joins the parts in order (the result
+// does not depend on who is last).
 //
 // A warp takes 16 keys of each tile and never waits for another warp: its
 // copies (cp.async, zero-filled past the sequence's end) go through its own
@@ -153,11 +153,15 @@ template <int D, int FMT, int MG>
 __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
 {
     using C = Few<D, FMT, MG>;
+    using Part = FewPart<C::kRows>;
     constexpr int kThreads = kFewThreads, kSlices = C::kSlices;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sums[kThreads / 32], s_start[2];
     __shared__ float s_m[kSlices][C::kRows], s_l[kSlices][C::kRows];
-    __shared__ int s_last;
+    __shared__ struct Broken {
+        int first, rows, head, last;
+        int64_t c0, c1;
+    } s_broken[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gr = lane >> 2, t4 = lane & 3;
     const int slice = warp / MG, mrow = 16 * (warp % MG);   // this warp's keys of a tile and first row
@@ -199,8 +203,47 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
     const float ks = g.c.k_scale ? *g.c.k_scale : 1.0f, vs = g.c.v_scale ? *g.c.v_scale : 1.0f;
     const uint32_t ring = smem_u32(smem) + slice * (C::kStages * C::kStage);
     float *merge = reinterpret_cast<float *>(smem);
-    const uint8_t *kbase = static_cast<const uint8_t *>(g.c.k), *vbase = static_cast<const uint8_t *>(g.c.v);
+    const int page_shift = 31 - __clz(g.c.page_size);
 
+    // This lane's copies of a slice's 16 rows: kRpi rows an instruction of a warp, kCh lanes a row.  One
+    // group: the warp copies keys and values; two groups: one warp each; four: half of one each.
+    constexpr int kRpi = 32 / C::kCh, kAll = 16 / kRpi, kMine = MG == 4 ? kAll / 2 : kAll;
+    const int cp_first = MG == 4 ? (warp & 1) * kMine : 0;                       // its first instruction
+    const int cp_row = cp_first * kRpi + lane / C::kCh, cp_chunk = lane % C::kCh;
+    const uint8_t *cp_src[2];
+    int64_t page_b[2], head_b[2];
+    uint32_t row_b[2], cp_dst[2], cp_flip[2];
+#pragma unroll
+    for (int k = 0; k < (MG == 1 ? 2 : 1); ++k) {
+        const bool v = MG == 1 ? k == 1 : MG == 2 ? (warp & 1) != 0 : (warp & 2) != 0;
+        row_b[k] = (uint32_t)(C::kEsz * (v ? g.c.v_row_stride : g.c.k_row_stride));
+        page_b[k] = C::kEsz * (v ? g.c.v_page_stride : g.c.k_page_stride);
+        head_b[k] = C::kEsz * (v ? g.c.v_head_stride : g.c.k_head_stride);
+        cp_src[k] = static_cast<const uint8_t *>(v ? g.c.v : g.c.k) + (int64_t)cp_row * row_b[k] + cp_chunk * 16;
+        const bool v8 = v && FMT != FP8_KV_BF16;
+        cp_dst[k] = (v ? C::kStage / 2 : 0) + (v8 ? few_at<C::kCh, true>(cp_row, cp_chunk) : few_at<C::kCh, false>(cp_row, cp_chunk));
+        // what few_at exchanges from one instruction to the next (kRpi rows on)
+        cp_flip[k] = C::kCh == 8 ? (v8 ? 64 : 32) : 0;
+    }
+    auto copy = [&](uint32_t dst, const uint8_t *src, uint32_t step, uint32_t flip, int left) {
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            const uint32_t d = C::kCh == 16 ? dst ^ ((e & 3) << 4) : (e & 1) ? dst ^ flip : dst;
+            cp_async16z(d + e * 512, src + (uint32_t)(e * kRpi) * step, e * kRpi < left ? 16u : 0u);
+        }
+    };
+
+    auto write_row = [&](int first, int h, int row, int d, float4 v, float mr, float lr) {
+        const float inv = lr > 0.0f ? vs / lr : 0.0f;
+        const int64_t tok = first + row / g.group;
+        const int head = h * g.group + row % g.group;
+        const int64_t at = tok * g.out_ld + (int64_t)head * D + d;
+        if (dbg_span(at, 4, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status))
+            *reinterpret_cast<uint2 *>(g.out + at) = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
+        if (g.lse && d == 0)
+            g.lse[tok * g.q_heads + head] = lr > 0.0f ? (mr - C::kOff + log2f(lr)) * kLn2 : -INFINITY;
+    };
+    int nbroken = 0;   // pairs of this run that others have parts of
     int pages = 0, pbase = 0, pages_of = -1;
     while (s < s_end && b < g.b.seqs) {   // (b ends the walk only if the lengths changed meanwhile)
         int first, rows, len;
@@ -241,35 +284,30 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
         // (the pages of 32 tiles at a time, a tile a lane; those at hand serve a sequence's next head too)
         if (pages_of != b || tile0 < pbase || tile0 >= pbase + 32) pbase = tile0 - 32;
         pages_of = b;
+        const uint8_t *ph[2];
+#pragma unroll
+        for (int k = 0; k < (MG == 1 ? 2 : 1); ++k) ph[k] = cp_src[k] + h * head_b[k];
         auto issue = [&](int i) {
             if (i < tile1) {
                 if (i - pbase >= 32) {
                     pbase = i;
                     const int key = (i + lane) * C::kTile + slice * 16;
-                    pages = (i + lane < nt && key < len) ? table[key / g.c.page_size] : 0;
+                    pages = (i + lane < nt && key < len) ? table[key >> page_shift] : 0;
                     if (pages < 0 || pages >= g.c.num_pages) {
                         set_status(g.status, FP8_ERR_INVALID_ARG);
                         pages = -1;
                     }
                 }
                 const int key0 = i * C::kTile + slice * 16;
-                const int64_t page = __shfl_sync(0xffffffffu, pages, i - pbase);
+                const int page = __shfl_sync(0xffffffffu, pages, i - pbase);
                 if (key0 < len && page >= 0) {
-                    const int rip = key0 & (g.c.page_size - 1);
-                    const uint8_t *kp = kbase + C::kEsz * (page * g.c.k_page_stride + h * g.c.k_head_stride + rip * g.c.k_row_stride);
-                    const uint8_t *vp = vbase + C::kEsz * (page * g.c.v_page_stride + h * g.c.v_head_stride + rip * g.c.v_row_stride);
-                    const uint32_t dst = ring + ((i - tile0) % C::kStages) * C::kStage;
-                    constexpr int kHalf = 16 * C::kCh / 32;   // of a warp's copies: keys, then values
-#pragma unroll
-                    for (int e0 = 0; e0 < 2 * kHalf / MG; ++e0) {
-                        const int e = MG == 1 ? e0 : e0 * MG + warp % MG, v = e >= kHalf;
-                        const int i32 = (e - v * kHalf) * 32 + lane, r = i32 / C::kCh, c = i32 % C::kCh;
-                        const uint32_t n = key0 + r < len ? 16u : 0u;
-                        if (!v)
-                            cp_async16z(dst + few_at<C::kCh, false>(r, c), kp + C::kEsz * r * g.c.k_row_stride + c * 16, n);
-                        else
-                            cp_async16z(dst + C::kStage / 2 + few_at<C::kCh, FMT != FP8_KV_BF16>(r, c),
-                                        vp + C::kEsz * r * g.c.v_row_stride + c * 16, n);
+                    const uint32_t rip = key0 & (g.c.page_size - 1), dst = ring + ((i - tile0) % C::kStages) * C::kStage;
+                    const int left = len - key0 - cp_row;   // rows of this lane at or past it: zeros
+                    if (MG == 1) {
+                        copy(dst + cp_dst[0], ph[0] + page * page_b[0] + rip * row_b[0], row_b[0], cp_flip[0], left);
+                        copy(dst + cp_dst[1], ph[1] + page * page_b[1] + rip * row_b[1], row_b[1], cp_flip[1], left);
+                    } else {
+                        copy(dst + cp_dst[0], ph[0] + page * page_b[0] + rip * row_b[0], row_b[0], cp_flip[0], left);
                     }
                 }
             }
@@ -463,18 +501,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
         }
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == nt;
-        using Part = FewPart<C::kRows>;
         Part *part = static_cast<Part *>(g.few_parts) + 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
-        auto write_row = [&](int row, int d, float4 v, float mr, float lr) {
-            const float inv = lr > 0.0f ? vs / lr : 0.0f;
-            const int64_t tok = first + row / g.group;
-            const int head = h * g.group + row % g.group;
-            const int64_t at = tok * g.out_ld + (int64_t)head * D + d;
-            if (dbg_span(at, 4, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status))
-                *reinterpret_cast<uint2 *>(g.out + at) = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
-            if (g.lse && d == 0)
-                g.lse[tok * g.q_heads + head] = lr > 0.0f ? (mr - C::kOff + log2f(lr)) * kLn2 : -INFINITY;
-        };
         for (int e = tid; e < rows * (D / 4); e += kThreads) {
             const int row = e / (D / 4), d = (e % (D / 4)) * 4;
             float mr = s_m[0][row];
@@ -493,7 +520,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
                 lr += f * s_l[w][row];
             }
             if (whole) {
-                write_row(row, d, a, mr, lr);
+                write_row(first, h, row, d, a, mr, lr);
             } else {
                 *reinterpret_cast<float4 *>(part->o + row * D + d) = a;
                 if (d == 0) {
@@ -503,40 +530,49 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
             }
         }
         if (!whole) {
-            // CTA c's run starts at floor(c total / ctas): c holds tile p iff c = ceil((p + 1) ctas / total) - 1
-            const int64_t c0 = div_short((pair0 + 1) * ctas + total - 1, total) - 1;
-            const int64_t c1 = div_short((pair0 + nt) * ctas + total - 1, total) - 1;
-            __syncthreads();   // the CTA's stores, then one thread's fence for them all
-            if (tid == 0) {
-                __threadfence();
-                s_last = atomicAdd(&g.few_count[c0], 1) == (int)(c1 - c0);
-                __threadfence();
-            }
-            __syncthreads();
-            if (s_last) {
-                const Part *parts = static_cast<const Part *>(g.few_parts);
-                for (int e = tid; e < rows * (D / 4); e += kThreads) {
-                    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-                    float mr = -INFINITY, lr = 0.0f;
-                    for (int64_t c = c0; c <= c1; ++c) mr = fmaxf(mr, __ldcg(&parts[2 * c + (c == c0)].m[row]));
-                    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const Part &q = parts[2 * c + (c == c0)];
-                        const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&q.m[row]) - mr);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(q.o + row * D + d));
-                        a.x += f * v.x;
-                        a.y += f * v.y;
-                        a.z += f * v.z;
-                        a.w += f * v.w;
-                        lr += f * __ldcg(&q.l[row]);
-                    }
-                    write_row(row, d, a, mr, lr);
-                }
-                if (tid == 0) g.few_count[c0] = 0;
-            }
+            // CTA c's run starts at floor(c total / ctas): c holds place p iff c = ceil((p + 1) ctas / total) - 1
+            if (tid == 0)
+                s_broken[nbroken] = {first, rows, h, 0, div_short((pair0 + 1) * ctas + total - 1, total) - 1,
+                                     div_short((pair0 + nt) * ctas + total - 1, total) - 1};
+            ++nbroken;
         }
         __syncthreads();    // the merge buffer becomes the ring again
+    }
+
+    // The broken pairs' parts are announced when the run is done: a fence in its middle waited several
+    // microseconds for the stores under the other CTAs' copies.
+    if (nbroken == 0) return;
+    if (tid == 0) {
+        __threadfence();    // the CTA's stores (the barrier above), by one thread for them all
+        for (int k = 0; k < nbroken; ++k)
+            s_broken[k].last = atomicAdd(&g.few_count[s_broken[k].c0], 1) == (int)(s_broken[k].c1 - s_broken[k].c0);
+        __threadfence();
+    }
+    __syncthreads();
+    for (int k = 0; k < nbroken; ++k) {
+        const Broken q = s_broken[k];
+        if (!q.last) continue;
+        const Part *parts = static_cast<const Part *>(g.few_parts);
+        for (int e = tid; e < q.rows * (D / 4); e += kThreads) {
+            const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+            float mr = -INFINITY, lr = 0.0f;
+#pragma unroll 4
+            for (int64_t c = q.c0; c <= q.c1; ++c) mr = fmaxf(mr, __ldcg(&parts[2 * c + (c == q.c0)].m[row]));
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int64_t c = q.c0; c <= q.c1; ++c) {
+                const Part &p = parts[2 * c + (c == q.c0)];
+                const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&p.m[row]) - mr);
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.o + row * D + d));
+                a.x += f * v.x;
+                a.y += f * v.y;
+                a.z += f * v.z;
+                a.w += f * v.w;
+                lr += f * __ldcg(&p.l[row]);
+            }
+            write_row(q.first, q.head, row, d, a, mr, lr);
+        }
+        if (tid == 0) g.few_count[q.c0] = 0;
     }
 }
 
