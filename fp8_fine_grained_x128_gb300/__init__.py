@@ -631,10 +631,12 @@ def rope_append_kv(cache, batch, k, v, rope=None, q=None, q_out=None, interleave
 
 
 def new_attention_workspace(device="cuda") -> torch.Tensor:
-    """A zeroed workspace of paged_attention (the same for every batch; the library leaves its
-    counters zeroed)."""
+    """A workspace of paged_attention (the same for every batch) with its counters zeroed; the library
+    leaves them zeroed."""
     n = (int(lib().fp8_paged_attention_workspace_bytes()) + 15) // 16 * 16
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:16384].zero_()
+    return ws
 
 
 def paged_attention(cache, batch, q, out, workspace, lse=None, scale=None, stream=None):

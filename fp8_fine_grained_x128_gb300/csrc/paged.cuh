@@ -51,6 +51,9 @@ constexpr float kLazy = 8.0f;
 constexpr int kFineKeys = 128, kExactKeys = 2048;
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
+// Debug build: a token's LSE of one head lies inside the output.
+__device__ __forceinline__ bool dbg_lse(const AttnArgs &g, int64_t at) { return dbg_span(at, 1, g.tokens * g.q_heads, g.status); }
+
 // Sequence b: its first row of q, its rows (new tokens x group; 0: none, or not
 // to be read) and its length.  false: a value outside its range.
 __device__ __forceinline__ bool seq_lengths(const AttnArgs &g, int b, int &first, int &rows, int &len)

@@ -96,6 +96,12 @@ __device__ __forceinline__ void store_row(void *base, int64_t at, int ea, int eb
     }
 }
 
+// Where the cache's last row begins (debug build).
+__device__ __forceinline__ int64_t last_row(const fp8_paged_kv_t &c, int64_t page, int64_t head, int64_t row)
+{
+    return (c.num_pages - 1) * page + (c.heads - 1) * head + (c.page_size - 1) * row;
+}
+
 template <int D, int FMT, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
 {
@@ -202,10 +208,12 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
             }
         } else if (is_v) {
             const int64_t at = page * g.c.v_page_stride + (row[i] - g.q_heads - g.c.heads) * g.c.v_head_stride + rip * g.c.v_row_stride;
-            store_row<FMT>(g.c.v, at, ea, eb, a, b, vd);
+            if (dbg_span(at, D, last_row(g.c, g.c.v_page_stride, g.c.v_head_stride, g.c.v_row_stride) + D, g.status))
+                store_row<FMT>(g.c.v, at, ea, eb, a, b, vd);
         } else {
             const int64_t at = page * g.c.k_page_stride + (row[i] - g.q_heads) * g.c.k_head_stride + rip * g.c.k_row_stride;
-            store_row<FMT>(g.c.k, at, ea, eb, a, b, kd);
+            if (dbg_span(at, D, last_row(g.c, g.c.k_page_stride, g.c.k_head_stride, g.c.k_row_stride) + D, g.status))
+                store_row<FMT>(g.c.k, at, ea, eb, a, b, kd);
         }
     }
 }

@@ -16,11 +16,13 @@
 namespace fp8fg {
 
 // Workspace: k_attn_few's counters and parts, then k_attn_many's.
+// The counters alone have to start as zeros; the header promises their place.
+constexpr size_t kCounterBytes = 16384;
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t paged_attention_workspace_bytes()
 {
-    return align256((size_t)few_grid() * sizeof(int)) + align256(few_parts_bytes()) + align256(many_joins_bytes()) +
+    return kCounterBytes + align256(few_parts_bytes()) + align256(many_joins_bytes()) +
            many_parts_bytes();
 }
 
@@ -41,9 +43,10 @@ int launch_paged_attention(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, 
     g.out_ld = out_ld;
     g.lse = lse;
     g.status = status;
+    if (few_grid() * sizeof(int) > kCounterBytes) return FP8_ERR_UNSUPPORTED;   // (over 1365 SMs)
     uint8_t *p = static_cast<uint8_t *>(ws);
     g.few_count = reinterpret_cast<int *>(p);
-    p += align256((size_t)few_grid() * sizeof(int));
+    p += kCounterBytes;
     g.few_parts = p;
     p += align256(few_parts_bytes());
     g.many_joins = p;

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
         const int64_t at = tok * g.out_ld + (int64_t)head * D + d;
         if (dbg_span(at, 4, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status))
             *reinterpret_cast<uint2 *>(g.out + at) = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
-        if (g.lse && d == 0)
+        if (g.lse && d == 0 && dbg_lse(g, tok * g.q_heads + head))
             g.lse[tok * g.q_heads + head] = lr > 0.0f ? (mr - C::kOff + log2f(lr)) * kLn2 : -INFINITY;
     };
     int nbroken = 0;   // pairs of this run that others have parts of

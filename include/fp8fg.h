@@ -495,8 +495,8 @@ FP8FG_API int fp8_rope_append_kv(const fp8_paged_kv_t *cache, const fp8_paged_ba
                                  void *stream);
 
 /* Bytes of the caller-owned workspace of fp8_paged_attention on the current
- * device (the same for every batch).  Zero it once before the first use;
- * every call that completes leaves its counters zeroed again. */
+ * device (the same for every batch).  Zero its first 16 KiB (its counters)
+ * once before the first use; every call that completes leaves them zeroed. */
 FP8FG_API size_t fp8_paged_attention_workspace_bytes(void);
 
 /* Attention of the new tokens over the cache (their own keys and values
