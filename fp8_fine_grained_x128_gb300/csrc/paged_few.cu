@@ -384,51 +384,59 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
                     }
                 }
                 // log2 scores; keys a row does not see: -inf
-                uint32_t pa[4], pl[4];   // P, and its second term
-                bool grow = false;
-                float up[2];
+                float v[2][4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    if (u == 1 && !two) {   // rows 8 to 15 of the group: none
-                        pa[1] = pa[3] = pl[1] = pl[3] = 0;
-                        up[1] = 1.0f;
-                        continue;
-                    }
-                    float v[4] = {x[0][2 * u], x[0][2 * u + 1], x[1][2 * u], x[1][2 * u + 1]};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] *= mul[u];
+                    for (int e = 0; e < 4; ++e) v[u][e] = x[e / 2][2 * u + (e & 1)] * mul[u];
                     if (key0 + 15 > len - new_tokens) {   // some row may not see some of the keys
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (key0 + (e / 2) * 8 + 2 * t4 + (e & 1) > pos[u]) v[e] = -INFINITY;
-                    }
-                    float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    up[u] = 1.0f;
-                    if (mx > m[u] + lazy) {
-                        up[u] = ex2_approx_ftz(m[u] - mx);
-                        m[u] = mx;
-                        grow = true;
-                    }
-                    const float base = m[u] == -INFINITY ? 0.0f : m[u] - C::kOff;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = ex2_approx_ftz(v[e] - base);
-                    l[u] = l[u] * up[u] + ((v[0] + v[1]) + (v[2] + v[3]));
-                    pa[u] = FMT == FP8_KV_BF16 ? bf16x2_rn(v[0], v[1]) : f16x2_rn(v[0], v[1]);
-                    pa[u + 2] = FMT == FP8_KV_BF16 ? bf16x2_rn(v[2], v[3]) : f16x2_rn(v[2], v[3]);
-                    if (FMT == FP8_KV_BF16) {
-                        pl[u] = bf16x2_rn(v[0] - bf16_lo(pa[u]), v[1] - bf16_hi(pa[u]));
-                        pl[u + 2] = bf16x2_rn(v[2] - bf16_lo(pa[u + 2]), v[3] - bf16_hi(pa[u + 2]));
+                            if (key0 + (e / 2) * 8 + 2 * t4 + (e & 1) > pos[u]) v[u][e] = -INFINITY;
                     }
                 }
-                if (__any_sync(0xffffffffu, grow)) {
+                // The four lanes of a row raise its maximum together, and only when one of them has to: the
+                // shuffles are left out of nearly every block.
+                float mx[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) mx[u] = fmaxf(fmaxf(v[u][0], v[u][1]), fmaxf(v[u][2], v[u][3]));
+                if (__any_sync(0xffffffffu, mx[0] > m[0] + lazy || mx[1] > m[1] + lazy)) {
+                    float up[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+                        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+                        up[u] = 1.0f;
+                        if (mx[u] > m[u] + lazy) {
+                            up[u] = ex2_approx_ftz(m[u] - mx[u]);
+                            m[u] = mx[u];
+                        }
+                        l[u] *= up[u];
+                    }
 #pragma unroll
                     for (int j = 0; j < D / 8; ++j) {
                         o[j][0] *= up[0];
                         o[j][1] *= up[0];
                         o[j][2] *= up[1];
                         o[j][3] *= up[1];
+                    }
+                }
+                uint32_t pa[4], pl[4];   // P, and its second term
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u == 1 && !two) {   // rows 8 to 15 of the group: none
+                        pa[1] = pa[3] = pl[1] = pl[3] = 0;
+                        continue;
+                    }
+                    const float base = m[u] == -INFINITY ? 0.0f : m[u] - C::kOff;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[u][e] = ex2_approx_ftz(v[u][e] - base);
+                    l[u] += (v[u][0] + v[u][1]) + (v[u][2] + v[u][3]);
+                    pa[u] = FMT == FP8_KV_BF16 ? bf16x2_rn(v[u][0], v[u][1]) : f16x2_rn(v[u][0], v[u][1]);
+                    pa[u + 2] = FMT == FP8_KV_BF16 ? bf16x2_rn(v[u][2], v[u][3]) : f16x2_rn(v[u][2], v[u][3]);
+                    if (FMT == FP8_KV_BF16) {
+                        pl[u] = bf16x2_rn(v[u][0] - bf16_lo(pa[u]), v[u][1] - bf16_hi(pa[u]));
+                        pl[u + 2] = bf16x2_rn(v[u][2] - bf16_lo(pa[u + 2]), v[u][3] - bf16_hi(pa[u + 2]));
                     }
                 }
                 if (FMT == FP8_KV_BF16) {
