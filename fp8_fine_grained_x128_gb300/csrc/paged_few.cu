@@ -19,6 +19,7 @@
 // FP8 codes become FP16 exactly (one conversion per two codes); Q is scaled
 // by a power of two per row to fit FP16, and P by 2^6.
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "paged.cuh"
@@ -26,6 +27,7 @@
 namespace fp8fg {
 
 constexpr int kFewThreads = 128, kFewCtas = 3;
+constexpr int kDirectParts = 12;   // up to so many parts of a pair are joined without finding the maxima first
 
 // MG groups of 16 rows (1, 2 or 4) and 4 / MG slices of 16 keys: a warp has one
 // group and one slice, and the MG warps of a slice share its ring.  Three CTAs
@@ -39,6 +41,8 @@ struct Few {
     static constexpr int kTile = 16 * kSlices;                  // keys
     static constexpr int kRows = 16 * MG;
     static constexpr int kPairCost = 2 * MG;                    // a pair's own time (start, join) in tiles' times
+    // A shorter run of places costs more in joining its part (16 MG rows) than its tiles take.
+    static constexpr int kMinRun = 2 * MG;
     static constexpr int kRowB = D * kEsz;
     static constexpr int kCh = kRowB / 16;                      // 16-byte chunks of a row
     static constexpr int kStage = 2 * 16 * kRowB;               // K and V of 16 keys
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
         total += sum;
     }
     if (total == 0) return;
-    ctas = min((int64_t)gridDim.x, total);
+    ctas = min((int64_t)gridDim.x, (total + C::kMinRun - 1) / C::kMinRun);
     if (blockIdx.x >= ctas) return;
     s = div_short(blockIdx.x * total, ctas);
     s_end = div_short((blockIdx.x + 1) * total, ctas);
@@ -561,26 +565,114 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
         const Broken q = s_broken[k];
         if (!q.last) continue;
         const Part *parts = static_cast<const Part *>(g.few_parts);
-        for (int e = tid; e < q.rows * (D / 4); e += kThreads) {
-            const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-            float mr = -INFINITY, lr = 0.0f;
+        const int parts_n = (int)(q.c1 - q.c0) + 1;
+        auto part_of = [&](int i) -> const Part & { return parts[2 * (q.c0 + i) + (i == 0)]; };
+        // Few parts: each thread takes the maxima itself.  More than kDirectParts: they are found once a
+        // row, the parts side by side (5 sequences x 8 rows, 45 parts: 32 against 23 us; 32 x 20 rows, 2 to
+        // 3 parts: 57 against 62 us).
+        auto direct = [&](auto elements) {
+            constexpr int kE = decltype(elements)::value;
+            for (int e0 = tid; e0 < q.rows * (D / 4); e0 += kThreads * kE) {
+                const int d = (e0 % (D / 4)) * 4;   // (kThreads is a multiple of D / 4)
+                int row[kE];
+                float mr[kE], lr[kE];
+                float4 acc[kE];
+#pragma unroll
+                for (int k = 0; k < kE; ++k) {
+                    row[k] = min(e0 / (D / 4) + k * (kThreads / (D / 4)), q.rows - 1);
+                    mr[k] = -INFINITY;
+                    lr[k] = 0.0f;
+                    acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
 #pragma unroll 4
-            for (int64_t c = q.c0; c <= q.c1; ++c) mr = fmaxf(mr, __ldcg(&parts[2 * c + (c == q.c0)].m[row]));
-            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i = 0; i < parts_n; ++i)
+#pragma unroll
+                    for (int k = 0; k < kE; ++k) mr[k] = fmaxf(mr[k], __ldcg(&part_of(i).m[row[k]]));
 #pragma unroll 4
-            for (int64_t c = q.c0; c <= q.c1; ++c) {
-                const Part &p = parts[2 * c + (c == q.c0)];
-                const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&p.m[row]) - mr);
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.o + row * D + d));
-                a.x += f * v.x;
-                a.y += f * v.y;
-                a.z += f * v.z;
-                a.w += f * v.w;
-                lr += f * __ldcg(&p.l[row]);
+                for (int i = 0; i < parts_n; ++i) {
+                    const Part &p = part_of(i);
+#pragma unroll
+                    for (int k = 0; k < kE; ++k) {
+                        const float f = mr[k] == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&p.m[row[k]]) - mr[k]);
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.o + row[k] * D + d));
+                        acc[k].x += f * v.x;
+                        acc[k].y += f * v.y;
+                        acc[k].z += f * v.z;
+                        acc[k].w += f * v.w;
+                        lr[k] += f * __ldcg(&p.l[row[k]]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kE; ++k)
+                    if (e0 + k * kThreads < q.rows * (D / 4)) write_row(q.first, q.head, row[k], d, acc[k], mr[k], lr[k]);
             }
-            write_row(q.first, q.head, row, d, a, mr, lr);
-        }
+        };
         if (tid == 0) g.few_count[q.c0] = 0;
+        if (parts_n <= kDirectParts) {
+            if (q.rows * (D / 4) <= kThreads)
+                direct(std::integral_constant<int, 1>());
+            else
+                direct(std::integral_constant<int, 4>());
+            continue;
+        }
+        constexpr int kR = 4;
+        for (int row0 = warp * kR; row0 < q.rows; row0 += kR * (kThreads / 32)) {
+            float mr[kR], lr[kR] = {};
+#pragma unroll
+            for (int k = 0; k < kR; ++k) mr[k] = -INFINITY;
+            for (int i = lane; i < parts_n; i += 32)   // (rows past the last exist in the part: unused)
+#pragma unroll
+                for (int k = 0; k < kR; ++k) mr[k] = fmaxf(mr[k], __ldcg(&part_of(i).m[row0 + k]));
+#pragma unroll
+            for (int k = 0; k < kR; ++k)
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mr[k] = fmaxf(mr[k], __shfl_xor_sync(0xffffffffu, mr[k], o));
+            for (int i = lane; i < parts_n; i += 32)
+#pragma unroll
+                for (int k = 0; k < kR; ++k)
+                    lr[k] += mr[k] == -INFINITY ? 0.0f
+                                                : ex2_approx_ftz(__ldcg(&part_of(i).m[row0 + k]) - mr[k]) * __ldcg(&part_of(i).l[row0 + k]);
+#pragma unroll
+            for (int k = 0; k < kR; ++k) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) lr[k] += __shfl_xor_sync(0xffffffffu, lr[k], o);
+                if (lane == 0) {
+                    s_m[0][row0 + k] = mr[k];
+                    s_l[0][row0 + k] = lr[k];
+                }
+            }
+        }
+        __syncthreads();
+        // the outputs: two elements a thread and eight parts at a time in flight
+        constexpr int kE = 2;
+        for (int e0 = tid; e0 < q.rows * (D / 4); e0 += kThreads * kE) {
+            const int d = (e0 % (D / 4)) * 4;   // (kThreads is a multiple of D / 4)
+            int row[kE];
+            float4 acc[kE];
+#pragma unroll
+            for (int k = 0; k < kE; ++k) {
+                row[k] = min(e0 / (D / 4) + k * (kThreads / (D / 4)), q.rows - 1);
+                acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll 8
+            for (int i = 0; i < parts_n; ++i) {
+                const Part &p = part_of(i);
+#pragma unroll
+                for (int k = 0; k < kE; ++k) {
+                    const float mr = s_m[0][row[k]];
+                    const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&p.m[row[k]]) - mr);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.o + row[k] * D + d));
+                    acc[k].x += f * v.x;
+                    acc[k].y += f * v.y;
+                    acc[k].z += f * v.z;
+                    acc[k].w += f * v.w;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kE; ++k)
+                if (e0 + k * kThreads < q.rows * (D / 4)) write_row(q.first, q.head, row[k], d, acc[k], s_m[0][row[k]], s_l[0][row[k]]);
+        }
+        __syncthreads();   // (the other broken pair's maxima replace these)
     }
 }
 

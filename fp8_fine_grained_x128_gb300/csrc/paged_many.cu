@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
 
 // The parts of the broken units added up: block (c, y) joins a slice of the
 // rows of the unit that CTA c of k_attn_many started and did not finish.
-constexpr int kJoinSlices = 8;
+constexpr int kJoinSlices = 16;
 
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_join(AttnArgs g, float off)
@@ -899,10 +899,12 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs g, float off)
     auto part = [&](int c) { return g.many_parts + (int64_t)(2 * c + (c == c0)) * kPartFloats; };
     const float vs = g.c.v_scale ? *g.c.v_scale : 1.0f;
     constexpr int kRows = kUnitRows / kJoinSlices;
+#pragma unroll 1
     for (int e = threadIdx.x; e < kRows * (D / 4); e += 256) {
         const int lrow = blockIdx.y * kRows + e % kRows, d4 = e / kRows;
         if (lrow >= j.rows) continue;
         float m = -INFINITY, l = 0.0f;
+#pragma unroll 16
         for (int c = c0; c <= j.last; ++c) m = fmaxf(m, part(c)[kUnitRows * 128 + lrow]);
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int c = c0; c <= j.last; ++c) {
