@@ -35,10 +35,10 @@ struct AttnArgs {
     int *status;
 };
 
-// A batch whose sequences have at most kFewMost rows (new tokens x group) goes to
-// k_attn_few as a whole; in others the sequences of up to kFewRows do, and the
-// rest to k_attn_many.
-constexpr int kFewRows = 16, kFewMost = 64;
+// Rows of a sequence (new tokens x group) that k_attn_few takes: up to kFewRows
+// from any batch, up to kFewMost if the whole batch keeps to that.
+constexpr int kFewRows = 16, kFewMost = 32;
+constexpr int kDirectParts = 12;   // up to so many parts of a pair k_attn_few joins without finding the maxima first
 
 // The maximum in use may lag behind the true one by 2^kLazy before the sums
 // are rescaled: no result depends on it but through roundings.

@@ -13,7 +13,13 @@
 //
 // Bound: HBM bandwidth.  A warp takes one token and a run of head rows; a
 // lane owns the same two 8-element chunks in each of its rows, so its part of
-// the table row (16 FP32 values) is loaded once and stays in registers.
+// the table row (16 FP32 values) is loaded once and stays in registers.  All of
+// a lane's loads are in flight together, and the query, key and value rows are dealt
+// over a token's warps in turn, since only keys and values cost divisions.
+// Measured, 32 query and 8 cache heads of 128: 8 x 4096 tokens into a BF16 cache
+// 123 us (0.97 of the measured copy rate), 8192 tokens into an E4M3 cache 37.6 us (0.74: the ramp and
+// the last wave; the FP8 divisions fill half the issue slots), 16 single tokens
+// 9.4 us (a launch's latency).
 #include <algorithm>
 
 #include "kernels.h"

@@ -10,6 +10,14 @@
 // (mma.sync); the others go to k_attn_many (tcgen05, 256 rows a unit).  Each
 // kernel reads the lengths on the device and leaves the other's sequences
 // alone; a batch that can hold only short ones launches k_attn_few alone.
+//
+// Up to 32 rows k_attn_few (two operands) still is the faster one where there
+// are pairs enough that few parts of each have to be joined: with 32 query and 8
+// cache heads of 128, k_attn_few / k_attn_many take 98 / 118 us for 32 sequences
+// x 8 tokens over 4000 E4M3 keys, 61 / 114 for 64 x 5 over 1000, 115 / 115 for
+// 32 x 5 over 4000 BF16 keys, 33 / 31 for 8 x 8 over 1500 (64 pairs), but 60 / 32
+// for 1 x 8 over 8000 (8 pairs).  From 33 rows on the tensor cores win: 157 / 117
+// for 32 x 12 over 4000 E4M3 keys, 201 / 115 over BF16 ones.
 #include "kernels.h"
 #include "paged.cuh"
 
@@ -52,8 +60,8 @@ int launch_paged_attention(const fp8_paged_kv_t &c, const fp8_paged_batch_t &b, 
     g.many_joins = p;
     p += align256(many_joins_bytes());
     g.many_parts = reinterpret_cast<float *>(p);
-    const int64_t rows = (int64_t)b.max_new * g.group;
-    if (rows <= kFewMost) return run_few(g, (int)rows, st);
+    const int64_t rows = (int64_t)b.max_new * g.group, pairs = (int64_t)b.seqs * c.heads;
+    if (rows <= kFewRows || (rows <= kFewMost && pairs * kDirectParts >= few_grid())) return run_few(g, (int)rows, st);
     const int rc = run_few(g, kFewRows, st);
     return rc != FP8_OK ? rc : run_many(g, st);
 }

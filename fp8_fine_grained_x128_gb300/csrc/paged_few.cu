@@ -1,8 +1,13 @@
-// paged_few.cu -- attention over a paged cache when up to 16 rows (new tokens x
+// paged_few.cu -- attention over a paged cache when up to 32 rows (new tokens x
 // query heads of a group) share a cache head: single tokens and short drafts
 // (sm_103a).
 //
-// Bound: HBM bandwidth, every key and value read once.  All (sequence, head)
+// Bound: HBM bandwidth, every key and value read once (32 query and 8 cache heads
+// of 128: 64 ragged sequences of up to 8000 BF16 keys 198 us, 0.94 of the measured
+// copy rate; 16 x 65536 E4M3 keys 333 us, 0.95; one of 524287 BF16 keys 320 us,
+// 0.99).  With two operands of rows the time is a warp's own chain of copy wait, Q K^T,
+// softmax and P V (about 1660 cycles a tile, three CTAs side by side): 32 x 5 tokens over up
+// to 4001 E4M3 keys 59 us against 20 us for the bytes.  All (sequence, head)
 // pairs' 64-key tiles stand in one line that is cut into equal runs, one per
 // CTA, so ragged batches and a single long cache balance alike; a CTA's run
 // covers whole pairs, which it finishes alone, and at most two broken ones,
@@ -27,9 +32,8 @@
 namespace fp8fg {
 
 constexpr int kFewThreads = 128, kFewCtas = 3;
-constexpr int kDirectParts = 12;   // up to so many parts of a pair are joined without finding the maxima first
 
-// MG groups of 16 rows (1, 2 or 4) and 4 / MG slices of 16 keys: a warp has one
+// MG groups of 16 rows (1 or 2) and 4 / MG slices of 16 keys: a warp has one
 // group and one slice, and the MG warps of a slice share its ring.  Three CTAs
 // of four warps per SM (168 registers a thread fill it): while one starts or
 // ends a pair, the others' copies go on.  (One CTA of twelve warps left the
@@ -210,16 +214,15 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
     const int page_shift = 31 - __clz(g.c.page_size);
 
     // This lane's copies of a slice's 16 rows: kRpi rows an instruction of a warp, kCh lanes a row.  One
-    // group: the warp copies keys and values; two groups: one warp each; four: half of one each.
-    constexpr int kRpi = 32 / C::kCh, kAll = 16 / kRpi, kMine = MG == 4 ? kAll / 2 : kAll;
-    const int cp_first = MG == 4 ? (warp & 1) * kMine : 0;                       // its first instruction
-    const int cp_row = cp_first * kRpi + lane / C::kCh, cp_chunk = lane % C::kCh;
+    // group: the warp copies keys and values; two groups: one warp each.
+    constexpr int kRpi = 32 / C::kCh;
+    const int cp_row = lane / C::kCh, cp_chunk = lane % C::kCh;
     const uint8_t *cp_src[2];
     int64_t page_b[2], head_b[2];
     uint32_t row_b[2], cp_dst[2], cp_flip[2];
 #pragma unroll
     for (int k = 0; k < (MG == 1 ? 2 : 1); ++k) {
-        const bool v = MG == 1 ? k == 1 : MG == 2 ? (warp & 1) != 0 : (warp & 2) != 0;
+        const bool v = MG == 1 ? k == 1 : (warp & 1) != 0;
         row_b[k] = (uint32_t)(C::kEsz * (v ? g.c.v_row_stride : g.c.k_row_stride));
         page_b[k] = C::kEsz * (v ? g.c.v_page_stride : g.c.k_page_stride);
         head_b[k] = C::kEsz * (v ? g.c.v_head_stride : g.c.k_head_stride);
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
     }
     auto copy = [&](uint32_t dst, const uint8_t *src, uint32_t step, uint32_t flip, int left) {
 #pragma unroll
-        for (int e = 0; e < kMine; ++e) {
+        for (int e = 0; e < 16 / kRpi; ++e) {
             const uint32_t d = C::kCh == 16 ? dst ^ ((e & 3) << 4) : (e & 1) ? dst ^ flip : dst;
             cp_async16z(d + e * 512, src + (uint32_t)(e * kRpi) * step, e * kRpi < left ? 16u : 0u);
         }
@@ -700,9 +703,7 @@ static int launch_few(const AttnArgs &g, cudaStream_t st)
 template <int D, int FMT>
 static int launch_few_rows(const AttnArgs &g, int rows, cudaStream_t st)
 {
-    if (rows <= 16) return launch_few<D, FMT, 1>(g, st);
-    if (rows <= 32) return launch_few<D, FMT, 2>(g, st);
-    return launch_few<D, FMT, 4>(g, st);
+    return rows <= 16 ? launch_few<D, FMT, 1>(g, st) : launch_few<D, FMT, 2>(g, st);
 }
 
 int run_few(const AttnArgs &g, int rows, cudaStream_t st)

@@ -2,7 +2,11 @@
 // tokens x query heads of a group) share a cache head: prompts, chunks and
 // longer drafts (sm_103a).
 //
-// Bound: the tensor cores.  A unit is 256 rows of one (sequence, cache head):
+// Bound: the tensor cores, in long series the rate that the power limit leaves
+// them (32 query and 8 cache heads of 128: an 8192-token prompt 384 us, 1430
+// TFLOP/s, 364 us in short bursts; 2048 tokens after 30720 E4M3 keys 702 and 675 us,
+// 1520 and 1580).  With head_dim 64 an exponential stands for half the
+// products, and the softmax chain sets the pace (about 1000 TFLOP/s).  A unit is 256 rows of one (sequence, cache head):
 // two 128-row halves that share every 128-key tile of K and V.  S = Q K^T is a
 // tcgen05.mma of 128 x 128 per half into tensor memory; the half's four
 // softmax warps (one row a thread, no exchange between threads) read it, write
@@ -17,8 +21,14 @@
 //
 // Warps: 0-3 and 4-7 the softmax of the two halves, 8 TMA, 9 MMA, 10 walks the
 // run and hands its segments to the others ahead of time, 11 sees that a tile's
-// operands have landed; with an FP8 cache 12-15 turn the code tiles into FP16 operand tiles (exactly), and Q is
-// scaled per row by a power of two to fit FP16, P by 2^6.
+// operands have landed; with an FP8 cache 12-15 turn the code tiles into FP16
+// operand tiles (exactly; 1700 of a tile's 3000 cycles), and Q is scaled per row
+// by a power of two to fit FP16, P by 2^6.
+//
+// With up to 128 rows one half is empty.  Giving its warps every second tile of
+// the same rows (both chains joined at the unit's end) was built and measured: 110
+// against 113 us for 32 sequences x 20 rows over 4000 BF16 keys, 129 against 118 for
+// 64 rows over E4M3 keys.  The copies and conversions set the pace there, so it was left out.
 #include <algorithm>
 #include <type_traits>
 
