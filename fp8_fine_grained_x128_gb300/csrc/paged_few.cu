@@ -53,7 +53,7 @@ struct Few {
     static constexpr int kFit = 64 * 1024 / (kSlices * kStage);
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kRing = kSlices * kStages * kStage;
-    static constexpr int kORow = D + 8;                         // floats of a merge row (bank spread)
+    static constexpr int kORow = D + (FMT == FP8_KV_BF16 ? 8 : 4);   // floats of a merge row (no bank met twice)
     static constexpr int kMerge = kSlices * kRows * kORow * 4;
     static constexpr int kBytes = kRing > kMerge ? kRing : kMerge;
     static constexpr float kOff = FMT == FP8_KV_BF16 ? 0.0f : 6.0f;   // P is kept as 2^kOff p
@@ -508,17 +508,19 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
                 float *p = merge + (slice * C::kRows + mrow + gr + 8 * u) * C::kORow;
                 if (FMT == FP8_KV_BF16)
                     *reinterpret_cast<float2 *>(p + 8 * j + 2 * t4) = make_float2(o[j][2 * u], o[j][2 * u + 1]);
-                else {
-                    p[(D / 8) * (2 * t4) + j] = o[j][2 * u];
-                    p[(D / 8) * (2 * t4 + 1) + j] = o[j][2 * u + 1];
-                }
+                else if (j % 4 == 0)   // column n's j-th four elements are the row's piece 8 (j / 4) + n
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<float4 *>(p + 4 * (2 * j + 2 * t4 + k)) =
+                            make_float4(o[j][2 * u + k], o[j + 1][2 * u + k], o[j + 2][2 * u + k], o[j + 3][2 * u + k]);
             }
         }
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == nt;
         Part *part = static_cast<Part *>(g.few_parts) + 2 * blockIdx.x + (tile0 == 0 ? 1 : 0);
         for (int e = tid; e < rows * (D / 4); e += kThreads) {
-            const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+            const int row = e / (D / 4), piece = e % (D / 4);
+            const int d = FMT == FP8_KV_BF16 ? 4 * piece : (D / 8) * (piece % 8) + 4 * (piece / 8);
             float mr = s_m[0][row];
 #pragma unroll
             for (int w = 1; w < kSlices; ++w) mr = fmaxf(mr, s_m[w][row]);
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
 #pragma unroll
             for (int w = 0; w < kSlices; ++w) {
                 const float f = mr == -INFINITY ? 0.0f : ex2_approx_ftz(s_m[w][row] - mr);
-                const float4 v = *reinterpret_cast<const float4 *>(merge + (w * C::kRows + row) * C::kORow + d);
+                const float4 v = *reinterpret_cast<const float4 *>(merge + (w * C::kRows + row) * C::kORow + 4 * piece);
                 a.x += f * v.x;
                 a.y += f * v.y;
                 a.z += f * v.z;
