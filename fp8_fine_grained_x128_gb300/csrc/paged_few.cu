@@ -3,11 +3,12 @@
 // (sm_103a).
 //
 // Bound: HBM bandwidth, every key and value read once (32 query and 8 cache heads
-// of 128: 64 ragged sequences of up to 8000 BF16 keys 198 us, 0.94 of the measured
-// copy rate; 16 x 65536 E4M3 keys 333 us, 0.95; one of 524287 BF16 keys 320 us,
-// 0.99).  With two operands of rows the time is a warp's own chain of copy wait, Q K^T,
-// softmax and P V (about 1660 cycles a tile, three CTAs side by side): 32 x 5 tokens over up
-// to 4001 E4M3 keys 59 us against 20 us for the bytes.  All (sequence, head)
+// of 128: 64 ragged sequences of up to 8000 BF16 keys 198 us, 0.95 of the measured
+// copy rate; 16 x 65536 E4M3 keys 332 us, 0.96; one of 524287 BF16 keys 324 us,
+// 0.98).  With two operands of rows and FP8 codes it is the warps' mix of
+// conversions, products and softmax (about 1900 cycles a tile, three CTAs side by side, no
+// unit above half its rate): 32 x 5 tokens over up to 4001 E4M3 keys 58 us against 20 us
+// for the bytes.  All (sequence, head)
 // pairs' 64-key tiles stand in one line that is cut into equal runs, one per
 // CTA, so ragged batches and a single long cache balance alike; a CTA's run
 // covers whole pairs, which it finishes alone, and at most two broken ones,
