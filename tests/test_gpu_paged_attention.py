@@ -121,6 +121,28 @@ def test_many_sequences(workspace):
     check(c, *attend(c, workspace))
 
 
+DRAFTS = [(5, 700), (8, 8), (0, 40), (8, 3), (1, 1), (6, 129), (3, 9001), (7, 64), (8, 511), (2, 33), (4, 1000), (5, 6)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", [1, 8], ids=["few pairs", "many pairs"])
+def test_drafts(workspace, kind, dim, heads):
+    """Up to 32 rows a sequence, among them none that sees a key, and one long cache: the batch's pairs
+    decide which kernel takes them."""
+    c = Case(DRAFTS, kind, heads=heads, dim=dim, page=32, seed=dim + heads)
+    check(c, *attend(c, workspace))
+
+
+@pytest.mark.parametrize("new", [8, 9, 16, 17])
+def test_rows_around_the_choice_of_kernel(workspace, new):
+    """Groups of 2 and 4 query heads: 16 to 68 rows."""
+    for group in (2, 4):
+        for kind in ("bf16", "e4m3"):
+            c = Case([(new, 300 + 41 * i) for i in range(10)], kind, heads=5, group=group, seed=new + group)
+            check(c, *attend(c, workspace))
+
+
 def test_large_scores_and_scale(workspace):
     """Scores of hundreds: the softmax is one key nearly everywhere."""
     for lens in ([(1, 400)], [(60, 400)]):
