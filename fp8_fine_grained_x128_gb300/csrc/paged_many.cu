@@ -51,6 +51,7 @@ struct Many {
     static constexpr int kThreads = kFp8 ? 512 : 384;
     static constexpr int kTileB = (D / 64) * kSub;         // an operand tile
     static constexpr int kStages = D == 64 ? 6 : kFp8 ? 4 : 5;
+    static_assert(kStages >= 3, "a segment's first tile holds two tiles of keys and one of values");
     static constexpr int kRawB = kFp8 ? kTile * D : 0;     // a tile of codes
     static constexpr int kRawStages = kFp8 ? (D == 64 ? 4 : 2) : 1;   // (BF16: an unused pair of barriers)
     static constexpr int kQ = 0;
@@ -726,7 +727,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                     qk(x, it % C::kStages);
                 }
                 if (!ok) break;
-                if (elect_one()) tc_commit(&empty[it % C::kStages]);
+                const int first_slot = it % C::kStages;
                 ++it;
                 for (int j = tile0; j < tile1; ++j) {
                     const int vslot = it % C::kStages, kslot = (it + 1) % C::kStages;
@@ -755,6 +756,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                     }
                     if (!ok) break;
                     if (elect_one()) {
+                        if (j == tile0) tc_commit(&empty[first_slot]);   // (the gate has seen it: p_ready above)
                         tc_commit(&empty[vslot]);
                         if (more) tc_commit(&empty[kslot]);
                     }
@@ -773,7 +775,10 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             // so that the MMA warp has one barrier to wait on (each wait costs it about 100 cycles).
             // Value rows past the sequence's end may hold anything, and 0 x NaN is NaN: they are
             // zeroed here (the FP8 form's are when the codes are converted).
-            // It sees every place of the ring in turn, so that no phase of a slot is mistaken for another.
+            // It sees every place of the ring in turn before the MMA warp can hand it back (which it does for all
+            // of a tile's operands, and for the segment's first keys, after the gate's arrival for that tile):
+            // were a slot filled again before the gate looked, the parity would be what it was, and the gate
+            // would wait for ever.
             uint32_t it = 0, done[2] = {0, 0};
             bool ok = true;
             auto tile = [&](uint32_t i) { return warp_wait(&full[i % C::kStages], (i / C::kStages) & 1, abort_flag, g.status); };
