@@ -19,6 +19,18 @@ __device__ __forceinline__ int seq_of_token(const int32_t *__restrict__ offsets,
     return n - 1;
 }
 
+// Whether a sequence's values in the batch's arrays are within their ranges: its
+// new tokens are rows [first, next) of `tokens`, len its tokens in the cache.  A
+// sequence without new tokens takes no part, and its length is not looked at.
+__device__ __forceinline__ bool seq_rows_ok(const fp8_paged_batch_t &b, int64_t tokens, int first, int next)
+{
+    return next == first || (first >= 0 && next > first && next <= tokens && next - first <= b.max_new);
+}
+__device__ __forceinline__ bool seq_len_ok(const fp8_paged_batch_t &b, int page_size, int len)
+{
+    return len >= 0 && len <= (int64_t)b.pages_per_seq * page_size;
+}
+
 struct AttnArgs {
     fp8_paged_kv_t c;
     fp8_paged_batch_t b;
@@ -59,13 +71,13 @@ __device__ __forceinline__ bool dbg_lse(const AttnArgs &g, int64_t at) { return 
 __device__ __forceinline__ bool seq_lengths(const AttnArgs &g, int b, int &first, int &rows, int &len)
 {
     first = g.b.q_offsets[b];
-    const int64_t n = (int64_t)g.b.q_offsets[b + 1] - first;
+    const int next = g.b.q_offsets[b + 1];
     len = g.b.kv_lens[b];
     rows = 0;
-    if (n == 0) return true;
-    if (first < 0 || n < 0 || first + n > g.tokens || n > g.b.max_new) return false;
-    rows = (int)n * g.group;
-    if (len < 0 || len > (int64_t)g.b.pages_per_seq * g.c.page_size) {
+    if (next == first) return true;
+    if (!seq_rows_ok(g.b, g.tokens, first, next)) return false;
+    rows = (next - first) * g.group;
+    if (!seq_len_ok(g.b, g.c.page_size, len)) {
         len = 0;
         return false;
     }

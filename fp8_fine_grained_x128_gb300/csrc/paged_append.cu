@@ -17,7 +17,7 @@
 // a lane's loads are in flight together, and the query, key and value rows are dealt
 // over a token's warps in turn, since only keys and values cost divisions.
 // Measured, 32 query and 8 cache heads of 128: 8 x 4096 tokens into a BF16 cache
-// 123 us (0.97 of the measured copy rate), 8192 tokens into an E4M3 cache 37.6 us (0.74: the ramp and
+// 118 us (the measured copy rate), 8192 tokens into an E4M3 cache 35.5 us (0.78 of it: the ramp and
 // the last wave; the FP8 divisions fill half the issue slots), 16 single tokens
 // 9.4 us (a launch's latency).
 #include <algorithm>
@@ -38,6 +38,7 @@ struct AppendArgs {
     const float *rope;
     uint16_t *q_out;
     int q_heads, rot_dim, parts;
+    unsigned check_ctas;   // CTAs that check the batch's arrays
     int *status;
 };
 
@@ -108,13 +109,12 @@ __device__ __forceinline__ int64_t last_row(const fp8_paged_kv_t &c, int64_t pag
     return (c.num_pages - 1) * page + (c.heads - 1) * head + (c.page_size - 1) * row;
 }
 
+// One warp's rows of its token.
 template <int D, int FMT, bool INTERLEAVED>
-__global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
+__device__ __forceinline__ void append_rows(const AppendArgs &g)
 {
     constexpr int kLanes = D / 16;             // lanes of a head row
     constexpr int kSlots = 32 / kLanes;        // head rows side by side in a warp
-    dependents_launch();
-    dependency_wait();
     const int lane = threadIdx.x & 31;
     const int64_t w = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 5;
     const int64_t t = w / g.parts;
@@ -144,18 +144,16 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
 
     const int seq = seq_of_token(g.b.q_offsets, g.b.seqs, t, lane);
     if (seq < 0 || seq >= g.b.seqs) return;   // a row of no sequence
-    const int64_t pos = (int64_t)g.b.kv_lens[seq] - g.b.q_offsets[seq + 1] + t;
-    const int64_t pg = pos >= 0 ? pos / g.c.page_size : -1;
+    const int first = g.b.q_offsets[seq], next = g.b.q_offsets[seq + 1], len = g.b.kv_lens[seq];
+    const int64_t pos = (int64_t)len - next + t;
+    const int64_t pg = pos >= 0 ? pos >> (31 - __clz(g.c.page_size)) : -1;
     int page = -1;
     if (pg >= 0 && pg < g.b.pages_per_seq) page = g.b.page_table[seq * g.b.page_table_ld + pg];
-    if (page < 0 || page >= g.c.num_pages || (g.rot_dim > 0 && pos >= g.rope_len)) {
-        if (lane == 0) set_status(g.status, FP8_ERR_INVALID_ARG);
-        return;
-    }
-    const int64_t rip = pos - pg * g.c.page_size;
 
+    // The table row does not wait for the page: both are on their way before either is looked at (the page
+    // first, then the row: 8 x 4096 tokens into a BF16 cache 128 us, FP8 prompt 38; side by side 118 and 35.5).
     float ca[8], sa[8], cb[8], sb[8];   // table values of chunk a and of chunk b
-    if (turn) {
+    if (turn && pos >= 0 && pos < g.rope_len) {
         const float *p = g.rope + pos * g.rot_dim;
         if (INTERLEAVED) {   // pair j of a chunk: elements 2j, 2j + 1
             const float4 c0 = *reinterpret_cast<const float4 *>(p + ea / 2);
@@ -178,6 +176,14 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
     }
     const Divider2 kd(FMT == FP8_KV_BF16 || !g.c.k_scale ? 1.0f : *g.c.k_scale);
     const Divider2 vd(FMT == FP8_KV_BF16 || !g.c.v_scale ? 1.0f : *g.c.v_scale);
+
+    // (offsets that decrease name a sequence whose rows the token is not among)
+    const bool ok = t >= first && t < next && seq_rows_ok(g.b, g.tokens, first, next) && seq_len_ok(g.b, g.c.page_size, len);
+    if (!ok || page < 0 || page >= g.c.num_pages || (g.rot_dim > 0 && pos >= g.rope_len)) {
+        if (lane == 0) set_status(g.status, FP8_ERR_INVALID_ARG);
+        return;
+    }
+    const int64_t rip = pos & (g.c.page_size - 1);
 
 #pragma unroll
     for (int i = 0; i < kAppendRows; ++i) {
@@ -224,6 +230,22 @@ __global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
     }
 }
 
+template <int D, int FMT, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppendThreads) k_rope_append(AppendArgs g)
+{
+    dependents_launch();
+    dependency_wait();
+    append_rows<D, FMT, INTERLEAVED>(g);
+    // Sequences whose values are out of range are announced even where no token falls to them, by the first
+    // CTAs (at the end: values loaded ahead cost the fifth CTA of an SM its registers).
+    if (blockIdx.x >= g.check_ctas) return;
+    for (int b = blockIdx.x * kAppendThreads + threadIdx.x; b < g.b.seqs; b += g.check_ctas * kAppendThreads) {
+        const int first = g.b.q_offsets[b], next = g.b.q_offsets[b + 1];
+        if (!seq_rows_ok(g.b, g.tokens, first, next) || (next != first && !seq_len_ok(g.b, g.c.page_size, g.b.kv_lens[b])))
+            set_status(g.status, FP8_ERR_INVALID_ARG);
+    }
+}
+
 template <int D, int FMT>
 static int run_append(AppendArgs &g, int interleaved, cudaStream_t st)
 {
@@ -231,6 +253,7 @@ static int run_append(AppendArgs &g, int interleaved, cudaStream_t st)
     g.parts = (g.q_heads + 2 * g.c.heads + per_warp - 1) / per_warp;
     const int64_t warps = g.tokens * g.parts, blocks = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (blocks >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
+    g.check_ctas = (unsigned)std::min<int64_t>(blocks, (g.b.seqs + kAppendThreads - 1) / kAppendThreads);
     return launch_dependent(interleaved ? k_rope_append<D, FMT, true> : k_rope_append<D, FMT, false>, dim3((unsigned)blocks),
                             kAppendThreads, 0, st, g);
 }

@@ -454,15 +454,17 @@ typedef struct {
  * kv_lens[b] - (q_offsets[b+1] - q_offsets[b]) + i.  Its token at position p
  * is row p % page_size of page page_table[b * page_table_ld + p / page_size].
  *   q_offsets: DEVICE int32[seqs + 1], non-decreasing.  Rows outside
- *   [q_offsets[0], q_offsets[seqs]) belong to no sequence: not read, and
- *   their outputs not written.
+ *   [q_offsets[0], q_offsets[seqs]) belong to no sequence: what they hold
+ *   has no effect, and their outputs are not written.
  *   kv_lens: DEVICE int32[seqs], 0 .. pages_per_seq * page_size (<= 2^31 - 1024).
  *   page_table: DEVICE int32, entries of the pages in use in [0, num_pages).
  *   max_new: an upper bound on the new tokens of any sequence.
  * These arrays are read on the device (a captured graph replays with what
  * they then hold) and checked there: a value outside its range records
  * FP8_ERR_INVALID_ARG, nothing outside the buffers is read or written, and
- * the outputs of that sequence are unspecified.  0 <= seqs <= 65536. */
+ * the outputs of that sequence are unspecified (the append writes no cache row
+ * for it).  A sequence without new tokens takes no part: its length is not
+ * looked at.  0 <= seqs <= 65536. */
 typedef struct {
     const int32_t *q_offsets, *kv_lens, *page_table;
     int64_t page_table_ld;
@@ -485,7 +487,8 @@ typedef struct {
  *   rot_dim: a multiple of 16, 0 (no rotation, rope NULL) .. head_dim.
  *   All pointers 16-byte aligned, leading dimensions multiples of 8.
  * A position outside the table or the page table records
- * FP8_ERR_INVALID_ARG and that token is not written.  A key or value that is
+ * FP8_ERR_INVALID_ARG and that token is not written, no more than a token whose
+ * sequence has a value outside its range.  A key or value that is
  * Inf or NaN records FP8_ERR_NONFINITE (what the cache then holds for that
  * token is unspecified).  Two new tokens must not share a cache row. */
 FP8FG_API int fp8_rope_append_kv(const fp8_paged_kv_t *cache, const fp8_paged_batch_t *batch, int64_t tokens,
