@@ -58,8 +58,13 @@ constexpr float kLazy = 8.0f;
 // With a BF16 cache P is rounded to BF16 (unit roundoff 2^-8).  A row's error
 // averages out over the keys that carry its weight, so where there may be few of
 // them more is done: below kFineKeys keys P is the sum of two BF16 terms (an error
-// of 2^-17, and a second product with V); below kExactKeys the maximum in use does
-// not lag, so that the key that carries most has p = 1, which is exact.
+// of 2^-17, and a second product with V), and the key that carries most has p = 1,
+// which is exact: k_attn_few's maximum never lags, nor k_attn_many's below kExactKeys,
+// and beyond that it lags by less than would let a key outweigh all before it.
+// k_attn_many's sum that divides the output then counts the heaviest keys as they were
+// rounded.  (k_attn_few without a lag: 118 instead of 114 us for 32 sequences x 5 tokens
+// over 4000 keys, no other case measured longer.  k_attn_many, an 8192-token prompt: 388
+// with neither the limit nor that sum, 395 with both, 419 without a lag.)
 constexpr int kFineKeys = 128, kExactKeys = 2048;
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
         }
 
         const bool fine = len - new_tokens < kFineKeys, two = rows > mrow + 8;
-        const float lazy = FMT == FP8_KV_BF16 && len < kExactKeys ? 0.0f : kLazy;
+        constexpr float lazy = FMT == FP8_KV_BF16 ? 0.0f : kLazy;
         float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;

@@ -93,3 +93,91 @@ def test_sequences_out_of_range_without_a_token(workspace):
         assert fg.device_status() == code
         fg.paged_attention(c.cache(), batch, c.q, torch.empty_like(c.q), workspace)
         assert fg.device_status() == code
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_units_of_one_or_two_tiles(workspace, kind, dim):
+    """Every CTA goes from unit to unit all the time, with one half of rows or both."""
+    lens = [(17 + i % 4 if i % 9 else 70, 70 + (37 * i) % 180) for i in range(220)]
+    c = Case(lens, kind, heads=4, group=2, dim=dim, page=32, seed=dim)
+    check(c, *attend(c, workspace))
+
+
+KEYS, PAGE = 4500, 64
+# sequences, new tokens of each, cache heads, query heads of a group: enough of them that a CTA's run holds a
+# sequence's first and last keys
+FORMS = {"few rows, one group": (100, 1, 8, 4), "few rows, two groups": (100, 5, 8, 4), "many rows": (80, 20, 4, 8)}
+
+
+def shared_pages(workspace, kind, dim, form, columns, amps):
+    """Sequences that share one sequence's pages, whose keys are `columns` [keys, n] in their first n elements
+    and whose values are random; row r's query is amps[r] [n].  Scale 1.  Returns out, lse, and the 64-bit
+    values: out, lse and the weighted mean of the absolute values."""
+    seqs, new, heads, group = FORMS[form]
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    pages = -(-KEYS // PAGE)
+    dtype = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}[kind]
+    k = torch.zeros((pages * PAGE, heads, dim), device="cuda")
+    k[:KEYS, :, :columns.shape[1]] = columns[:, None]
+    v = torch.randn((pages * PAGE, heads, dim), generator=g, device="cuda")
+    k, v = ((x.view(pages, PAGE, heads, dim).transpose(1, 2).contiguous()).to(dtype) for x in (k, v))
+    tokens, H = seqs * new, heads * group
+    q = torch.zeros((tokens, H, dim), dtype=torch.bfloat16, device="cuda")
+    q[..., :columns.shape[1]] = amps[torch.arange(tokens * H, device="cuda") % amps.shape[0]].view(tokens, H, -1)
+    ints = dict(dtype=torch.int32, device="cuda")
+    batch = fg.PagedBatch(torch.arange(seqs + 1, **ints) * new, torch.full((seqs,), KEYS, **ints),
+                          torch.arange(pages, **ints).repeat(seqs, 1), new)
+    out, lse = torch.empty_like(q), torch.empty((tokens, H), device="cuda")
+    fg.paged_attention(fg.PagedKV(k, v), batch, q, out, workspace, lse=lse, scale=1.0)
+    assert_status_ok()
+    kk, vv = (x.float().transpose(1, 2).reshape(-1, heads, dim)[:KEYS].double() for x in (k, v))
+    after = torch.arange(KEYS, device="cuda") > (KEYS - new + torch.arange(tokens, device="cuda") % new)[:, None]
+    ref, size, rlse = torch.empty(q.shape, dtype=torch.float64, device="cuda"), torch.empty_like(out, dtype=torch.float64), lse.double()
+    for h in range(H):
+        x = (q[:, h].double() @ kk[:, h // group].T).masked_fill(after, -float("inf"))
+        w = torch.softmax(x, -1)
+        ref[:, h], size[:, h], rlse[:, h] = w @ vv[:, h // group], w @ vv[:, h // group].abs(), torch.logsumexp(x, -1)
+    return out.double(), lse.double(), ref, rlse, size
+
+
+def half_ulp(ref):
+    return 2.0 ** (torch.floor(torch.log2(ref.abs().clamp(min=2.0 ** -126))) - 8)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_one_late_key_carries_the_row(workspace, kind, dim, form):
+    """A late key 2^5 to 2^8 times as heavy as the only other one that counts, the other one in the tile before
+    its own and in the same 16 keys of it: too little for a lagging maximum to be raised.  The output is that
+    key's value but for at most 2^-5 of the weight, so P's rounding must not show: 2^-13 of it from the light
+    key in BF16, 2^-11 in FP16 (FP8 caches)."""
+    at = 30 * 128 + 5
+    c = torch.full((KEYS, 1), -16.0, device="cuda")
+    c[at], c[at - 128] = 1.0, 0.0
+    amps = (3.5 + torch.arange(128, device="cuda") / 64)[:, None]       # times log2 e: 5.05 to 7.91
+    out, lse, ref, rlse, size = shared_pages(workspace, kind, dim, form, c, amps)
+    bad = (out - ref).abs() > 2.0 ** -10 * size + half_ulp(ref)
+    assert not bool(bad.any()), (int(bad.sum()), float(((out - ref).abs() / (2.0 ** -10 * size + half_ulp(ref))).max()))
+    assert float((lse - rlse).abs().max()) < 2.0 ** -16
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("amp", [5.46875, 5.59375, 3.984375], ids=["steps of 7.89", "steps of 8.07", "steps of 5.75"])
+def test_maximum_that_grows_from_tile_to_tile(workspace, kind, dim, form, amp):
+    """Scores that rise in log2 by just under or just over 8 with every 128 keys, so that a lagging maximum is
+    raised at every tile, every second, or after a part of one.  The weight lies on the last keys, evenly, and
+    their rounding may go one way: P's unit roundoff, 2^-8 for BF16 and 2^-11 for FP16."""
+    t = torch.arange(KEYS, device="cuda") // 128
+    c = torch.stack([t % 8, t // 8], 1).float()      # exact in every format
+    amps = torch.tensor([[amp, 8 * amp]], device="cuda")
+    out, lse, ref, rlse, size = shared_pages(workspace, kind, dim, form, c, amps)
+    # FP32: the score of up to 8 x 36 x amp rounds by 2^-24 of itself a few times, the sum of 128 keys by 2^-17
+    e32 = 4 * 2.0 ** -24 * 36 * 8 * amp + 2.0 ** -16
+    tol = (2.0 ** (-8 if kind == "bf16" else -11) + e32) * size + half_ulp(ref)
+    bad = (out - ref).abs() > tol
+    assert not bool(bad.any()), (int(bad.sum()), float(((out - ref).abs() / tol).max()))
+    assert float((lse - rlse).abs().max()) < e32 + 2.0 ** -22 * float(rlse.abs().max())
