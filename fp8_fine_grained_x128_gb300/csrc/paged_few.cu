@@ -242,14 +242,14 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
     };
 
     auto write_row = [&](int first, int h, int row, int d, float4 v, float mr, float lr) {
-        const float inv = lr > 0.0f ? vs / lr : 0.0f;
+        const float inv = lr == 0.0f ? 0.0f : vs / lr;   // (a NaN stays one)
         const int64_t tok = first + row / g.group;
         const int head = h * g.group + row % g.group;
         const int64_t at = tok * g.out_ld + (int64_t)head * D + d;
         if (dbg_span(at, 4, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status))
             *reinterpret_cast<uint2 *>(g.out + at) = make_uint2(bf16x2_rn(v.x * inv, v.y * inv), bf16x2_rn(v.z * inv, v.w * inv));
         if (g.lse && d == 0 && dbg_lse(g, tok * g.q_heads + head))
-            g.lse[tok * g.q_heads + head] = lr > 0.0f ? (mr - C::kOff + log2f(lr)) * kLn2 : -INFINITY;
+            g.lse[tok * g.q_heads + head] = lr == 0.0f ? -INFINITY : (mr - C::kOff + log2f(lr)) * kLn2;
     };
     int nbroken = 0;   // pairs of this run that others have parts of
     int pages = 0, pbase = 0, pages_of = -1;
@@ -636,8 +636,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
             for (int i = lane; i < parts_n; i += 32)
 #pragma unroll
                 for (int k = 0; k < kR; ++k)
-                    lr[k] += mr[k] == -INFINITY ? 0.0f
-                                                : ex2_approx_ftz(__ldcg(&part_of(i).m[row0 + k]) - mr[k]) * __ldcg(&part_of(i).l[row0 + k]);
+                    lr[k] += (mr[k] == -INFINITY ? 0.0f : ex2_approx_ftz(__ldcg(&part_of(i).m[row0 + k]) - mr[k])) *
+                             __ldcg(&part_of(i).l[row0 + k]);
 #pragma unroll
             for (int k = 0; k < kR; ++k) {
 #pragma unroll

@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             if (!warp_wait(&o_full[x], un & 1, abort_flag, g.status)) break;
             ++un;
             tc_fence_after();
-            const float inv = lp > 0.0f ? vs / lp : 0.0f;
+            const float inv = lp == 0.0f ? 0.0f : vs / lp;   // (a NaN stays one)
             const int lrow = x * 128 + r;
             const bool mine = lrow < q.rows;
             if (q.whole) {
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                     }
                 }
                 if (mine && g.lse && dbg_lse(g, (int64_t)th.x * g.q_heads + th.y))
-                    g.lse[(int64_t)th.x * g.q_heads + th.y] = l > 0.0f ? (m * mul - C::kOff + log2f(l)) * kLn2 : -INFINITY;
+                    g.lse[(int64_t)th.x * g.q_heads + th.y] = l == 0.0f ? -INFINITY : (m * mul - C::kOff + log2f(l)) * kLn2;
             } else {
                 float *part = g.many_parts + (int64_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * kPartFloats;
 #pragma unroll
@@ -959,14 +959,14 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs g, float off)
             l += f * p[kUnitRows * 128 + kUnitRows + lrow];
             lp += f * p[kUnitRows * 128 + 2 * kUnitRows + lrow];
         }
-        const float inv = lp > 0.0f ? vs / lp : 0.0f;
+        const float inv = lp == 0.0f ? 0.0f : vs / lp;
         const int row = j.row0 + lrow;
         const int64_t tok = j.first + row / g.group;
         const int head = j.head * g.group + row % g.group;
         const int64_t at = tok * g.out_ld + (int64_t)head * D + 4 * d4;
         if (dbg_span(at, 4, (g.tokens - 1) * g.out_ld + (int64_t)g.q_heads * D, g.status))
             *reinterpret_cast<uint2 *>(g.out + at) = make_uint2(bf16x2_rn(a.x * inv, a.y * inv), bf16x2_rn(a.z * inv, a.w * inv));
-        if (g.lse && d4 == 0 && dbg_lse(g, tok * g.q_heads + head)) g.lse[tok * g.q_heads + head] = l > 0.0f ? (m - off + log2f(l)) * kLn2 : -INFINITY;
+        if (g.lse && d4 == 0 && dbg_lse(g, tok * g.q_heads + head)) g.lse[tok * g.q_heads + head] = l == 0.0f ? -INFINITY : (m - off + log2f(l)) * kLn2;
     }
 }
 

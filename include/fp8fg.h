@@ -515,7 +515,8 @@ FP8FG_API size_t fp8_paged_attention_workspace_bytes(void);
  *   lse (optional) [tokens][q_heads] FP32.  q_heads a multiple of heads.
  * Cache rows at positions >= kv_lens[b] may hold anything.  A key or value
  * below it that is Inf or NaN makes the outputs of that sequence's tokens
- * unspecified.
+ * unspecified.  A NaN in a query makes its row's outputs and lse NaN, and no
+ * other row's.
  * workspace: fp8_paged_attention_workspace_bytes() bytes, 16-byte aligned;
  * calls sharing one must not overlap on the GPU. */
 FP8FG_API int fp8_paged_attention(const fp8_paged_kv_t *cache, const fp8_paged_batch_t *batch, int64_t tokens,

@@ -181,3 +181,18 @@ def test_maximum_that_grows_from_tile_to_tile(workspace, kind, dim, form, amp):
     bad = (out - ref).abs() > tol
     assert not bool(bad.any()), (int(bad.sum()), float(((out - ref).abs() / tol).max()))
     assert float((lse - rlse).abs().max()) < e32 + 2.0 ** -22 * float(rlse.abs().max())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e5m2"])
+@pytest.mark.parametrize("lens", [[(1, 77), (1, 3)], [(5, 400), (1, 9)], [(1, 30000)], [(60, 300), (3, 3)], [(40, 9000)]],
+                         ids=["single", "drafts", "long single", "chunks", "long chunk"])
+def test_query_that_is_no_number_stays_in_its_row(workspace, kind, lens):
+    """Output and LSE of that row are NaN (not the LSE of a row that sees no key); no other row changes."""
+    c = Case(lens, kind, heads=1, page=64)
+    want, want_lse = attend(c, workspace)
+    c.q[0, 2, 17] = float("nan")
+    out, lse = attend(c, workspace)
+    assert_status_ok()
+    assert bool(torch.isnan(out[0, 2]).all()) and bool(torch.isnan(lse[0, 2]))
+    out[0, 2], lse[0, 2] = want[0, 2], want_lse[0, 2]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
