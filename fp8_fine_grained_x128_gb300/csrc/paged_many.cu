@@ -393,12 +393,13 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
         };
         // The warp's 32 rows of Q into the swizzled operand tile, D / 8 lanes side by side on a row (a row
         // a lane met 32 lines an instruction: 3000 cycles); returns the factor from the lane's row's
-        // products to log2 scores.
+        // products to log2 scores, which is positive, so that the largest product has the largest score: with
+        // an FP8 cache Q takes the key scale's sign (or its NaN).
         auto load_q = [&](const Segment &q) {
             constexpr int kLanes = D / 8, kRows = 32 / kLanes;   // lanes of a row, rows an instruction
             const int2 at = q_row(q);
             const int64_t off = (int64_t)at.x * g.q_ld + (int64_t)at.y * D;
-            float mul = fmaxf(g.scale * kLog2e * ks, 1.17549435e-38f);
+            float mul = fmaxf(g.scale * kLog2e * fabsf(ks), 1.17549435e-38f);
             uint4 v[D / 8];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
@@ -407,13 +408,14 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
             }
             if (C::kFp8) {   // a power of two that brings each row's largest value into [2^14, 2^15)
                 int mine = 0;
+                const float sign = ks < 0.0f ? -1.0f : ks >= 0.0f ? 1.0f : ks;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
                     uint32_t m = absmax8(v[i]);
 #pragma unroll
                     for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
                     const int e = min(max((int)(m >> 7), 15), 254) - 127;
-                    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+                    const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23) * sign;
                     uint32_t h[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) h[k] = f16x2_rn(bf16_lo(h[k]) * up, bf16_hi(h[k]) * up);

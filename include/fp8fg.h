@@ -437,8 +437,8 @@ typedef enum { FP8_KV_E4M3 = 0, FP8_KV_E5M2 = 1, FP8_KV_BF16 = 2 } fp8_kv_format
  * V interleaved in one allocation, are strides.
  *   k, v: 16-byte aligned; every stride a positive multiple of 16 bytes, row
  *   strides below 2^22 elements.
- *   k_scale, v_scale: DEVICE float[1]; an element stands for code * scale.
- *   NULL = 1.  Must be NULL for FP8_KV_BF16.
+ *   k_scale, v_scale: DEVICE float[1]; an element stands for code * scale, of
+ *   either sign.  NULL = 1.  Must be NULL for FP8_KV_BF16.
  *   page_size: 16, 32, 64, 128 or 256.  head_dim: 64 or 128.  heads >= 1. */
 typedef struct {
     void *k, *v;

@@ -196,3 +196,26 @@ def test_query_that_is_no_number_stays_in_its_row(workspace, kind, lens):
     assert bool(torch.isnan(out[0, 2]).all()) and bool(torch.isnan(lse[0, 2]))
     out[0, 2], lse[0, 2] = want[0, 2], want_lse[0, 2]
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("lens", [[(1, 77), (1, 300)], [(5, 400), (8, 9)], [(60, 300), (3, 3)], [(40, 9000)]],
+                         ids=["single", "drafts", "chunks", "long chunk"])
+@pytest.mark.parametrize("signs", [(-1.0, 1.0), (1.0, -1.0), (-1.0, -1.0), (0.0, 1.0)], ids=str)
+def test_scales_of_either_sign(workspace, kind, lens, signs):
+    """An element stands for code times scale, whatever the scale's sign."""
+    c = Case(lens, kind, heads=2, group=4, page=64)
+    c.k_scale *= signs[0]
+    c.v_scale *= signs[1]
+    check(c, *attend(c, workspace))
+
+
+@pytest.mark.parametrize("lens", [[(1, 77), (1, 300)], [(60, 300), (40, 90)]], ids=["single", "chunks"])
+def test_scale_that_is_no_number_is_not_hidden(workspace, lens):
+    for name in ("k_scale", "v_scale"):
+        c = Case(lens, "e4m3", heads=2, group=4, page=64)
+        setattr(c, name, torch.full((1,), float("nan"), device="cuda"))
+        out, lse = attend(c, workspace)
+        assert_status_ok()
+        assert bool(torch.isnan(out).all())
+        assert bool(torch.isnan(lse).all()) == (name == "k_scale")
