@@ -535,12 +535,25 @@ def adamw_step_fp8_states(param, grad, m, m_scales, v, v_scales, hparams: AdamWH
 
 # ------------------------------------------------------------------ paged key / value cache
 
-class PagedKV:
+class _Marshalled:
+    """What the C descriptor holds cannot be assigned afterwards: the descriptor would go on pointing to the
+    old tensors, and nothing would keep them alive."""
+
+    def __setattr__(self, name, value):
+        if name in self._fixed and hasattr(self, "_ref"):
+            raise AttributeError(f"{name}: marshalled when the {type(self).__name__} was made; update the tensor in place "
+                                 f"or make another one")
+        super().__setattr__(name, value)
+
+
+class PagedKV(_Marshalled):
     """One layer's paged cache: ``k`` and ``v`` [num_pages, heads, page_size, head_dim], any strides
     with contiguous elements (a [num_pages, page_size, heads, head_dim] pool is passed as
     ``pool.transpose(1, 2)``).  BF16, or FP8 codes with device scales [1] (None = 1): torch's float8
     types name their format, ``torch.uint8`` codes take ``fmt`` (KV_E4M3 or KV_E5M2).  Checked and
-    marshalled once; keeps the tensors alive."""
+    marshalled once; keeps the tensors alive (new scales are written into theirs)."""
+
+    _fixed = frozenset(("k", "v", "k_scale", "v_scale", "heads", "head_dim", "device"))
 
     def __init__(self, k, v, k_scale=None, v_scale=None, fmt=KV_E4M3):
         kinds = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.float8_e5m2: KV_E5M2, torch.uint8: fmt}
@@ -569,18 +582,31 @@ class PagedKV:
         self._ref = ctypes.byref(st)
 
 
-class PagedBatch:
+class PagedBatch(_Marshalled):
     """The sequences of a call: ``q_offsets`` [seqs + 1], ``kv_lens`` [seqs] (new tokens included),
     ``page_table`` [seqs, pages_per_seq], int32 on the device and read there by every call, so a serving
-    loop updates them in place; ``max_new`` bounds the new tokens of a sequence."""
+    loop updates them in place; ``max_new`` bounds the new tokens of a sequence (it may be assigned, for
+    the calls that follow)."""
+
+    _fixed = frozenset(("q_offsets", "kv_lens", "page_table", "device"))
 
     def __init__(self, q_offsets, kv_lens, page_table, max_new):
         pt, seqs, width, ld = _mat(page_table, "page_table", _I32)
-        st = _PagedBatch(_buf(q_offsets, "q_offsets", _I32, seqs + 1), _buf(kv_lens, "kv_lens", _I32, seqs), pt, ld,
-                         seqs, width, int(max_new))
-        self.q_offsets, self.kv_lens, self.page_table, self.max_new = q_offsets, kv_lens, page_table, int(max_new)
+        self._st = _PagedBatch(_buf(q_offsets, "q_offsets", _I32, seqs + 1), _buf(kv_lens, "kv_lens", _I32, seqs), pt, ld,
+                               seqs, width)
+        self.q_offsets, self.kv_lens, self.page_table, self.max_new = q_offsets, kv_lens, page_table, max_new
         self.device, self._device = page_table.device, page_table.get_device()
-        self._ref = ctypes.byref(st)
+        self._ref = ctypes.byref(self._st)
+
+    @property
+    def max_new(self):
+        return self._st.max_new
+
+    @max_new.setter
+    def max_new(self, n):
+        if not 0 <= int(n) < 1 << 31:
+            raise ValueError(f"max_new: {n}, expected 0 to 2^31 - 1")
+        self._st.max_new = int(n)
 
 
 def _paged(cache, batch):

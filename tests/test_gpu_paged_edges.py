@@ -219,3 +219,29 @@ def test_scale_that_is_no_number_is_not_hidden(workspace, lens):
         assert_status_ok()
         assert bool(torch.isnan(out).all())
         assert bool(torch.isnan(lse).all()) == (name == "k_scale")
+
+
+def test_descriptors_do_not_go_stale(workspace):
+    """An assigned max_new counts from the next call on; an assigned tensor, which the descriptor would not
+    follow, is refused."""
+    c = Case([(5, 60), (9, 30)], "e4m3")
+    cache, batch = c.cache(), fg.PagedBatch(c.q_offsets, c.kv_lens, c.table, 1)
+    out = torch.empty_like(c.q)
+    fg.paged_attention(cache, batch, c.q, out, workspace)
+    assert fg.device_status() == fg.ERR_INVALID_ARG
+    batch.max_new = 9
+    assert batch.max_new == 9
+    fg.paged_attention(cache, batch, c.q, out, workspace)
+    want, _ = attend(c, workspace)
+    assert_status_ok()
+    assert torch.equal(out, want)
+    for n in (-1, 1 << 31):
+        with pytest.raises(ValueError, match="max_new"):
+            batch.max_new = n
+    assert batch.max_new == 9
+    for name in ("q_offsets", "kv_lens", "page_table"):
+        with pytest.raises(AttributeError, match="marshalled"):
+            setattr(batch, name, getattr(batch, name).clone())
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError, match="marshalled"):
+            setattr(cache, name, getattr(cache, name).clone())
