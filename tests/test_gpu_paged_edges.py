@@ -245,3 +245,73 @@ def test_descriptors_do_not_go_stale(workspace):
     for name in ("k", "v", "k_scale", "v_scale"):
         with pytest.raises(AttributeError, match="marshalled"):
             setattr(cache, name, getattr(cache, name).clone())
+
+
+@pytest.mark.parametrize("group,new,past,dim", [(32, 264, 40, 64), (16, 529, 7, 128), (16, 1100, 300, 64), (8, 1024, 0, 64)],
+                         ids=["33 units", "34 units", "69 units", "32 units"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_more_units_of_a_head_than_a_warp_has_lanes(workspace, kind, group, new, past, dim):
+    """The walk counts 32 units of 256 rows a step; runs start inside later ones, and last units are short."""
+    c = Case([(3, 50), (new, new + past), (20, 300)], kind, heads=2, group=group, dim=dim, page=64, seed=new)
+    check(c, *attend(c, workspace))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bound", [17, 40, 4096])
+def test_max_new_above_every_sequence(workspace, kind, bound):
+    """A captured step's bound: it alone chooses the kernels, the lengths on the device what they do."""
+    for lens in ([(1, 1 + 67 * i) for i in range(30)], [(0, 5), (4, 4), (3, 700), (1, 2000), (0, 0)], [(0, 9), (0, 0)]):
+        c = Case(lens, kind, heads=2, group=4, page=32, spare_tokens=2)
+        c.max_new = bound
+        check(c, *attend(c, workspace))
+
+
+@pytest.mark.parametrize("seqs", [129, 700, 2500])
+def test_batches_of_a_serving_size(workspace, seqs):
+    """More sequences than a CTA has threads: single tokens alone, with a few chunks, and their append."""
+    lens = [(1, 1 + (37 * i) % 90) for i in range(seqs)]
+    for kind in ("bf16", "e4m3"):
+        c = Case(lens, kind, heads=1, group=4, dim=64, seed=seqs)
+        check(c, *attend(c, workspace))
+        mixed = [(40, 300) if i % 401 == 128 else (1, 1 + (37 * i) % 90) if i % 3 else (0, i % 7) for i in range(seqs)]
+        c = Case(mixed, kind, heads=1, group=4, dim=64, seed=seqs)
+        check(c, *attend(c, workspace))
+    c = Case(mixed, "bf16", heads=1, group=1, dim=64)
+    q, k, v = inputs(c)
+    fg.rope_append_kv(c.cache(), c.batch(), k, v)
+    assert_status_ok()
+    tok, seq, pos = places(c)
+    pg, r = c.table[seq, pos // c.page].long(), pos % c.page
+    assert torch.equal(c.k[pg, :, r], k[tok]) and torch.equal(c.v[pg, :, r], v[tok])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens", [[(1, 77), (1, 9000)], [(5, 400), (8, 9000)], [(60, 300), (40, 9000)]],
+                         ids=["single", "drafts", "chunks"])
+def test_outputs_without_lse(workspace, kind, lens):
+    c = Case(lens, kind, heads=2, group=4, page=64)
+    want, _ = attend(c, workspace)
+    out = torch.empty_like(c.q)
+    fg.paged_attention(c.cache(), c.batch(), c.q, out, workspace)
+    assert_status_ok()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("lens", [[(1, 100), (1, 9000)], [(40, 100), (30, 9000)]], ids=["single", "chunks"])
+def test_fp8_call_after_a_reported_page(workspace, kind, lens):
+    """A page out of range in a sequence that is split over CTAs leaves nothing behind for the next call."""
+    c = Case(lens, kind, heads=2, group=4, page=32)
+    want, want_lse = attend(c, workspace)
+    assert_status_ok()
+    held = c.table[1, 100].clone()
+    for bad in (c.k.shape[0], -1):
+        c.table[1, 100] = bad
+        out, lse = attend(c, workspace)
+        assert fg.device_status() == fg.ERR_INVALID_ARG
+        first = lens[0][0]
+        assert torch.equal(out[:first], want[:first]) and torch.equal(lse[:first], want_lse[:first])
+        c.table[1, 100] = held
+        out, lse = attend(c, workspace)
+        assert_status_ok()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
