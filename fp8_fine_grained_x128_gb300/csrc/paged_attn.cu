@@ -11,13 +11,13 @@
 // kernel reads the lengths on the device and leaves the other's sequences
 // alone; a batch that can hold only short ones launches k_attn_few alone.
 //
-// Up to 32 rows k_attn_few (two operands) still is the faster one where there
+// Up to 32 rows k_attn_few (two groups of rows) still is the faster one where there
 // are pairs enough that few parts of each have to be joined: with 32 query and 8
-// cache heads of 128, k_attn_few / k_attn_many take 97 / 118 us for 32 sequences
-// x 8 tokens over 4000 E4M3 keys, 61 / 114 for 64 x 5 over 1000, 115 / 115 for
-// 32 x 5 over 4000 BF16 keys, 33 / 31 for 8 x 8 over 1500 (64 pairs), but 60 / 32
-// for 1 x 8 over 8000 (8 pairs).  From 33 rows on the tensor cores win: 157 / 117
-// for 32 x 12 over 4000 E4M3 keys, 201 / 115 over BF16 ones.
+// cache heads of 128, k_attn_few / k_attn_many take 96 / 119 us for 32 sequences
+// x 8 tokens over 4000 E4M3 keys, 60 / 106 for 64 x 5 over 1000 (75 / 99 BF16), 118 / 115
+// for 32 x 5 over 4000 BF16 keys, 30 / 30 for 8 x 8 over 1500 (64 pairs), but 53 / 33
+// for 1 x 8 over 8000 (8 pairs).  From 33 rows on the tensor cores win: 157 (with a form of
+// k_attn_few that had four groups) / 119 for 32 x 12 over 4000 E4M3 keys, 201 / 116 over BF16 ones.
 #include "kernels.h"
 #include "paged.cuh"
 

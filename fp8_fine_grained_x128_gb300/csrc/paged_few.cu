@@ -3,22 +3,27 @@
 // (sm_103a).
 //
 // Bound: HBM bandwidth, every key and value read once (32 query and 8 cache heads
-// of 128: 64 ragged sequences of up to 8000 BF16 keys 198 us, 0.95 of the measured
-// copy rate; 16 x 65536 E4M3 keys 332 us, 0.96; one of 524287 BF16 keys 324 us,
-// 0.98).  With two operands of rows and FP8 codes it is the warps' mix of
+// of 128: 64 ragged sequences of up to 8000 BF16 keys 201 us, 0.93 of the measured
+// copy rate; 16 x 65536 E4M3 keys 338 us, 0.94; one of 524287 BF16 keys 327 us,
+// 0.97).  With two groups of rows and FP8 codes it is the warps' mix of
 // conversions, products and softmax (about 1900 cycles a tile, three CTAs side by side, no
-// unit above half its rate): 32 x 5 tokens over up to 4001 E4M3 keys 58 us against 20 us
-// for the bytes.  All (sequence, head)
-// pairs' 64-key tiles stand in one line that is cut into equal runs, one per
+// unit above half its rate), and the two warps of a slice each convert all of its codes:
+// 32 x 5 tokens over up to 4001 E4M3 keys 58 us against 20 us for the bytes.  Of 20 rows, 12
+// places of the second group stand empty besides.
+//
+// All (sequence, head) pairs' tiles (64 keys with one group of rows, 32 with two) stand
+// in one line that is cut into equal runs, one per
 // CTA, so ragged batches and a single long cache balance alike; a CTA's run
 // covers whole pairs, which it finishes alone, and at most two broken ones,
 // whose partial maxima, sums and outputs go to the workspace.  The last CTA
 // to announce its part of a broken pair joins the parts in order (the result
 // does not depend on who is last).
 //
-// A warp takes 16 keys of each tile and never waits for another warp: its
-// copies (cp.async, zero-filled past the sequence's end) go through its own
-// ring.  S = Q K^T and O += P V run on m16n8k16 mma.sync; its rate is far
+// One group of rows: a warp takes 16 keys of each tile and never waits for another
+// warp; its copies (cp.async, zero-filled past the sequence's end) go through its own
+// ring.  Two groups: the two warps that share 16 keys share a ring too, one copies the
+// keys and the other the values, and they meet at a named barrier every tile.
+// S = Q K^T and O += P V run on m16n8k16 mma.sync; its rate is far
 // from binding here (the rows are padded to 16 and the copies still take
 // longer).  The contraction order over head_dim is free, so a lane reads 16
 // contiguous bytes of a key as operand registers, and Q is laid out to match.

@@ -3,9 +3,9 @@
 // longer drafts (sm_103a).
 //
 // Bound: the tensor cores, in long series the rate that the power limit leaves
-// them (32 query and 8 cache heads of 128: an 8192-token prompt 387 us, 1420
-// TFLOP/s, 364 us in short bursts; 2048 tokens after 30720 E4M3 keys 678 and 640 us,
-// 1570 and 1660).  With head_dim 64 an exponential stands for half the
+// them (32 query and 8 cache heads of 128: an 8192-token prompt 394 us, 1400
+// TFLOP/s, 379 us in short bursts; 2048 tokens after 30720 E4M3 keys 679 and 648 us,
+// 1570 and 1640).  With head_dim 64 an exponential stands for half the
 // products, and the softmax chain sets the pace (about 1000 TFLOP/s).  A unit is 256 rows of one (sequence, cache head):
 // two 128-row halves that share every 128-key tile of K and V.  S = Q K^T is a
 // tcgen05.mma of 128 x 128 per half into tensor memory; the half's four
