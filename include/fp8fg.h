@@ -510,9 +510,10 @@ FP8FG_API size_t fp8_paged_attention_workspace_bytes(void);
  * with k_j, v_j the values the cache stands for.  Scores, the running maximum
  * and sum and the output's sum are FP32; the probabilities are rounded to 16
  * bits for the product with the values (to BF16 with a BF16 cache, two terms of
- * it for rows near the first 128 positions; to FP16 with an FP8 one).  A token at
- * a negative position (more new tokens than kv_lens counts) sees no key: out = 0,
- * lse = -inf.
+ * it for rows near the first 128 positions; to FP16 with an FP8 one, where those
+ * below 2^-20 of the row's largest lose bits and those below 2^-31 count as zero).
+ * A token at a negative position (more new tokens than kv_lens counts) sees no
+ * key: out = 0, lse = -inf.
  *   q, out [tokens][q_ld / out_ld] BF16 (q_heads heads of head_dim);
  *   lse (optional) [tokens][q_heads] FP32.  q_heads a multiple of heads.
  * Cache rows at positions >= kv_lens[b] may hold anything.  A key or value
