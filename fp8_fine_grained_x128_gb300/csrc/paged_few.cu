@@ -65,22 +65,21 @@ struct Few {
     static constexpr float kOff = FMT == FP8_KV_BF16 ? 0.0f : 6.0f;   // P is kept as 2^kOff p
 };
 
-// Tiles of a pair of sequence b (0: not one of this kernel's), and its places in
-// the line: kPairCost for the pair, then its tiles.
+// Tiles of a pair of a sequence of these lengths (0: not one of this kernel's), and
+// sequence b's places in the line: kPairCost for a pair, then its tiles.
 template <class C>
-__device__ __forceinline__ int few_tiles(const AttnArgs &g, int b)
+__device__ __forceinline__ int few_tiles(int rows, int len)
 {
-    if (b >= g.b.seqs) return 0;
-    int first, rows, len;
-    if (!seq_lengths(g, b, first, rows, len)) set_status(g.status, FP8_ERR_INVALID_ARG);
-    if (rows < 1 || rows > C::kRows) return 0;
-    return max(1, (len + C::kTile - 1) / C::kTile);
+    return rows < 1 || rows > C::kRows ? 0 : max(1, (len + C::kTile - 1) / C::kTile);
 }
 
 template <class C>
 __device__ __forceinline__ int64_t few_places(const AttnArgs &g, int b)
 {
-    const int nt = few_tiles<C>(g, b);
+    if (b >= g.b.seqs) return 0;
+    int first, rows, len;
+    if (!seq_lengths(g, b, first, rows, len)) set_status(g.status, FP8_ERR_INVALID_ARG);
+    const int nt = few_tiles<C>(rows, len);
     return nt > 0 ? (int64_t)(C::kPairCost + nt) * g.c.heads : 0;
 }
 
@@ -261,7 +260,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
     while (s < s_end && b < g.b.seqs) {   // (b ends the walk only if the lengths changed meanwhile)
         int first, rows, len;
         seq_lengths(g, b, first, rows, len);
-        const int nt = few_tiles<C>(g, b);
+        const int nt = few_tiles<C>(rows, len);   // (of this read: rows and tiles fit the buffers whatever it gave)
         const int64_t seq_end = before + (nt > 0 ? (int64_t)(C::kPairCost + nt) * g.c.heads : 0);
         if (seq_end <= s) {   // the next sequence with tiles
             before = seq_end;
@@ -556,7 +555,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas) k_attn_few(AttnArgs g)
             // CTA c's run starts at floor(c total / ctas): c holds place p iff c = ceil((p + 1) ctas / total) - 1
             if (tid == 0)
                 s_broken[nbroken] = {first, rows, h, 0, div_short((pair0 + 1) * ctas + total - 1, total) - 1,
-                                     div_short((pair0 + nt) * ctas + total - 1, total) - 1};
+                                     min(div_short((pair0 + nt) * ctas + total - 1, total), ctas) - 1};
             ++nbroken;
         }
         __syncthreads();    // the merge buffer becomes the ring again

@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(Many<D, FMT>::kThreads, 1)
                 if (!more) break;
                 if (!q.whole && q.tile0 == 0) {
                     j.rows = q.rows;
-                    j.last = (int)(((w.unit0 + kUnitCost + w.nt) * ctas + total - 1) / total - 1);
+                    j.last = (int)(min(((w.unit0 + kUnitCost + w.nt) * ctas + total - 1) / total, ctas) - 1);
                     j.row0 = q.row0;
                     j.head = q.head;
                     j.first = q.first;

@@ -464,7 +464,9 @@ typedef struct {
  * FP8_ERR_INVALID_ARG, nothing outside the buffers is read or written, and
  * the outputs of that sequence are unspecified (the append writes no cache row
  * for it).  A sequence without new tokens takes no part: its length is not
- * looked at.  0 <= seqs <= 65536. */
+ * looked at.  They must not change while a call that reads them runs (its
+ * outputs would be unspecified, and the attention's workspace would have to be
+ * zeroed again).  0 <= seqs <= 65536. */
 typedef struct {
     const int32_t *q_offsets, *kv_lens, *page_table;
     int64_t page_table_ld;
