@@ -581,4 +581,192 @@ FP8FG_API int fp8_swiglu_bwd_quant(const void *gu, const void *dh, int64_t rows,
     return launch_swiglu_quant(gu, dh, rows, F, fmt, q, s, qT, sT, st, S(stream));
 }
 
+// A BF16 (or, elt = 4, FP32) matrix whose rows of `cols` elements are `ld` apart.
+static int rows_check(const void *p, int64_t ld, int64_t cols, int elt = 2)
+{
+    if (!p) return FP8_ERR_INVALID_ARG;
+    if (ld < cols) return FP8_ERR_SHAPE;
+    if (!aligned16(p) || ld % (16 / elt) != 0) return FP8_ERR_ALIGNMENT;
+    return FP8_OK;
+}
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int norm_checks(int64_t rows, int64_t cols, int fmt)
+{
+    if (!fmt_ok(fmt)) return FP8_ERR_INVALID_ARG;
+    if (rows < 0 || cols < 0 || cols % 128 != 0 || cols > kNormMaxCols || rows >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
+    return FP8_OK;
+}
+
+FP8FG_API int fp8_rmsnorm_fwd_ckpt(const void *x, int64_t rows, int64_t cols, int64_t ldx, const void *res,
+                                   int64_t ldres, const void *w, float eps, int fmt, void *y, int64_t ldy, void *sum,
+                                   int64_t ldsum, void *c, float *cs, float *rstd, void *stream)
+{
+    int rc = norm_checks(rows, cols, fmt);
+    if (rc != FP8_OK) return rc;
+    if (!(eps > 0.0f) || eps > 3.0e38f || (res == nullptr) != (sum == nullptr)) return FP8_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return FP8_OK;
+    if ((rc = rows_check(x, ldx, cols)) != FP8_OK || (rc = rows_check(y, ldy, cols)) != FP8_OK ||
+        (rc = rows_check(w, cols, cols)) != FP8_OK || (rc = rows_check(c, cols, cols)) != FP8_OK)
+        return rc;
+    if (res && ((rc = rows_check(res, ldres, cols)) != FP8_OK || (rc = rows_check(sum, ldsum, cols)) != FP8_OK)) return rc;
+    if (!cs || !rstd) return FP8_ERR_INVALID_ARG;
+    if (!aligned4(cs) || !aligned4(rstd)) return FP8_ERR_ALIGNMENT;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_rmsnorm_fwd_ckpt(x, rows, cols, ldx, res, ldres, w, eps, fmt, y, ldy, sum, ldsum, c, cs, rstd, st, S(stream));
+}
+
+FP8FG_API size_t fp8_rmsnorm_workspace_bytes(int64_t cols)
+{
+    return cols < 0 || cols > kNormMaxCols ? 0 : rmsnorm_workspace_bytes(cols);
+}
+
+FP8FG_API int fp8_rmsnorm_bwd_ckpt(const void *c, const float *cs, const float *rstd, int fmt, int64_t rows,
+                                   int64_t cols, const void *w, const void *dy, int64_t lddy, const void *dsum,
+                                   int64_t lddsum, void *dx, int64_t lddx, float *dw, int accumulate, void *workspace,
+                                   void *stream)
+{
+    int rc = norm_checks(rows, cols, fmt);
+    if (rc != FP8_OK || cols == 0) return rc;
+    if (!dw) return FP8_ERR_INVALID_ARG;
+    if (!aligned4(dw)) return FP8_ERR_ALIGNMENT;
+    if (rows > 0) {
+        if ((rc = rows_check(c, cols, cols)) != FP8_OK || (rc = rows_check(w, cols, cols)) != FP8_OK ||
+            (rc = rows_check(dy, lddy, cols)) != FP8_OK || (rc = rows_check(dx, lddx, cols)) != FP8_OK ||
+            (dsum && (rc = rows_check(dsum, lddsum, cols)) != FP8_OK))
+            return rc;
+        if (!cs || !rstd || !workspace) return FP8_ERR_INVALID_ARG;
+        if (!aligned4(cs) || !aligned4(rstd) || !aligned16(workspace)) return FP8_ERR_ALIGNMENT;
+    }
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_rmsnorm_bwd_ckpt(c, cs, rstd, fmt, rows, cols, w, dy, lddy, dsum, lddsum, dx, lddx, dw, accumulate, workspace, st, S(stream));
+}
+
+static int swiglu_ckpt_checks(const void *bf16, const void *out, int64_t rows, int64_t F, int fmt, const void *c, const float *cs)
+{
+    if (!fmt_ok(fmt)) return FP8_ERR_INVALID_ARG;
+    if (rows < 0 || F < 0 || F % 128 != 0 || F >= (int64_t)1 << 24 || rows >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
+    if (rows == 0 || F == 0) return FP8_OK;
+    if (!bf16 || !out || !c || !cs) return FP8_ERR_INVALID_ARG;
+    if (!aligned16(bf16) || !aligned16(out) || !aligned16(c) || !aligned4(cs)) return FP8_ERR_ALIGNMENT;
+    return FP8_OK;
+}
+
+FP8FG_API int fp8_swiglu_fwd_ckpt(const void *gu, int64_t rows, int64_t F, int fmt, void *h, void *c, float *cs,
+                                  void *stream)
+{
+    const int rc = swiglu_ckpt_checks(gu, h, rows, F, fmt, c, cs);
+    if (rc != FP8_OK || rows == 0 || F == 0) return rc;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_swiglu_fwd_ckpt(gu, rows, F, fmt, h, c, cs, st, S(stream));
+}
+
+FP8FG_API int fp8_swiglu_bwd_ckpt(const void *c, const float *cs, const void *dh, int64_t rows, int64_t F, int fmt,
+                                  void *dgu, void *stream)
+{
+    const int rc = swiglu_ckpt_checks(dh, dgu, rows, F, fmt, c, cs);
+    if (rc != FP8_OK || rows == 0 || F == 0) return rc;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_swiglu_bwd_ckpt(c, cs, dh, rows, F, fmt, dgu, st, S(stream));
+}
+
+static int embedding_checks(int64_t tokens, int64_t vocab, int64_t dim, float scale)
+{
+    if (tokens < 0 || vocab < 0 || dim < 0 || dim % 8 != 0) return FP8_ERR_SHAPE;
+    if (tokens > (int64_t)1 << 30 || vocab > (int64_t)1 << 30 || dim >= (int64_t)1 << 24) return FP8_ERR_SHAPE;
+    return scale == scale ? FP8_OK : FP8_ERR_INVALID_ARG;
+}
+
+FP8FG_API int fp8_embedding_fwd(const int32_t *ids, int64_t tokens, const void *w, int64_t vocab, int64_t dim,
+                                int64_t ldw, float scale, void *out, int64_t ldo, void *stream)
+{
+    int rc = embedding_checks(tokens, vocab, dim, scale);
+    if (rc != FP8_OK || tokens == 0 || dim == 0) return rc;
+    if (!ids) return FP8_ERR_INVALID_ARG;
+    if (!aligned4(ids)) return FP8_ERR_ALIGNMENT;
+    if ((vocab > 0 && (rc = rows_check(w, ldw, dim)) != FP8_OK) || (rc = rows_check(out, ldo, dim)) != FP8_OK) return rc;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_embedding_fwd(ids, tokens, w, vocab, dim, ldw, scale, out, ldo, st, S(stream));
+}
+
+FP8FG_API size_t fp8_embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim)
+{
+    return embedding_checks(tokens, vocab, dim, 1.0f) != FP8_OK ? 0 : embedding_workspace_bytes(tokens, vocab, dim);
+}
+
+FP8FG_API int fp8_embedding_bwd(const int32_t *ids, int64_t tokens, const void *dout, int64_t lddo, int64_t vocab,
+                                int64_t dim, float scale, void *dw, int dw_dtype, int64_t lddw, int accumulate,
+                                void *workspace, void *stream)
+{
+    int rc = embedding_checks(tokens, vocab, dim, scale);
+    if (rc != FP8_OK) return rc;
+    if (dw_dtype != FP8_OUT_BF16 && dw_dtype != FP8_OUT_F32) return FP8_ERR_INVALID_ARG;
+    if (accumulate && dw_dtype != FP8_OUT_F32) return FP8_ERR_UNSUPPORTED;
+    if (dim == 0 || vocab == 0) return FP8_OK;
+    if ((rc = rows_check(dw, lddw, dim, dw_dtype == FP8_OUT_F32 ? 4 : 2)) != FP8_OK) return rc;
+    if (tokens > 0) {
+        if (!ids || !workspace) return FP8_ERR_INVALID_ARG;
+        if (!aligned4(ids) || !aligned16(workspace)) return FP8_ERR_ALIGNMENT;
+        if ((rc = rows_check(dout, lddo, dim)) != FP8_OK) return rc;
+    }
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_embedding_bwd(ids, tokens, dout, lddo, vocab, dim, scale, dw, dw_dtype, lddw, accumulate, workspace, st, S(stream));
+}
+
+static int xent_checks(int64_t tokens, int64_t vocab, int64_t dim, float scale)
+{
+    constexpr int64_t kMost = (int64_t)1 << 28;
+    if (tokens < 0 || vocab < 0 || dim < 0 || dim % 8 != 0) return FP8_ERR_SHAPE;
+    if (tokens >= kMost || vocab >= kMost || dim >= kMost) return FP8_ERR_SHAPE;
+    if (!(scale > 0.0f) || scale > 3.0e38f) return FP8_ERR_INVALID_ARG;
+    return FP8_OK;
+}
+
+FP8FG_API size_t fp8_linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim, int backward)
+{
+    if (xent_checks(tokens, vocab, dim, 1.0f) != FP8_OK || tokens == 0 || vocab == 0 || dim == 0) return 0;
+    return linear_xent_workspace_bytes(tokens, vocab, dim, backward != 0);
+}
+
+FP8FG_API int fp8_linear_xent_fwd(const void *x, int64_t tokens, int64_t dim, int64_t ldx, const void *w,
+                                  int64_t vocab, int64_t ldw, const int32_t *target, float scale, float *loss,
+                                  float *lse, void *workspace, void *stream)
+{
+    int rc = xent_checks(tokens, vocab, dim, scale);
+    if (rc != FP8_OK || tokens == 0) return rc;
+    if (vocab == 0 || dim == 0) return FP8_ERR_SHAPE;
+    if ((rc = rows_check(x, ldx, dim)) != FP8_OK || (rc = rows_check(w, ldw, dim)) != FP8_OK) return rc;
+    if (!target || !loss || !lse || !workspace) return FP8_ERR_INVALID_ARG;
+    if (!aligned4(target) || !aligned4(loss) || !aligned4(lse) || !aligned16(workspace)) return FP8_ERR_ALIGNMENT;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_linear_xent_fwd(x, ldx, w, ldw, target, tokens, vocab, dim, scale, loss, lse, workspace, st, S(stream));
+}
+
+FP8FG_API int fp8_linear_xent_bwd(const void *x, int64_t tokens, int64_t dim, int64_t ldx, const void *w,
+                                  int64_t vocab, int64_t ldw, const int32_t *target, float scale, const float *loss,
+                                  const float *lse, const float *dloss, const float *dlse, void *dx, int64_t lddx,
+                                  void *dw, int dw_dtype, int64_t lddw, int accumulate, void *workspace, void *stream)
+{
+    int rc = xent_checks(tokens, vocab, dim, scale);
+    if (rc != FP8_OK) return rc;
+    if (dw_dtype != FP8_OUT_BF16 && dw_dtype != FP8_OUT_F32) return FP8_ERR_INVALID_ARG;
+    if (accumulate && dw_dtype != FP8_OUT_F32) return FP8_ERR_UNSUPPORTED;
+    const int elt = dw_dtype == FP8_OUT_F32 ? 4 : 2;
+    if (tokens == 0) {      // no tokens, no gradient
+        if (accumulate || vocab == 0 || dim == 0) return FP8_OK;
+        if ((rc = rows_check(dw, lddw, dim, elt)) != FP8_OK) return rc;
+        return cudaMemset2DAsync(dw, (size_t)lddw * elt, 0, (size_t)dim * elt, (size_t)vocab, S(stream)) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    }
+    if (vocab == 0 || dim == 0) return FP8_ERR_SHAPE;
+    if ((rc = rows_check(x, ldx, dim)) != FP8_OK || (rc = rows_check(w, ldw, dim)) != FP8_OK ||
+        (rc = rows_check(dx, lddx, dim)) != FP8_OK || (rc = rows_check(dw, lddw, dim, elt)) != FP8_OK)
+        return rc;
+    if (!target || !loss || !lse || !dloss || !workspace) return FP8_ERR_INVALID_ARG;
+    if (!aligned4(target) || !aligned4(loss) || !aligned4(lse) || !aligned4(dloss) || !aligned4(dlse) || !aligned16(workspace))
+        return FP8_ERR_ALIGNMENT;
+    FP8FG_STATUS_OR_RETURN(st);
+    return launch_linear_xent_bwd(x, ldx, w, ldw, target, loss, lse, dloss, dlse, tokens, vocab, dim, scale, dx, lddx, dw, dw_dtype, lddw,
+                                  accumulate, workspace, st, S(stream));
+}
+
 }  // extern "C"

@@ -635,6 +635,36 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t *bar, uint32_t parit
     return ok;
 }
 
+// Bounded wait on an mbarrier phase for roles that hand over many times a
+// microsecond: the clock is read only after 256 polls (reading it at once, as
+// mbar_wait_bounded does, put about 1 us on every wait that had to wait).
+__device__ __forceinline__ bool wait_slow(uint32_t addr, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait_a(addr, parity)) return true;
+        if ((i & 255u) != 0u) continue;
+        if (*abort_flag) return false;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitTimeoutNs) {
+            if (!*abort_flag) {
+                *abort_flag = 1;
+                set_status(status, FP8_ERR_TIMEOUT);
+            }
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool thread_wait(uint32_t addr, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    return mbar_try_wait_a(addr, parity) || wait_slow(addr, parity, abort_flag, status);
+}
+// The same for a whole warp, which stays converged.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    return __all_sync(0xffffffffu, thread_wait(smem_u32(bar), parity, abort_flag, status));
+}
 
 // ---------------------------------------------------------------------- TMA
 
@@ -976,6 +1006,92 @@ __host__ __device__ constexpr uint32_t idesc_mxf8f6f4(int fmtA, int fmtB, int M,
 __host__ __device__ constexpr uint32_t idesc_mx_block(uint32_t idesc, uint32_t j)
 {
     return idesc | (j << 4) | (j << 29);
+}
+
+// ---------------------------------------------------------------- CTA pairs
+// tcgen05 with cta_group::2: a cluster of two CTAs works on one tile.  The
+// even CTA (rank 0) issues the instructions; each CTA holds half the rows of A
+// and half the columns of B in its shared memory, and the accumulator rows of
+// its half of A in its tensor memory.
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Shared-memory address of `p`'s place in the CTA of rank `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// All threads of both CTAs.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// 2-D tiled load into this CTA's shared memory, its bytes counted on a barrier
+// of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const CUtensorMap *map, uint32_t cluster_bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst_smem, uint32_t ncols)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void tmem_relinquish_pair()
+{
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives once on `bar` in both CTAs when every tcgen05 operation issued so
+// far by this thread has completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Instruction descriptor of tcgen05.mma .kind::f16 with BF16 A and B and an
+// FP32 accumulator; a_mn, b_mn: the operand is MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
 }
 
 }  // namespace fp8fg

@@ -92,4 +92,36 @@ int launch_swiglu_bwd(const void *gu, const void *dh, int64_t rows, int64_t F, v
 int launch_swiglu_quant(const void *gu, const void *dh, int64_t rows, int64_t F, int fmt, void *q, float *s,
                         void *qT, float *sT, int *status, cudaStream_t st);
 
+// norm_act.cu
+constexpr int64_t kNormMaxCols = 16384;
+int launch_rmsnorm_fwd_ckpt(const void *x, int64_t rows, int64_t cols, int64_t ldx, const void *res, int64_t ldres,
+                            const void *w, float eps, int fmt, void *y, int64_t ldy, void *sum, int64_t ldsum, void *c,
+                            float *cs, float *rstd, int *status, cudaStream_t st);
+size_t rmsnorm_workspace_bytes(int64_t cols);
+int launch_rmsnorm_bwd_ckpt(const void *c, const float *cs, const float *rstd, int fmt, int64_t rows, int64_t cols,
+                            const void *w, const void *dy, int64_t lddy, const void *dsum, int64_t lddsum, void *dx,
+                            int64_t lddx, float *dw, int accumulate, void *ws, int *status, cudaStream_t st);
+int launch_swiglu_fwd_ckpt(const void *gu, int64_t rows, int64_t F, int fmt, void *h, void *c, float *cs, int *status,
+                           cudaStream_t st);
+int launch_swiglu_bwd_ckpt(const void *c, const float *cs, const void *dh, int64_t rows, int64_t F, int fmt, void *dgu,
+                           int *status, cudaStream_t st);
+
+// embed.cu
+int launch_embedding_fwd(const int32_t *ids, int64_t tokens, const void *w, int64_t vocab, int64_t dim, int64_t ldw,
+                         float scale, void *out, int64_t ldo, int *status, cudaStream_t st);
+size_t embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
+int launch_embedding_bwd(const int32_t *ids, int64_t tokens, const void *dout, int64_t lddo, int64_t vocab, int64_t dim,
+                         float scale, void *dw, int dw_dtype, int64_t lddw, int accumulate, void *ws, int *status,
+                         cudaStream_t st);
+
+// xent.cu
+size_t linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim, bool backward);
+int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target,
+                           int64_t tokens, int64_t vocab, int64_t dim, float scale, float *loss, float *lse, void *ws,
+                           int *status, cudaStream_t st);
+int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target,
+                           const float *loss, const float *lse, const float *dloss, const float *dlse, int64_t tokens,
+                           int64_t vocab, int64_t dim, float scale, void *dx, int64_t lddx, void *dw, int dw_dtype,
+                           int64_t lddw, int accumulate, void *ws, int *status, cudaStream_t st);
+
 }  // namespace fp8fg

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "launch.cuh"
 
 namespace fp8fg {
 
@@ -113,28 +114,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-// Programmatic dependent launch: the kernels of this family let the next kernel
-// of the stream be set up while they run, and wait, before they touch memory, for
-// the one before them to be complete (about 1 us less between two short calls).
-__device__ __forceinline__ void dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... P, typename... A>
-inline int launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args)
-{
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
-}
-
 // a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division takes hundreds of cycles).
 __device__ __forceinline__ int64_t div_short(int64_t a, int64_t b)
 {
@@ -160,37 +139,6 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t *warp_sums, int64
         total += warp_sums[i];
     }
     return v + before;
-}
-
-// Bounded wait on an mbarrier phase for roles that hand over many times a
-// microsecond: the clock is read only after 256 polls (reading it at once, as
-// mbar_wait_bounded does, put about 1 us on every wait that had to wait).
-__device__ __forceinline__ bool wait_slow(uint32_t addr, uint32_t parity, volatile int *abort_flag, int *status)
-{
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait_a(addr, parity)) return true;
-        if ((i & 255u) != 0u) continue;
-        if (*abort_flag) return false;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > kWaitTimeoutNs) {
-            if (!*abort_flag) {
-                *abort_flag = 1;
-                set_status(status, FP8_ERR_TIMEOUT);
-            }
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool thread_wait(uint32_t addr, uint32_t parity, volatile int *abort_flag, int *status)
-{
-    return mbar_try_wait_a(addr, parity) || wait_slow(addr, parity, abort_flag, status);
-}
-// The same for a whole warp, which stays converged.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
-{
-    return __all_sync(0xffffffffu, thread_wait(smem_u32(bar), parity, abort_flag, status));
 }
 
 // paged_few.cu, paged_many.cu

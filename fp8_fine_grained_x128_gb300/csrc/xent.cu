@@ -1,0 +1,767 @@
+// xent.cu -- softmax cross entropy of a linear head, and its gradient, without
+// keeping the logits (sm_103a).
+//
+// With z = scale * x w^T over a vocabulary of V rows of w, per counted token:
+//   lse = log sum_v exp z_v,  loss = lse - z_t,
+// and for the gradients gl, gz of loss and lse
+//   g_v = scale * ((gl + gz) p_v - gl [v = t]),  p_v = exp(z_v - lse),
+//   dx = g w,  dw = g^T x.
+// p_t - 1 is taken as expm1(-loss), not as a difference, so that a token the
+// model is sure of keeps its small gradient; and the loss itself is formed as
+// log(1 + sum_{v != t} exp(z_v - z_t)) from a sum that leaves the target out,
+// so that it does not vanish in the rounding of lse.
+//
+// Everything is a product on the tensor cores (BF16 operands, FP32
+// accumulators): the forward's logits, and per piece of the vocabulary the
+// backward's logits (again), g w and g^T x.  One kernel does all four; they
+// differ in which operands run along K (k_xent<MODE>).
+//
+// Forward: the epilogue keeps, per row, a running maximum and sum over a unit
+// of up to 8 tiles and writes 8 bytes a row and unit, 1/64 of a BF16 logit row
+// and less; k_xent_join adds the units in order.
+// Backward: for a piece of the vocabulary, g is rounded to BF16 (the tensor
+// cores' operand type; it costs each of the products 2^-9 a term, random over
+// the terms, beside the same rounding of the BF16 results) and kept in the
+// workspace, [tokens][piece]; dx is summed over the pieces in FP32.
+//
+// Tokens that do not count are left out from the start: k_xent_pack copies the
+// counted rows of x together, so neither the work nor the results see the
+// others, whatever they hold.
+//
+// k_xent is a persistent kernel of CTA pairs (cta_group::2): a pair computes
+// 256 x 256 tiles, each CTA holding 128 rows of A and 128 columns of B of every
+// 64-deep stage, so that an SM fetches 32 KB where a CTA alone would fetch 48 KB
+// for its half of the tile.  Warp 0 copies (TMA, 6 stages), one thread of the
+// even CTA's warp 1 issues the MMAs, warps 2..5 drain one of two accumulators
+// while the next tile fills the other.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "tmap.h"
+
+namespace fp8fg {
+
+namespace {
+
+enum { XENT_LOSS = 0, XENT_GRAD = 1, XENT_DX = 2, XENT_DW = 3 };
+
+constexpr int kTile = 256;              // rows and columns of a pair's tile
+constexpr int kBK = 64;                 // K of a stage
+constexpr int kStages = 6;
+constexpr int kHalf = 128 * kBK * 2;    // bytes of one operand's half in one CTA's stage
+constexpr int kStage = 2 * kHalf;
+constexpr int kThreads = 192;
+constexpr int kEpiWarp0 = 2, kEpiWarps = 4;
+constexpr int kBars = 2 * kStages + 2 * 2 + 1;
+constexpr int kSmem = 1024 + kStages * kStage + kBars * 8 + 16;
+
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+struct XentArgs {
+    const int *count;           // counted tokens (nullptr: all `tokens` rows)
+    const int32_t *map;         // packed row -> token (nullptr: the same)
+    const int32_t *target;
+    int tokens, vocab, dim;
+    int v0, vn;                 // this piece's vocabulary: columns [v0, v0 + vn)
+    int per_unit;               // LOSS: tiles of a unit
+    int splits;                 // DX: parts of K
+    int band;                   // M tiles of a raster band
+    float scale;
+    // LOSS
+    float2 *part;               // [unit][rows]: maximum (times scale log2 e), sum of 2^(. - maximum)
+    float *z_target;            // [rows]: the target's logit, times log2 e
+    int64_t rows;               // rows of the packed buffers
+    // GRAD
+    const float *loss, *lse, *dloss, *dlse;
+    uint16_t *g;
+    int64_t ldg;
+    // DX, DW
+    float *acc;                 // DX: [splits][rows][dim]
+    int add, last;              // DX: add to acc; write dx (BF16) instead of acc
+    uint16_t *dx;
+    int64_t lddx;
+    void *dw;
+    int64_t lddw;
+    int dw_f32, accumulate;
+    int *status;
+};
+
+// A pair's tiles, in the same order for every role: unit u of the pair, its
+// tiles' columns [nt0, nt1), K blocks [k0, k1).
+struct Walk {
+    int num_mt, num_nt, num_ng, per, units, nkb, per_split;
+    int band;
+    __device__ __forceinline__ void unit(int u, int &mt, int &nt0, int &nt1, int &k0, int &k1, int &split) const
+    {
+        const int flat = num_mt * num_ng;
+        split = u / flat;
+        int ng;
+        tile_coords_raster(u - split * flat, num_mt, num_ng, band, mt, ng);
+        nt0 = ng * per;
+        nt1 = min(num_nt, nt0 + per);
+        k0 = min(nkb, split * per_split);
+        k1 = min(nkb, k0 + per_split);
+    }
+};
+
+template <int MODE>
+__device__ __forceinline__ Walk make_walk(const XentArgs &a)
+{
+    const int rows = a.count ? *a.count : a.tokens;
+    const int M = MODE == XENT_DW ? a.vn : rows, N = MODE >= XENT_DX ? a.dim : a.vn;
+    const int K = MODE == XENT_DX ? a.vn : MODE == XENT_DW ? rows : a.dim;
+    Walk w;
+    w.num_mt = (M + kTile - 1) / kTile;
+    w.num_nt = (N + kTile - 1) / kTile;
+    w.per = MODE == XENT_LOSS ? a.per_unit : 1;
+    w.num_ng = (w.num_nt + w.per - 1) / w.per;
+    w.nkb = (K + kBK - 1) / kBK;
+    const int splits = MODE == XENT_DX ? a.splits : 1;
+    w.per_split = (w.nkb + splits - 1) / splits;
+    w.units = w.num_mt * w.num_ng * splits;
+    w.band = a.band;
+    return w;
+}
+
+// 8 FP32 values to 16 bytes of BF16.
+__device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
+{
+    auto f = [&](int i) { return __uint_as_float(r[i]); };
+    return make_uint4(bf16x2_rn(f(0), f(1)), bf16x2_rn(f(2), f(3)), bf16x2_rn(f(4), f(5)), bf16x2_rn(f(6), f(7)));
+}
+
+}  // namespace
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_xent(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const XentArgs a)
+{
+    constexpr bool kMnA = MODE == XENT_DW, kMnB = MODE >= XENT_DX;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage);
+    uint64_t *empty = full + kStages;
+    uint64_t *tfull = empty + kStages;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *mma_done = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 2 * kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();     // the pair's barriers are there before either CTA signals the other's
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    dependents_launch();
+    dependency_wait();
+    const Walk w = make_walk<MODE>(a);
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------ TMA producer
+        uint32_t it = 0;
+        bool ok = true;
+        for (int u = pair; u < w.units && ok; u += pairs) {
+            int mt, nt0, nt1, k0, k1, split;
+            w.unit(u, mt, nt0, nt1, k0, k1, split);
+            const int m = mt * kTile + rank * 128;
+            for (int nt = nt0; nt < nt1 && ok; ++nt) {
+                const int n = nt * kTile + rank * 128;
+                for (int kb = k0; kb < k1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!thread_wait(smem_u32(&empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
+                    // what lies outside a matrix is filled with zeros and counts its bytes all the same
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+                    const uint32_t bar = cluster_addr(&full[s], 0);
+                    uint8_t *sa = smem + s * kStage, *sb = sa + kHalf;
+                    if (kMnA) {
+                        tma_load_2d_pair(sa, &tmA, bar, m, kb * kBK);
+                        tma_load_2d_pair(sa + 8192, &tmA, bar, m + 64, kb * kBK);
+                    } else {
+                        tma_load_2d_pair(sa, &tmA, bar, kb * kBK, m);
+                    }
+                    if (kMnB) {
+                        const int v = (MODE == XENT_DX ? a.v0 : 0) + kb * kBK;
+                        tma_load_2d_pair(sb, &tmB, bar, n, v);
+                        tma_load_2d_pair(sb + 8192, &tmB, bar, n + 64, v);
+                    } else {
+                        tma_load_2d_pair(sb, &tmB, bar, kb * kBK, a.v0 + n);
+                    }
+                }
+            }
+        }
+        // the copies in flight land (the even CTA's barrier counts both CTAs'),
+        // and the last stages' releases arrive, before the pair may leave
+        const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0;
+        for (uint32_t j = first; j < it; ++j) {
+            if (rank == 0) mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1, nullptr);
+            if (ok) mbar_wait_bounded(&empty[j % kStages], (j / kStages) & 1, abort_flag);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ------------------------------------------------------ MMA issuer
+        if (rank == 0) {
+            constexpr uint32_t idesc = idesc_bf16(256, kTile, kMnA, kMnB);
+            uint32_t it = 0, tc = 0;
+            bool ok = true;
+            for (int u = pair; u < w.units && ok; u += pairs) {
+                int mt, nt0, nt1, k0, k1, split;
+                w.unit(u, mt, nt0, nt1, k0, k1, split);
+                for (int nt = nt0; nt < nt1 && ok; ++nt, ++tc) {
+                    const uint32_t buf = tc & 1;
+                    if (!thread_wait(smem_u32(&tempty[buf]), ((tc >> 1) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + buf * kTile;
+                    for (int kb = k0; kb < k1; ++kb, ++it) {
+                        const int s = it % kStages;
+                        if (!thread_wait(smem_u32(&full[s]), (it / kStages) & 1, abort_flag, a.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + s * kStage), sb = sa + kHalf;
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k) {
+                            // 16 of K: 32 bytes along a row, or two 1024-byte swizzle atoms of rows
+                            const uint64_t ad = kMnA ? sdesc_mnmajor_sw128(sa + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sa + k * 32);
+                            const uint64_t bd = kMnB ? sdesc_mnmajor_sw128(sb + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sb + k * 32);
+                            tc_mma_f16_pair(d, ad, bd, idesc, (kb > k0 || k > 0) ? 1u : 0u);
+                        }
+                        tc_commit_pair(&empty[s]);
+                    }
+                    if (ok) tc_commit_pair(&tfull[buf]);
+                }
+            }
+            tc_commit_pair(mma_done);
+        }
+        mbar_wait_bounded(mma_done, 0, nullptr);
+    } else if (warp >= kEpiWarp0) {
+        // ------------------------------------------------------ epilogue
+        const int lq = warp & 3;                 // TMEM lane quarter of this warp
+        const uint32_t tm_lane = tmem_base + ((uint32_t)(lq * 32) << 16);
+        const int rows = a.count ? *a.count : a.tokens;
+        uint32_t tc = 0;
+        bool ok = true;
+        for (int u = pair; u < w.units && ok; u += pairs) {
+            int mt, nt0, nt1, k0, k1, split;
+            w.unit(u, mt, nt0, nt1, k0, k1, split);
+            const int row = mt * kTile + rank * 128 + lq * 32 + lane;
+            // per row of LOSS and GRAD
+            const int token = MODE <= XENT_DX && row < rows ? (a.map ? a.map[row] : row) : -1;
+            const int target = MODE <= XENT_GRAD && token >= 0 ? a.target[token] - a.v0 : -1;
+            const float c = a.scale * kLog2e;
+            float top = -INFINITY, sum = 0.0f;              // LOSS
+            float lse2 = 0.0f, coef = 0.0f, at_target = 0.0f;   // GRAD
+            if (MODE == XENT_GRAD && token >= 0) {
+                const float lse = a.lse[token], loss = a.loss[token], gl = a.dloss[token], gz = a.dlse ? a.dlse[token] : 0.0f;
+                lse2 = lse * kLog2e;
+                coef = a.scale * (gl + gz);
+                at_target = a.scale * (gl * expm1f(-loss) + gz * expf(-loss));
+            }
+            for (int nt = nt0; nt < nt1; ++nt, ++tc) {
+                const uint32_t buf = tc & 1;
+                if (!(ok = __all_sync(0xffffffffu, thread_wait(smem_u32(&tfull[buf]), (tc >> 1) & 1, abort_flag, a.status)))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < kTile / 32; ++j) {
+                    uint32_t r[32];
+                    tc_ld_32x32b_x32(tm_lane + buf * kTile + j * 32, r);
+                    tc_wait_ld();
+                    const int col = nt * kTile + j * 32;    // in the piece, or of dx / dw
+                    if (MODE == XENT_LOSS) {
+                        const int lim = a.vn - col;
+                        if (lim < 32) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i >= lim) r[i] = __float_as_uint(-INFINITY);
+                        }
+                        const int t = target - col;
+                        if (t >= 0 && t < min(32, lim)) {       // kept apart, and out of the sum
+                            float z = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i == t) {
+                                    z = __uint_as_float(r[i]);
+                                    r[i] = __float_as_uint(-INFINITY);
+                                }
+                            if (dbg_span(row, 1, a.rows, a.status)) a.z_target[row] = z * c;
+                        }
+                        float m = top;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(r[i]) * c);
+                        if (m > top) {
+                            sum *= ex2_approx_ftz(top - m);
+                            top = m;
+                        }
+                        const float off = top == -INFINITY ? 0.0f : -top;
+                        float s[4] = {};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[i & 3] += ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, off));
+                        sum += (s[0] + s[1]) + (s[2] + s[3]);
+                    } else if (MODE == XENT_GRAD) {
+                        const int lim = token >= 0 ? a.vn - col : 0, t = target - col;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            float g = coef * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -lse2));
+                            if (i == t) g = at_target;
+                            r[i] = __float_as_uint(i < lim ? g : 0.0f);
+                        }
+                        const int64_t at = (int64_t)row * a.ldg + col;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (dbg_cell(row, col + i, 8, a.rows, a.ldg, a.status)) *reinterpret_cast<uint4 *>(a.g + at + i) = bf16x8(r + i);
+                    } else {
+                        if (k0 == k1) {     // no K: the accumulator was not written
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[i] = 0;
+                        }
+                        if (MODE == XENT_DX && token >= 0) {
+                            float *acc = a.acc + ((int64_t)split * a.rows + row) * a.dim;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                if (col + i >= a.dim) break;
+                                if (a.add) {
+                                    const float4 x = *reinterpret_cast<const float4 *>(acc + col + i), y = *reinterpret_cast<const float4 *>(acc + col + i + 4);
+                                    const float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) r[i + e] = __float_as_uint(__uint_as_float(r[i + e]) + o[e]);
+                                }
+                                if (a.last) {
+                                    if (dbg_span((int64_t)token * a.lddx + col + i, 8, (int64_t)(a.tokens - 1) * a.lddx + a.dim, a.status))
+                                        *reinterpret_cast<uint4 *>(a.dx + (int64_t)token * a.lddx + col + i) = bf16x8(r + i);
+                                } else if (dbg_cell((int64_t)split * a.rows + row, col + i, 8, (int64_t)a.splits * a.rows, a.dim, a.status)) {
+                                    *reinterpret_cast<uint4 *>(acc + col + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                                    *reinterpret_cast<uint4 *>(acc + col + i + 4) = make_uint4(r[i + 4], r[i + 5], r[i + 6], r[i + 7]);
+                                }
+                            }
+                        }
+                        if (MODE == XENT_DW && row < a.vn) {
+                            const int64_t at = (int64_t)(a.v0 + row) * a.lddw + col;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                if (col + i >= a.dim) break;
+                                if (!dbg_span(at + i, 8, (int64_t)(a.vocab - 1) * a.lddw + a.dim, a.status)) continue;
+                                if (a.dw_f32) {
+                                    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.dw) + at + i);
+                                    if (a.accumulate) {
+                                        const float4 x = p[0], y = p[1];
+                                        const float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) r[i + e] = __float_as_uint(__uint_as_float(r[i + e]) + o[e]);
+                                    }
+                                    *reinterpret_cast<uint4 *>(p) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                                    *reinterpret_cast<uint4 *>(p + 1) = make_uint4(r[i + 4], r[i + 5], r[i + 6], r[i + 7]);
+                                } else {
+                                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dw) + at + i) = bf16x8(r + i);
+                                }
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
+            }
+            if (MODE == XENT_LOSS && ok && row < a.rows) {
+                const int64_t at = (int64_t)(nt0 / w.per) * a.rows + row;
+                if (dbg_span(at, 1, (int64_t)w.num_ng * a.rows, a.status)) a.part[at] = make_float2(top, sum);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();     // neither CTA leaves while the other may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The counted tokens' rows of x, one behind another, zeros up to the next
+// multiple of 256, and the token of each.  Every CTA takes a range of tokens and
+// counts the ones before it by itself.  Rows of the outputs that belong to
+// tokens left out are zeroed here.
+// ---------------------------------------------------------------------------
+struct PackArgs {
+    const int32_t *target;
+    const uint16_t *x;
+    int64_t ldx;
+    int tokens, vocab, dim;
+    uint16_t *xp;               // [rows][dim]
+    int64_t rows;
+    int32_t *map;
+    int *count;
+    float *loss, *lse;          // forward: zeroed where a token does not count
+    uint16_t *dx;               // backward: the same
+    int64_t lddx;
+    int *status;
+};
+
+__global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
+{
+    __shared__ int warp_n[8];
+    __shared__ int32_t src[256];
+    dependents_launch();
+    dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (g.tokens + gridDim.x - 1) / gridDim.x;
+    const int t0 = min(g.tokens, (int)blockIdx.x * per), t1 = min(g.tokens, t0 + per);
+    auto counts = [&](int t) { const int v = g.target[t]; return v >= 0 && v < g.vocab; };
+    auto cta_sum = [&](int n) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        __syncthreads();
+        if (lane == 0) warp_n[warp] = n;
+        __syncthreads();
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n += warp_n[i];
+        return n;
+    };
+    int n = 0;
+    for (int t = threadIdx.x; t < t0; t += 256) n += counts(t);
+    int at = cta_sum(n);
+    const int nv = g.dim / 8;
+    for (int base = t0; base < t1; base += 256) {
+        const int t = base + threadIdx.x;
+        const bool mine = t < t1, in = mine && counts(t);
+        if (mine && g.target[t] >= g.vocab) set_status(g.status, FP8_ERR_INVALID_ARG);
+        const unsigned votes = __ballot_sync(0xffffffffu, in);
+        __syncthreads();
+        if (lane == 0) warp_n[warp] = __popc(votes);
+        __syncthreads();
+        int before = __popc(votes & ((1u << lane) - 1)), total = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i < warp) before += warp_n[i];
+            total += warp_n[i];
+        }
+        if (in) {
+            src[before] = t;
+            if (dbg_span(at + before, 1, g.rows, g.status)) g.map[at + before] = t;
+        } else if (mine && g.loss) {
+            if (dbg_span(t, 1, g.tokens, g.status)) g.loss[t] = g.lse[t] = 0.0f;
+        }
+        __syncthreads();
+        for (int r = warp; r < total; r += 8) {
+            const uint16_t *from = g.x + (int64_t)src[r] * g.ldx;
+            for (int v = lane; v < nv; v += 32)
+                if (dbg_cell(at + r, v * 8, 8, g.rows, g.dim, g.status))
+                    *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r) * g.dim + v * 8) = ldg_stream(from + v * 8);
+        }
+        if (g.dx)
+            for (int r = warp; r < min(256, t1 - base); r += 8)
+                if (!counts(base + r))
+                    for (int v = lane; v < nv; v += 32)
+                        if (dbg_span((base + r) * g.lddx + v * 8, 8, (g.tokens - 1) * g.lddx + g.dim, g.status))
+                            *reinterpret_cast<uint4 *>(g.dx + (base + r) * g.lddx + v * 8) = make_uint4(0, 0, 0, 0);
+        at += total;
+    }
+    if (t1 == g.tokens && (t0 < g.tokens || blockIdx.x == 0)) {   // the CTA with the last token
+        if (threadIdx.x == 0) *g.count = at;
+        const int end = (at + kTile - 1) / kTile * kTile;
+        for (int r = at + warp; r < end; r += 8)
+            for (int v = lane; v < nv; v += 32)
+                if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status))
+                    *reinterpret_cast<uint4 *>(g.xp + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward, last step: a row's units added in a fixed order.  32 rows a CTA, its
+// 32 warps take every 32nd unit.  M, S: maximum and sum without the target.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) k_xent_join(const float2 *part, const float *z_target, int units, int64_t rows, const int *count,
+                                                  const int32_t *map, const int32_t *target, int tokens, int vocab, float *loss, float *lse,
+                                                  int *status)
+{
+    __shared__ float tops[32][33], sums[32][33];
+    dependents_launch();
+    dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * 32 + lane, n = count ? *count : tokens;
+    if (blockIdx.x * 32 >= n) return;
+    float M = -INFINITY, S = 0.0f;
+    if (row < n) {
+#pragma unroll 4
+        for (int u = warp; u < units; u += 32) {
+            const float2 p = part[(int64_t)u * rows + row];
+            const float m = fmaxf(M, p.x);
+            if (m > -INFINITY) S = S * exp2f(M - m) + p.y * exp2f(p.x - m);
+            else S += p.y;      // 0, or the NaN of a row of NaN
+            M = m;
+        }
+    }
+    tops[warp][lane] = M;
+    sums[warp][lane] = S;
+    __syncthreads();
+    if (warp != 0 || row >= n) return;
+    for (int i = 1; i < 32; ++i) {
+        const float top = tops[i][lane], m = fmaxf(M, top);
+        if (m > -INFINITY) S = S * exp2f(M - m) + sums[i][lane] * exp2f(top - m);
+        else S += sums[i][lane];
+        M = m;
+    }
+    const int t = map ? map[row] : row;
+    const int at = target[t];
+    float l = 0.0f, z = 0.0f;
+    if (at >= 0 && at < vocab) {
+        const float zt = z_target[row];
+        if (zt >= M) {          // the target leads: log(1 + the rest relative to it)
+            l = log1pf(S * exp2f(M - zt));
+            z = zt * kLn2 + l;
+        } else {
+            const float s = logf(S + exp2f(zt - M));
+            l = (M - zt) * kLn2 + s;
+            z = M * kLn2 + s;
+        }
+        if (zt != zt) l = z = zt;
+    } else if (at >= vocab) {
+        set_status(status, FP8_ERR_INVALID_ARG);
+    }
+    if (dbg_span(t, 1, tokens, status)) {
+        loss[t] = l;
+        lse[t] = z;
+    }
+}
+
+// Backward with K of dx split: the parts added in order, rounded to BF16.
+__global__ void __launch_bounds__(256) k_xent_dx_join(const float *acc, int splits, int64_t rows, const int *count, const int32_t *map, int dim,
+                                                    uint16_t *dx, int64_t lddx, int tokens, int *status)
+{
+    dependents_launch();
+    dependency_wait();
+    const int nv = dim / 8;
+    const int64_t items = (int64_t)*count * nv;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / nv;
+        const int col = (int)(i - row * nv) * 8;
+        float v[8] = {};
+        for (int s = 0; s < splits; ++s) {
+            const float4 *p = reinterpret_cast<const float4 *>(acc + (s * rows + row) * dim + col);
+            const float4 x = p[0], y = p[1];
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+        }
+        const int64_t at = (int64_t)map[row] * lddx + col;
+        if (dbg_span(at, 8, (int64_t)(tokens - 1) * lddx + dim, status))
+            *reinterpret_cast<uint4 *>(dx + at) = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+    }
+}
+
+// ------------------------------------------------------------------ launchers
+
+namespace {
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// A single tile of rows saves nothing by packing them.
+bool packs(int64_t tokens) { return tokens > kTile; }
+
+// Sizes that follow from those of the call alone.
+struct XentPlan {
+    int64_t rows;                   // of the packed buffers
+    int per_unit, units;            // forward: tiles of a unit, units of a row
+    int64_t piece;                  // backward: vocabulary of a piece
+    int splits;                     // backward: parts of dx's K
+    bool sums;                      // backward: dx goes through the FP32 buffer
+    int64_t count, map, xp, part, z, g, acc, bytes;     // byte offsets
+    XentPlan(int64_t tokens, int64_t vocab, int64_t dim, bool backward)
+    {
+        rows = up(tokens, kTile);
+        const int64_t mt = rows / kTile, nt = (vocab + kTile - 1) / kTile, pairs = std::max(1, sm_count() / 2);
+        int64_t at = 0;
+        auto take = [&](int64_t n) { const int64_t p = at; at += up(n, 256); return p; };
+        count = take(16);
+        map = take(rows * 4);
+        xp = backward || packs(tokens) ? take(rows * dim * 2) : 0;
+        if (!backward) {
+            // long units write less; 16 of them a pair keep the pairs' shares even
+            per_unit = 8;
+            while (per_unit > 1 && mt * ((nt + per_unit - 1) / per_unit) < 16 * pairs) per_unit /= 2;
+            units = (int)((nt + per_unit - 1) / per_unit);
+            part = take((int64_t)units * rows * 8);
+            z = take(rows * 4);
+        } else {
+            // pieces of equal length whose gradient takes up to 256 MB
+            const int64_t most = std::max<int64_t>(kTile, ((int64_t)128 << 20) / rows / kTile * kTile);
+            const int64_t pieces = (up(vocab, kTile) + most - 1) / most;
+            piece = up((vocab + pieces - 1) / pieces, kTile);
+            const int64_t tiles = mt * ((dim + kTile - 1) / kTile);
+            splits = (int)std::max<int64_t>(1, std::min(pairs / tiles, piece / kBK / 8));
+            sums = splits > 1 || piece < vocab;
+            g = take(rows * piece * 2);
+            acc = sums ? take((int64_t)splits * rows * dim * 4) : 0;
+        }
+        bytes = at;
+    }
+};
+
+template <int MODE>
+int run(const CUtensorMap &mA, const CUtensorMap &mB, const XentArgs &a, cudaStream_t st)
+{
+    static_assert(kSmem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_done[dev & 63]) {
+        if (cudaFuncSetAttribute(k_xent<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return FP8_ERR_CUDA;
+        attr_done[dev & 63] = true;
+    }
+    return launch_dependent(k_xent<MODE>, dim3((unsigned)(sm_count() / 2 * 2)), kThreads, kSmem, st, mA, mB, a);
+}
+
+// K-major operand: rows of K, 128 of them a box; MN-major: rows along K, boxes of 64 columns.
+bool map_k(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t ld)
+{
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, kBK, 128,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+bool map_mn(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t ld)
+{
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, 64, kBK,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+int pack(const XentPlan &p, uint8_t *ws, const int32_t *target, const void *x, int64_t ldx, int64_t tokens, int64_t vocab, int64_t dim, float *loss,
+         float *lse, void *dx, int64_t lddx, int *status, cudaStream_t st)
+{
+    PackArgs g{};
+    g.target = target;
+    g.x = static_cast<const uint16_t *>(x);
+    g.ldx = ldx;
+    g.tokens = (int)tokens;
+    g.vocab = (int)vocab;
+    g.dim = (int)dim;
+    g.xp = reinterpret_cast<uint16_t *>(ws + p.xp);
+    g.rows = p.rows;
+    g.map = reinterpret_cast<int32_t *>(ws + p.map);
+    g.count = reinterpret_cast<int *>(ws + p.count);
+    g.loss = loss;
+    g.lse = lse;
+    g.dx = static_cast<uint16_t *>(dx);
+    g.lddx = lddx;
+    g.status = status;
+    const int64_t grid = std::min<int64_t>((tokens + 7) / 8, (int64_t)sm_count() * 4);
+    return launch_dependent(k_xent_pack, dim3((unsigned)grid), 256, 0, st, g);
+}
+
+}  // namespace
+
+size_t linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim, bool backward)
+{
+    return (size_t)XentPlan(tokens, vocab, dim, backward).bytes;
+}
+
+int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target, int64_t tokens, int64_t vocab,
+                           int64_t dim, float scale, float *loss, float *lse, void *workspace, int *status, cudaStream_t st)
+{
+    const XentPlan p(tokens, vocab, dim, false);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    XentArgs a{};
+    int rc;
+    const void *xp = x;
+    int64_t ldxp = ldx, xrows = tokens;
+    if (packs(tokens)) {
+        if ((rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, loss, lse, nullptr, 0, status, st)) != FP8_OK) return rc;
+        xp = ws + p.xp;
+        ldxp = dim;
+        xrows = p.rows;
+        a.count = reinterpret_cast<int *>(ws + p.count);
+        a.map = reinterpret_cast<int32_t *>(ws + p.map);
+    }
+    CUtensorMap mX, mW;
+    if (!map_k(&mX, xp, dim, xrows, ldxp) || !map_k(&mW, w, dim, vocab, ldw)) return FP8_ERR_CUDA;
+    a.target = target;
+    a.tokens = (int)tokens;
+    a.vocab = a.vn = (int)vocab;
+    a.dim = (int)dim;
+    a.per_unit = p.per_unit;
+    a.splits = 1;
+    a.band = 16;
+    a.scale = scale;
+    a.part = reinterpret_cast<float2 *>(ws + p.part);
+    a.z_target = reinterpret_cast<float *>(ws + p.z);
+    a.rows = p.rows;
+    a.status = status;
+    if ((rc = run<XENT_LOSS>(mX, mW, a, st)) != FP8_OK) return rc;
+    return launch_dependent(k_xent_join, dim3((unsigned)((tokens + 31) / 32)), 1024, 0, st, static_cast<const float2 *>(a.part),
+                            static_cast<const float *>(a.z_target), p.units, p.rows, a.count, a.map, target, a.tokens, a.vocab, loss, lse, status);
+}
+
+int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target, const float *loss, const float *lse,
+                           const float *dloss, const float *dlse, int64_t tokens, int64_t vocab, int64_t dim, float scale, void *dx, int64_t lddx,
+                           void *dw, int dw_dtype, int64_t lddw, int accumulate, void *workspace, int *status, cudaStream_t st)
+{
+    const XentPlan p(tokens, vocab, dim, true);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    int rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, nullptr, nullptr, dx, lddx, status, st);
+    if (rc != FP8_OK) return rc;
+    XentArgs a{};
+    a.count = reinterpret_cast<int *>(ws + p.count);
+    a.map = reinterpret_cast<int32_t *>(ws + p.map);
+    a.target = target;
+    a.tokens = (int)tokens;
+    a.vocab = (int)vocab;
+    a.dim = (int)dim;
+    a.splits = p.splits;
+    a.per_unit = 1;
+    a.scale = scale;
+    a.rows = p.rows;
+    a.loss = loss;
+    a.lse = lse;
+    a.dloss = dloss;
+    a.dlse = dlse;
+    a.g = reinterpret_cast<uint16_t *>(ws + p.g);
+    a.ldg = p.piece;
+    a.acc = reinterpret_cast<float *>(ws + p.acc);
+    a.dx = static_cast<uint16_t *>(dx);
+    a.lddx = lddx;
+    a.dw = dw;
+    a.lddw = lddw;
+    a.dw_f32 = dw_dtype == FP8_OUT_F32;
+    a.accumulate = accumulate;
+    a.status = status;
+    const void *xp = ws + p.xp, *g = ws + p.g;
+    CUtensorMap kX, kW, kG, mnW, mnG, mnX;
+    if (!map_k(&kX, xp, dim, p.rows, dim) || !map_k(&kW, w, dim, vocab, ldw) || !map_k(&kG, g, p.piece, p.rows, p.piece) ||
+        !map_mn(&mnW, w, dim, vocab, ldw) || !map_mn(&mnG, g, p.piece, p.rows, p.piece) || !map_mn(&mnX, xp, dim, p.rows, dim))
+        return FP8_ERR_CUDA;
+    for (int64_t v = 0; v < vocab; v += p.piece) {
+        a.v0 = (int)v;
+        a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
+        a.band = 16;
+        if ((rc = run<XENT_GRAD>(kX, kW, a, st)) != FP8_OK) return rc;
+        a.add = v > 0;
+        a.last = p.splits == 1 && v + p.piece >= vocab;
+        a.band = 8;
+        if ((rc = run<XENT_DX>(kG, mnW, a, st)) != FP8_OK) return rc;
+        if ((rc = run<XENT_DW>(mnG, mnX, a, st)) != FP8_OK) return rc;
+    }
+    if (p.splits == 1) return FP8_OK;
+    const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + 255) / 256, (int64_t)sm_count() * 8);
+    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), 256, 0, st, static_cast<const float *>(a.acc), p.splits, p.rows, a.count, a.map,
+                            a.dim, a.dx, lddx, a.tokens, status);
+}
+
+}  // namespace fp8fg

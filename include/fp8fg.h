@@ -588,6 +588,122 @@ FP8FG_API int fp8_swiglu_quant_fwd(const void *gu, int64_t rows, int64_t F, int 
 FP8FG_API int fp8_swiglu_bwd_quant(const void *gu, const void *dh, int64_t rows, int64_t F, int fmt,
                                    void *q, float *s, void *qT, float *sT, void *stream);
 
+/* ------------------------------------------- activations kept in 8 bits
+ *
+ * [Ling] "Fine-grained quantization" applied to what a backward pass needs of
+ * its forward: the input of a norm or of SwiGLU is kept as 1x128 codes and
+ * scales (c [rows][cols], cs S[cols/128][rows]: what fp8_quant_1x128 writes for
+ * it, code for code), 1.03 bytes an element instead of 2, and the backward reads
+ * those.  The pages describe neither the operators nor which tensors are kept:
+ * both are this library's own. */
+
+/* Residual add and RMSNorm.  With h = x, or h = RN_bf16(x + res) where res is
+ * given (h is then written to sum):
+ *   rstd = (sum_c h^2 / cols + eps)^(-1/2),  y = RN_bf16(h * rstd * w)
+ * in FP32, and c, cs = the quantization of h.
+ *   x, res, y, sum: BF16 [rows][ld...]; res and sum both NULL or both set.
+ *   sum may be x or res, and y any of them (each element is read before it is
+ *   written).  w: BF16 [cols].  rstd: FP32 [rows].
+ *   cols % 128 == 0, cols <= 16384, eps > 0; BF16 pointers and c 16-byte
+ *   aligned, leading dimensions >= cols and multiples of 8.
+ * A chunk of h holding Inf/NaN records FP8_ERR_NONFINITE (its codes are
+ * unspecified; y is what the formula gives). */
+FP8FG_API int fp8_rmsnorm_fwd_ckpt(const void *x, int64_t rows, int64_t cols, int64_t ldx, const void *res,
+                                   int64_t ldres, const void *w, float eps, int fmt, void *y, int64_t ldy, void *sum,
+                                   int64_t ldsum, void *c, float *cs, float *rstd, void *stream);
+
+/* Bytes of the caller-owned workspace of fp8_rmsnorm_bwd_ckpt on the current
+ * device (any content; calls sharing one must not overlap on the GPU). */
+FP8FG_API size_t fp8_rmsnorm_workspace_bytes(int64_t cols);
+
+/* Its gradient from the codes.  With n = h * rstd, h the values that c and cs
+ * stand for and rstd the forward's:
+ *   dx = RN_bf16((dy w - n * mean_c(dy w n)) * rstd + dsum),   dw (+)= sum_r dy n
+ * dsum (optional): the gradient that reaches the sum by other ways, so dx is the
+ * gradient of both x and res.  dw: FP32 [cols], added to where accumulate is
+ * nonzero, in an order that is the same in every run.  dx may be dy or dsum.
+ * Sizes, layouts and alignment as above; workspace 16-byte aligned. */
+FP8FG_API int fp8_rmsnorm_bwd_ckpt(const void *c, const float *cs, const float *rstd, int fmt, int64_t rows,
+                                   int64_t cols, const void *w, const void *dy, int64_t lddy, const void *dsum,
+                                   int64_t lddsum, void *dx, int64_t lddx, float *dw, int accumulate, void *workspace,
+                                   void *stream);
+
+/* fp8_swiglu_fwd (h [rows][F], the same values) that also keeps gu [rows][2F]:
+ * c [rows][2F], cs S[2F/128][rows].  F % 128 == 0; all pointers 16-byte
+ * aligned, cs 4-byte.  A chunk holding Inf/NaN records FP8_ERR_NONFINITE. */
+FP8FG_API int fp8_swiglu_fwd_ckpt(const void *gu, int64_t rows, int64_t F, int fmt, void *h, void *c, float *cs,
+                                  void *stream);
+
+/* fp8_swiglu_bwd from the values that c and cs stand for: dgu BF16 [rows][2F]. */
+FP8FG_API int fp8_swiglu_bwd_ckpt(const void *c, const float *cs, const void *dh, int64_t rows, int64_t F, int fmt,
+                                  void *dgu, void *stream);
+
+/* ------------------------------------------------ the two ends of a step
+ *
+ * The embedding and the loss, which FP8 training leaves in BF16 ([Infra]
+ * "Transformer Engine" runs the Linear layers in FP8; the pages have no
+ * counterpart of these operators: their definitions are this library's own). */
+
+/* out[t] = RN_bf16(scale * w[ids[t]]).  ids: DEVICE int32[tokens]; a negative id
+ * is padding and gives zeros, one >= vocab records FP8_ERR_INVALID_ARG and
+ * gives zeros.  w: BF16 [vocab][ldw], out: BF16 [tokens][ldo], dim % 8 == 0,
+ * 16-byte aligned, leading dimensions >= dim and multiples of 8; tokens <= 2^30. */
+FP8FG_API int fp8_embedding_fwd(const int32_t *ids, int64_t tokens, const void *w, int64_t vocab, int64_t dim,
+                                int64_t ldw, float scale, void *out, int64_t ldo, void *stream);
+
+/* Bytes of the caller-owned workspace of fp8_embedding_bwd (any content; calls
+ * sharing one must not overlap on the GPU). */
+FP8FG_API size_t fp8_embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
+
+/* dw[v] (+)= scale * sum over t with ids[t] = v of dout[t], summed in FP32 in an
+ * order that the ids alone decide (no floating-point atomics).  dw [vocab][lddw]
+ * FP32 or BF16 (dw_dtype); accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): added
+ * to, rows without tokens untouched; else every row of dw is written, zeros where
+ * no token has its id.  Negative ids are left out, whatever their dout holds; ids
+ * >= vocab too, and record FP8_ERR_INVALID_ARG.  Sizes and alignment as above;
+ * vocab <= 2^30, lddw * element size a multiple of 16; workspace 16-byte aligned. */
+FP8FG_API int fp8_embedding_bwd(const int32_t *ids, int64_t tokens, const void *dout, int64_t lddo, int64_t vocab,
+                                int64_t dim, float scale, void *dw, int dw_dtype, int64_t lddw, int accumulate,
+                                void *workspace, void *stream);
+
+/* Bytes of the caller-owned workspace of fp8_linear_xent_fwd (backward = 0) or
+ * fp8_linear_xent_bwd (1) on the current device (any content; calls sharing one
+ * must not overlap on the GPU; the two calls of a step may share the larger). */
+FP8FG_API size_t fp8_linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim, int backward);
+
+/* Softmax cross entropy of a linear head, without keeping the logits.  With
+ * z_v = scale * sum_d x[t][d] w[v][d]:
+ *   lse[t] = log sum_v exp z_v,   loss[t] = lse[t] - z_target[t]
+ * Products of BF16 values summed in FP32; loss is formed without the cancellation
+ * that this difference has when the target carries the sum.
+ *   x: BF16 [tokens][ldx], w: BF16 [vocab][ldw], dim % 8 == 0, 16-byte aligned,
+ *   leading dimensions >= dim and multiples of 8; tokens, vocab, dim < 2^28.
+ *   target: DEVICE int32[tokens].  A token with a negative target does not count:
+ *   loss = lse = 0, whatever its row of x holds.  One >= vocab records
+ *   FP8_ERR_INVALID_ARG and does not count either.
+ *   loss, lse: FP32 [tokens].  scale > 0.  vocab or dim 0: FP8_ERR_SHAPE where
+ *   there are tokens.
+ * A counted row whose logits hold NaN or +Inf gives NaN, for itself alone. */
+FP8FG_API int fp8_linear_xent_fwd(const void *x, int64_t tokens, int64_t dim, int64_t ldx, const void *w,
+                                  int64_t vocab, int64_t ldw, const int32_t *target, float scale, float *loss,
+                                  float *lse, void *workspace, void *stream);
+
+/* Its gradient.  With gl = dloss[t], gz = dlse[t] (dlse NULL: 0), p_v = exp(z_v - lse):
+ *   g[t][v] = scale * ((gl + gz) p_v - gl [v = target[t]])
+ *   dx = g w (BF16),   dw (+)= g^T x (BF16 or FP32; dw_dtype)
+ * p_target - 1 is taken from loss, as expm1(-loss).  g is rounded to BF16 (the
+ * operands of the two products), everything else is FP32 up to the results.
+ * loss, lse: as fp8_linear_xent_fwd left them for the same x, w, target, scale.
+ * accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): added to dw; else every row is
+ * written.  Tokens that do not count get dx = 0 and add nothing to dw, whatever
+ * their rows of x, dloss and dlse hold.
+ * dx [tokens][lddx], dw [vocab][lddw]: 16-byte aligned rows of at least dim.
+ * The results are the same in every run. */
+FP8FG_API int fp8_linear_xent_bwd(const void *x, int64_t tokens, int64_t dim, int64_t ldx, const void *w,
+                                  int64_t vocab, int64_t ldw, const int32_t *target, float scale, const float *loss,
+                                  const float *lse, const float *dloss, const float *dlse, void *dx, int64_t lddx,
+                                  void *dw, int dw_dtype, int64_t lddw, int accumulate, void *workspace, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
