@@ -3,11 +3,10 @@
 // Forward: out[t] = scale * w[ids[t]], a copy bound by HBM.
 // Backward: dw[v] (+)= scale * sum of dout[t] over the tokens with ids[t] = v.
 // Adding rows with atomics would give sums that change from run to run with
-// their order; here the tokens are sorted by id (a stable radix sort, so that
-// each id's tokens stay in order), and every id's rows are summed in FP32 in
-// that order: by one warp per 256 columns where they lie in one piece of
-// kPiece sorted tokens, else piece by piece and then over the pieces.  The
-// order depends on the ids alone, so the results do too.
+// their order; here the tokens are sorted by id, each id's in their order, and
+// every id's rows are summed in FP32 in that order: by one warp per 256 columns
+// where they lie in one piece of the sorted tokens, else piece by piece and then
+// over the pieces.  The order depends on the ids alone, so the results do too.
 #include <algorithm>
 
 #include "common.cuh"
@@ -50,18 +49,180 @@ __global__ void __launch_bounds__(256) k_embedding_fwd(const int32_t *__restrict
 }
 
 // ---------------------------------------------------------------------------
-// Backward: stable radix sort of (id, token) by digits of up to 9 bits.
-// Tokens without an id, or with one out of range, sort behind the vocabulary.
+// Backward, sorting.  Tokens without an id, or with one out of range, sort
+// behind the vocabulary.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 256, kSortKeys = 8, kSortTile = kSortThreads * kSortKeys;   // keys of one CTA
-constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
-constexpr int kPiece = 32;      // sorted tokens of one warp's sum
-
 __device__ __forceinline__ int sort_key(int32_t id, int vocab) { return id < 0 || id >= vocab ? vocab : id; }
 
-// counts[digit][block]; the first pass also marks the ids that occur.
-__global__ void __launch_bounds__(kSortThreads) k_sort_count(const int32_t *__restrict__ keys, int tokens, int vocab, int shift, int first,
-                                                           int *__restrict__ counts, uint8_t *__restrict__ occurs, int *status)
+// Both sorts are stable radix sorts by digits of 9 bits.  A warp ranks 32 * K
+// consecutive keys, 32 at a time: lanes of equal digits find one another by a
+// match, and the warp's counter of that digit holds how many came before.
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+
+template <int K, typename N>
+__device__ __forceinline__ void rank_keys(const int (&key)[K], int shift, N *counter, int (&rank)[K])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int d = key[k] < 0 ? kDigits : (key[k] >> shift) & (kDigits - 1);
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        const int had = d < kDigits ? counter[d] : 0;
+        rank[k] = had + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (d < kDigits && lane == __ffs(same) - 1) counter[d] = (N)(had + __popc(same));
+        __syncwarp();
+    }
+}
+
+// Up to 65536 tokens: all passes in one launch, by one cluster of up to 8 CTAs
+// that hold the keys in their shared memory, add their digits' counts up and
+// send each key to the CTA of its place.
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kClusterCtas = 8, kClusterKeys = 8;
+constexpr int kClusterMost = kClusterThreads * kClusterCtas * kClusterKeys;
+
+template <int K>
+struct ClusterSort {
+    uint16_t cnt[kClusterWarps][kDigits];   // a CTA's keys fit 16 bits
+    int tot[2][kDigits], start[kDigits];
+    int sums[kClusterWarps];
+    int2 held[2][K * kClusterThreads];      // key, token
+};
+
+__device__ __forceinline__ int ld_cluster(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, int x, int y)
+{
+    asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+
+// The sort by CTA `me` of `ctas`; emit(place, key, token) gets every token.
+template <int K, typename Emit>
+__device__ __forceinline__ void sort_cluster(ClusterSort<K> &m, const int32_t *__restrict__ ids, int tokens, int vocab, int passes, int ctas,
+                                             int me, int *status, Emit &&emit)
+{
+    constexpr int kOwn = K * kClusterThreads;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int at = warp * 32 * K + lane;        // this thread's keys: at + 32 k of the CTA's
+    int key[K], val[K], rank[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int i = me * kOwn + at + 32 * k;
+        val[k] = i;
+        key[k] = -1;
+        if (i < tokens) {
+            const int id = ids[i];
+            if (id >= vocab) set_status(status, FP8_ERR_INVALID_ARG);
+            key[k] = sort_key(id, vocab);
+        }
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * kDigitBits;
+        int *tot = m.tot[p & 1];
+        for (int i = t; i < kClusterWarps * kDigits / 2; i += kClusterThreads) reinterpret_cast<int *>(m.cnt)[i] = 0;
+        __syncthreads();
+        rank_keys<K>(key, shift, m.cnt[warp], rank);
+        __syncthreads();
+        int n = 0;
+        if (t < kDigits) {      // a thread per digit: exclusive over the warps
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const int c = m.cnt[w][t];
+                m.cnt[w][t] = (uint16_t)n;
+                n += c;
+            }
+            tot[t] = n;
+        }
+        if (ctas > 1) cluster_sync();
+        int before = 0, all = n;
+        if (ctas > 1 && t < kDigits) {      // the CTAs before this one, and all of them
+            all = 0;
+#pragma unroll
+            for (int c = 0; c < kClusterCtas; ++c) {
+                const int of = c < ctas ? ld_cluster(cluster_addr(&tot[t], c)) : 0;
+                all += of;
+                before += c < me ? of : 0;
+            }
+        }
+        int sum = all;          // exclusive over the digits
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        if (lane == 31) m.sums[warp] = sum;
+        __syncthreads();
+        if (t < kDigits) {
+            int base = sum - all + before;
+            for (int w = 0; w < warp; ++w) base += m.sums[w];
+            m.start[t] = base;
+        }
+        __syncthreads();
+        const bool last = p + 1 == passes;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (key[k] < 0) continue;
+            const int d = (key[k] >> shift) & (kDigits - 1), to = m.start[d] + m.cnt[warp][d] + rank[k];
+            if (last) emit(to, key[k], val[k]);
+            else if (ctas == 1) m.held[p & 1][to] = make_int2(key[k], val[k]);
+            else st_cluster(cluster_addr(&m.held[p & 1][to % kOwn], to / kOwn), key[k], val[k]);
+        }
+        // the keys are there; nobody still reads this CTA's counts
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
+        if (last) break;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int2 h = m.held[p & 1][at + 32 * k];
+            const bool in = me * kOwn + at + 32 * k < tokens;
+            key[k] = in ? h.x : -1;
+            val[k] = h.y;
+        }
+    }
+}
+
+// The first cluster sorts.  The CTAs behind it meanwhile clear dw where it is not
+// added to (the rows that have tokens too, which are not known yet: they are
+// written twice, but the sort of 32768 tokens is hidden).
+struct ClearArgs {
+    uint4 *dw;
+    int64_t rows, ld;       // ld, n: vectors of a row and of its part that is cleared
+    int n;
+};
+
+template <int K>
+__global__ void __launch_bounds__(kClusterThreads) k_sort_cluster(const int32_t *__restrict__ ids, int tokens, int vocab, int passes, int ctas,
+                                                                ClearArgs clear, int32_t *__restrict__ keys_out, int32_t *__restrict__ vals_out,
+                                                                int *status)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    dependency_wait();
+    if ((int)blockIdx.x >= ctas) {
+        const int warps = (gridDim.x - ctas) * kClusterWarps;
+        for (int64_t r = (blockIdx.x - ctas) * kClusterWarps + (threadIdx.x >> 5); r < clear.rows; r += warps)
+            for (int v = threadIdx.x & 31; v < clear.n; v += 32)
+                if (dbg_cell(r, v, 1, clear.rows, clear.ld, status)) clear.dw[r * clear.ld + v] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    sort_cluster<K>(*reinterpret_cast<ClusterSort<K> *>(raw), ids, tokens, vocab, passes, ctas, (int)blockIdx.x, status,
+                    [&](int to, int key, int val) {
+                        if (!dbg_span(to, 1, tokens, status)) return;
+                        keys_out[to] = key;
+                        vals_out[to] = val;
+                    });
+}
+
+// More tokens: through memory, a kernel that counts and one a digit.
+constexpr int kSortThreads = 256, kSortKeys = 8, kSortTile = kSortThreads * kSortKeys;   // keys of one CTA
+static_assert(kDigits == 2 * kSortThreads, "two digits a thread");
+
+// counts[digit][block] of the first digit; the other digits' are cleared.
+__global__ void __launch_bounds__(kSortThreads) k_sort_count(const int32_t *__restrict__ ids, int tokens, int vocab, int *__restrict__ counts,
+                                                           int passes, int *status)
 {
     __shared__ int n[kDigits];
     dependents_launch();
@@ -72,55 +233,29 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(const int32_t *__re
     for (int k = 0; k < kSortKeys; ++k) {
         const int i = blockIdx.x * kSortTile + k * kSortThreads + threadIdx.x;
         if (i >= tokens) break;
-        const int32_t id = keys[i];
-        const int key = first ? sort_key(id, vocab) : id;
-        if (first && id >= vocab) set_status(status, FP8_ERR_INVALID_ARG);
-        if (occurs && key < vocab && dbg_span(key, 1, vocab, status)) occurs[key] = 1;
-        atomicAdd(&n[(key >> shift) & (kDigits - 1)], 1);
+        if (ids[i] >= vocab) set_status(status, FP8_ERR_INVALID_ARG);
+        atomicAdd(&n[sort_key(ids[i], vocab) & (kDigits - 1)], 1);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kDigits; i += kSortThreads) counts[i * gridDim.x + blockIdx.x] = n[i];
-}
-
-// Exclusive sums of counts[0 .. n), in place, by one CTA.
-__global__ void __launch_bounds__(1024) k_sort_scan(int *counts, int n)
-{
-    __shared__ int sums[32];
-    dependents_launch();
-    dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (n + 1023) / 1024, i0 = min(n, (int)threadIdx.x * per), i1 = min(n, i0 + per);
-    int mine = 0;
-    for (int i = i0; i < i1; ++i) mine += counts[i];
-    int v = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    if (lane == 31) sums[warp] = v;
-    __syncthreads();
-    int before = v - mine;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    for (int i = i0; i < i1; ++i) {
-        const int c = counts[i];
-        counts[i] = before;
-        before += c;
+    for (int i = threadIdx.x; i < kDigits; i += kSortThreads) {
+        counts[(int64_t)i * gridDim.x + blockIdx.x] = n[i];
+        for (int p = 1; p < passes; ++p) counts[((int64_t)p * kDigits + i) * gridDim.x + blockIdx.x] = 0;
     }
 }
 
-// Places every key behind the equal digits before it.  A warp ranks 32 * 8
-// consecutive keys, 32 at a time: lanes of equal digits find one another by a
-// match, and the warp's counter of that digit holds how many came before.
+// Places every key behind the equal digits before it.  Each CTA adds the counts
+// up for itself.  The next digit is counted for the block that a key goes to
+// (whole numbers: the atomics' order changes nothing).
 __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t *__restrict__ keys, const int32_t *__restrict__ vals, int tokens,
-                                                           int vocab, int shift, int first, const int *__restrict__ starts,
+                                                           int vocab, int shift, int *__restrict__ counts, int *__restrict__ next_counts,
                                                            int32_t *__restrict__ keys_out, int32_t *__restrict__ vals_out, int *status)
 {
     constexpr int kWarps = kSortThreads / 32;
     __shared__ int n[kWarps][kDigits];
+    __shared__ int warp_sums[kWarps];
     dependents_launch();
     dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = gridDim.x;
     for (int i = threadIdx.x; i < kWarps * kDigits; i += kSortThreads) n[i / kDigits][i % kDigits] = 0;
     __syncthreads();
     int key[kSortKeys], rank[kSortKeys];
@@ -128,206 +263,307 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t *__re
 #pragma unroll
     for (int k = 0; k < kSortKeys; ++k) {
         const int i = i0 + 32 * k;
-        key[k] = i < tokens ? (first ? sort_key(keys[i], vocab) : keys[i]) : -1;
+        key[k] = i < tokens ? (vals ? keys[i] : sort_key(keys[i], vocab)) : -1;
     }
+    // this thread's digits 2t, 2t + 1: keys of the blocks before this one, and of all
+    int before[2], total[2];
 #pragma unroll
-    for (int k = 0; k < kSortKeys; ++k) {
-        const int d = key[k] < 0 ? kDigits : (key[k] >> shift) & (kDigits - 1);
-        const unsigned same = __match_any_sync(0xffffffffu, d);
-        const int before = d < kDigits ? n[warp][d] : 0;
-        rank[k] = before + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-        if (d < kDigits && lane == __ffs(same) - 1) n[warp][d] = before + __popc(same);
-        __syncwarp();
+    for (int h = 0; h < 2; ++h) {
+        const int *c = counts + (int64_t)(2 * threadIdx.x + h) * blocks;
+        before[h] = total[h] = 0;
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) {
+            total[h] += c[b];
+            before[h] += b < (int)blockIdx.x ? c[b] : 0;
+        }
     }
+    rank_keys<kSortKeys>(key, shift, n[warp], rank);
+    int start = total[0] + total[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, start, o);
+        if (lane >= o) start += u;
+    }
+    if (lane == 31) warp_sums[warp] = start;
     __syncthreads();
-    for (int d = threadIdx.x; d < kDigits; d += kSortThreads) {     // exclusive over the warps, from the block's start
-        int at = starts[d * gridDim.x + blockIdx.x];
+    start -= total[0] + total[1];
+    for (int w = 0; w < warp; ++w) start += warp_sums[w];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {       // exclusive over the warps, from the block's start
+        const int d = 2 * threadIdx.x + h;
+        int at = start + before[h];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const int c = n[w][d];
             n[w][d] = at;
             at += c;
         }
+        start += total[h];
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kSortKeys; ++k) {
-        if (key[k] < 0) continue;
-        const int at = n[warp][(key[k] >> shift) & (kDigits - 1)] + rank[k], i = i0 + 32 * k;
-        if (!dbg_span(at, 1, tokens, status)) continue;
-        keys_out[at] = key[k];
-        vals_out[at] = first ? i : vals[i];
+        const int at = key[k] < 0 ? -1 : n[warp][(key[k] >> shift) & (kDigits - 1)] + rank[k], i = i0 + 32 * k;
+        if (at >= 0 && dbg_span(at, 1, tokens, status)) {
+            keys_out[at] = key[k];
+            vals_out[at] = vals ? vals[i] : i;
+        }
+        if (next_counts) {      // one addition for the lanes of one digit and block: a frequent id has thousands
+            const int d = (key[k] >> (shift + kDigitBits)) & (kDigits - 1), block = at / kSortTile;
+            const unsigned same = __match_any_sync(0xffffffffu, at < 0 ? -1 : block << kDigitBits | d);
+            if (at >= 0 && lane == __ffs(same) - 1) atomicAdd(&next_counts[(int64_t)d * blocks + block], __popc(same));
+        }
     }
 }
 
 // ---------------------------------------------------------------------------
-// The sums over the sorted tokens.
+// Backward, sums over the sorted tokens, in pieces of 8 (up to kFewTokens: more
+// warps share the work, and none waits for more than one round of loads) or 32
+// of them (fewer runs that reach over pieces).
 // ---------------------------------------------------------------------------
+constexpr int kFewTokens = 8192;
+
 struct EmbedSumArgs {
     const int32_t *keys, *vals;     // sorted
     const uint16_t *dout;
-    const uint8_t *occurs;          // accumulate = 0: the ids that have tokens
     void *dw;
-    float *part;                    // [pieces][2][dim]: sums of a piece's first and last run that reach beyond it
+    float *part;                    // [pieces][2][dim]: sums of runs that begin before a piece, and that reach beyond it
     int64_t lddo, lddw;
-    int tokens, vocab, dim, pieces, segs;
-    unsigned sum_ctas;
+    int tokens, vocab, dim, piece, pieces, segs;
     float scale;
-    int accumulate;
     int *status;
 };
 
-template <bool F32>
+enum { SUM_F32 = 0, SUM_ADD = 1, SUM_BF16 = 2 };
+
+// a, times scale, to row v of dw.  SUM_ADD: added by the L2 (one addition an
+// element and call, so its order is not in question), which spares the round
+// trip of reading it here.
+template <int OUT>
 __device__ __forceinline__ void store_row8(const EmbedSumArgs &g, int64_t v, int col, const float (&a)[8])
 {
     if (!dbg_span(v * g.lddw + col, 8, (int64_t)(g.vocab - 1) * g.lddw + g.dim, g.status)) return;
-    if (F32) {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(g.dw) + v * g.lddw + col);
-        float4 x = make_float4(a[0], a[1], a[2], a[3]), y = make_float4(a[4], a[5], a[6], a[7]);
-        if (g.accumulate) {
-            const float4 p0 = p[0], p1 = p[1];
-            x = make_float4(p0.x + x.x, p0.y + x.y, p0.z + x.z, p0.w + x.w);
-            y = make_float4(p1.x + y.x, p1.y + y.y, p1.z + y.z, p1.w + y.w);
-        }
-        p[0] = x;
-        p[1] = y;
-    } else {
+    const float s = g.scale;
+    if (OUT == SUM_BF16) {
         *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(g.dw) + v * g.lddw + col) =
-            make_uint4(bf16x2_rn(a[0], a[1]), bf16x2_rn(a[2], a[3]), bf16x2_rn(a[4], a[5]), bf16x2_rn(a[6], a[7]));
-    }
-}
-
-// One warp sums 256 columns of one piece, 8 rows' loads in flight.  A run of
-// equal ids that lies inside the piece goes to dw; one that reaches beyond its
-// first or last token goes to the workspace.  The CTAs behind the pieces'
-// write zeros to the rows without tokens.
-template <bool F32>
-__global__ void __launch_bounds__(256) k_embedding_sums(EmbedSumArgs g)
-{
-    dependents_launch();
-    dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x >= g.sum_ctas) {
-        const float zero[8] = {};
-        const int stride = (gridDim.x - g.sum_ctas) * 8;
-        for (int v = (blockIdx.x - g.sum_ctas) * 8 + warp; v < g.vocab; v += stride)
-            if (!g.occurs[v])
-                for (int col = lane * 8; col < g.dim; col += 256) store_row8<F32>(g, v, col, zero);
+            make_uint4(bf16x2_rn(a[0] * s, a[1] * s), bf16x2_rn(a[2] * s, a[3] * s), bf16x2_rn(a[4] * s, a[5] * s), bf16x2_rn(a[6] * s, a[7] * s));
         return;
     }
+    float *p = static_cast<float *>(g.dw) + v * g.lddw + col;
+    if (OUT == SUM_ADD) {
+#pragma unroll
+        for (int h = 0; h < 8; h += 4)
+            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + h), "f"(a[h] * s), "f"(a[h + 1] * s),
+                         "f"(a[h + 2] * s), "f"(a[h + 3] * s)
+                         : "memory");
+        return;
+    }
+    reinterpret_cast<float4 *>(p)[0] = make_float4(a[0] * s, a[1] * s, a[2] * s, a[3] * s);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(a[4] * s, a[5] * s, a[6] * s, a[7] * s);
+}
+
+// One warp sums 256 columns of one piece, 8 rows' loads in flight.  A run of equal ids inside the piece goes to
+// dw, one that reaches beyond it to the workspace.
+template <int OUT>
+__global__ void __launch_bounds__(256) k_embedding_sums(EmbedSumArgs g)
+{
+    dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t item = (int64_t)blockIdx.x * 8 + warp;
     const int piece = (int)(item / g.segs), col = (int)(item - (int64_t)piece * g.segs) * 256 + lane * 8;
     if (piece >= g.pieces) return;
-    const int a = piece * kPiece, n = min(kPiece, g.tokens - a);
+    const int a = piece * g.piece, n = min(g.piece, g.tokens - a);
     const int key = lane < n ? g.keys[a + lane] : g.vocab, tok = lane < n ? g.vals[a + lane] : 0;
     const int prev = a > 0 ? g.keys[a - 1] : -1, next = a + n < g.tokens ? g.keys[a + n] : -1;
+    const int after = lane + 1 < n ? g.keys[a + lane + 1] : -1;
+    // this lane's token ends its run in the piece; the run lies inside the piece
+    const unsigned ends = __ballot_sync(0xffffffffu, lane < n && key < g.vocab && after != key);
+    const unsigned back = __ballot_sync(0xffffffffu, key == prev), on = __ballot_sync(0xffffffffu, lane == n - 1 && key == next);
     const bool in = col < g.dim;
     float acc[8] = {};
-    bool first = true;
     for (int i0 = 0; i0 < n; i0 += 8) {
         uint4 x[8];
+        int kk[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int kk = __shfl_sync(0xffffffffu, key, i0 + k), tt = __shfl_sync(0xffffffffu, tok, i0 + k);
-            x[k] = in && kk < g.vocab ? ldg_stream(g.dout + (int64_t)tt * g.lddo + col) : make_uint4(0, 0, 0, 0);
+            kk[k] = __shfl_sync(0xffffffffu, key, i0 + k);
+            const int tt = __shfl_sync(0xffffffffu, tok, i0 + k);
+            x[k] = in && kk[k] < g.vocab ? ldg_stream(g.dout + (int64_t)tt * g.lddo + col) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int i = i0 + k;
-            const int kk = __shfl_sync(0xffffffffu, key, i);
-            const int then = i + 1 < kPiece ? __shfl_sync(0xffffffffu, key, (i + 1) & 31) : -2;
-            if (kk >= g.vocab) return;      // the tokens without an id are the last
+            if (kk[k] >= g.vocab) return;      // the tokens without an id are the last
             const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 acc[2 * e] += bf16_lo(w[e]);
                 acc[2 * e + 1] += bf16_hi(w[e]);
             }
-            if (i + 1 < n && then == kk) continue;
-            // the run ends here, or with the piece
-            const bool whole = !(first && kk == prev) && !(i + 1 == n && kk == next);
-            if (in) {
-                if (whole) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] *= g.scale;
-                    store_row8<F32>(g, kk, col, acc);
-                } else {
-                    const int64_t at = ((int64_t)piece * 2 + (first && kk == prev ? 0 : 1)) * g.dim + col;
-                    if (dbg_span(at, 8, (int64_t)g.pieces * 2 * g.dim, g.status)) {
-                        *reinterpret_cast<float4 *>(g.part + at) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                        *reinterpret_cast<float4 *>(g.part + at + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
-                    }
+            if (!(ends >> i & 1)) continue;
+            if (in && !((back | on) >> i & 1)) {
+                store_row8<OUT>(g, kk[k], col, acc);
+            } else if (in) {
+                const int64_t at = ((int64_t)piece * 2 + (back >> i & 1 ? 0 : 1)) * g.dim + col;
+                if (dbg_span(at, 8, (int64_t)g.pieces * 2 * g.dim, g.status)) {
+                    *reinterpret_cast<float4 *>(g.part + at) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    *reinterpret_cast<float4 *>(g.part + at + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
                 }
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-            first = false;
         }
     }
 }
 
-// The runs that reach over pieces: the piece where one begins owns it.  Each
-// CTA looks at 8 pieces (one a warp) for 256 columns; for each owned run its 8
-// warps add every 8th of the run's pieces, and their sums are added in order.
-template <bool F32>
+// The runs that reach over pieces: the piece where one begins owns it.  A warp
+// looks at one piece for 256 columns, and adds up an owned run of up to
+// kJoinAlone pieces by itself, in order; of a longer one the CTA's 8 warps take
+// every 8th piece each, and their sums are added in order.
+constexpr int kJoinAlone = 16;
+
+template <int OUT>
 __global__ void __launch_bounds__(256) k_embedding_joins(EmbedSumArgs g)
 {
-    __shared__ int run_last[8];         // last piece of the run that piece w owns, or -1
+    __shared__ int run_last[8];         // last piece of the long run that piece w owns, or -1
     __shared__ float sums[8][256];
     dependents_launch();
     dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int p0 = blockIdx.x * 8, col = blockIdx.y * 256 + lane * 8;
-    if (lane == 0) {
+    const bool in = col < g.dim;
+    // the run is its first piece's last, and every other piece's first
+    auto add_pieces = [&](float (&acc)[8], int p, int r0, int last, int step) {
+        if (!in) return;
+#pragma unroll 4
+        for (int r = r0; r <= last; r += step) {
+            const float4 *src = reinterpret_cast<const float4 *>(g.part + ((int64_t)r * 2 + (r == p ? 1 : 0)) * g.dim + col);
+            const float4 x = src[0], y = src[1];
+            acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+            acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+        }
+    };
+    {
         int last = -1;
-        const int p = p0 + warp, end = p * kPiece + kPiece;    // one behind the piece's last token
-        if (end < g.tokens) {
-            const int key = g.keys[end - 1];
-            if (key < g.vocab && g.keys[end] == key) {
-                // it begins here unless the whole piece, and the token before it, has this id
-                const bool begins = p == 0 || g.keys[end - kPiece - 1] != key;
-                if (begins) {
-                    int lo = end, hi = g.tokens;     // first token behind the run, by bisection
-                    while (lo < hi) {
-                        const int mid = lo + (hi - lo) / 2;
-                        if (g.keys[mid] > key) hi = mid;
-                        else lo = mid + 1;
-                    }
-                    last = (lo - 1) / kPiece;
+        const int p = p0 + warp, end = (p + 1) * g.piece;    // one behind the piece's last token
+        if (p < g.pieces && end < g.tokens) {
+            const int key = g.keys[end - 1], then = g.keys[end], before = p > 0 ? g.keys[end - g.piece - 1] : -1;
+            // it begins here unless the whole piece, and the token before it, has this id
+            if (key < g.vocab && then == key && before != key) {
+                for (last = p;;) {      // pieces that begin with it follow one another
+                    const int q = last + 1 + lane;
+                    const unsigned same = __ballot_sync(0xffffffffu, q < g.pieces && g.keys[q * g.piece] == key);
+                    last += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+                    if (same != 0xffffffffu) break;
+                }
+                if (last - p < kJoinAlone) {
+                    float acc[8] = {};
+                    add_pieces(acc, p, p, last, 1);
+                    if (in) store_row8<OUT>(g, key, col, acc);
+                    last = -1;
                 }
             }
         }
-        run_last[warp] = last;
+        if (lane == 0) run_last[warp] = last;
     }
     __syncthreads();
     for (int w = 0; w < 8; ++w) {
         const int p = p0 + w, last = run_last[w];
         if (last < 0) continue;
         float acc[8] = {};
-        if (col < g.dim) {
-#pragma unroll 4
-            for (int r = p + warp; r <= last; r += 8) {
-                // the run is its first piece's last, and every other piece's first
-                const float4 *src = reinterpret_cast<const float4 *>(g.part + ((int64_t)r * 2 + (r == p ? 1 : 0)) * g.dim + col);
-                const float4 x = src[0], y = src[1];
-                acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-                acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
-            }
-        }
+        add_pieces(acc, p, p + warp, last, 8);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sums[warp][e * 32 + lane] = acc[e];
         __syncthreads();
-        if (warp == 0 && col < g.dim) {
+        if (warp == 0 && in) {
+            const int v = g.keys[(p + 1) * g.piece - 1];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                for (int v = 1; v < 8; ++v) acc[e] += sums[v][e * 32 + lane];
-                acc[e] *= g.scale;
-            }
-            store_row8<F32>(g, g.keys[p * kPiece + kPiece - 1], col, acc);
+            for (int e = 0; e < 8; ++e)
+                for (int o = 1; o < 8; ++o) acc[e] += sums[o][e * 32 + lane];
+            store_row8<OUT>(g, v, col, acc);
         }
         __syncthreads();
     }
+}
+
+// ---------------------------------------------------------------------------
+// Backward of few tokens in one launch: every CTA sorts all of them for itself
+// (2 keys a thread, in its shared memory) and then sums 32 columns: 4 lanes take
+// a piece of 8 sorted tokens, and the runs that reach over pieces are added up
+// from shared memory.  Three launches of the form above took 16 us at 1000 x 1024.
+// ---------------------------------------------------------------------------
+constexpr int kSmallKeys = 2, kSmallMost = kSmallKeys * kClusterThreads, kSmallPieces = kSmallMost / 8;
+
+static_assert(sizeof(ClusterSort<kSmallKeys>) % 16 == 0, "16-byte vectors follow");
+
+struct SmallEmbed {
+    ClusterSort<kSmallKeys> sort;
+    int2 sorted[kSmallMost + 1];            // key, token; behind the last: -1
+    alignas(16) float part[kSmallPieces][2][32];
+};
+
+template <int OUT>
+__global__ void __launch_bounds__(kClusterThreads) k_embedding_small(const int32_t *__restrict__ ids, int passes, EmbedSumArgs g)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    SmallEmbed &m = *reinterpret_cast<SmallEmbed *>(raw);
+    dependents_launch();
+    dependency_wait();
+    sort_cluster<kSmallKeys>(m.sort, ids, g.tokens, g.vocab, passes, 1, 0, g.status, [&](int to, int key, int val) { m.sorted[to] = make_int2(key, val); });
+    if (threadIdx.x == 0) m.sorted[g.tokens] = make_int2(-1, 0);
+    __syncthreads();
+
+    const int piece = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8, col = blockIdx.x * 32 + c, a = piece * 8;
+    const int n = min(8, g.tokens - a);     // may be negative
+    const bool in = col < g.dim;
+    const int prev = a > 0 && n > 0 ? m.sorted[a - 1].x : -1;
+    auto add8 = [](float (&x)[8], const float4 *p) {
+        const float4 u = p[0], v = p[1];
+        x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+        x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+    };
+    {
+        uint4 x[8];
+        int key[9];
+#pragma unroll
+        for (int k = 0; k < 9; ++k) key[k] = k <= n ? m.sorted[a + k].x : -1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const bool use = k < n && in && key[k] < g.vocab;
+            x[k] = use ? ldg_stream(g.dout + (int64_t)m.sorted[a + k].y * g.lddo + col) : make_uint4(0, 0, 0, 0);
+        }
+        float acc[8] = {};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k >= n || key[k] >= g.vocab) break;
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[2 * e] += bf16_lo(w[e]);
+                acc[2 * e + 1] += bf16_hi(w[e]);
+            }
+            const bool on = key[k + 1] == key[k];
+            if (on && k + 1 < n) continue;
+            // the run ends here, or with the piece
+            if (!on && key[k] != prev) {
+                if (in) store_row8<OUT>(g, key[k], col, acc);
+            } else {
+                float4 *p = reinterpret_cast<float4 *>(&m.part[piece][key[k] == prev ? 0 : 1][c]);
+                p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+        }
+    }
+    __syncthreads();
+    if (n < 8 || !in) return;       // the last piece owns no run that goes on
+    const int key = m.sorted[a + 7].x;
+    if (key >= g.vocab || key == prev || m.sorted[a + 8].x != key) return;
+    float acc[8] = {};
+    add8(acc, reinterpret_cast<const float4 *>(&m.part[piece][1][c]));
+    for (int q = a + 8; q < g.tokens && m.sorted[q].x == key; q += 8) add8(acc, reinterpret_cast<const float4 *>(&m.part[q / 8][0][c]));
+    store_row8<OUT>(g, key, col, acc);
 }
 
 // ------------------------------------------------------------------ launchers
@@ -337,26 +573,96 @@ namespace {
 int64_t up16(int64_t n) { return (n + 15) & ~(int64_t)15; }
 
 struct EmbedLayout {    // byte offsets in the workspace
-    int64_t keys[2], vals[2], counts, occurs, part, bytes;
-    int blocks, pieces;
+    int64_t keys[2], vals[2], counts, part, bytes;
+    int blocks, passes, piece, pieces;
     EmbedLayout(int64_t tokens, int64_t vocab, int64_t dim)
     {
         blocks = (int)((tokens + kSortTile - 1) / kSortTile);
-        pieces = (int)((tokens + kPiece - 1) / kPiece);
+        int bits = 1;       // of the largest key, which is vocab itself
+        while ((vocab >> bits) != 0) ++bits;
+        passes = (bits + kDigitBits - 1) / kDigitBits;
+        piece = tokens <= kFewTokens ? 8 : 16;
+        pieces = (int)((tokens + piece - 1) / piece);
         int64_t at = 0;
         auto take = [&](int64_t n) { const int64_t p = at; at += up16(n); return p; };
-        for (int i = 0; i < 2; ++i) keys[i] = take(tokens * 4);
-        for (int i = 0; i < 2; ++i) vals[i] = take(tokens * 4);
-        counts = take((int64_t)blocks * kDigits * 4);
-        occurs = take(vocab);
+        for (int i = 0; i < 2; ++i) {
+            keys[i] = take(tokens * 4);
+            vals[i] = take(tokens * 4);
+        }
+        counts = take(tokens <= kClusterMost ? 0 : (int64_t)passes * kDigits * blocks * 4);
         part = take((int64_t)pieces * 2 * dim * 4);
         bytes = at;
     }
 };
 
+template <typename K>
+int allow_smem(K kernel, int bytes)
+{
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+}
+
+template <int K>
+int run_sort_cluster(const int32_t *ids, int tokens, int vocab, int passes, int ctas, const ClearArgs &clear, int32_t *keys, int32_t *vals,
+                     int *status, cudaStream_t st)
+{
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_done[dev & 63]) {
+        const int rc = allow_smem(k_sort_cluster<K>, (int)sizeof(ClusterSort<K>));
+        if (rc != FP8_OK) return rc;
+        attr_done[dev & 63] = true;
+    }
+    const int64_t clearing = clear.dw ? std::min<int64_t>((clear.rows + kClusterWarps - 1) / kClusterWarps, (int64_t)sm_count() * 2) : 0;
+    const unsigned grid = (unsigned)(ctas + (clearing + ctas - 1) / ctas * ctas);
+    return launch_dependent_cluster(k_sort_cluster<K>, dim3(grid), (unsigned)ctas, kClusterThreads, sizeof(ClusterSort<K>), st, ids, tokens, vocab,
+                                    passes, ctas, clear, keys, vals, status);
+}
+
+// The most CTAs with a key a thread first: the passes' rounds are what takes time.
+int run_sort(const int32_t *ids, int tokens, int vocab, int passes, const ClearArgs &clear, int32_t *keys, int32_t *vals, int *status,
+             cudaStream_t st)
+{
+    int ctas = 1;
+    while (ctas < kClusterCtas && ctas * kClusterThreads < tokens) ctas *= 2;
+    const int per = (tokens + ctas * kClusterThreads - 1) / (ctas * kClusterThreads);
+    if (per <= 1) return run_sort_cluster<1>(ids, tokens, vocab, passes, ctas, clear, keys, vals, status, st);
+    if (per <= 2) return run_sort_cluster<2>(ids, tokens, vocab, passes, ctas, clear, keys, vals, status, st);
+    if (per <= 4) return run_sort_cluster<4>(ids, tokens, vocab, passes, ctas, clear, keys, vals, status, st);
+    return run_sort_cluster<8>(ids, tokens, vocab, passes, ctas, clear, keys, vals, status, st);
+}
+
+template <int OUT>
+int embed_small(const int32_t *ids, int passes, const EmbedSumArgs &g, cudaStream_t st)
+{
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_done[dev & 63]) {
+        const int rc = allow_smem(k_embedding_small<OUT>, (int)sizeof(SmallEmbed));
+        if (rc != FP8_OK) return rc;
+        attr_done[dev & 63] = true;
+    }
+    return launch_dependent(k_embedding_small<OUT>, dim3((unsigned)((g.dim + 31) / 32)), kClusterThreads, sizeof(SmallEmbed), st, ids, passes, g);
+}
+
+template <int OUT>
+int embed_sums(EmbedSumArgs &g, cudaStream_t st)
+{
+    const int64_t ctas = ((int64_t)g.pieces * g.segs + 7) / 8;
+    if (ctas >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
+    const int rc = launch_dependent(k_embedding_sums<OUT>, dim3((unsigned)ctas), 256, 0, st, g);
+    if (rc != FP8_OK) return rc;
+    return launch_dependent(k_embedding_joins<OUT>, dim3((unsigned)((g.pieces + 7) / 8), (unsigned)g.segs), 256, 0, st, g);
+}
+
 }  // namespace
 
-size_t embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) { return (size_t)EmbedLayout(tokens, vocab, dim).bytes; }
+// Enough for fewer tokens too, whose pieces are shorter.
+size_t embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim)
+{
+    return (size_t)std::max(EmbedLayout(tokens, vocab, dim).bytes, EmbedLayout(std::min<int64_t>(tokens, kFewTokens), vocab, dim).bytes);
+}
 
 int launch_embedding_fwd(const int32_t *ids, int64_t tokens, const void *w, int64_t vocab, int64_t dim, int64_t ldw, float scale, void *out,
                          int64_t ldo, int *status, cudaStream_t st)
@@ -372,58 +678,69 @@ int launch_embedding_bwd(const int32_t *ids, int64_t tokens, const void *dout, i
                          int out_dtype, int64_t lddw, int accumulate, void *ws, int *status, cudaStream_t st)
 {
     const bool f32 = out_dtype == FP8_OUT_F32;
-    const int64_t row = dim * (f32 ? 4 : 2);
-    if (tokens == 0) {
-        if (accumulate) return FP8_OK;
-        return cudaMemset2DAsync(dw, (size_t)lddw * (f32 ? 4 : 2), 0, (size_t)row, (size_t)vocab, st) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
-    }
+    const int esz = f32 ? 4 : 2;
+    auto clear = [&] {
+        if (lddw == dim) return cudaMemsetAsync(dw, 0, (size_t)(vocab * dim * esz), st) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+        return cudaMemset2DAsync(dw, (size_t)lddw * esz, 0, (size_t)dim * esz, (size_t)vocab, st) == cudaSuccess ? FP8_OK : FP8_ERR_CUDA;
+    };
+    if (tokens == 0) return accumulate ? FP8_OK : clear();
     const EmbedLayout L(tokens, vocab, dim);
+    const int n = (int)tokens, V = (int)vocab;
     uint8_t *base = static_cast<uint8_t *>(ws);
-    int *counts = reinterpret_cast<int *>(base + L.counts);
-    uint8_t *occurs = accumulate ? nullptr : base + L.occurs;
-    if (occurs && cudaMemsetAsync(occurs, 0, (size_t)vocab, st) != cudaSuccess) return FP8_ERR_CUDA;
-    const int n = (int)tokens;
-    int bits = 1;       // of the largest key, which is vocab itself
-    while ((vocab >> bits) != 0) ++bits;
-    const int32_t *keys = ids, *vals = nullptr;
-    int rc, to = 0;
-    for (int shift = 0, first = 1; shift < bits; shift += kDigitBits, first = 0, to ^= 1) {
-        int32_t *k2 = reinterpret_cast<int32_t *>(base + L.keys[to]), *v2 = reinterpret_cast<int32_t *>(base + L.vals[to]);
-        if ((rc = launch_dependent(k_sort_count, dim3(L.blocks), kSortThreads, 0, st, keys, n, (int)vocab, shift, first, counts,
-                                   first ? occurs : static_cast<uint8_t *>(nullptr), status)) != FP8_OK ||
-            (rc = launch_dependent(k_sort_scan, dim3(1), 1024, 0, st, counts, L.blocks * kDigits)) != FP8_OK ||
-            (rc = launch_dependent(k_sort_place, dim3(L.blocks), kSortThreads, 0, st, keys, vals, n, (int)vocab, shift, first,
-                                   static_cast<const int *>(counts), k2, v2, status)) != FP8_OK)
-            return rc;
-        keys = k2;
-        vals = v2;
+    int32_t *keys[2], *vals[2];
+    for (int i = 0; i < 2; ++i) {
+        keys[i] = reinterpret_cast<int32_t *>(base + L.keys[i]);
+        vals[i] = reinterpret_cast<int32_t *>(base + L.vals[i]);
     }
     EmbedSumArgs g{};
-    g.keys = keys;
-    g.vals = vals;
     g.dout = static_cast<const uint16_t *>(dout);
-    g.occurs = occurs;
     g.dw = dw;
     g.part = reinterpret_cast<float *>(base + L.part);
     g.lddo = lddo;
     g.lddw = lddw;
     g.tokens = n;
-    g.vocab = (int)vocab;
+    g.vocab = V;
     g.dim = (int)dim;
+    g.piece = L.piece;
     g.pieces = L.pieces;
     g.segs = (int)((dim + 255) / 256);
     g.scale = scale;
-    g.accumulate = accumulate;
     g.status = status;
-    const int64_t sum_ctas = ((int64_t)L.pieces * g.segs + 7) / 8;
-    const int64_t zero_ctas = accumulate ? 0 : std::min<int64_t>((vocab + 7) / 8, (int64_t)sm_count() * 4);
-    if (sum_ctas + zero_ctas >= (int64_t)1 << 31) return FP8_ERR_SHAPE;
-    g.sum_ctas = (unsigned)sum_ctas;
-    if ((rc = launch_dependent(f32 ? k_embedding_sums<true> : k_embedding_sums<false>, dim3((unsigned)(sum_ctas + zero_ctas)), 256, 0, st, g)) !=
-        FP8_OK)
-        return rc;
-    return launch_dependent(f32 ? k_embedding_joins<true> : k_embedding_joins<false>, dim3((unsigned)((L.pieces + 7) / 8), (unsigned)g.segs), 256,
-                            0, st, g);
+    if (g.segs > 65535) return FP8_ERR_SHAPE;
+    int rc, sorted = 0;
+    if (n <= kSmallMost) {
+        if (!accumulate && (rc = clear()) != FP8_OK) return rc;
+        return !f32 ? embed_small<SUM_BF16>(ids, L.passes, g, st)
+                    : accumulate ? embed_small<SUM_ADD>(ids, L.passes, g, st) : embed_small<SUM_F32>(ids, L.passes, g, st);
+    }
+    if (n <= kClusterMost) {
+        ClearArgs c{};
+        if (!accumulate) {
+            c.dw = static_cast<uint4 *>(dw);
+            c.rows = vocab;
+            c.ld = lddw * esz / 16;
+            c.n = (int)(dim * esz / 16);
+        }
+        if ((rc = run_sort(ids, n, V, L.passes, c, keys[0], vals[0], status, st)) != FP8_OK) return rc;
+    } else {
+        if (!accumulate && (rc = clear()) != FP8_OK) return rc;
+        int *counts = reinterpret_cast<int *>(base + L.counts);
+        const int64_t stride = (int64_t)kDigits * L.blocks;
+        if ((rc = launch_dependent(k_sort_count, dim3((unsigned)L.blocks), kSortThreads, 0, st, ids, n, V, counts, L.passes, status)) != FP8_OK)
+            return rc;
+        for (int p = 0; p < L.passes; ++p) {
+            const int from = (p + 1) & 1;
+            sorted = p & 1;
+            if ((rc = launch_dependent(k_sort_place, dim3((unsigned)L.blocks), kSortThreads, 0, st, p == 0 ? ids : static_cast<const int32_t *>(keys[from]),
+                                       p == 0 ? static_cast<const int32_t *>(nullptr) : static_cast<const int32_t *>(vals[from]), n, V, p * kDigitBits,
+                                       counts + p * stride, p + 1 < L.passes ? counts + (p + 1) * stride : static_cast<int *>(nullptr), keys[sorted],
+                                       vals[sorted], status)) != FP8_OK)
+                return rc;
+        }
+    }
+    g.keys = keys[sorted];
+    g.vals = vals[sorted];
+    return !f32 ? embed_sums<SUM_BF16>(g, st) : accumulate ? embed_sums<SUM_ADD>(g, st) : embed_sums<SUM_F32>(g, st);
 }
 
 }  // namespace fp8fg

@@ -106,11 +106,12 @@ struct NormFwdArgs {
     int *status;
 };
 
-// A CTA's threads and rows: NT threads to one row, or 8 rows of a warp each.
+// Forward: a CTA's threads and rows: NT threads to one row, or 8 rows of a warp each.
 template <int NT> constexpr int norm_threads() { return NT == 32 ? 256 : NT; }
 template <int NT> constexpr int norm_rows() { return NT == 32 ? 8 : 1; }
-// CTAs an SM of the backward's persistent grid: what its registers allow.
-template <int NT> constexpr int norm_ctas() { return NT == 512 ? 1 : NT == 128 ? 6 : 3; }
+// Backward: CTAs an SM of its persistent grid (a row each), and most rows of its ring.
+template <int NT, int VPT> constexpr int norm_ctas() { return NT == 32 ? 16 : NT == 64 ? 12 : NT == 128 ? 6 : NT == 256 ? 3 : VPT == 2 ? 2 : 1; }
+constexpr int kNormStages = 4;
 
 template <int FMT, int NT, int VPT>
 __global__ void __launch_bounds__(norm_threads<NT>()) k_rmsnorm_fwd(NormFwdArgs g)
@@ -195,10 +196,12 @@ __global__ void __launch_bounds__(norm_threads<NT>()) k_rmsnorm_fwd(NormFwdArgs 
 // ---------------------------------------------------------------------------
 // RMSNorm backward.  With n = h rstd (h the values the codes stand for),
 //   dh = (dy w - n mean(dy w n)) rstd (+ dsum),   dw = sum_rows dy n.
-// A persistent grid walks the rows, the next row's loads in flight while the
-// current one is reduced; every thread sees the same columns of all its rows
-// and sums their dw in registers.  The CTAs' sums go to the workspace and are
-// added in a fixed order by k_column_sums.
+// A persistent grid walks the rows.  A row's codes, dy and dsum are fetched by
+// bulk copies into a ring of up to 4 rows, so that the next rows are on their way
+// while the current one is reduced (rows prefetched into registers, one ahead,
+// kept half as many bytes in flight: 46 us at 8192 x 4096).  Every thread sees
+// the same columns of all its rows and sums their dw in registers; the CTAs' sums
+// go to the workspace and are added in a fixed order by k_column_sums.
 // ---------------------------------------------------------------------------
 struct NormBwdArgs {
     const uint8_t *c;
@@ -207,111 +210,124 @@ struct NormBwdArgs {
     uint16_t *dx;
     float *part;        // [gridDim.x][cols]
     int64_t rows, lddy, lddsum, lddx;
-    int cols;
+    int cols, stages;
     int *status;
 };
 
-template <int VPT>
-struct NormRow {
-    uint2 c[VPT];
-    uint4 dy[VPT], ds[VPT];
-    float s[VPT], rstd;
-};
-
 template <int FMT, int NT, int VPT>
-__global__ void __launch_bounds__(norm_threads<NT>(), norm_ctas<NT>()) k_rmsnorm_bwd(NormBwdArgs g)
+__global__ void __launch_bounds__(NT, norm_ctas<NT, VPT>()) k_rmsnorm_bwd(NormBwdArgs g)
 {
-    extern __shared__ float sums[];    // NT = 32: the warps' dw [8][cols]
+    extern __shared__ __align__(128) uint8_t ring[];    // [stages][codes | dy | dsum]
+    __shared__ __align__(8) uint64_t full[kNormStages];
     __shared__ float part[2][32];
-    dependents_launch();
+    __shared__ int abort_flag;
+    const int t = threadIdx.x, nv = g.cols / 8, S = g.stages;
+    const uint32_t bytes = (uint32_t)g.cols * (g.dsum ? 5 : 3);
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
     dependency_wait();
-    constexpr int kRows = norm_rows<NT>();
-    const int t = threadIdx.x % NT, sub = threadIdx.x / NT;
-    const int nv = g.cols / 8;
-    float acc[VPT][8];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
-
-    auto load = [&](NormRow<VPT> &r, int64_t row) {
-        if (row >= g.rows) return;
-        r.rstd = g.rstd[row];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int at = t + NT * i;
-            const bool in = at < nv;
-            r.c[i] = in ? __ldg(reinterpret_cast<const uint2 *>(g.c + row * g.cols + at * 8)) : make_uint2(0, 0);
-            r.s[i] = in ? __ldg(g.cs + (int64_t)(at >> 4) * g.rows + row) : 0.0f;
-            r.dy[i] = in ? load_once(g.dy + row * g.lddy + at * 8) : make_uint4(0, 0, 0, 0);
-            r.ds[i] = in && g.dsum ? load_once(g.dsum + row * g.lddsum + at * 8) : make_uint4(0, 0, 0, 0);
-        }
+    const int64_t row0 = blockIdx.x, step = gridDim.x;
+    auto fetch = [&](int64_t row, int s) {      // thread 0
+        uint8_t *to = ring + (size_t)s * bytes;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        bulk_load(to, g.c + row * g.cols, (uint32_t)g.cols, &full[s]);
+        bulk_load(to + g.cols, g.dy + row * g.lddy, (uint32_t)g.cols * 2, &full[s]);
+        if (g.dsum) bulk_load(to + 3 * g.cols, g.dsum + row * g.lddsum, (uint32_t)g.cols * 2, &full[s]);
     };
+    // a row's scales (4 bytes apart from the next row's: no copy fetches them) and rstd
+    float scale[VPT], rstd = 0.0f;
+    auto scales = [&](int64_t row) {
+        if (row >= g.rows) return;
+        rstd = __ldg(g.rstd + row);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) scale[i] = t + NT * i < nv ? __ldg(g.cs + (int64_t)((t + NT * i) >> 4) * g.rows + row) : 0.0f;
+    };
+    if (t == 0)
+        for (int s = 0; s < S && row0 + s * step < g.rows; ++s) fetch(row0 + s * step, s);
+    scales(row0);
 
-    int64_t row = (int64_t)blockIdx.x * kRows + sub;
-    const int64_t step = (int64_t)gridDim.x * kRows;
-    NormRow<VPT> now, next;
-    load(now, row);
-    for (int it = 0; row < g.rows; row += step, it ^= 1) {
-        load(next, row + step);
-        float dot = 0.0f;
+    uint4 w[VPT];
+    uint64_t acc[VPT][4];       // packed pairs
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        w[i] = t + NT * i < nv ? __ldg(reinterpret_cast<const uint4 *>(g.w) + t + NT * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] = 0;
+    }
+    int s = 0;
+    uint32_t phase = 0;
+    int it = 0;
+    for (int64_t row = row0; row < g.rows; row += step, ++it) {
+        float use[VPT];
+        const float r = rstd;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) use[i] = scale[i] * r;
+        scales(row + step);
+        thread_wait(smem_u32(&full[s]), phase, &abort_flag, g.status);
+        const uint8_t *at = ring + (size_t)s * bytes;
+        uint64_t n[VPT][4], dot2 = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int at = t + NT * i;
-            if (at >= nv) continue;
-            float n[8], dy[8], w[8];
-            kept8<FMT>(now.c[i], now.s[i], n);
-            widen8(now.dy[i], dy);
-            widen8(*reinterpret_cast<const uint4 *>(g.w + at * 8), w);
+            const int v = t + NT * i;
+            if (v >= nv) continue;
+            const uint2 q = reinterpret_cast<const uint2 *>(at)[v];
+            const uint4 d4 = reinterpret_cast<const uint4 *>(at + g.cols)[v];
+            const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            const uint64_t u2 = p2(use[i], use[i]);
+            float f[8];
+            kept8<FMT>(q, 1.0f, f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float p = dy[k] * (n[k] * now.rstd);
-                acc[i][k] += p;
-                dot = fmaf(p, w[k], dot);
+            for (int k = 0; k < 4; ++k) {
+                n[i][k] = p2_mul(p2(f[2 * k], f[2 * k + 1]), u2);
+                const uint64_t p = p2_mul(p2_bf16x2(d[k]), n[i][k]);
+                acc[i][k] = f2_add(acc[i][k], p);
+                dot2 = p2_fma(p, p2_bf16x2(ww[k]), dot2);
             }
         }
-        const float mean = row_sum<NT>(dot, part[it]) / (float)g.cols;
+        float lo, hi;
+        f2_unpack(dot2, lo, hi);
+        const float mean = row_sum<NT>(lo + hi, part[it & 1]) / (float)g.cols;
+        // all threads are past the row before this one: its place takes the next to come
+        if (NT == 32) __syncwarp();
+        if (t == 0 && it > 0 && row + (S - 1) * step < g.rows) fetch(row + (S - 1) * step, s == 0 ? S - 1 : s - 1);
+        const uint64_t m2 = p2(-mean, -mean), r2 = p2(r, r);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int at = t + NT * i;
-            if (at >= nv) continue;
-            float n[8], dy[8], w[8], ds[8];
-            kept8<FMT>(now.c[i], now.s[i], n);
-            widen8(now.dy[i], dy);
-            widen8(*reinterpret_cast<const uint4 *>(g.w + at * 8), w);
-            widen8(now.ds[i], ds);
+            const int v = t + NT * i;
+            if (v >= nv) continue;
+            const uint4 d4 = reinterpret_cast<const uint4 *>(at + g.cols)[v];
+            const uint4 e4 = g.dsum ? reinterpret_cast<const uint4 *>(at + 3 * g.cols)[v] : make_uint4(0, 0, 0, 0);
+            const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, e[4] = {e4.x, e4.y, e4.z, e4.w}, ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dy[k] = fmaf(dy[k] * w[k] - n[k] * now.rstd * mean, now.rstd, ds[k]);
-            if (dbg_span(row * g.lddx + at * 8, 8, (g.rows - 1) * g.lddx + g.cols, g.status))
-                *reinterpret_cast<uint4 *>(g.dx + row * g.lddx + at * 8) = round8(dy);
+            for (int k = 0; k < 4; ++k)
+                o[k] = p2_bf16(p2_fma(p2_fma(n[i][k], m2, p2_mul(p2_bf16x2(d[k]), p2_bf16x2(ww[k]))), r2, p2_bf16x2(e[k])));
+            if (dbg_span(row * g.lddx + v * 8, 8, (g.rows - 1) * g.lddx + g.cols, g.status))
+                *reinterpret_cast<uint4 *>(g.dx + row * g.lddx + v * 8) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        now = next;
-    }
-    if (NT == 32) {     // the CTA's 8 warps, one after another
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int at = t + NT * i;
-            if (at >= nv) continue;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sums[sub * g.cols + at * 8 + k] = acc[i][k];
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < g.cols; c += 256) {
-            float v = sums[c];
-#pragma unroll
-            for (int w = 1; w < 8; ++w) v += sums[w * g.cols + c];
-            if (dbg_cell(blockIdx.x, c, 1, gridDim.x, g.cols, g.status)) g.part[(int64_t)blockIdx.x * g.cols + c] = v;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int at = t + NT * i;
-            if (at >= nv || !dbg_cell(blockIdx.x, at * 8, 8, gridDim.x, g.cols, g.status)) continue;
-            float4 *p = reinterpret_cast<float4 *>(g.part + (int64_t)blockIdx.x * g.cols + at * 8);
-            p[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-            p[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+        if (++s == S) {
+            s = 0;
+            phase ^= 1;
         }
     }
+    dependents_launch();
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = t + NT * i;
+        if (v >= nv || !dbg_cell(blockIdx.x, v * 8, 8, gridDim.x, g.cols, g.status)) continue;
+        float a[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f2_unpack(acc[i][k], a[2 * k], a[2 * k + 1]);
+        float4 *p = reinterpret_cast<float4 *>(g.part + (int64_t)blockIdx.x * g.cols + v * 8);
+        p[0] = make_float4(a[0], a[1], a[2], a[3]);
+        p[1] = make_float4(a[4], a[5], a[6], a[7]);
+    }
+    if (abort_flag && t == 0)       // copies that were given up on land before the CTA leaves
+        for (int i = 0; i < S; ++i) mbar_wait_bounded(&full[i], i < s ? phase ^ 1 : phase, nullptr);
 }
 
 // dw[c] (+)= sum over n rows of part[.][c]: 32 columns a CTA, its 32 warps
@@ -442,15 +458,13 @@ __global__ void __launch_bounds__(256) k_swiglu_bwd_ckpt(const uint8_t *__restri
 namespace {
 
 // Calls f(NT, VPT) as compile-time numbers for rows of `cols` columns (up to
-// kNormMaxCols): at most two vectors a thread while the CTA stays within 512
-// threads, since the backward holds a row twice (this one and the next) beside
-// its sums and would spill with four of them in 80 registers.
+// kNormMaxCols).
 template <int N> struct Int { static constexpr int v = N; };
 template <typename F>
 int norm_shape(int64_t cols, F &&f)
 {
     if (cols <= 256) return f(Int<32>{}, Int<1>{});
-    if (cols <= 512) return f(Int<32>{}, Int<2>{});
+    if (cols <= 512) return f(Int<64>{}, Int<1>{});
     if (cols <= 1024) return f(Int<128>{}, Int<1>{});
     if (cols <= 2048) return f(Int<256>{}, Int<1>{});
     if (cols <= 4096) return f(Int<256>{}, Int<2>{});
@@ -472,10 +486,20 @@ template <int FMT>
 int norm_bwd(NormBwdArgs &g, float *dw, int accumulate, cudaStream_t st)
 {
     return norm_shape(g.cols, [&](auto nt, auto vpt) {
-        constexpr int NT = decltype(nt)::v, VPT = decltype(vpt)::v;
-        const int64_t grid = std::min<int64_t>((g.rows + norm_rows<NT>() - 1) / norm_rows<NT>(), (int64_t)sm_count() * norm_ctas<NT>());
-        const size_t smem = NT == 32 ? (size_t)g.cols * 8 * sizeof(float) : 0;
-        const int rc = launch_dependent(k_rmsnorm_bwd<FMT, NT, VPT>, dim3((unsigned)grid), norm_threads<NT>(), smem, st, g);
+        constexpr int NT = decltype(nt)::v, VPT = decltype(vpt)::v, kCtas = norm_ctas<NT, VPT>();
+        constexpr int kRing = 220 * 1024 / kCtas - 2048;    // an SM's shared memory, shared by its CTAs
+        const int row = g.cols * (g.dsum ? 5 : 3);
+        g.stages = std::min(kNormStages, kRing / row);
+        static bool attr_done[64] = {};
+        int dev = 0;
+        cudaGetDevice(&dev);
+        if (!attr_done[dev & 63]) {
+            if (cudaFuncSetAttribute(k_rmsnorm_bwd<FMT, NT, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) != cudaSuccess)
+                return (int)FP8_ERR_CUDA;
+            attr_done[dev & 63] = true;
+        }
+        const int64_t grid = std::min<int64_t>(g.rows, (int64_t)sm_count() * kCtas);
+        const int rc = launch_dependent(k_rmsnorm_bwd<FMT, NT, VPT>, dim3((unsigned)grid), NT, (size_t)g.stages * row, st, g);
         if (rc != FP8_OK) return rc;
         return launch_dependent(k_column_sums, dim3((unsigned)(g.cols / 32)), 1024, 0, st, static_cast<const float *>(g.part), (int)grid, g.cols,
                                 dw, accumulate, g.status);
@@ -510,7 +534,7 @@ int launch_rmsnorm_fwd_ckpt(const void *x, int64_t rows, int64_t cols, int64_t l
 
 size_t rmsnorm_workspace_bytes(int64_t cols)
 {
-    const int ctas = norm_shape(cols, [](auto nt, auto) { return norm_ctas<decltype(nt)::v>(); });
+    const int ctas = norm_shape(cols, [](auto nt, auto vpt) { return norm_ctas<decltype(nt)::v, decltype(vpt)::v>(); });
     return (size_t)sm_count() * ctas * (size_t)cols * sizeof(float);
 }
 

@@ -17,8 +17,8 @@
 // differ in which operands run along K (k_xent<MODE>).
 //
 // Forward: the epilogue keeps, per row, a running maximum and sum over a unit
-// of up to 8 tiles and writes 8 bytes a row and unit, 1/64 of a BF16 logit row
-// and less; k_xent_join adds the units in order.
+// of up to 8 tiles and writes 8 bytes a row and half unit, 1/32 of a BF16 logit row
+// and less; k_xent_join adds them in order.
 // Backward: for a piece of the vocabulary, g is rounded to BF16 (the tensor
 // cores' operand type; it costs each of the products 2^-9 a term, random over
 // the terms, beside the same rounding of the BF16 results) and kept in the
@@ -32,8 +32,10 @@
 // 256 x 256 tiles, each CTA holding 128 rows of A and 128 columns of B of every
 // 64-deep stage, so that an SM fetches 32 KB where a CTA alone would fetch 48 KB
 // for its half of the tile.  Warp 0 copies (TMA, 6 stages), one thread of the
-// even CTA's warp 1 issues the MMAs, warps 2..5 drain one of two accumulators
+// even CTA's warp 1 issues the MMAs, warps 2..9 drain one of two accumulators
 // while the next tile fills the other.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -52,10 +54,13 @@ constexpr int kBK = 64;                 // K of a stage
 constexpr int kStages = 6;
 constexpr int kHalf = 128 * kBK * 2;    // bytes of one operand's half in one CTA's stage
 constexpr int kStage = 2 * kHalf;
-constexpr int kThreads = 192;
-constexpr int kEpiWarp0 = 2, kEpiWarps = 4;
+constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kEpiCols = kTile / 2;     // columns of an epilogue warp: half the tile, of a quarter of its rows
 constexpr int kBars = 2 * kStages + 2 * 2 + 1;
-constexpr int kSmem = 1024 + kStages * kStage + kBars * 8 + 16;
+constexpr int kBox = 4096;              // staging for one store: 32 rows of 128 bytes
+constexpr int kStaging = kEpiWarps * kBox;
+constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBars * 8 + 16;
 
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
@@ -70,21 +75,12 @@ struct XentArgs {
     int band;                   // M tiles of a raster band
     float scale;
     // LOSS
-    float2 *part;               // [unit][rows]: maximum (times scale log2 e), sum of 2^(. - maximum)
-    float *z_target;            // [rows]: the target's logit, times log2 e
+    float2 *part;               // [unit][half][rows]: maximum (times scale log2 e), sum of 2^(. - maximum)
     int64_t rows;               // rows of the packed buffers
     // GRAD
     const float *loss, *lse, *dloss, *dlse;
-    uint16_t *g;
-    int64_t ldg;
-    // DX, DW
-    float *acc;                 // DX: [splits][rows][dim]
-    int add, last;              // DX: add to acc; write dx (BF16) instead of acc
-    uint16_t *dx;
-    int64_t lddx;
-    void *dw;
-    int64_t lddw;
-    int dw_f32, accumulate;
+    // DX (into FP32 sums, [splits][rows][dim]), DW
+    int f32, add;               // FP32 results; added to what is there
     int *status;
 };
 
@@ -136,12 +132,13 @@ __device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    k_xent(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const XentArgs a)
+    k_xent(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmD,
+           const XentArgs a)
 {
     constexpr bool kMnA = MODE == XENT_DW, kMnB = MODE >= XENT_DX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage + kStaging);
     uint64_t *empty = full + kStages;
     uint64_t *tfull = empty + kStages;
     uint64_t *tempty = tfull + 2;
@@ -176,7 +173,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();     // the pair's barriers are there before either CTA signals the other's
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    dependents_launch();
     dependency_wait();
     const Walk w = make_walk<MODE>(a);
 
@@ -213,6 +209,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        // the next kernel may be set up (k_xent_join reads this call's inputs before it waits: so not before this one has)
+        dependents_launch();
         // the copies in flight land (the even CTA's barrier counts both CTAs'),
         // and the last stages' releases arrive, before the pair may leave
         const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0;
@@ -257,16 +255,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------ epilogue
         const int lq = warp & 3;                 // TMEM lane quarter of this warp
+        const int half = (warp - kEpiWarp0) >> 2;       // and its columns
         const uint32_t tm_lane = tmem_base + ((uint32_t)(lq * 32) << 16);
         const int rows = a.count ? *a.count : a.tokens;
+        uint8_t *box = smem + kStages * kStage + (warp - kEpiWarp0) * kBox;
         uint32_t tc = 0;
         bool ok = true;
+
+        // 32 values of this lane's row, columns [col, col + 32) of the result, to
+        // the warp's staging (rows of 128 bytes, 16-byte chunks swizzled as the
+        // copy expects them, so that neither side meets a bank twice); a full
+        // box of 32 rows is copied out.  FP32: every call; BF16: every other.
+        auto put = [&](const uint32_t (&r)[32], int col, int row0, int cols, int rows_end, bool f32, bool add) {
+            const bool begins = f32 || (col & 32) == 0, ends = f32 || (col & 32) != 0;
+            if (begins) {       // the last copy out of it has been read
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
+            }
+            if (f32) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4 *>(box + lane * 128 + (((j + ((col & 32) >> 3)) ^ (lane & 7)) << 4)) = bf16x8(r + 8 * j);
+            }
+            if (!ends) return;
+            fence_proxy_async_smem();
+            __syncwarp();
+            const int x = f32 ? col : col - 32;
+            // what reaches over the matrix's edge is not written; a box beyond it is not sent
+            if (x >= cols || row0 >= rows_end) return;
+            if (lane == 0) {
+                if (add) tma_reduce_add_2d(&tmD, box, x, row0);
+                else tma_store_2d(&tmD, box, x, row0);
+                bulk_commit_group();
+            }
+        };
+
         for (int u = pair; u < w.units && ok; u += pairs) {
             int mt, nt0, nt1, k0, k1, split;
             w.unit(u, mt, nt0, nt1, k0, k1, split);
-            const int row = mt * kTile + rank * 128 + lq * 32 + lane;
+            const int row0 = mt * kTile + rank * 128 + lq * 32, row = row0 + lane;
             // per row of LOSS and GRAD
-            const int token = MODE <= XENT_DX && row < rows ? (a.map ? a.map[row] : row) : -1;
+            const int token = MODE <= XENT_GRAD && row < rows ? (a.map ? a.map[row] : row) : -1;
             const int target = MODE <= XENT_GRAD && token >= 0 ? a.target[token] - a.v0 : -1;
             const float c = a.scale * kLog2e;
             float top = -INFINITY, sum = 0.0f;              // LOSS
@@ -282,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!(ok = __all_sync(0xffffffffu, thread_wait(smem_u32(&tfull[buf]), (tc >> 1) & 1, abort_flag, a.status)))) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int j = 0; j < kTile / 32; ++j) {
+                for (int j = half * (kEpiCols / 32); j < (half + 1) * (kEpiCols / 32); ++j) {
                     uint32_t r[32];
                     tc_ld_32x32b_x32(tm_lane + buf * kTile + j * 32, r);
                     tc_wait_ld();
@@ -295,15 +328,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 if (i >= lim) r[i] = __float_as_uint(-INFINITY);
                         }
                         const int t = target - col;
-                        if (t >= 0 && t < min(32, lim)) {       // kept apart, and out of the sum
-                            float z = 0.0f;
+                        if (t >= 0 && t < 32) {     // left out of the sum
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (i == t) {
-                                    z = __uint_as_float(r[i]);
-                                    r[i] = __float_as_uint(-INFINITY);
-                                }
-                            if (dbg_span(row, 1, a.rows, a.status)) a.z_target[row] = z * c;
+                                if (i == t) r[i] = __float_as_uint(-INFINITY);
                         }
                         float m = top;
 #pragma unroll
@@ -325,56 +353,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (i == t) g = at_target;
                             r[i] = __float_as_uint(i < lim ? g : 0.0f);
                         }
-                        const int64_t at = (int64_t)row * a.ldg + col;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (dbg_cell(row, col + i, 8, a.rows, a.ldg, a.status)) *reinterpret_cast<uint4 *>(a.g + at + i) = bf16x8(r + i);
+                        put(r, col, row0, INT_MAX, INT_MAX, false, false);
                     } else {
                         if (k0 == k1) {     // no K: the accumulator was not written
 #pragma unroll
                             for (int i = 0; i < 32; ++i) r[i] = 0;
                         }
-                        if (MODE == XENT_DX && token >= 0) {
-                            float *acc = a.acc + ((int64_t)split * a.rows + row) * a.dim;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                if (col + i >= a.dim) break;
-                                if (a.add) {
-                                    const float4 x = *reinterpret_cast<const float4 *>(acc + col + i), y = *reinterpret_cast<const float4 *>(acc + col + i + 4);
-                                    const float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) r[i + e] = __float_as_uint(__uint_as_float(r[i + e]) + o[e]);
-                                }
-                                if (a.last) {
-                                    if (dbg_span((int64_t)token * a.lddx + col + i, 8, (int64_t)(a.tokens - 1) * a.lddx + a.dim, a.status))
-                                        *reinterpret_cast<uint4 *>(a.dx + (int64_t)token * a.lddx + col + i) = bf16x8(r + i);
-                                } else if (dbg_cell((int64_t)split * a.rows + row, col + i, 8, (int64_t)a.splits * a.rows, a.dim, a.status)) {
-                                    *reinterpret_cast<uint4 *>(acc + col + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-                                    *reinterpret_cast<uint4 *>(acc + col + i + 4) = make_uint4(r[i + 4], r[i + 5], r[i + 6], r[i + 7]);
-                                }
-                            }
-                        }
-                        if (MODE == XENT_DW && row < a.vn) {
-                            const int64_t at = (int64_t)(a.v0 + row) * a.lddw + col;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 8) {
-                                if (col + i >= a.dim) break;
-                                if (!dbg_span(at + i, 8, (int64_t)(a.vocab - 1) * a.lddw + a.dim, a.status)) continue;
-                                if (a.dw_f32) {
-                                    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.dw) + at + i);
-                                    if (a.accumulate) {
-                                        const float4 x = p[0], y = p[1];
-                                        const float o[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e) r[i + e] = __float_as_uint(__uint_as_float(r[i + e]) + o[e]);
-                                    }
-                                    *reinterpret_cast<uint4 *>(p) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-                                    *reinterpret_cast<uint4 *>(p + 1) = make_uint4(r[i + 4], r[i + 5], r[i + 6], r[i + 7]);
-                                } else {
-                                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dw) + at + i) = bf16x8(r + i);
-                                }
-                            }
-                        }
+                        if (MODE == XENT_DX) put(r, col, (int)(split * a.rows) + row0, a.dim, INT_MAX, true, a.add);
+                        else if (a.f32) put(r, col, a.v0 + row0, a.dim, a.vocab, true, a.add);
+                        else put(r, col, a.v0 + row0, a.dim, a.vocab, false, false);
                     }
                 }
                 tc_fence_before();
@@ -382,10 +369,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
             }
             if (MODE == XENT_LOSS && ok && row < a.rows) {
-                const int64_t at = (int64_t)(nt0 / w.per) * a.rows + row;
-                if (dbg_span(at, 1, (int64_t)w.num_ng * a.rows, a.status)) a.part[at] = make_float2(top, sum);
+                const int64_t at = (int64_t)(nt0 / w.per * 2 + half) * a.rows + row;
+                if (dbg_span(at, 1, (int64_t)w.num_ng * 2 * a.rows, a.status)) a.part[at] = make_float2(top, sum);
             }
         }
+        if (lane == 0) bulk_wait_all();     // the results are there before the kernel is done
     }
     tc_fence_before();
     __syncthreads();
@@ -438,9 +426,15 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
         for (int i = 0; i < 8; ++i) n += warp_n[i];
         return n;
     };
-    int n = 0;
-    for (int t = threadIdx.x; t < t0; t += 256) n += counts(t);
+    int n = 0, all = 0;
+#pragma unroll 8
+    for (int t = threadIdx.x; t < g.tokens; t += 256) {
+        const int c = counts(t);
+        all += c;
+        n += t < t0 ? c : 0;
+    }
     int at = cta_sum(n);
+    all = cta_sum(all);
     const int nv = g.dim / 8;
     for (int base = t0; base < t1; base += 256) {
         const int t = base + threadIdx.x;
@@ -465,9 +459,17 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
         __syncthreads();
         for (int r = warp; r < total; r += 8) {
             const uint16_t *from = g.x + (int64_t)src[r] * g.ldx;
-            for (int v = lane; v < nv; v += 32)
-                if (dbg_cell(at + r, v * 8, 8, g.rows, g.dim, g.status))
-                    *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r) * g.dim + v * 8) = ldg_stream(from + v * 8);
+            for (int v0 = lane; v0 < nv; v0 += 128) {
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = v0 + 32 * i < nv ? ldg_stream(from + (v0 + 32 * i) * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int v = v0 + 32 * i;
+                    if (v < nv && dbg_cell(at + r, v * 8, 8, g.rows, g.dim, g.status))
+                        *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r) * g.dim + v * 8) = x[i];
+                }
+            }
         }
         if (g.dx)
             for (int r = warp; r < min(256, t1 - base); r += 8)
@@ -477,75 +479,111 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
                             *reinterpret_cast<uint4 *>(g.dx + (base + r) * g.lddx + v * 8) = make_uint4(0, 0, 0, 0);
         at += total;
     }
-    if (t1 == g.tokens && (t0 < g.tokens || blockIdx.x == 0)) {   // the CTA with the last token
-        if (threadIdx.x == 0) *g.count = at;
-        const int end = (at + kTile - 1) / kTile * kTile;
-        for (int r = at + warp; r < end; r += 8)
-            for (int v = lane; v < nv; v += 32)
-                if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status))
-                    *reinterpret_cast<uint4 *>(g.xp + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
-    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *g.count = all;
+    const int end = (all + kTile - 1) / kTile * kTile;
+    for (int r = all + blockIdx.x * 8 + warp; r < end; r += gridDim.x * 8)
+        for (int v = lane; v < nv; v += 32)
+            if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status))
+                *reinterpret_cast<uint4 *>(g.xp + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
-// Forward, last step: a row's units added in a fixed order.  32 rows a CTA, its
-// 32 warps take every 32nd unit.  M, S: maximum and sum without the target.
+// Forward, last step: a CTA adds a row's parts in a fixed order (M, S: maximum
+// and sum without the target) and forms the target's logit by itself, in FP32
+// with a rounding to nearest for every addition: the tensor cores' sums lean
+// towards zero by up to a last place a step, 3e-6 of a logit of 16 at dim 4096,
+// and the loss would inherit it.  That logit is formed before k_xent has ended.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(1024) k_xent_join(const float2 *part, const float *z_target, int units, int64_t rows, const int *count,
-                                                  const int32_t *map, const int32_t *target, int tokens, int vocab, float *loss, float *lse,
-                                                  int *status)
+struct JoinArgs {
+    const float2 *part;
+    int parts;
+    int64_t rows;
+    const int *count;
+    const int32_t *map, *target;
+    const uint16_t *x, *w;      // as k_xent read them: packed rows where there is a map
+    int64_t ldx, ldw;
+    int tokens, vocab, dim;
+    float scale;
+    float *loss, *lse;
+    int *status;
+};
+
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float acc)
 {
-    __shared__ float tops[32][33], sums[32][33];
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc = fmaf(bf16_hi(x[k]), bf16_hi(y[k]), fmaf(bf16_lo(x[k]), bf16_lo(y[k]), acc));
+    return acc;
+}
+
+constexpr int kJoinThreads = 128;
+
+__global__ void __launch_bounds__(kJoinThreads) k_xent_join(JoinArgs g)
+{
+    __shared__ float dots[4], tops[4], sums[4];
     dependents_launch();
-    dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x * 32 + lane, n = count ? *count : tokens;
-    if (blockIdx.x * 32 >= n) return;
-    float M = -INFINITY, S = 0.0f;
-    if (row < n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x;
+    const bool here = row < (g.count ? *g.count : g.tokens);
+    const int t = here ? (g.map ? g.map[row] : row) : 0, at = here ? g.target[t] : -1;
+    const bool counts = at >= 0 && at < g.vocab;
+    float dot = 0.0f, M = -INFINITY, S = 0.0f;
+    if (counts) {
+        const uint4 *px = reinterpret_cast<const uint4 *>(g.x + (int64_t)row * g.ldx), *pw = reinterpret_cast<const uint4 *>(g.w + (int64_t)at * g.ldw);
+        const int nv = g.dim / 8;
 #pragma unroll 4
-        for (int u = warp; u < units; u += 32) {
-            const float2 p = part[(int64_t)u * rows + row];
-            const float m = fmaxf(M, p.x);
-            if (m > -INFINITY) S = S * exp2f(M - m) + p.y * exp2f(p.x - m);
-            else S += p.y;      // 0, or the NaN of a row of NaN
-            M = m;
-        }
+        for (int v = threadIdx.x; v < nv; v += kJoinThreads) dot = dot8(px[v], pw[v], dot);
     }
-    tops[warp][lane] = M;
-    sums[warp][lane] = S;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    dependency_wait();      // k_xent's sums
+    const float2 *part = g.part + row;
+    if (counts)
+#pragma unroll 4
+        for (int u = threadIdx.x; u < g.parts; u += kJoinThreads) M = fmaxf(M, part[u * g.rows].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) {
+        dots[warp] = dot;
+        tops[warp] = M;
+    }
     __syncthreads();
-    if (warp != 0 || row >= n) return;
-    for (int i = 1; i < 32; ++i) {
-        const float top = tops[i][lane], m = fmaxf(M, top);
-        if (m > -INFINITY) S = S * exp2f(M - m) + sums[i][lane] * exp2f(top - m);
-        else S += sums[i][lane];
-        M = m;
-    }
-    const int t = map ? map[row] : row;
-    const int at = target[t];
+    M = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    const float off = M == -INFINITY ? 0.0f : M;    // -inf: no other logit, or all of them -inf (or NaN)
+    if (counts)
+#pragma unroll 4
+        for (int u = threadIdx.x; u < g.parts; u += kJoinThreads) {
+            const float2 p = part[u * g.rows];
+            S += p.y * exp2f(p.x - off);
+        }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+    if (lane == 0) sums[warp] = S;
+    __syncthreads();
+    if (threadIdx.x != 0 || !here) return;
     float l = 0.0f, z = 0.0f;
-    if (at >= 0 && at < vocab) {
-        const float zt = z_target[row];
-        if (zt >= M) {          // the target leads: log(1 + the rest relative to it)
-            l = log1pf(S * exp2f(M - zt));
-            z = zt * kLn2 + l;
+    if (counts) {
+        S = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        const float zt = ((dots[0] + dots[1]) + (dots[2] + dots[3])) * g.scale, yt = zt * kLog2e;
+        if (yt >= M) {          // the target leads: log(1 + the rest relative to it)
+            l = log1pf(S * exp2f(off - yt));
+            z = zt + l;
         } else {
-            const float s = logf(S + exp2f(zt - M));
-            l = (M - zt) * kLn2 + s;
+            const float s = logf(S + exp2f(yt - M));
+            l = (M - yt) * kLn2 + s;
             z = M * kLn2 + s;
         }
-        if (zt != zt) l = z = zt;
-    } else if (at >= vocab) {
-        set_status(status, FP8_ERR_INVALID_ARG);
+        if (zt != zt || zt == INFINITY) l = z = NAN;
+    } else if (at >= g.vocab) {
+        set_status(g.status, FP8_ERR_INVALID_ARG);
     }
-    if (dbg_span(t, 1, tokens, status)) {
-        loss[t] = l;
-        lse[t] = z;
+    if (dbg_span(t, 1, g.tokens, g.status)) {
+        g.loss[t] = l;
+        g.lse[t] = z;
     }
 }
 
-// Backward with K of dx split: the parts added in order, rounded to BF16.
+// Backward, last step: the parts of dx's K added in order, rounded to BF16, each
+// row where its token is.
 __global__ void __launch_bounds__(256) k_xent_dx_join(const float *acc, int splits, int64_t rows, const int *count, const int32_t *map, int dim,
                                                     uint16_t *dx, int64_t lddx, int tokens, int *status)
 {
@@ -584,8 +622,7 @@ struct XentPlan {
     int per_unit, units;            // forward: tiles of a unit, units of a row
     int64_t piece;                  // backward: vocabulary of a piece
     int splits;                     // backward: parts of dx's K
-    bool sums;                      // backward: dx goes through the FP32 buffer
-    int64_t count, map, xp, part, z, g, acc, bytes;     // byte offsets
+    int64_t count, map, xp, part, g, acc, bytes;    // byte offsets
     XentPlan(int64_t tokens, int64_t vocab, int64_t dim, bool backward)
     {
         rows = up(tokens, kTile);
@@ -600,8 +637,7 @@ struct XentPlan {
             per_unit = 8;
             while (per_unit > 1 && mt * ((nt + per_unit - 1) / per_unit) < 16 * pairs) per_unit /= 2;
             units = (int)((nt + per_unit - 1) / per_unit);
-            part = take((int64_t)units * rows * 8);
-            z = take(rows * 4);
+            part = take((int64_t)units * 2 * rows * 8);
         } else {
             // pieces of equal length whose gradient takes up to 256 MB
             const int64_t most = std::max<int64_t>(kTile, ((int64_t)128 << 20) / rows / kTile * kTile);
@@ -609,16 +645,15 @@ struct XentPlan {
             piece = up((vocab + pieces - 1) / pieces, kTile);
             const int64_t tiles = mt * ((dim + kTile - 1) / kTile);
             splits = (int)std::max<int64_t>(1, std::min(pairs / tiles, piece / kBK / 8));
-            sums = splits > 1 || piece < vocab;
             g = take(rows * piece * 2);
-            acc = sums ? take((int64_t)splits * rows * dim * 4) : 0;
+            acc = take((int64_t)splits * rows * dim * 4);
         }
         bytes = at;
     }
 };
 
 template <int MODE>
-int run(const CUtensorMap &mA, const CUtensorMap &mB, const XentArgs &a, cudaStream_t st)
+int run(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorMap &mD, const XentArgs &a, cudaStream_t st)
 {
     static_assert(kSmem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
     static bool attr_done[64] = {};
@@ -628,7 +663,7 @@ int run(const CUtensorMap &mA, const CUtensorMap &mB, const XentArgs &a, cudaStr
         if (cudaFuncSetAttribute(k_xent<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return FP8_ERR_CUDA;
         attr_done[dev & 63] = true;
     }
-    return launch_dependent(k_xent<MODE>, dim3((unsigned)(sm_count() / 2 * 2)), kThreads, kSmem, st, mA, mB, a);
+    return launch_dependent(k_xent<MODE>, dim3((unsigned)(sm_count() / 2 * 2)), kThreads, kSmem, st, mA, mB, mD, a);
 }
 
 // K-major operand: rows of K, 128 of them a box; MN-major: rows along K, boxes of 64 columns.
@@ -641,6 +676,12 @@ bool map_mn(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t l
 {
     return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, 64, kBK,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+// Results: boxes of 32 rows of 128 bytes.
+bool map_out(CUtensorMap *m, void *p, bool f32, int64_t cols, int64_t rows, int64_t ld)
+{
+    return make_map_2d(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)cols, (uint64_t)rows,
+                       (uint64_t)ld * (f32 ? 4 : 2), f32 ? 32 : 64, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 int pack(const XentPlan &p, uint8_t *ws, const int32_t *target, const void *x, int64_t ldx, int64_t tokens, int64_t vocab, int64_t dim, float *loss,
@@ -701,12 +742,28 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.band = 16;
     a.scale = scale;
     a.part = reinterpret_cast<float2 *>(ws + p.part);
-    a.z_target = reinterpret_cast<float *>(ws + p.z);
     a.rows = p.rows;
     a.status = status;
-    if ((rc = run<XENT_LOSS>(mX, mW, a, st)) != FP8_OK) return rc;
-    return launch_dependent(k_xent_join, dim3((unsigned)((tokens + 31) / 32)), 1024, 0, st, static_cast<const float2 *>(a.part),
-                            static_cast<const float *>(a.z_target), p.units, p.rows, a.count, a.map, target, a.tokens, a.vocab, loss, lse, status);
+    if ((rc = run<XENT_LOSS>(mX, mW, mX, a, st)) != FP8_OK) return rc;
+    JoinArgs j{};
+    j.part = a.part;
+    j.parts = p.units * 2;
+    j.rows = p.rows;
+    j.count = a.count;
+    j.map = a.map;
+    j.target = target;
+    j.x = static_cast<const uint16_t *>(xp);
+    j.w = static_cast<const uint16_t *>(w);
+    j.ldx = ldxp;
+    j.ldw = ldw;
+    j.tokens = (int)tokens;
+    j.vocab = (int)vocab;
+    j.dim = (int)dim;
+    j.scale = scale;
+    j.loss = loss;
+    j.lse = lse;
+    j.status = status;
+    return launch_dependent(k_xent_join, dim3((unsigned)tokens), kJoinThreads, 0, st, j);
 }
 
 int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target, const float *loss, const float *lse,
@@ -732,36 +789,31 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.lse = lse;
     a.dloss = dloss;
     a.dlse = dlse;
-    a.g = reinterpret_cast<uint16_t *>(ws + p.g);
-    a.ldg = p.piece;
-    a.acc = reinterpret_cast<float *>(ws + p.acc);
-    a.dx = static_cast<uint16_t *>(dx);
-    a.lddx = lddx;
-    a.dw = dw;
-    a.lddw = lddw;
-    a.dw_f32 = dw_dtype == FP8_OUT_F32;
-    a.accumulate = accumulate;
     a.status = status;
-    const void *xp = ws + p.xp, *g = ws + p.g;
-    CUtensorMap kX, kW, kG, mnW, mnG, mnX;
+    void *xp = ws + p.xp, *g = ws + p.g, *acc = ws + p.acc;
+    const bool f32 = dw_dtype == FP8_OUT_F32;
+    CUtensorMap kX, kW, kG, mnW, mnG, mnX, outG, outX, outW;
     if (!map_k(&kX, xp, dim, p.rows, dim) || !map_k(&kW, w, dim, vocab, ldw) || !map_k(&kG, g, p.piece, p.rows, p.piece) ||
-        !map_mn(&mnW, w, dim, vocab, ldw) || !map_mn(&mnG, g, p.piece, p.rows, p.piece) || !map_mn(&mnX, xp, dim, p.rows, dim))
+        !map_mn(&mnW, w, dim, vocab, ldw) || !map_mn(&mnG, g, p.piece, p.rows, p.piece) || !map_mn(&mnX, xp, dim, p.rows, dim) ||
+        !map_out(&outG, g, false, p.piece, p.rows, p.piece) || !map_out(&outX, acc, true, dim, p.splits * p.rows, dim) ||
+        !map_out(&outW, dw, f32, dim, vocab, lddw))
         return FP8_ERR_CUDA;
     for (int64_t v = 0; v < vocab; v += p.piece) {
         a.v0 = (int)v;
         a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
         a.band = 16;
-        if ((rc = run<XENT_GRAD>(kX, kW, a, st)) != FP8_OK) return rc;
-        a.add = v > 0;
-        a.last = p.splits == 1 && v + p.piece >= vocab;
+        if ((rc = run<XENT_GRAD>(kX, kW, outG, a, st)) != FP8_OK) return rc;
         a.band = 8;
-        if ((rc = run<XENT_DX>(kG, mnW, a, st)) != FP8_OK) return rc;
-        if ((rc = run<XENT_DW>(mnG, mnX, a, st)) != FP8_OK) return rc;
+        a.f32 = 1;
+        a.add = v > 0;
+        if ((rc = run<XENT_DX>(kG, mnW, outX, a, st)) != FP8_OK) return rc;
+        a.f32 = f32;
+        a.add = accumulate;
+        if ((rc = run<XENT_DW>(mnG, mnX, outW, a, st)) != FP8_OK) return rc;
     }
-    if (p.splits == 1) return FP8_OK;
     const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + 255) / 256, (int64_t)sm_count() * 8);
-    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), 256, 0, st, static_cast<const float *>(a.acc), p.splits, p.rows, a.count, a.map,
-                            a.dim, a.dx, lddx, a.tokens, status);
+    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), 256, 0, st, static_cast<const float *>(acc), p.splits, p.rows, a.count, a.map,
+                            a.dim, static_cast<uint16_t *>(dx), lddx, a.tokens, status);
 }
 
 }  // namespace fp8fg

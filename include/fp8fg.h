@@ -651,14 +651,15 @@ FP8FG_API int fp8_swiglu_bwd_ckpt(const void *c, const float *cs, const void *dh
 FP8FG_API int fp8_embedding_fwd(const int32_t *ids, int64_t tokens, const void *w, int64_t vocab, int64_t dim,
                                 int64_t ldw, float scale, void *out, int64_t ldo, void *stream);
 
-/* Bytes of the caller-owned workspace of fp8_embedding_bwd (any content; calls
- * sharing one must not overlap on the GPU). */
+/* Bytes of the caller-owned workspace of fp8_embedding_bwd for calls of up to
+ * these sizes (any content; calls sharing one must not overlap on the GPU). */
 FP8FG_API size_t fp8_embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
 
 /* dw[v] (+)= scale * sum over t with ids[t] = v of dout[t], summed in FP32 in an
- * order that the ids alone decide (no floating-point atomics).  dw [vocab][lddw]
- * FP32 or BF16 (dw_dtype); accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): added
- * to, rows without tokens untouched; else every row of dw is written, zeros where
+ * order that the ids alone decide.  dw [vocab][lddw] FP32 or BF16 (dw_dtype);
+ * accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): each sum is added to dw in one
+ * addition (whose operands and result count as zero below 2^-126), rows without
+ * tokens stay as they are; else every row of dw is written, zeros where
  * no token has its id.  Negative ids are left out, whatever their dout holds; ids
  * >= vocab too, and record FP8_ERR_INVALID_ARG.  Sizes and alignment as above;
  * vocab <= 2^30, lddw * element size a multiple of 16; workspace 16-byte aligned. */
@@ -694,8 +695,9 @@ FP8FG_API int fp8_linear_xent_fwd(const void *x, int64_t tokens, int64_t dim, in
  * p_target - 1 is taken from loss, as expm1(-loss).  g is rounded to BF16 (the
  * operands of the two products), everything else is FP32 up to the results.
  * loss, lse: as fp8_linear_xent_fwd left them for the same x, w, target, scale.
- * accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): added to dw; else every row is
- * written.  Tokens that do not count get dx = 0 and add nothing to dw, whatever
+ * accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): added to dw in one addition an
+ * element (operands and results below 2^-126 count as zero there); else every row
+ * is written.  Tokens that do not count get dx = 0 and add nothing to dw, whatever
  * their rows of x, dloss and dlse hold.
  * dx [tokens][lddx], dw [vocab][lddw]: 16-byte aligned rows of at least dim.
  * The results are the same in every run. */

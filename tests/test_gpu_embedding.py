@@ -26,7 +26,8 @@ def words(T, V, kind, seed=0):
 
 
 SIZES = [(1, 1, 8), (1, 1000, 64), (31, 7, 16), (32, 600, 256), (33, 511, 264), (100, 512, 1000), (2048, 513, 128), (2049, 100003, 72),
-         (5000, 262145, 64), (9001, 32001, 520)]
+         (5000, 262145, 64), (8192, 2000, 40), (8193, 700, 40), (9001, 32001, 520), (16385, 511, 24), (40000, 300000, 16), (65536, 1 << 18, 8),
+         (65537, (1 << 18) - 1, 8), (150001, 3000, 16)]
 
 
 @pytest.mark.parametrize("T,V,D", SIZES)
