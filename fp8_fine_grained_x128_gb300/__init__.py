@@ -185,10 +185,12 @@ _OUT = (torch.bfloat16, torch.float32)
 
 
 _cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_Tensor = torch.Tensor
 
 
 def _on_device(t, name, dtypes):
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.get_device() == _cuda_device():
+    # (get_device() of a host tensor is -1; every look at a tensor costs about 0.1 us a call)
+    if isinstance(t, _Tensor) and -1 != t.get_device() == _cuda_device() and t.dtype in dtypes:
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
@@ -204,6 +206,9 @@ def _on_device(t, name, dtypes):
 def _buf(t, name, dtypes, numel, optional=False):
     """Device pointer of an array the library reads or writes as `numel`
     contiguous elements."""
+    if t.__class__ is _Tensor and -1 != t.get_device() == _cuda_device() and t.dtype in dtypes and t.is_contiguous() and \
+            t.numel() >= numel:
+        return t.data_ptr()
     if t is None:
         if optional:
             return None
@@ -221,19 +226,21 @@ def _buf(t, name, dtypes, numel, optional=False):
 def _mat(t, name, dtypes):
     """(pointer, rows, cols, leading dimension) of a row-major 2-D view."""
     _on_device(t, name, dtypes)
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(t.shape)}")
-    R, C = t.shape
-    if C > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: columns must be contiguous (stride {t.stride(1)})")
-    ld = t.stride(0) if R > 1 else C
-    return t.data_ptr(), R, C, ld
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(shape)}")
+    R, C = shape
+    ld, step = t.stride()
+    if C > 1 and step != 1:
+        raise ValueError(f"{name}: columns must be contiguous (stride {step})")
+    return t.data_ptr(), R, C, ld if R > 1 else C
 
 
 def _shape(t, name, dims):
-    if isinstance(t, torch.Tensor) and t.dim() != dims:
-        raise ValueError(f"{name}: expected a {dims}-D tensor, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    shape = t.shape
+    if isinstance(t, _Tensor) and len(shape) != dims:
+        raise ValueError(f"{name}: expected a {dims}-D tensor, got shape {tuple(shape)}")
+    return shape
 
 
 def _gran_scales(gran, rows, cols):

@@ -31,9 +31,9 @@
 // k_xent is a persistent kernel of CTA pairs (cta_group::2): a pair computes
 // 256 x 256 tiles, each CTA holding 128 rows of A and 128 columns of B of every
 // 64-deep stage, so that an SM fetches 32 KB where a CTA alone would fetch 48 KB
-// for its half of the tile.  Warp 0 copies (TMA, 6 stages), one thread of the
+// for its half of the tile.  Warp 0 copies (TMA, 5 to 8 stages), one thread of the
 // even CTA's warp 1 issues the MMAs, warps 2..9 drain one of two accumulators
-// while the next tile fills the other.
+// while the next tile fills the other.  Few tokens take tiles of single CTAs.
 #include <limits.h>
 
 #include <algorithm>
@@ -51,16 +51,23 @@ enum { XENT_LOSS = 0, XENT_GRAD = 1, XENT_DX = 2, XENT_DW = 3 };
 
 constexpr int kTile = 256;              // rows and columns of a pair's tile
 constexpr int kBK = 64;                 // K of a stage
-constexpr int kStages = 6;
-constexpr int kHalf = 128 * kBK * 2;    // bytes of one operand's half in one CTA's stage
-constexpr int kStage = 2 * kHalf;
 constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kEpiCols = kTile / 2;     // columns of an epilogue warp: half the tile, of a quarter of its rows
-constexpr int kBars = 2 * kStages + 2 * 2 + 1;
-constexpr int kBox = 4096;              // staging for one store: 32 rows of 128 bytes
-constexpr int kStaging = kEpiWarps * kBox;
-constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBars * 8 + 16;
+constexpr int kBox = 4096;              // staging for one copy: 32 rows of 128 bytes
+
+// PAIR: 256 x BN tiles by two CTAs, of 128 rows and BN / 2 columns each; else
+// 128 x BN tiles by one.  BOXES of staging for every epilogue warp (LOSS has no
+// matrix to write); the rest of the shared memory is stages.
+template <int MODE, bool PAIR, int BN, int BOXES>
+struct Form {
+    static constexpr int kM = PAIR ? 256 : 128, kOwnN = PAIR ? BN / 2 : BN;
+    static constexpr int kA = 128 * kBK * 2, kB = kOwnN * kBK * 2, kStage = kA + kB;
+    static constexpr int kStaging = kEpiWarps * BOXES * kBox;
+    static constexpr int kMostStages = (226 * 1024 - 1024 - kStaging) / kStage, kStages = kMostStages < 8 ? kMostStages : 8;
+    static constexpr int kBars = 2 * kStages + 2 * 2 + 1;
+    static constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBars * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
+};
 
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
@@ -84,33 +91,47 @@ struct XentArgs {
     int *status;
 };
 
-// A pair's tiles, in the same order for every role: unit u of the pair, its
-// tiles' columns [nt0, nt1), K blocks [k0, k1).
+// The units of a pair (or single CTA), in the same order for every role: tiles
+// in columns [nt0, nt1) of row mt, K blocks [k0, k1).  Where a unit lies takes
+// several divisions, half a microsecond for one thread, so a warp works them out
+// for 32 units at a time.
+struct Unit { int mt, nt0, nt1, k0, k1, split; };
+
 struct Walk {
     int num_mt, num_nt, num_ng, per, units, nkb, per_split;
     int band;
-    __device__ __forceinline__ void unit(int u, int &mt, int &nt0, int &nt1, int &k0, int &k1, int &split) const
+    template <typename Body>
+    __device__ __forceinline__ void each(int first, int step, bool &ok, Body &&body) const
     {
-        const int flat = num_mt * num_ng;
-        split = u / flat;
-        int ng;
-        tile_coords_raster(u - split * flat, num_mt, num_ng, band, mt, ng);
-        nt0 = ng * per;
-        nt1 = min(num_nt, nt0 + per);
-        k0 = min(nkb, split * per_split);
-        k1 = min(nkb, k0 + per_split);
+        const int lane = threadIdx.x & 31, flat = num_mt * num_ng;
+        for (int64_t base = first; base < units && ok; base += (int64_t)32 * step) {
+            const int u = (int)min(base + (int64_t)lane * step, (int64_t)units - 1), of = u / flat;
+            int m, g;
+            tile_coords_raster(u - of * flat, num_mt, num_ng, band, m, g);
+            for (int i = 0; i < 32 && base + (int64_t)i * step < units && ok; ++i) {
+                Unit t;
+                t.mt = __shfl_sync(0xffffffffu, m, i);
+                t.nt0 = __shfl_sync(0xffffffffu, g, i) * per;
+                t.nt1 = min(num_nt, t.nt0 + per);
+                t.split = __shfl_sync(0xffffffffu, of, i);
+                t.k0 = min(nkb, t.split * per_split);
+                t.k1 = min(nkb, t.k0 + per_split);
+                body(t);
+            }
+        }
     }
 };
 
-template <int MODE>
+template <int MODE, bool PAIR, int BN>
 __device__ __forceinline__ Walk make_walk(const XentArgs &a)
 {
+    constexpr int kM = PAIR ? 256 : 128;
     const int rows = a.count ? *a.count : a.tokens;
     const int M = MODE == XENT_DW ? a.vn : rows, N = MODE >= XENT_DX ? a.dim : a.vn;
     const int K = MODE == XENT_DX ? a.vn : MODE == XENT_DW ? rows : a.dim;
     Walk w;
-    w.num_mt = (M + kTile - 1) / kTile;
-    w.num_nt = (N + kTile - 1) / kTile;
+    w.num_mt = (M + kM - 1) / kM;
+    w.num_nt = (N + BN - 1) / BN;
     w.per = MODE == XENT_LOSS ? a.per_unit : 1;
     w.num_ng = (w.num_nt + w.per - 1) / w.per;
     w.nkb = (K + kBK - 1) / kBK;
@@ -130,15 +151,17 @@ __device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
 
 }  // namespace
 
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int MODE, bool PAIR, int BN, int BOXES>
+__global__ void __launch_bounds__(kThreads, 1)
     k_xent(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmD,
            const XentArgs a)
 {
+    using F = Form<MODE, PAIR, BN, BOXES>;
     constexpr bool kMnA = MODE == XENT_DW, kMnB = MODE >= XENT_DX;
+    constexpr int kStages = F::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStage + kStaging);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * F::kStage + F::kStaging);
     uint64_t *empty = full + kStages;
     uint64_t *tfull = empty + kStages;
     uint64_t *tempty = tfull + 2;
@@ -147,8 +170,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t rank = PAIR ? cluster_rank() : 0;
+    const int mine = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -156,7 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 2 * kEpiWarps);
+            mbar_init(&tempty[b], (PAIR ? 2 : 1) * kEpiWarps);
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -165,223 +188,396 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc_pair(tmem_slot, 512);
-        tmem_relinquish_pair();
+        if (PAIR) {
+            tmem_alloc_pair(tmem_slot, 2 * BN);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, 2 * BN);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();     // the pair's barriers are there before either CTA signals the other's
+    if (PAIR) cluster_sync();   // the pair's barriers are there before either CTA signals the other's
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     dependency_wait();
-    const Walk w = make_walk<MODE>(a);
+    const Walk w = make_walk<MODE, PAIR, BN>(a);
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         uint32_t it = 0;
         bool ok = true;
-        for (int u = pair; u < w.units && ok; u += pairs) {
-            int mt, nt0, nt1, k0, k1, split;
-            w.unit(u, mt, nt0, nt1, k0, k1, split);
-            const int m = mt * kTile + rank * 128;
-            for (int nt = nt0; nt < nt1 && ok; ++nt) {
-                const int n = nt * kTile + rank * 128;
-                for (int kb = k0; kb < k1; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (!thread_wait(smem_u32(&empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
+        w.each(mine, step, ok, [&](const Unit &t) {
+            const int m = t.mt * F::kM + rank * 128, blocks = (t.nt1 - t.nt0) * (t.k1 - t.k0);
+            if (lane == 0) {
+                int nt = t.nt0, kb = t.k0;
+                for (int i = 0; i < blocks; ++i) {
+                    const uint32_t n_it = it + i;
+                    const int s = n_it % kStages, n = nt * BN + rank * F::kOwnN;
+                    if (!thread_wait(smem_u32(&empty[s]), ((n_it / kStages) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
                     // what lies outside a matrix is filled with zeros and counts its bytes all the same
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
-                    const uint32_t bar = cluster_addr(&full[s], 0);
-                    uint8_t *sa = smem + s * kStage, *sb = sa + kHalf;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * F::kStage);
+                    const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
+                    uint8_t *sa = smem + s * F::kStage, *sb = sa + F::kA;
+                    auto load = [&](uint8_t *to, const CUtensorMap *map, int x, int y) {
+                        if (PAIR) tma_load_2d_pair(to, map, bar, x, y);
+                        else tma_load_2d(to, map, &full[s], x, y);
+                    };
                     if (kMnA) {
-                        tma_load_2d_pair(sa, &tmA, bar, m, kb * kBK);
-                        tma_load_2d_pair(sa + 8192, &tmA, bar, m + 64, kb * kBK);
+                        load(sa, &tmA, m, kb * kBK);
+                        load(sa + 8192, &tmA, m + 64, kb * kBK);
                     } else {
-                        tma_load_2d_pair(sa, &tmA, bar, kb * kBK, m);
+                        load(sa, &tmA, kb * kBK, m);
                     }
                     if (kMnB) {
                         const int v = (MODE == XENT_DX ? a.v0 : 0) + kb * kBK;
-                        tma_load_2d_pair(sb, &tmB, bar, n, v);
-                        tma_load_2d_pair(sb + 8192, &tmB, bar, n + 64, v);
+#pragma unroll
+                        for (int j = 0; j < F::kOwnN / 64; ++j) load(sb + j * 8192, &tmB, n + 64 * j, v);
                     } else {
-                        tma_load_2d_pair(sb, &tmB, bar, kb * kBK, a.v0 + n);
+#pragma unroll
+                        for (int j = 0; j < F::kOwnN; j += 128) load(sb + j * 128, &tmB, kb * kBK, a.v0 + n + j);
+                    }
+                    if (++kb == t.k1) {
+                        kb = t.k0;
+                        ++nt;
                     }
                 }
             }
-        }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (ok) it += blocks;
+        });
         // the next kernel may be set up (k_xent_join reads this call's inputs before it waits: so not before this one has)
         dependents_launch();
         // the copies in flight land (the even CTA's barrier counts both CTAs'),
         // and the last stages' releases arrive, before the pair may leave
-        const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0;
-        for (uint32_t j = first; j < it; ++j) {
-            if (rank == 0) mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1, nullptr);
-            if (ok) mbar_wait_bounded(&empty[j % kStages], (j / kStages) & 1, abort_flag);
+        if (lane == 0) {
+            const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0, end = ok ? it : it + kStages;
+            for (uint32_t j = first; j < end; ++j) {
+                if (rank == 0) mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1, nullptr);
+                if (ok) mbar_wait_bounded(&empty[j % kStages], (j / kStages) & 1, abort_flag);
+            }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer
+        auto commit = [&](uint64_t *bar) {
+            if (PAIR) tc_commit_pair(bar);
+            else tc_commit(bar);
+        };
         if (rank == 0) {
-            constexpr uint32_t idesc = idesc_bf16(256, kTile, kMnA, kMnB);
+            constexpr uint32_t idesc = idesc_bf16(F::kM, BN, kMnA, kMnB);
             uint32_t it = 0, tc = 0;
             bool ok = true;
-            for (int u = pair; u < w.units && ok; u += pairs) {
-                int mt, nt0, nt1, k0, k1, split;
-                w.unit(u, mt, nt0, nt1, k0, k1, split);
-                for (int nt = nt0; nt < nt1 && ok; ++nt, ++tc) {
-                    const uint32_t buf = tc & 1;
-                    if (!thread_wait(smem_u32(&tempty[buf]), ((tc >> 1) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t d = tmem_base + buf * kTile;
-                    for (int kb = k0; kb < k1; ++kb, ++it) {
-                        const int s = it % kStages;
-                        if (!thread_wait(smem_u32(&full[s]), (it / kStages) & 1, abort_flag, a.status)) { ok = false; break; }
+            w.each(mine, step, ok, [&](const Unit &t) {
+                if (lane == 0) {
+                    for (int nt = t.nt0; nt < t.nt1 && ok; ++nt, ++tc) {
+                        const uint32_t buf = tc & 1;
+                        if (!thread_wait(smem_u32(&tempty[buf]), ((tc >> 1) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(smem + s * kStage), sb = sa + kHalf;
+                        const uint32_t d = tmem_base + buf * BN;
+                        for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+                            const int s = it % kStages;
+                            if (!thread_wait(smem_u32(&full[s]), (it / kStages) & 1, abort_flag, a.status)) { ok = false; break; }
+                            tc_fence_after();
+                            const uint32_t sa = smem_u32(smem + s * F::kStage), sb = sa + F::kA;
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k) {
-                            // 16 of K: 32 bytes along a row, or two 1024-byte swizzle atoms of rows
-                            const uint64_t ad = kMnA ? sdesc_mnmajor_sw128(sa + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sa + k * 32);
-                            const uint64_t bd = kMnB ? sdesc_mnmajor_sw128(sb + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sb + k * 32);
-                            tc_mma_f16_pair(d, ad, bd, idesc, (kb > k0 || k > 0) ? 1u : 0u);
+                            for (int k = 0; k < kBK / 16; ++k) {
+                                // 16 of K: 32 bytes along a row, or two 1024-byte swizzle atoms of rows
+                                const uint64_t ad = kMnA ? sdesc_mnmajor_sw128(sa + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sa + k * 32);
+                                const uint64_t bd = kMnB ? sdesc_mnmajor_sw128(sb + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sb + k * 32);
+                                const uint32_t more = kb > t.k0 || k > 0;
+                                if (PAIR) tc_mma_f16_pair(d, ad, bd, idesc, more);
+                                else tc_mma_f16(d, ad, bd, idesc, more);
+                            }
+                            commit(&empty[s]);
                         }
-                        tc_commit_pair(&empty[s]);
+                        if (ok) commit(&tfull[buf]);
                     }
-                    if (ok) tc_commit_pair(&tfull[buf]);
                 }
-            }
-            tc_commit_pair(mma_done);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+            });
+            if (lane == 0) commit(mma_done);
         }
-        mbar_wait_bounded(mma_done, 0, nullptr);
+        if (lane == 0) mbar_wait_bounded(mma_done, 0, nullptr);
+        __syncwarp();
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------ epilogue
         const int lq = warp & 3;                 // TMEM lane quarter of this warp
         const int half = (warp - kEpiWarp0) >> 2;       // and its columns
         const uint32_t tm_lane = tmem_base + ((uint32_t)(lq * 32) << 16);
         const int rows = a.count ? *a.count : a.tokens;
-        uint8_t *box = smem + kStages * kStage + (warp - kEpiWarp0) * kBox;
+        constexpr int kCols = BN / 2, kQ = kCols / 32;  // of this warp
+        uint8_t *staging = smem + kStages * F::kStage + (warp - kEpiWarp0) * BOXES * kBox;
         uint32_t tc = 0;
         bool ok = true;
 
-        // 32 values of this lane's row, columns [col, col + 32) of the result, to
-        // the warp's staging (rows of 128 bytes, 16-byte chunks swizzled as the
-        // copy expects them, so that neither side meets a bank twice); a full
-        // box of 32 rows is copied out.  FP32: every call; BF16: every other.
-        auto put = [&](const uint32_t (&r)[32], int col, int row0, int cols, int rows_end, bool f32, bool add) {
-            const bool begins = f32 || (col & 32) == 0, ends = f32 || (col & 32) != 0;
-            if (begins) {       // the last copy out of it has been read
-                if (lane == 0) bulk_wait_read_all();
-                __syncwarp();
-            }
+        // A result leaves through this warp's staging: boxes of 32 rows of 128 bytes,
+        // 16-byte chunks swizzled as the copies expect them (neither side meets a bank
+        // twice), BOXES of them before they are sent.  stage: 32 values of this lane's
+        // row to columns 32 q of the boxes; send: `boxes` of them to row row0, columns
+        // col and on.  What reaches over the matrix's edge is not written; a box beyond
+        // it is not sent.
+        auto free_boxes = [&] {
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+        };
+        auto stage = [&](const uint32_t (&r)[32], int q, bool f32) {
+            uint8_t *to = staging + (f32 ? q : q >> 1) * kBox + lane * 128;
             if (f32) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    *reinterpret_cast<uint4 *>(to + ((j ^ (lane & 7)) << 4)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4 *>(box + lane * 128 + (((j + ((col & 32) >> 3)) ^ (lane & 7)) << 4)) = bf16x8(r + 8 * j);
-            }
-            if (!ends) return;
-            fence_proxy_async_smem();
-            __syncwarp();
-            const int x = f32 ? col : col - 32;
-            // what reaches over the matrix's edge is not written; a box beyond it is not sent
-            if (x >= cols || row0 >= rows_end) return;
-            if (lane == 0) {
-                if (add) tma_reduce_add_2d(&tmD, box, x, row0);
-                else tma_store_2d(&tmD, box, x, row0);
-                bulk_commit_group();
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(to + (((j + 4 * (q & 1)) ^ (lane & 7)) << 4)) = bf16x8(r + 8 * j);
             }
         };
-
-        for (int u = pair; u < w.units && ok; u += pairs) {
-            int mt, nt0, nt1, k0, k1, split;
-            w.unit(u, mt, nt0, nt1, k0, k1, split);
-            const int row0 = mt * kTile + rank * 128 + lq * 32, row = row0 + lane;
-            // per row of LOSS and GRAD
-            const int token = MODE <= XENT_GRAD && row < rows ? (a.map ? a.map[row] : row) : -1;
-            const int target = MODE <= XENT_GRAD && token >= 0 ? a.target[token] - a.v0 : -1;
-            const float c = a.scale * kLog2e;
-            float top = -INFINITY, sum = 0.0f;              // LOSS
-            float lse2 = 0.0f, coef = 0.0f, at_target = 0.0f;   // GRAD
-            if (MODE == XENT_GRAD && token >= 0) {
-                const float lse = a.lse[token], loss = a.loss[token], gl = a.dloss[token], gz = a.dlse ? a.dlse[token] : 0.0f;
-                lse2 = lse * kLog2e;
-                coef = a.scale * (gl + gz);
-                at_target = a.scale * (gl * expm1f(-loss) + gz * expf(-loss));
+        auto send = [&](int boxes, int col, int row0, int cols, int rows_end, bool f32, bool add) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane != 0 || row0 >= rows_end) return;
+            for (int b = 0; b < boxes; ++b) {
+                const int x = col + b * (f32 ? 32 : 64);
+                if (x >= cols) break;
+                if (add) tma_reduce_add_2d(&tmD, staging + b * kBox, x, row0);
+                else tma_store_2d(&tmD, staging + b * kBox, x, row0);
             }
-            for (int nt = nt0; nt < nt1; ++nt, ++tc) {
-                const uint32_t buf = tc & 1;
-                if (!(ok = __all_sync(0xffffffffu, thread_wait(smem_u32(&tfull[buf]), (tc >> 1) & 1, abort_flag, a.status)))) break;
+            bulk_commit_group();
+        };
+
+        int at_mt = -1;
+        int token = -1, target = -1;                        // of this lane's row, LOSS and GRAD
+        float lse2 = 0.0f, coef = 0.0f, at_target = 0.0f;   // GRAD
+        const float c = a.scale * kLog2e;
+        w.each(mine, step, ok, [&](const Unit &t) {
+            const int row0 = t.mt * F::kM + rank * 128 + lq * 32, row = row0 + lane;
+            if (MODE <= XENT_GRAD && t.mt != at_mt) {
+                at_mt = t.mt;
+                token = row < rows ? (a.map ? a.map[row] : row) : -1;
+                target = token >= 0 ? a.target[token] - a.v0 : -1;
+                if (MODE == XENT_GRAD && token >= 0) {
+                    const float lse = a.lse[token], loss = a.loss[token], gl = a.dloss[token], gz = a.dlse ? a.dlse[token] : 0.0f;
+                    lse2 = lse * kLog2e;
+                    coef = a.scale * (gl + gz);
+                    at_target = a.scale * (gl * expm1f(-loss) + gz * expf(-loss));
+                }
+            }
+            float top = -INFINITY, sum = 0.0f;              // LOSS
+            for (int nt = t.nt0; nt < t.nt1; ++nt, ++tc) {
+                const uint32_t buf = tc & 1, from = tm_lane + buf * BN + half * kCols;
+                const int col0 = nt * BN + half * kCols;    // in the piece, or of dx / dw
+                if (!(ok = __all_sync(0xffffffffu, thread_wait(smem_u32(&tfull[buf]), (tc >> 1) & 1, abort_flag, a.status)))) return;
                 tc_fence_after();
+                auto release = [&] {    // the next tile but one may have the accumulator
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
+                        else mbar_arrive(&tempty[buf]);
+                    }
+                };
+                if constexpr (MODE <= XENT_GRAD) {
+                    // rolled: unrolled over all its columns, the code of these two takes longer to fetch than to run
 #pragma unroll 1
-                for (int j = half * (kEpiCols / 32); j < (half + 1) * (kEpiCols / 32); ++j) {
-                    uint32_t r[32];
-                    tc_ld_32x32b_x32(tm_lane + buf * kTile + j * 32, r);
+                    for (int q = 0; q < kQ; ++q) {
+                        uint32_t r[32];
+                        tc_ld_32x32b_x32(from + q * 32, r);
+                        tc_wait_ld();
+                        const int col = col0 + q * 32, at = target - col;
+                        if (MODE == XENT_LOSS) {
+                            const int lim = a.vn - col;
+                            if (lim < 32) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i >= lim) r[i] = __float_as_uint(-INFINITY);
+                            }
+                            if (at >= 0 && at < 32) {       // left out of the sum
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i == at) r[i] = __float_as_uint(-INFINITY);
+                            }
+                            float m[2] = {-INFINITY, -INFINITY}, s[4] = {};
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) m[i & 1] = fmaxf(m[i & 1], __uint_as_float(r[i]));
+                            const float high = fmaxf(m[0], m[1]) * c;
+                            if (high > top) {
+                                sum *= ex2_approx_ftz(top - high);
+                                top = high;
+                            }
+                            const float off = top == -INFINITY ? 0.0f : -top;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[i & 3] += ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, off));
+                            sum += (s[0] + s[1]) + (s[2] + s[3]);
+                        }
+                        if constexpr (MODE == XENT_GRAD) {
+                            const int lim = token >= 0 ? a.vn - col : 0;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                float g = coef * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -lse2));
+                                if (i == at) g = at_target;
+                                r[i] = __float_as_uint(i < lim ? g : 0.0f);
+                            }
+                            const int in = q & (2 * BOXES - 1);     // of the boxes' quarter of a row
+                            if (in == 0) free_boxes();
+                            stage(r, in, false);
+                            if (in == 2 * BOXES - 1 || q == kQ - 1) {
+                                if (q == kQ - 1) release();
+                                send(in / 2 + 1, col - 32 * in, row0, INT_MAX, INT_MAX, false, false);
+                            }
+                        }
+                    }
+                    if (MODE == XENT_LOSS) release();
+                } else {
+                    uint32_t r[kQ][32];
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q) tc_ld_32x32b_x32(from + q * 32, r[q]);
                     tc_wait_ld();
-                    const int col = nt * kTile + j * 32;    // in the piece, or of dx / dw
-                    if (MODE == XENT_LOSS) {
-                        const int lim = a.vn - col;
-                        if (lim < 32) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i >= lim) r[i] = __float_as_uint(-INFINITY);
-                        }
-                        const int t = target - col;
-                        if (t >= 0 && t < 32) {     // left out of the sum
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i == t) r[i] = __float_as_uint(-INFINITY);
-                        }
-                        float m = top;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(r[i]) * c);
-                        if (m > top) {
-                            sum *= ex2_approx_ftz(top - m);
-                            top = m;
-                        }
-                        const float off = top == -INFINITY ? 0.0f : -top;
-                        float s[4] = {};
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[i & 3] += ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, off));
-                        sum += (s[0] + s[1]) + (s[2] + s[3]);
-                    } else if (MODE == XENT_GRAD) {
-                        const int lim = token >= 0 ? a.vn - col : 0, t = target - col;
+                    for (int q = 0; q < kQ; ++q)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            float g = coef * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -lse2));
-                            if (i == t) g = at_target;
-                            r[i] = __float_as_uint(i < lim ? g : 0.0f);
+                            asm volatile("" : "+r"(r[q][i]));       // not used before the wait
+                            if (t.k0 == t.k1) r[q][i] = 0;          // no K: the accumulator was not written
                         }
-                        put(r, col, row0, INT_MAX, INT_MAX, false, false);
-                    } else {
-                        if (k0 == k1) {     // no K: the accumulator was not written
+                    release();
+                    const bool f32 = MODE == XENT_DX || a.f32;
+                    const int to = MODE == XENT_DX ? (int)(t.split * a.rows) + row0 : a.v0 + row0, end = MODE == XENT_DX ? INT_MAX : a.vocab;
+                    if (f32) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = 0;
+                        for (int q = 0; q < kQ; ++q) {
+                            const int in = q % BOXES;
+                            if (in == 0) free_boxes();
+                            stage(r[q], in, true);
+                            if (in == BOXES - 1) send(BOXES, col0 + 32 * (q - in), to, a.dim, end, true, a.add);
                         }
-                        if (MODE == XENT_DX) put(r, col, (int)(split * a.rows) + row0, a.dim, INT_MAX, true, a.add);
-                        else if (a.f32) put(r, col, a.v0 + row0, a.dim, a.vocab, true, a.add);
-                        else put(r, col, a.v0 + row0, a.dim, a.vocab, false, false);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q) {
+                            const int in = q % (2 * BOXES);
+                            if (in == 0) free_boxes();
+                            stage(r[q], in, false);
+                            if (in == 2 * BOXES - 1 || q == kQ - 1) send(in / 2 + 1, col0 + 32 * (q - in), to, a.dim, end, false, false);
+                        }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
             }
-            if (MODE == XENT_LOSS && ok && row < a.rows) {
-                const int64_t at = (int64_t)(nt0 / w.per * 2 + half) * a.rows + row;
+            if (MODE == XENT_LOSS && row < a.rows) {
+                const int64_t at = (int64_t)(t.nt0 / w.per * 2 + half) * a.rows + row;
                 if (dbg_span(at, 1, (int64_t)w.num_ng * 2 * a.rows, a.status)) a.part[at] = make_float2(top, sum);
             }
-        }
+        });
         if (lane == 0) bulk_wait_all();     // the results are there before the kernel is done
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();     // neither CTA leaves while the other may still signal it
+    if (PAIR) cluster_sync();   // neither CTA leaves while the other may still signal it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, 512);
+        if (PAIR) tmem_dealloc_pair(tmem_base, 2 * BN);
+        else tmem_dealloc(tmem_base, 2 * BN);
     }
+}
+
+// ---------------------------------------------------------------------------
+// Forward of up to 4 tokens: bound by reading W once, so it is read straight into
+// registers and multiplied there in FP32.  A warp takes 4 rows of W at a time, x
+// lies in shared memory as FP32 (each vector of 8 in two halves, so that lanes read
+// neighbouring 16 bytes); every CTA leaves one maximum and sum a token.  No tensor
+// memory, no barriers to set up, and W's lines are not waited for behind those of x,
+// which all SMs would ask one place of the L2 for (1 x 128000 x 4096: 208 us on the
+// tensor cores).
+// ---------------------------------------------------------------------------
+constexpr int kFewTokens = 4, kFewRows = 4, kFewThreads = 256, kFewSmem = 96 * 1024;
+
+template <int T>
+__global__ void __launch_bounds__(kFewThreads, 2) k_xent_few(const uint16_t *__restrict__ x, int64_t ldx, const uint16_t *__restrict__ w, int64_t ldw,
+                                                          const int32_t *__restrict__ target, int tokens, int vocab, int dim, float scale,
+                                                          float2 *__restrict__ part, int64_t rows, int *status)
+{
+    extern __shared__ __align__(16) float4 xs[];    // [T][2][dim / 8]
+    __shared__ float2 warps[kFewThreads / 32][T];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nv = dim / 8;
+    dependency_wait();
+    dependents_launch();        // k_xent_join reads this call's inputs before it waits
+    for (int i = threadIdx.x; i < T * nv; i += kFewThreads) {
+        const int t = i / nv, v = i - t * nv;
+        const uint4 q = t < tokens ? *(reinterpret_cast<const uint4 *>(x + t * ldx) + v) : make_uint4(0, 0, 0, 0);
+        xs[(2 * t) * nv + v] = make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
+        xs[(2 * t + 1) * nv + v] = make_float4(bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w));
+    }
+    int at[T];
+    float top[T], sum[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        at[t] = t < tokens ? target[t] : -1;
+        top[t] = -INFINITY;
+        sum[t] = 0.0f;
+    }
+    __syncthreads();
+    const float c = scale * kLog2e;
+    const int groups = (vocab + kFewRows - 1) / kFewRows;
+    for (int g = blockIdx.x * (kFewThreads / 32) + warp; g < groups; g += gridDim.x * (kFewThreads / 32)) {
+        const int v0 = g * kFewRows;
+        const uint4 *row[kFewRows];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r) row[r] = reinterpret_cast<const uint4 *>(w + (int64_t)min(v0 + r, vocab - 1) * ldw);
+        uint64_t acc[kFewRows][T] = {};     // packed pairs
+#pragma unroll 2
+        for (int v = lane; v < nv; v += 32) {
+            uint4 q[kFewRows];
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) q[r] = ldg_stream(row[r] + v);
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const float4 a = xs[(2 * t) * nv + v], b = xs[(2 * t + 1) * nv + v];
+                const uint64_t p[4] = {p2(a.x, a.y), p2(a.z, a.w), p2(b.x, b.y), p2(b.z, b.w)};
+#pragma unroll
+                for (int r = 0; r < kFewRows; ++r) {
+                    const uint32_t k[4] = {q[r].x, q[r].y, q[r].z, q[r].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][t] = p2_fma(p2_bf16x2(k[e]), p[e], acc[r][t]);
+                }
+            }
+        }
+        float z[kFewRows][T];
+#pragma unroll
+        for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                float lo, hi;
+                f2_unpack(acc[r][t], lo, hi);
+                z[r][t] = lo + hi;
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r)
+#pragma unroll
+                for (int t = 0; t < T; ++t) z[r][t] += __shfl_xor_sync(0xffffffffu, z[r][t], o);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+            float high = top[t];
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) {
+                z[r][t] = v0 + r < vocab && v0 + r != at[t] ? z[r][t] * c : -INFINITY;
+                high = fmaxf(high, z[r][t]);
+            }
+            const float off = high == -INFINITY ? 0.0f : high;
+            sum[t] *= ex2_approx_ftz(top[t] - off);
+            top[t] = high;
+#pragma unroll
+            for (int r = 0; r < kFewRows; ++r) sum[t] += ex2_approx_ftz(z[r][t] - off);
+        }
+    }
+    if (lane == 0)
+#pragma unroll
+        for (int t = 0; t < T; ++t) warps[warp][t] = make_float2(top[t], sum[t]);
+    __syncthreads();
+    if ((int)threadIdx.x >= min(T, tokens)) return;
+    float M = -INFINITY, S = 0.0f;
+    for (int i = 0; i < kFewThreads / 32; ++i) M = fmaxf(M, warps[i][threadIdx.x].x);
+    for (int i = 0; i < kFewThreads / 32; ++i) S += warps[i][threadIdx.x].y * exp2f(warps[i][threadIdx.x].x - (M == -INFINITY ? 0.0f : M));
+    if (dbg_cell(blockIdx.x, threadIdx.x, 1, gridDim.x, rows, status)) part[(int64_t)blockIdx.x * rows + threadIdx.x] = make_float2(M, S);
 }
 
 // ---------------------------------------------------------------------------
@@ -584,17 +780,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_xent_join(JoinArgs g)
 
 // Backward, last step: the parts of dx's K added in order, rounded to BF16, each
 // row where its token is.
-__global__ void __launch_bounds__(256) k_xent_dx_join(const float *acc, int splits, int64_t rows, const int *count, const int32_t *map, int dim,
+constexpr int kSumThreads = 128;
+
+__global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, int splits, int64_t rows, const int *count, const int32_t *map, int dim,
                                                     uint16_t *dx, int64_t lddx, int tokens, int *status)
 {
     dependents_launch();
     dependency_wait();
     const int nv = dim / 8;
     const int64_t items = (int64_t)*count * nv;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; i < items; i += (int64_t)gridDim.x * kSumThreads) {
         const int64_t row = i / nv;
         const int col = (int)(i - row * nv) * 8;
         float v[8] = {};
+#pragma unroll 8
         for (int s = 0; s < splits; ++s) {
             const float4 *p = reinterpret_cast<const float4 *>(acc + (s * rows + row) * dim + col);
             const float4 x = p[0], y = p[1];
@@ -616,35 +815,54 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // A single tile of rows saves nothing by packing them.
 bool packs(int64_t tokens) { return tokens > kTile; }
 
+// Up to 128 tokens, one CTA's tiles hold them all, and a pair's would be half
+// empty: W streams past at 128 x BN tiles by single CTAs (64 x 128000 x 4096:
+// 100 us a pass over half of W in pairs' tiles, HBM's floor is 78).
+bool single(int64_t tokens) { return tokens <= 128; }
+
+// Whether k_xent_few takes the forward: its x has to fit, twice an SM.
+bool few(int64_t tokens, int64_t dim) { return tokens <= kFewTokens && (tokens > 2 ? 4 : tokens) * dim * 4 <= kFewSmem; }
+
+// Up to so many tokens (dw's K) a tile of dw takes longer to write than to
+// compute, and a second box of staging an epilogue warp is worth more than a sixth
+// stage (64 x 64000 x 4096: dw 131 -> 117 us; 8192 tokens: 1% slower).
+constexpr int64_t kShallow = 512;
+
 // Sizes that follow from those of the call alone.
 struct XentPlan {
     int64_t rows;                   // of the packed buffers
-    int per_unit, units;            // forward: tiles of a unit, units of a row
+    int bn;                         // columns of a tile over the vocabulary
+    int per_unit, parts;            // forward: tiles of a unit, maxima and sums of a row
     int64_t piece;                  // backward: vocabulary of a piece
     int splits;                     // backward: parts of dx's K
     int64_t count, map, xp, part, g, acc, bytes;    // byte offsets
     XentPlan(int64_t tokens, int64_t vocab, int64_t dim, bool backward)
     {
+        const bool one = single(tokens);
         rows = up(tokens, kTile);
-        const int64_t mt = rows / kTile, nt = (vocab + kTile - 1) / kTile, pairs = std::max(1, sm_count() / 2);
+        const int64_t mt = rows / kTile, groups = std::max(1, one ? sm_count() : sm_count() / 2);
+        // narrower tiles where the wider ones would leave CTAs without any
+        bn = one && (vocab + 255) / 256 < 2 * groups ? 128 : 256;
+        const int64_t nt = (vocab + bn - 1) / bn;
         int64_t at = 0;
         auto take = [&](int64_t n) { const int64_t p = at; at += up(n, 256); return p; };
         count = take(16);
         map = take(rows * 4);
         xp = backward || packs(tokens) ? take(rows * dim * 2) : 0;
         if (!backward) {
-            // long units write less; 16 of them a pair keep the pairs' shares even
+            // long units write less; 16 of them a group keep the groups' shares even
             per_unit = 8;
-            while (per_unit > 1 && mt * ((nt + per_unit - 1) / per_unit) < 16 * pairs) per_unit /= 2;
-            units = (int)((nt + per_unit - 1) / per_unit);
-            part = take((int64_t)units * 2 * rows * 8);
+            while (per_unit > 1 && mt * ((nt + per_unit - 1) / per_unit) < 16 * groups) per_unit /= 2;
+            parts = (int)((nt + per_unit - 1) / per_unit) * 2;
+            if (few(tokens, dim)) parts = (int)std::min<int64_t>((vocab + kFewRows * 8 - 1) / (kFewRows * 8), (int64_t)sm_count() * 2);
+            part = take((int64_t)parts * rows * 8);
         } else {
             // pieces of equal length whose gradient takes up to 256 MB
             const int64_t most = std::max<int64_t>(kTile, ((int64_t)128 << 20) / rows / kTile * kTile);
             const int64_t pieces = (up(vocab, kTile) + most - 1) / most;
             piece = up((vocab + pieces - 1) / pieces, kTile);
             const int64_t tiles = mt * ((dim + kTile - 1) / kTile);
-            splits = (int)std::max<int64_t>(1, std::min(pairs / tiles, piece / kBK / 8));
+            splits = (int)std::max<int64_t>(1, std::min(groups / tiles, piece / kBK / 8));
             g = take(rows * piece * 2);
             acc = take((int64_t)splits * rows * dim * 4);
         }
@@ -652,18 +870,35 @@ struct XentPlan {
     }
 };
 
-template <int MODE>
+template <int MODE, bool PAIR, int BN, int BOXES>
 int run(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorMap &mD, const XentArgs &a, cudaStream_t st)
 {
-    static_assert(kSmem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
+    using F = Form<MODE, PAIR, BN, BOXES>;
     static bool attr_done[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!attr_done[dev & 63]) {
-        if (cudaFuncSetAttribute(k_xent<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return FP8_ERR_CUDA;
+        if (cudaFuncSetAttribute(k_xent<MODE, PAIR, BN, BOXES>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess) return FP8_ERR_CUDA;
         attr_done[dev & 63] = true;
     }
-    return launch_dependent(k_xent<MODE>, dim3((unsigned)(sm_count() / 2 * 2)), kThreads, kSmem, st, mA, mB, mD, a);
+    const int sms = sm_count();
+    return launch_dependent_cluster(k_xent<MODE, PAIR, BN, BOXES>, dim3((unsigned)(PAIR ? sms / 2 * 2 : sms)), PAIR ? 2 : 1, kThreads, F::kSmem, st, mA,
+                                    mB, mD, a);
+}
+
+template <int T>
+int run_few(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_t *target, int64_t tokens, int64_t vocab, int64_t dim, float scale,
+            float2 *part, const XentPlan &p, int *status, cudaStream_t st)
+{
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_done[dev & 63]) {
+        if (cudaFuncSetAttribute(k_xent_few<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess) return FP8_ERR_CUDA;
+        attr_done[dev & 63] = true;
+    }
+    return launch_dependent(k_xent_few<T>, dim3((unsigned)p.parts), kFewThreads, (size_t)(T * dim * 4), st, static_cast<const uint16_t *>(x), ldx,
+                            static_cast<const uint16_t *>(w), ldw, target, (int)tokens, (int)vocab, (int)dim, scale, part, p.rows, status);
 }
 
 // K-major operand: rows of K, 128 of them a box; MN-major: rows along K, boxes of 64 columns.
@@ -731,23 +966,32 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.count = reinterpret_cast<int *>(ws + p.count);
         a.map = reinterpret_cast<int32_t *>(ws + p.map);
     }
-    CUtensorMap mX, mW;
-    if (!map_k(&mX, xp, dim, xrows, ldxp) || !map_k(&mW, w, dim, vocab, ldw)) return FP8_ERR_CUDA;
-    a.target = target;
-    a.tokens = (int)tokens;
-    a.vocab = a.vn = (int)vocab;
-    a.dim = (int)dim;
-    a.per_unit = p.per_unit;
-    a.splits = 1;
-    a.band = 16;
-    a.scale = scale;
     a.part = reinterpret_cast<float2 *>(ws + p.part);
     a.rows = p.rows;
-    a.status = status;
-    if ((rc = run<XENT_LOSS>(mX, mW, mX, a, st)) != FP8_OK) return rc;
+    if (few(tokens, dim)) {
+        rc = tokens == 1 ? run_few<1>(x, ldx, w, ldw, target, tokens, vocab, dim, scale, a.part, p, status, st)
+             : tokens == 2 ? run_few<2>(x, ldx, w, ldw, target, tokens, vocab, dim, scale, a.part, p, status, st)
+                           : run_few<4>(x, ldx, w, ldw, target, tokens, vocab, dim, scale, a.part, p, status, st);
+    } else {
+        CUtensorMap mX, mW;
+        if (!map_k(&mX, xp, dim, xrows, ldxp) || !map_k(&mW, w, dim, vocab, ldw)) return FP8_ERR_CUDA;
+        a.target = target;
+        a.tokens = (int)tokens;
+        a.vocab = a.vn = (int)vocab;
+        a.dim = (int)dim;
+        a.per_unit = p.per_unit;
+        a.splits = 1;
+        a.band = 16;
+        a.scale = scale;
+        a.status = status;
+        rc = !single(tokens) ? run<XENT_LOSS, true, 256, 0>(mX, mW, mX, a, st)
+             : p.bn == 256   ? run<XENT_LOSS, false, 256, 0>(mX, mW, mX, a, st)
+                             : run<XENT_LOSS, false, 128, 0>(mX, mW, mX, a, st);
+    }
+    if (rc != FP8_OK) return rc;
     JoinArgs j{};
     j.part = a.part;
-    j.parts = p.units * 2;
+    j.parts = p.parts;
     j.rows = p.rows;
     j.count = a.count;
     j.map = a.map;
@@ -802,17 +1046,22 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.v0 = (int)v;
         a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
         a.band = 16;
-        if ((rc = run<XENT_GRAD>(kX, kW, outG, a, st)) != FP8_OK) return rc;
+        rc = !single(tokens) ? run<XENT_GRAD, true, 256, 1>(kX, kW, outG, a, st)
+             : p.bn == 256   ? run<XENT_GRAD, false, 256, 2>(kX, kW, outG, a, st)
+                             : run<XENT_GRAD, false, 128, 1>(kX, kW, outG, a, st);
+        if (rc != FP8_OK) return rc;
         a.band = 8;
         a.f32 = 1;
         a.add = v > 0;
-        if ((rc = run<XENT_DX>(kG, mnW, outX, a, st)) != FP8_OK) return rc;
+        rc = single(tokens) ? run<XENT_DX, false, 256, 2>(kG, mnW, outX, a, st) : run<XENT_DX, true, 256, 1>(kG, mnW, outX, a, st);
+        if (rc != FP8_OK) return rc;
         a.f32 = f32;
         a.add = accumulate;
-        if ((rc = run<XENT_DW>(mnG, mnX, outW, a, st)) != FP8_OK) return rc;
+        rc = tokens <= kShallow ? run<XENT_DW, true, 256, 2>(mnG, mnX, outW, a, st) : run<XENT_DW, true, 256, 1>(mnG, mnX, outW, a, st);
+        if (rc != FP8_OK) return rc;
     }
-    const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + 255) / 256, (int64_t)sm_count() * 8);
-    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), 256, 0, st, static_cast<const float *>(acc), p.splits, p.rows, a.count, a.map,
+    const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + kSumThreads - 1) / kSumThreads, (int64_t)sm_count() * 16);
+    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), kSumThreads, 0, st, static_cast<const float *>(acc), p.splits, p.rows, a.count, a.map,
                             a.dim, static_cast<uint16_t *>(dx), lddx, a.tokens, status);
 }
 

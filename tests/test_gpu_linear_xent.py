@@ -60,7 +60,7 @@ def forward(x, w, t, scale=1.0, ws=None):
 
 
 SIZES = [(1, 1, 8), (1, 257, 64), (2, 7, 8), (3, 5003, 72), (127, 256, 128), (128, 255, 200), (129, 1000, 64), (255, 513, 136),
-         (256, 256, 256), (257, 1025, 64), (300, 2000, 512), (513, 300, 1024), (1000, 9001, 320), (5, 40000, 1024)]
+         (256, 256, 256), (257, 1025, 64), (300, 2000, 512), (513, 300, 1024), (1000, 9001, 320), (5, 40000, 1024), (4, 10007, 1032), (2, 31, 4096), (1, 70001, 8)]
 
 
 @pytest.mark.parametrize("T,V,D", SIZES)
