@@ -13,16 +13,17 @@
 //
 // Everything is a product on the tensor cores (BF16 operands, FP32
 // accumulators): the forward's logits, and per piece of the vocabulary the
-// backward's logits (again), g w and g^T x.  One kernel does all four; they
-// differ in which operands run along K (k_xent<MODE>).
+// backward's logits (again), g w and g^T x.  One kernel does all (k_xent<MODE>);
+// they differ in which operands run along K.
 //
 // Forward: the epilogue keeps, per row, a running maximum and sum over a unit
 // of up to 8 tiles and writes 8 bytes a row and half unit, 1/32 of a BF16 logit row
 // and less; k_xent_join adds them in order.
 // Backward: for a piece of the vocabulary, g is rounded to BF16 (the tensor
-// cores' operand type; it costs each of the products 2^-9 a term, random over
-// the terms, beside the same rounding of the BF16 results) and kept in the
-// workspace, [tokens][piece]; dx is summed over the pieces in FP32.
+// cores' operand type; it costs each of the products up to 2^-8 a term, random
+// over the terms, beside the same rounding of the BF16 results; up to 128 tokens
+// it keeps a second term) and kept in the workspace, [tokens][piece]; dx is summed
+// over the pieces in FP32.
 //
 // Tokens that do not count are left out from the start: k_xent_pack copies the
 // counted rows of x together, so neither the work nor the results see the
@@ -38,6 +39,8 @@
 
 #include <algorithm>
 
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -47,7 +50,7 @@ namespace fp8fg {
 
 namespace {
 
-enum { XENT_LOSS = 0, XENT_GRAD = 1, XENT_DX = 2, XENT_DW = 3 };
+enum { XENT_LOSS = 0, XENT_GRAD = 1, XENT_SUMS = 2 };     // SUMS: dx and dw
 
 constexpr int kTile = 256;              // rows and columns of a pair's tile
 constexpr int kBK = 64;                 // K of a stage
@@ -69,6 +72,11 @@ struct Form {
     static_assert(kSmem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
 };
 
+// The tensor cores' sums lean towards zero, by up to a last place for every 16 of K
+// (1.1e-6 of the loss at dim 4096): the forward sums 2048 of K at a time, and adds
+// those to nearest.
+constexpr int kChunk = 2048 / kBK;
+
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 struct XentArgs {
@@ -78,7 +86,7 @@ struct XentArgs {
     int tokens, vocab, dim;
     int v0, vn;                 // this piece's vocabulary: columns [v0, v0 + vn)
     int per_unit;               // LOSS: tiles of a unit
-    int splits;                 // DX: parts of K
+    int splits;                 // dx: parts of K
     int band;                   // M tiles of a raster band
     float scale;
     // LOSS
@@ -86,61 +94,99 @@ struct XentArgs {
     int64_t rows;               // rows of the packed buffers
     // GRAD
     const float *loss, *lse, *dloss, *dlse;
-    // DX (into FP32 sums, [splits][rows][dim]), DW
-    int f32, add;               // FP32 results; added to what is there
+    // SUMS
+    int low;                    // kLow where g has second terms, else 0
+    int dx_add;                 // dx's parts (FP32, [splits][rows][dim]) are added to
+    int dw_f32, dw_add;
     int *status;
 };
+
+// Up to 128 tokens (GRAD by single CTAs) g keeps a second term, what its BF16
+// rounding leaves, as the rows from kLow on: the products are bound by memory there,
+// dx's tile of 256 rows has room for them, and few tokens' roundings do not average
+// out.  x lies twice in its buffer, at rows 0 and kLow, as dw's K runs over both.
+constexpr int kLow = 128;
 
 // The units of a pair (or single CTA), in the same order for every role: tiles
 // in columns [nt0, nt1) of row mt, K blocks [k0, k1).  Where a unit lies takes
 // several divisions, half a microsecond for one thread, so a warp works them out
 // for 32 units at a time.
-struct Unit { int mt, nt0, nt1, k0, k1, split; };
+struct Unit { int mt, nt0, nt1, k0, k1, split, dw; };
 
-struct Walk {
-    int num_mt, num_nt, num_ng, per, units, nkb, per_split;
-    int band;
-    template <typename Body>
-    __device__ __forceinline__ void each(int first, int step, bool &ok, Body &&body) const
+struct Grid {       // of one product
+    int num_mt, num_nt, num_ng, per, units, nkb, per_split, band;
+    __device__ __forceinline__ Grid(int M, int N, int K, int kM, int kN, int per_, int splits, int band_) : per(per_), band(band_)
     {
-        const int lane = threadIdx.x & 31, flat = num_mt * num_ng;
-        for (int64_t base = first; base < units && ok; base += (int64_t)32 * step) {
-            const int u = (int)min(base + (int64_t)lane * step, (int64_t)units - 1), of = u / flat;
-            int m, g;
-            tile_coords_raster(u - of * flat, num_mt, num_ng, band, m, g);
-            for (int i = 0; i < 32 && base + (int64_t)i * step < units && ok; ++i) {
+        num_mt = (M + kM - 1) / kM;
+        num_nt = (N + kN - 1) / kN;
+        num_ng = (num_nt + per - 1) / per;
+        nkb = (K + kBK - 1) / kBK;
+        per_split = (nkb + splits - 1) / splits;
+        units = num_mt * num_ng * splits;
+    }
+};
+
+// What a DW tile costs at least, in K blocks of 64: its writing.
+constexpr int kTileCost = 6;
+
+template <int MODE, bool PAIR, int BN>
+struct Walk {
+    static constexpr int kM = PAIR ? 256 : 128;
+    const int mine, step;
+    Grid p, w;          // LOSS, GRAD: p; SUMS: p is dx, w is dw
+    // SUMS: dx's units go round the pairs first.  The pairs past the last, unfinished
+    // round (from `rem` on) then take `extra` rounds of dw's, as long as one of dx's
+    // units lasts, and the rest of dw's go round all pairs.
+    int rem, extra;
+    __device__ __forceinline__ Walk(const XentArgs &a, int rows, int mine_, int step_)
+        : mine(mine_), step(step_), p(rows ? rows + a.low : 0, MODE == XENT_SUMS ? a.dim : a.vn, MODE == XENT_SUMS ? a.vn : a.dim, kM, BN,
+                                      MODE == XENT_LOSS ? a.per_unit : 1, MODE == XENT_SUMS ? a.splits : 1, a.band),
+          w(MODE == XENT_SUMS ? a.vn : 0, a.dim, rows ? rows + a.low : 0, kM, BN, 1, 1, a.band)
+    {
+        rem = p.units % step;
+        extra = rem == 0 ? 0 : min(p.per_split / max(w.nkb, kTileCost), w.units / (step - rem));
+    }
+    template <typename Body>
+    __device__ __forceinline__ void each(bool &ok, Body &&body) const
+    {
+        const int lane = threadIdx.x & 31, first = p.units / step + (mine < rem);    // units of p that are this pair's
+        for (int base = 0; ok; base += 32) {
+            const int i = base + lane, j = i - first;
+            const bool dw = MODE == XENT_SUMS && j >= 0;
+            int64_t u = mine + (int64_t)i * step;
+            if (dw) {
+                const int ahead = mine >= rem ? extra : 0;
+                u = j < ahead ? (int64_t)j * (step - rem) + mine - rem : (int64_t)extra * (step - rem) + (int64_t)(j - ahead) * step + mine;
+            }
+            const Grid &g = dw ? w : p;
+            const bool valid = u < g.units;
+            int of = 0, m = 0, n = 0;
+            if (valid) {
+                const int flat = g.num_mt * g.num_ng;
+                of = (int)u / flat;
+                tile_coords_raster((int)u - of * flat, g.num_mt, g.num_ng, g.band, m, n);
+            }
+            const int todo = __popc(__ballot_sync(0xffffffffu, valid));     // the valid ones are the first
+            for (int k = 0; k < todo && ok; ++k) {
                 Unit t;
-                t.mt = __shfl_sync(0xffffffffu, m, i);
-                t.nt0 = __shfl_sync(0xffffffffu, g, i) * per;
-                t.nt1 = min(num_nt, t.nt0 + per);
-                t.split = __shfl_sync(0xffffffffu, of, i);
+                t.dw = MODE == XENT_SUMS ? __shfl_sync(0xffffffffu, (int)dw, k) : 0;
+                t.mt = __shfl_sync(0xffffffffu, m, k);
+                t.nt0 = __shfl_sync(0xffffffffu, n, k) * p.per;
+                t.nt1 = min(t.dw ? w.num_nt : p.num_nt, t.nt0 + p.per);
+                t.split = __shfl_sync(0xffffffffu, of, k);
+                const int nkb = t.dw ? w.nkb : p.nkb, per_split = t.dw ? w.per_split : p.per_split;
                 t.k0 = min(nkb, t.split * per_split);
                 t.k1 = min(nkb, t.k0 + per_split);
                 body(t);
             }
+            if (todo < 32) break;
         }
     }
 };
 
-template <int MODE, bool PAIR, int BN>
-__device__ __forceinline__ Walk make_walk(const XentArgs &a)
-{
-    constexpr int kM = PAIR ? 256 : 128;
-    const int rows = a.count ? *a.count : a.tokens;
-    const int M = MODE == XENT_DW ? a.vn : rows, N = MODE >= XENT_DX ? a.dim : a.vn;
-    const int K = MODE == XENT_DX ? a.vn : MODE == XENT_DW ? rows : a.dim;
-    Walk w;
-    w.num_mt = (M + kM - 1) / kM;
-    w.num_nt = (N + BN - 1) / BN;
-    w.per = MODE == XENT_LOSS ? a.per_unit : 1;
-    w.num_ng = (w.num_nt + w.per - 1) / w.per;
-    w.nkb = (K + kBK - 1) / kBK;
-    const int splits = MODE == XENT_DX ? a.splits : 1;
-    w.per_split = (w.nkb + splits - 1) / splits;
-    w.units = w.num_mt * w.num_ng * splits;
-    w.band = a.band;
-    return w;
-}
+// Tensor maps: A, B and the result, of dx and then of dw for SUMS.
+template <int MODE>
+struct Maps { CUtensorMap m[MODE == XENT_SUMS ? 6 : 3]; };
 
 // 8 FP32 values to 16 bytes of BF16.
 __device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
@@ -153,11 +199,10 @@ __device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
 
 template <int MODE, bool PAIR, int BN, int BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_xent(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmD,
-           const XentArgs a)
+    k_xent(const __grid_constant__ Maps<MODE> maps, const XentArgs a)
 {
     using F = Form<MODE, PAIR, BN, BOXES>;
-    constexpr bool kMnA = MODE == XENT_DW, kMnB = MODE >= XENT_DX;
+    constexpr bool kSums = MODE == XENT_SUMS;
     constexpr int kStages = F::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -171,7 +216,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_rank() : 0;
-    const int mine = PAIR ? blockIdx.x >> 1 : blockIdx.x, step = PAIR ? gridDim.x >> 1 : gridDim.x;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -184,8 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_barrier_init();
-        prefetch_tensormap(&tmA);
-        prefetch_tensormap(&tmB);
+        for (const CUtensorMap &m : maps.m) prefetch_tensormap(&m);
     }
     if (warp == 1) {
         if (PAIR) {
@@ -202,13 +245,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     dependency_wait();
-    const Walk w = make_walk<MODE, PAIR, BN>(a);
+    const int rows = a.count ? *a.count : a.tokens;
+    // accumulators of a tile of LOSS, one for every kChunk blocks of K
+    const int chunks = MODE == XENT_LOSS ? max(1, ((a.dim + kBK - 1) / kBK + kChunk - 1) / kChunk) : 1;
+    const Walk<MODE, PAIR, BN> walk(a, rows, PAIR ? blockIdx.x >> 1 : blockIdx.x, PAIR ? gridDim.x >> 1 : gridDim.x);
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         uint32_t it = 0;
         bool ok = true;
-        w.each(mine, step, ok, [&](const Unit &t) {
+        walk.each(ok, [&](const Unit &t) {
             const int m = t.mt * F::kM + rank * 128, blocks = (t.nt1 - t.nt0) * (t.k1 - t.k0);
             if (lane == 0) {
                 int nt = t.nt0, kb = t.k0;
@@ -224,19 +270,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (PAIR) tma_load_2d_pair(to, map, bar, x, y);
                         else tma_load_2d(to, map, &full[s], x, y);
                     };
-                    if (kMnA) {
-                        load(sa, &tmA, m, kb * kBK);
-                        load(sa + 8192, &tmA, m + 64, kb * kBK);
-                    } else {
-                        load(sa, &tmA, kb * kBK, m);
-                    }
-                    if (kMnB) {
-                        const int v = (MODE == XENT_DX ? a.v0 : 0) + kb * kBK;
+                    if (kSums) {        // dx: g along K, W across it; dw: both across
+                        const CUtensorMap *A = &maps.m[t.dw ? 3 : 0], *B = A + 1;
+                        if (t.dw) {
+                            load(sa, A, m, kb * kBK);
+                            load(sa + 8192, A, m + 64, kb * kBK);
+                        } else {
+                            load(sa, A, kb * kBK, m);
+                        }
+                        const int k = (t.dw ? 0 : a.v0) + kb * kBK;
 #pragma unroll
-                        for (int j = 0; j < F::kOwnN / 64; ++j) load(sb + j * 8192, &tmB, n + 64 * j, v);
-                    } else {
+                        for (int j = 0; j < F::kOwnN / 64; ++j) load(sb + j * 8192, B, n + 64 * j, k);
+                    } else {            // x and W along K
+                        load(sa, &maps.m[0], kb * kBK, m);
 #pragma unroll
-                        for (int j = 0; j < F::kOwnN; j += 128) load(sb + j * 128, &tmB, kb * kBK, a.v0 + n + j);
+                        for (int j = 0; j < F::kOwnN; j += 128) load(sb + j * 128, &maps.m[1], kb * kBK, a.v0 + n + j);
                     }
                     if (++kb == t.k1) {
                         kb = t.k0;
@@ -265,29 +313,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tc_commit(bar);
         };
         if (rank == 0) {
-            constexpr uint32_t idesc = idesc_bf16(F::kM, BN, kMnA, kMnB);
             uint32_t it = 0, tc = 0;
             bool ok = true;
-            w.each(mine, step, ok, [&](const Unit &t) {
+            walk.each(ok, [&](const Unit &t) {
                 if (lane == 0) {
-                    for (int nt = t.nt0; nt < t.nt1 && ok; ++nt, ++tc) {
+                    const uint32_t idesc = kSums && t.dw ? idesc_bf16(F::kM, BN, true, true) : idesc_bf16(F::kM, BN, false, kSums);
+                    const int parts = (t.nt1 - t.nt0) * chunks;     // of the unit, an accumulator each
+                    for (int i = 0; i < parts && ok; ++i, ++tc) {
+                        const int c0 = chunks == 1 ? t.k0 : i % chunks * kChunk, c1 = chunks == 1 ? t.k1 : min(t.k1, c0 + kChunk);
                         const uint32_t buf = tc & 1;
                         if (!thread_wait(smem_u32(&tempty[buf]), ((tc >> 1) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t d = tmem_base + buf * BN;
-                        for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+                        for (int kb = c0; kb < c1; ++kb, ++it) {
                             const int s = it % kStages;
                             if (!thread_wait(smem_u32(&full[s]), (it / kStages) & 1, abort_flag, a.status)) { ok = false; break; }
                             tc_fence_after();
                             const uint32_t sa = smem_u32(smem + s * F::kStage), sb = sa + F::kA;
+                            // 16 of K: 32 bytes along a row, or two 1024-byte swizzle atoms of rows
+                            const uint64_t ad = kSums && t.dw ? sdesc_mnmajor_sw128(sa, 8192, 1024) : sdesc_kmajor_sw128(sa);
+                            const uint64_t bd = kSums ? sdesc_mnmajor_sw128(sb, 8192, 1024) : sdesc_kmajor_sw128(sb);
+                            const uint64_t a_step = (kSums && t.dw ? 2048 : 32) >> 4, b_step = (kSums ? 2048 : 32) >> 4;
 #pragma unroll
                             for (int k = 0; k < kBK / 16; ++k) {
-                                // 16 of K: 32 bytes along a row, or two 1024-byte swizzle atoms of rows
-                                const uint64_t ad = kMnA ? sdesc_mnmajor_sw128(sa + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sa + k * 32);
-                                const uint64_t bd = kMnB ? sdesc_mnmajor_sw128(sb + k * 2048, 8192, 1024) : sdesc_kmajor_sw128(sb + k * 32);
-                                const uint32_t more = kb > t.k0 || k > 0;
-                                if (PAIR) tc_mma_f16_pair(d, ad, bd, idesc, more);
-                                else tc_mma_f16(d, ad, bd, idesc, more);
+                                const uint32_t more = kb > c0 || k > 0;
+                                if (PAIR) tc_mma_f16_pair(d, ad + k * a_step, bd + k * b_step, idesc, more);
+                                else tc_mma_f16(d, ad + k * a_step, bd + k * b_step, idesc, more);
                             }
                             commit(&empty[s]);
                         }
@@ -305,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lq = warp & 3;                 // TMEM lane quarter of this warp
         const int half = (warp - kEpiWarp0) >> 2;       // and its columns
         const uint32_t tm_lane = tmem_base + ((uint32_t)(lq * 32) << 16);
-        const int rows = a.count ? *a.count : a.tokens;
         constexpr int kCols = BN / 2, kQ = kCols / 32;  // of this warp
         uint8_t *staging = smem + kStages * F::kStage + (warp - kEpiWarp0) * BOXES * kBox;
         uint32_t tc = 0;
@@ -332,16 +382,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(to + (((j + 4 * (q & 1)) ^ (lane & 7)) << 4)) = bf16x8(r + 8 * j);
             }
         };
-        auto send = [&](int boxes, int col, int row0, int cols, int rows_end, bool f32, bool add) {
+        auto send = [&](const CUtensorMap *to, int boxes, int col, int row0, int cols, int rows_end, bool f32, bool add) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane != 0 || row0 >= rows_end) return;
             for (int b = 0; b < boxes; ++b) {
                 const int x = col + b * (f32 ? 32 : 64);
                 if (x >= cols) break;
-                if (add) tma_reduce_add_2d(&tmD, staging + b * kBox, x, row0);
-                else tma_store_2d(&tmD, staging + b * kBox, x, row0);
+                if (add) tma_reduce_add_2d(to, staging + b * kBox, x, row0);
+                else tma_store_2d(to, staging + b * kBox, x, row0);
             }
+            bulk_commit_group();
+        };
+
+        // GRAD of single CTAs: the first box to row row0, the second to its lower terms' row
+        auto send_terms = [&](int col, int row0) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane != 0) return;
+            tma_store_2d(&maps.m[2], staging, col, row0);
+            tma_store_2d(&maps.m[2], staging + (BOXES > 1 ? kBox : 0), col, row0 + kLow);
             bulk_commit_group();
         };
 
@@ -349,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int token = -1, target = -1;                        // of this lane's row, LOSS and GRAD
         float lse2 = 0.0f, coef = 0.0f, at_target = 0.0f;   // GRAD
         const float c = a.scale * kLog2e;
-        w.each(mine, step, ok, [&](const Unit &t) {
+        walk.each(ok, [&](const Unit &t) {
             const int row0 = t.mt * F::kM + rank * 128 + lq * 32, row = row0 + lane;
             if (MODE <= XENT_GRAD && t.mt != at_mt) {
                 at_mt = t.mt;
@@ -364,69 +424,109 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float top = -INFINITY, sum = 0.0f;              // LOSS
             for (int nt = t.nt0; nt < t.nt1; ++nt, ++tc) {
-                const uint32_t buf = tc & 1, from = tm_lane + buf * BN + half * kCols;
-                const int col0 = nt * BN + half * kCols;    // in the piece, or of dx / dw
-                if (!(ok = __all_sync(0xffffffffu, thread_wait(smem_u32(&tfull[buf]), (tc >> 1) & 1, abort_flag, a.status)))) return;
-                tc_fence_after();
-                auto release = [&] {    // the next tile but one may have the accumulator
+                auto full_accumulator = [&] {
+                    const bool there = __all_sync(0xffffffffu, thread_wait(smem_u32(&tfull[tc & 1]), (tc >> 1) & 1, abort_flag, a.status));
+                    tc_fence_after();
+                    return there;
+                };
+                auto release = [&] {    // the next accumulation but one may have it
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(cluster_addr(&tempty[buf], 0));
-                        else mbar_arrive(&tempty[buf]);
+                        if (PAIR) mbar_arrive_cluster(cluster_addr(&tempty[tc & 1], 0));
+                        else mbar_arrive(&tempty[tc & 1]);
                     }
                 };
-                if constexpr (MODE <= XENT_GRAD) {
-                    // rolled: unrolled over all its columns, the code of these two takes longer to fetch than to run
+                if (!(ok = full_accumulator())) return;
+                const uint32_t from = tm_lane + (tc & 1) * BN + half * kCols;
+                const int col0 = nt * BN + half * kCols;    // in the piece, or of dx / dw
+                if constexpr (MODE == XENT_LOSS) {
+                    uint32_t r[kQ][32];
+                    auto load = [&](uint32_t (&to)[32], int q) {
+                        tc_ld_32x32b_x32(tm_lane + (tc & 1) * BN + half * kCols + q * 32, to);
+                    };
+                    auto settle = [](uint32_t (&v)[32]) {       // not used before the wait
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+                    };
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q) load(r[q], q);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q) settle(r[q]);
+                    release();
+                    for (int i = 1; i < chunks; ++i) {
+                        ++tc;
+                        if (!(ok = full_accumulator())) return;
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q) {
+                            uint32_t v[32];
+                            load(v, q);
+                            tc_wait_ld();
+                            settle(v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[q][e] = __float_as_uint(__uint_as_float(r[q][e]) + __uint_as_float(v[e]));
+                        }
+                        release();
+                    }
+                    const int lim = a.vn - col0, at = target - col0;
+                    if (lim < kCols || (at >= 0 && at < kCols)) {   // beyond the vocabulary; the target is left out of the sum
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (q * 32 + i >= lim || q * 32 + i == at) r[q][i] = __float_as_uint(-INFINITY);
+                    }
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s[4] = {};
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], __uint_as_float(r[q][i]));
+                    const float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
+                    if (high > top) {
+                        sum *= ex2_approx_ftz(top - high);
+                        top = high;
+                    }
+                    const float off = top == -INFINITY ? 0.0f : -top;
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[i & 3] += ex2_approx_ftz(fmaf(__uint_as_float(r[q][i]), c, off));
+                    sum += (s[0] + s[1]) + (s[2] + s[3]);
+                } else if constexpr (MODE == XENT_GRAD) {
 #pragma unroll 1
                     for (int q = 0; q < kQ; ++q) {
                         uint32_t r[32];
                         tc_ld_32x32b_x32(from + q * 32, r);
                         tc_wait_ld();
                         const int col = col0 + q * 32, at = target - col;
-                        if (MODE == XENT_LOSS) {
-                            const int lim = a.vn - col;
-                            if (lim < 32) {
+                        const int lim = token >= 0 ? a.vn - col : 0;
+                        uint32_t low[PAIR ? 1 : 32];
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (i >= lim) r[i] = __float_as_uint(-INFINITY);
-                            }
-                            if (at >= 0 && at < 32) {       // left out of the sum
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (i == at) r[i] = __float_as_uint(-INFINITY);
-                            }
-                            float m[2] = {-INFINITY, -INFINITY}, s[4] = {};
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) m[i & 1] = fmaxf(m[i & 1], __uint_as_float(r[i]));
-                            const float high = fmaxf(m[0], m[1]) * c;
-                            if (high > top) {
-                                sum *= ex2_approx_ftz(top - high);
-                                top = high;
-                            }
-                            const float off = top == -INFINITY ? 0.0f : -top;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i & 3] += ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, off));
-                            sum += (s[0] + s[1]) + (s[2] + s[3]);
+                        for (int i = 0; i < 32; ++i) {
+                            float g = coef * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -lse2));
+                            if (i == at) g = at_target;
+                            g = i < lim ? g : 0.0f;
+                            r[i] = __float_as_uint(g);
+                            if (!PAIR) low[PAIR ? 0 : i] = __float_as_uint(g - __bfloat162float(__float2bfloat16_rn(g)));
                         }
-                        if constexpr (MODE == XENT_GRAD) {
-                            const int lim = token >= 0 ? a.vn - col : 0;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                float g = coef * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -lse2));
-                                if (i == at) g = at_target;
-                                r[i] = __float_as_uint(i < lim ? g : 0.0f);
-                            }
-                            const int in = q & (2 * BOXES - 1);     // of the boxes' quarter of a row
+                        if constexpr (PAIR) {
+                            const int in = q & (2 * BOXES - 1);     // quarter of the boxes
                             if (in == 0) free_boxes();
                             stage(r, in, false);
                             if (in == 2 * BOXES - 1 || q == kQ - 1) {
                                 if (q == kQ - 1) release();
-                                send(in / 2 + 1, col - 32 * in, row0, INT_MAX, INT_MAX, false, false);
+                                send(&maps.m[2], in / 2 + 1, col - 32 * in, row0, INT_MAX, INT_MAX, false, false);
                             }
+                        } else {        // two terms: one box each
+                            static_assert(PAIR || BOXES == 2, "a box for each term");
+                            if ((q & 1) == 0) free_boxes();
+                            stage(r, q & 1, false);
+                            stage(low, 2 + (q & 1), false);
+                            if (q == kQ - 1) release();
+                            if (q & 1) send_terms(col - 32, row0);
                         }
                     }
-                    if (MODE == XENT_LOSS) release();
                 } else {
                     uint32_t r[kQ][32];
 #pragma unroll
@@ -440,15 +540,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (t.k0 == t.k1) r[q][i] = 0;          // no K: the accumulator was not written
                         }
                     release();
-                    const bool f32 = MODE == XENT_DX || a.f32;
-                    const int to = MODE == XENT_DX ? (int)(t.split * a.rows) + row0 : a.v0 + row0, end = MODE == XENT_DX ? INT_MAX : a.vocab;
+                    const bool f32 = !t.dw || a.dw_f32, add = t.dw ? a.dw_add : a.dx_add;
+                    const CUtensorMap *map = &maps.m[t.dw ? 5 : 2];
+                    const int to = t.dw ? a.v0 + row0 : (int)(t.split * a.rows) + row0, end = t.dw ? a.vocab : INT_MAX;
                     if (f32) {
 #pragma unroll
                         for (int q = 0; q < kQ; ++q) {
                             const int in = q % BOXES;
                             if (in == 0) free_boxes();
                             stage(r[q], in, true);
-                            if (in == BOXES - 1) send(BOXES, col0 + 32 * (q - in), to, a.dim, end, true, a.add);
+                            if (in == BOXES - 1) send(map, BOXES, col0 + 32 * (q - in), to, a.dim, end, true, add);
                         }
                     } else {
 #pragma unroll
@@ -456,14 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int in = q % (2 * BOXES);
                             if (in == 0) free_boxes();
                             stage(r[q], in, false);
-                            if (in == 2 * BOXES - 1 || q == kQ - 1) send(in / 2 + 1, col0 + 32 * (q - in), to, a.dim, end, false, false);
+                            if (in == 2 * BOXES - 1 || q == kQ - 1) send(map, in / 2 + 1, col0 + 32 * (q - in), to, a.dim, end, false, false);
                         }
                     }
                 }
             }
             if (MODE == XENT_LOSS && row < a.rows) {
-                const int64_t at = (int64_t)(t.nt0 / w.per * 2 + half) * a.rows + row;
-                if (dbg_span(at, 1, (int64_t)w.num_ng * 2 * a.rows, a.status)) a.part[at] = make_float2(top, sum);
+                const int64_t at = (int64_t)(t.nt0 / walk.p.per * 2 + half) * a.rows + row;
+                if (dbg_span(at, 1, (int64_t)walk.p.num_ng * 2 * a.rows, a.status)) a.part[at] = make_float2(top, sum);
             }
         });
         if (lane == 0) bulk_wait_all();     // the results are there before the kernel is done
@@ -593,6 +694,7 @@ struct PackArgs {
     int tokens, vocab, dim;
     uint16_t *xp;               // [rows][dim]
     int64_t rows;
+    int twice;                  // up to kLow tokens: x at rows 0 and kLow
     int32_t *map;
     int *count;
     float *loss, *lse;          // forward: zeroed where a token does not count
@@ -662,8 +764,9 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int v = v0 + 32 * i;
-                    if (v < nv && dbg_cell(at + r, v * 8, 8, g.rows, g.dim, g.status))
-                        *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r) * g.dim + v * 8) = x[i];
+                    if (v >= nv || !dbg_cell(at + r + (g.twice ? kLow : 0), v * 8, 8, g.rows, g.dim, g.status)) continue;
+                    *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r) * g.dim + v * 8) = x[i];
+                    if (g.twice) *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r + kLow) * g.dim + v * 8) = x[i];
                 }
             }
         }
@@ -676,11 +779,13 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
         at += total;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *g.count = all;
-    const int end = (all + kTile - 1) / kTile * kTile;
-    for (int r = all + blockIdx.x * 8 + warp; r < end; r += gridDim.x * 8)
+    const int end = g.twice ? kTile : (all + kTile - 1) / kTile * kTile;
+    for (int r = all + blockIdx.x * 8 + warp; r < end; r += gridDim.x * 8) {
+        if (g.twice && r >= kLow && r < kLow + all) continue;
         for (int v = lane; v < nv; v += 32)
             if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status))
                 *reinterpret_cast<uint4 *>(g.xp + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -782,7 +887,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_xent_join(JoinArgs g)
 // row where its token is.
 constexpr int kSumThreads = 128;
 
-__global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, int splits, int64_t rows, const int *count, const int32_t *map, int dim,
+__global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, int splits, int low, int64_t rows, const int *count, const int32_t *map, int dim,
                                                     uint16_t *dx, int64_t lddx, int tokens, int *status)
 {
     dependents_launch();
@@ -794,8 +899,8 @@ __global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, 
         const int col = (int)(i - row * nv) * 8;
         float v[8] = {};
 #pragma unroll 8
-        for (int s = 0; s < splits; ++s) {
-            const float4 *p = reinterpret_cast<const float4 *>(acc + (s * rows + row) * dim + col);
+        for (int s = 0; s < (low ? 2 * splits : splits); ++s) {     // the second terms' first: they are the smaller
+            const float4 *p = reinterpret_cast<const float4 *>(acc + (s < splits ? s * rows + row + low : (s - splits) * rows + row) * dim + col);
             const float4 x = p[0], y = p[1];
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
             v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
@@ -823,7 +928,7 @@ bool single(int64_t tokens) { return tokens <= 128; }
 // Whether k_xent_few takes the forward: its x has to fit, twice an SM.
 bool few(int64_t tokens, int64_t dim) { return tokens <= kFewTokens && (tokens > 2 ? 4 : tokens) * dim * 4 <= kFewSmem; }
 
-// Up to so many tokens (dw's K) a tile of dw takes longer to write than to
+// Up to so many tokens (dw's K), a tile of dw takes longer to write than to
 // compute, and a second box of staging an epilogue warp is worth more than a sixth
 // stage (64 x 64000 x 4096: dw 131 -> 117 us; 8192 tokens: 1% slower).
 constexpr int64_t kShallow = 512;
@@ -861,8 +966,10 @@ struct XentPlan {
             const int64_t most = std::max<int64_t>(kTile, ((int64_t)128 << 20) / rows / kTile * kTile);
             const int64_t pieces = (up(vocab, kTile) + most - 1) / most;
             piece = up((vocab + pieces - 1) / pieces, kTile);
-            const int64_t tiles = mt * ((dim + kTile - 1) / kTile);
-            splits = (int)std::max<int64_t>(1, std::min(groups / tiles, piece / kBK / 8));
+            // dx's K is split until a part lasts no longer than a pair's share of dx and dw
+            const int64_t nd = (dim + kTile - 1) / kTile, kv = piece / kBK, kt = std::max<int64_t>(kTileCost, (tokens + kBK - 1) / kBK);
+            const int64_t share = (mt * nd * kv + piece / kTile * nd * kt) / std::max(1, sm_count() / 2);
+            splits = (int)std::max<int64_t>(1, std::min((kv + share) / (share + 1), kv / 8));
             g = take(rows * piece * 2);
             acc = take((int64_t)splits * rows * dim * 4);
         }
@@ -871,7 +978,7 @@ struct XentPlan {
 };
 
 template <int MODE, bool PAIR, int BN, int BOXES>
-int run(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorMap &mD, const XentArgs &a, cudaStream_t st)
+int run(const Maps<MODE> &maps, const XentArgs &a, cudaStream_t st)
 {
     using F = Form<MODE, PAIR, BN, BOXES>;
     static bool attr_done[64] = {};
@@ -882,8 +989,8 @@ int run(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorMap &mD, con
         attr_done[dev & 63] = true;
     }
     const int sms = sm_count();
-    return launch_dependent_cluster(k_xent<MODE, PAIR, BN, BOXES>, dim3((unsigned)(PAIR ? sms / 2 * 2 : sms)), PAIR ? 2 : 1, kThreads, F::kSmem, st, mA,
-                                    mB, mD, a);
+    return launch_dependent_cluster(k_xent<MODE, PAIR, BN, BOXES>, dim3((unsigned)(PAIR ? sms / 2 * 2 : sms)), PAIR ? 2 : 1, kThreads, F::kSmem, st, maps,
+                                    a);
 }
 
 template <int T>
@@ -920,7 +1027,7 @@ bool map_out(CUtensorMap *m, void *p, bool f32, int64_t cols, int64_t rows, int6
 }
 
 int pack(const XentPlan &p, uint8_t *ws, const int32_t *target, const void *x, int64_t ldx, int64_t tokens, int64_t vocab, int64_t dim, float *loss,
-         float *lse, void *dx, int64_t lddx, int *status, cudaStream_t st)
+         float *lse, void *dx, int64_t lddx, bool twice, int *status, cudaStream_t st)
 {
     PackArgs g{};
     g.target = target;
@@ -931,6 +1038,7 @@ int pack(const XentPlan &p, uint8_t *ws, const int32_t *target, const void *x, i
     g.dim = (int)dim;
     g.xp = reinterpret_cast<uint16_t *>(ws + p.xp);
     g.rows = p.rows;
+    g.twice = twice;
     g.map = reinterpret_cast<int32_t *>(ws + p.map);
     g.count = reinterpret_cast<int *>(ws + p.count);
     g.loss = loss;
@@ -959,7 +1067,7 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
     const void *xp = x;
     int64_t ldxp = ldx, xrows = tokens;
     if (packs(tokens)) {
-        if ((rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, loss, lse, nullptr, 0, status, st)) != FP8_OK) return rc;
+        if ((rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, loss, lse, nullptr, 0, false, status, st)) != FP8_OK) return rc;
         xp = ws + p.xp;
         ldxp = dim;
         xrows = p.rows;
@@ -973,8 +1081,9 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
              : tokens == 2 ? run_few<2>(x, ldx, w, ldw, target, tokens, vocab, dim, scale, a.part, p, status, st)
                            : run_few<4>(x, ldx, w, ldw, target, tokens, vocab, dim, scale, a.part, p, status, st);
     } else {
-        CUtensorMap mX, mW;
-        if (!map_k(&mX, xp, dim, xrows, ldxp) || !map_k(&mW, w, dim, vocab, ldw)) return FP8_ERR_CUDA;
+        Maps<XENT_LOSS> maps;
+        if (!map_k(&maps.m[0], xp, dim, xrows, ldxp) || !map_k(&maps.m[1], w, dim, vocab, ldw)) return FP8_ERR_CUDA;
+        maps.m[2] = maps.m[0];      // there is no matrix to write
         a.target = target;
         a.tokens = (int)tokens;
         a.vocab = a.vn = (int)vocab;
@@ -984,9 +1093,9 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.band = 16;
         a.scale = scale;
         a.status = status;
-        rc = !single(tokens) ? run<XENT_LOSS, true, 256, 0>(mX, mW, mX, a, st)
-             : p.bn == 256   ? run<XENT_LOSS, false, 256, 0>(mX, mW, mX, a, st)
-                             : run<XENT_LOSS, false, 128, 0>(mX, mW, mX, a, st);
+        rc = !single(tokens) ? run<XENT_LOSS, true, 256, 0>(maps, a, st)
+             : p.bn == 256   ? run<XENT_LOSS, false, 256, 0>(maps, a, st)
+                             : run<XENT_LOSS, false, 128, 0>(maps, a, st);
     }
     if (rc != FP8_OK) return rc;
     JoinArgs j{};
@@ -1016,7 +1125,7 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
 {
     const XentPlan p(tokens, vocab, dim, true);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    int rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, nullptr, nullptr, dx, lddx, status, st);
+    int rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, nullptr, nullptr, dx, lddx, single(tokens), status, st);
     if (rc != FP8_OK) return rc;
     XentArgs a{};
     a.count = reinterpret_cast<int *>(ws + p.count);
@@ -1035,33 +1144,33 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.dlse = dlse;
     a.status = status;
     void *xp = ws + p.xp, *g = ws + p.g, *acc = ws + p.acc;
-    const bool f32 = dw_dtype == FP8_OUT_F32;
-    CUtensorMap kX, kW, kG, mnW, mnG, mnX, outG, outX, outW;
-    if (!map_k(&kX, xp, dim, p.rows, dim) || !map_k(&kW, w, dim, vocab, ldw) || !map_k(&kG, g, p.piece, p.rows, p.piece) ||
-        !map_mn(&mnW, w, dim, vocab, ldw) || !map_mn(&mnG, g, p.piece, p.rows, p.piece) || !map_mn(&mnX, xp, dim, p.rows, dim) ||
-        !map_out(&outG, g, false, p.piece, p.rows, p.piece) || !map_out(&outX, acc, true, dim, p.splits * p.rows, dim) ||
-        !map_out(&outW, dw, f32, dim, vocab, lddw))
+    a.dw_f32 = dw_dtype == FP8_OUT_F32;
+    a.dw_add = accumulate;
+    Maps<XENT_GRAD> grad;
+    Maps<XENT_SUMS> sums;
+    if (!map_k(&grad.m[0], xp, dim, p.rows, dim) || !map_k(&grad.m[1], w, dim, vocab, ldw) ||
+        !map_out(&grad.m[2], g, false, p.piece, p.rows, p.piece) || !map_k(&sums.m[0], g, p.piece, p.rows, p.piece) ||
+        !map_mn(&sums.m[1], w, dim, vocab, ldw) || !map_out(&sums.m[2], acc, true, dim, p.splits * p.rows, dim) ||
+        !map_mn(&sums.m[3], g, p.piece, p.rows, p.piece) || !map_mn(&sums.m[4], xp, dim, p.rows, dim) ||
+        !map_out(&sums.m[5], dw, a.dw_f32, dim, vocab, lddw))
         return FP8_ERR_CUDA;
     for (int64_t v = 0; v < vocab; v += p.piece) {
         a.v0 = (int)v;
         a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
+        a.low = 0;
         a.band = 16;
-        rc = !single(tokens) ? run<XENT_GRAD, true, 256, 1>(kX, kW, outG, a, st)
-             : p.bn == 256   ? run<XENT_GRAD, false, 256, 2>(kX, kW, outG, a, st)
-                             : run<XENT_GRAD, false, 128, 1>(kX, kW, outG, a, st);
+        rc = !single(tokens) ? run<XENT_GRAD, true, 256, 1>(grad, a, st)
+             : p.bn == 256   ? run<XENT_GRAD, false, 256, 2>(grad, a, st)
+                             : run<XENT_GRAD, false, 128, 2>(grad, a, st);
         if (rc != FP8_OK) return rc;
+        a.low = single(tokens) ? kLow : 0;
         a.band = 8;
-        a.f32 = 1;
-        a.add = v > 0;
-        rc = single(tokens) ? run<XENT_DX, false, 256, 2>(kG, mnW, outX, a, st) : run<XENT_DX, true, 256, 1>(kG, mnW, outX, a, st);
-        if (rc != FP8_OK) return rc;
-        a.f32 = f32;
-        a.add = accumulate;
-        rc = tokens <= kShallow ? run<XENT_DW, true, 256, 2>(mnG, mnX, outW, a, st) : run<XENT_DW, true, 256, 1>(mnG, mnX, outW, a, st);
+        a.dx_add = v > 0;
+        rc = tokens <= kShallow ? run<XENT_SUMS, true, 256, 2>(sums, a, st) : run<XENT_SUMS, true, 256, 1>(sums, a, st);
         if (rc != FP8_OK) return rc;
     }
     const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + kSumThreads - 1) / kSumThreads, (int64_t)sm_count() * 16);
-    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), kSumThreads, 0, st, static_cast<const float *>(acc), p.splits, p.rows, a.count, a.map,
+    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), kSumThreads, 0, st, static_cast<const float *>(acc), p.splits, a.low, p.rows, a.count, a.map,
                             a.dim, static_cast<uint16_t *>(dx), lddx, a.tokens, status);
 }
 
