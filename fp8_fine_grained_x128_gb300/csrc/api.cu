@@ -718,6 +718,8 @@ static int xent_checks(int64_t tokens, int64_t vocab, int64_t dim, float scale)
     constexpr int64_t kMost = (int64_t)1 << 28;
     if (tokens < 0 || vocab < 0 || dim < 0 || dim % 8 != 0) return FP8_ERR_SHAPE;
     if (tokens >= kMost || vocab >= kMost || dim >= kMost) return FP8_ERR_SHAPE;
+    constexpr int64_t kTiles = (int64_t)1 << 46;    // 2^30 tiles of 256 x 256 in any of the products
+    if (tokens * vocab >= kTiles || tokens * dim >= kTiles || vocab * dim >= kTiles) return FP8_ERR_SHAPE;
     if (!(scale > 0.0f) || scale > 3.0e38f) return FP8_ERR_INVALID_ARG;
     return FP8_OK;
 }

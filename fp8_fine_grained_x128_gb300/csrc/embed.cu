@@ -581,7 +581,7 @@ struct EmbedLayout {    // byte offsets in the workspace
         int bits = 1;       // of the largest key, which is vocab itself
         while ((vocab >> bits) != 0) ++bits;
         passes = (bits + kDigitBits - 1) / kDigitBits;
-        piece = tokens <= kFewTokens ? 8 : 16;
+        piece = tokens <= kFewTokens ? 8 : 32;
         pieces = (int)((tokens + piece - 1) / piece);
         int64_t at = 0;
         auto take = [&](int64_t n) { const int64_t p = at; at += up16(n); return p; };

@@ -106,15 +106,15 @@ struct NormFwdArgs {
     int *status;
 };
 
-// Forward: a CTA's threads and rows: NT threads to one row, or 8 rows of a warp each.
+// A CTA's threads and rows: NT threads to one row, or 8 rows of a warp each.
 template <int NT> constexpr int norm_threads() { return NT == 32 ? 256 : NT; }
 template <int NT> constexpr int norm_rows() { return NT == 32 ? 8 : 1; }
-// Backward: CTAs an SM of its persistent grid (a row each), and most rows of its ring.
-template <int NT, int VPT> constexpr int norm_ctas() { return NT == 32 ? 16 : NT == 64 ? 12 : NT == 128 ? 6 : NT == 256 ? 3 : VPT == 2 ? 2 : 1; }
+// Backward: CTAs an SM of its persistent grid, and most rows of a ring.
+template <int NT, int VPT> constexpr int norm_ctas() { return NT == 512 ? (VPT == 2 ? 2 : 1) : VPT <= 2 ? 3 : 2; }
 constexpr int kNormStages = 4;
 
 template <int FMT, int NT, int VPT>
-__global__ void __launch_bounds__(norm_threads<NT>()) k_rmsnorm_fwd(NormFwdArgs g)
+__global__ void __launch_bounds__(norm_threads<NT>(), NT == 512 ? 2 : NT == 256 ? 5 : 1) k_rmsnorm_fwd(NormFwdArgs g)
 {
     __shared__ float part[32];
     dependents_launch();
@@ -196,10 +196,11 @@ __global__ void __launch_bounds__(norm_threads<NT>()) k_rmsnorm_fwd(NormFwdArgs 
 // ---------------------------------------------------------------------------
 // RMSNorm backward.  With n = h rstd (h the values the codes stand for),
 //   dh = (dy w - n mean(dy w n)) rstd (+ dsum),   dw = sum_rows dy n.
-// A persistent grid walks the rows.  A row's codes, dy and dsum are fetched by
-// bulk copies into a ring of up to 4 rows, so that the next rows are on their way
-// while the current one is reduced (rows prefetched into registers, one ahead,
-// kept half as many bytes in flight: 46 us at 8192 x 4096).  Every thread sees
+// A persistent grid walks the rows, NT threads one.  A row's codes, dy and dsum
+// are fetched by bulk copies into a ring of up to 4 rows (short rows: one for each
+// warp), so that the next rows are on their way while the current one is reduced
+// (rows prefetched into registers, one ahead, kept half as many bytes in flight:
+// 46 us at 8192 x 4096).  Every thread sees
 // the same columns of all its rows and sums their dw in registers; the CTAs' sums
 // go to the workspace and are added in a fixed order by k_column_sums.
 // ---------------------------------------------------------------------------
@@ -215,23 +216,27 @@ struct NormBwdArgs {
 };
 
 template <int FMT, int NT, int VPT>
-__global__ void __launch_bounds__(NT, norm_ctas<NT, VPT>()) k_rmsnorm_bwd(NormBwdArgs g)
+__global__ void __launch_bounds__(norm_threads<NT>(), norm_ctas<NT, VPT>()) k_rmsnorm_bwd(NormBwdArgs g)
 {
-    extern __shared__ __align__(128) uint8_t ring[];    // [stages][codes | dy | dsum]
-    __shared__ __align__(8) uint64_t full[kNormStages];
+    constexpr int kRows = norm_rows<NT>();
+    extern __shared__ __align__(128) uint8_t rings[];   // [rows of the CTA][stages][codes | dy | dsum]
+    __shared__ __align__(8) uint64_t bars[kRows][kNormStages];
     __shared__ float part[2][32];
     __shared__ int abort_flag;
-    const int t = threadIdx.x, nv = g.cols / 8, S = g.stages;
+    const int t = threadIdx.x % NT, sub = threadIdx.x / NT, nv = g.cols / 8, S = g.stages;
     const uint32_t bytes = (uint32_t)g.cols * (g.dsum ? 5 : 3);
-    if (t == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    uint8_t *ring = rings + (size_t)sub * S * bytes;
+    uint64_t *full = bars[sub];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRows; ++i)
+            for (int s = 0; s < S; ++s) mbar_init(&bars[i][s], 1);
         abort_flag = 0;
         fence_barrier_init();
     }
     __syncthreads();
     dependency_wait();
-    const int64_t row0 = blockIdx.x, step = gridDim.x;
-    auto fetch = [&](int64_t row, int s) {      // thread 0
+    const int64_t row0 = (int64_t)blockIdx.x * kRows + sub, step = (int64_t)gridDim.x * kRows;
+    auto fetch = [&](int64_t row, int s) {      // thread 0 of the row
         uint8_t *to = ring + (size_t)s * bytes;
         mbar_arrive_expect_tx(&full[s], bytes);
         bulk_load(to, g.c + row * g.cols, (uint32_t)g.cols, &full[s]);
@@ -315,19 +320,41 @@ __global__ void __launch_bounds__(NT, norm_ctas<NT, VPT>()) k_rmsnorm_bwd(NormBw
         }
     }
     dependents_launch();
+    if (abort_flag && t == 0)       // copies that were given up on land before the CTA leaves
+        for (int i = 0; i < S; ++i) mbar_wait_bounded(&full[i], i < s ? phase ^ 1 : phase, nullptr);
+    float a[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f2_unpack(acc[i][k], a[i][2 * k], a[i][2 * k + 1]);
+    if (NT == 32) {     // the CTA's 8 warps' sums, one after another, through the rings
+        float *sums = reinterpret_cast<float *>(rings);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = t + NT * i;
+            if (v >= nv) continue;
+            float4 *p = reinterpret_cast<float4 *>(sums + sub * g.cols + v * 8);
+            p[0] = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+            p[1] = make_float4(a[i][4], a[i][5], a[i][6], a[i][7]);
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < g.cols; c += 256) {
+            float x = sums[c];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) x += sums[w * g.cols + c];
+            if (dbg_cell(blockIdx.x, c, 1, gridDim.x, g.cols, g.status)) g.part[(int64_t)blockIdx.x * g.cols + c] = x;
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = t + NT * i;
         if (v >= nv || !dbg_cell(blockIdx.x, v * 8, 8, gridDim.x, g.cols, g.status)) continue;
-        float a[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f2_unpack(acc[i][k], a[2 * k], a[2 * k + 1]);
         float4 *p = reinterpret_cast<float4 *>(g.part + (int64_t)blockIdx.x * g.cols + v * 8);
-        p[0] = make_float4(a[0], a[1], a[2], a[3]);
-        p[1] = make_float4(a[4], a[5], a[6], a[7]);
+        p[0] = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+        p[1] = make_float4(a[i][4], a[i][5], a[i][6], a[i][7]);
     }
-    if (abort_flag && t == 0)       // copies that were given up on land before the CTA leaves
-        for (int i = 0; i < S; ++i) mbar_wait_bounded(&full[i], i < s ? phase ^ 1 : phase, nullptr);
 }
 
 // dw[c] (+)= sum over n rows of part[.][c]: 32 columns a CTA, its 32 warps
@@ -407,8 +434,9 @@ __global__ void __launch_bounds__(256, 4) k_swiglu_fwd_ckpt(const uint16_t *__re
 // ---------------------------------------------------------------------------
 // SwiGLU backward from gu's codes: dgate = dh u sig (1 + g (1 - sig)), dup =
 // dh g sig.  A warp takes 512 columns of one row (16 a lane, 16-byte loads of
-// codes); a CTA takes 8 rows of them, whose scales, 4 bytes apart, share the
-// sectors that a warp alone would read an eighth of.
+// codes); a CTA's 8 warps take as much of one row as it has, then further rows
+// (8192 x 14336: 151 us, 6.28 TB/s; with 8 rows of 512 columns each, whose scales
+// would share sectors, 156 us).
 // ---------------------------------------------------------------------------
 template <bool LEFT>
 __device__ __forceinline__ void swiglu_grad8_f32(const float (&g)[8], const float (&u)[8], const float (&d)[8], uint4 &dg, uint4 &du)
@@ -422,12 +450,14 @@ __device__ __forceinline__ void swiglu_grad8_f32(const float (&g)[8], const floa
 
 template <int FMT>
 __global__ void __launch_bounds__(256) k_swiglu_bwd_ckpt(const uint8_t *__restrict__ c, const float *__restrict__ cs,
-                                                      const uint16_t *__restrict__ dh, int64_t rows, int64_t F, uint16_t *__restrict__ dgu, int *status)
+                                                      const uint16_t *__restrict__ dh, int64_t rows, int64_t F, int log_rows,
+                                                      uint16_t *__restrict__ dgu, int *status)
 {
     dependents_launch();
     dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), j = (int64_t)blockIdx.y * 512 + lane * 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t r = ((int64_t)blockIdx.x << log_rows) + (warp & ((1 << log_rows) - 1));
+    const int64_t j = (((int64_t)blockIdx.y << (3 - log_rows)) + (warp >> log_rows)) * 512 + lane * 16;
     if (r >= rows || j >= F) return;
     const uint8_t *src = c + r * 2 * F + j;
     const uint4 qg = ldg_stream(src), qu = ldg_stream(src + F);
@@ -458,14 +488,16 @@ __global__ void __launch_bounds__(256) k_swiglu_bwd_ckpt(const uint8_t *__restri
 namespace {
 
 // Calls f(NT, VPT) as compile-time numbers for rows of `cols` columns (up to
-// kNormMaxCols).
+// kNormMaxCols).  Rows of 513 to 1024 columns: a warp each where they come in
+// order through a ring, 128 threads each where a CTA has one row and no more
+// (8192 x 1024 forward: 14.8 us, a warp each 18.1).
 template <int N> struct Int { static constexpr int v = N; };
-template <typename F>
+template <bool RING, typename F>
 int norm_shape(int64_t cols, F &&f)
 {
     if (cols <= 256) return f(Int<32>{}, Int<1>{});
-    if (cols <= 512) return f(Int<64>{}, Int<1>{});
-    if (cols <= 1024) return f(Int<128>{}, Int<1>{});
+    if (cols <= 512) return f(Int<32>{}, Int<2>{});
+    if (cols <= 1024) return f(Int<RING ? 32 : 128>{}, Int<RING ? 4 : 1>{});
     if (cols <= 2048) return f(Int<256>{}, Int<1>{});
     if (cols <= 4096) return f(Int<256>{}, Int<2>{});
     if (cols <= 8192) return f(Int<512>{}, Int<2>{});
@@ -475,7 +507,7 @@ int norm_shape(int64_t cols, F &&f)
 template <int FMT>
 int norm_fwd(const NormFwdArgs &g, cudaStream_t st)
 {
-    return norm_shape(g.cols, [&](auto nt, auto vpt) {
+    return norm_shape<false>(g.cols, [&](auto nt, auto vpt) {
         constexpr int NT = decltype(nt)::v, VPT = decltype(vpt)::v;
         const int64_t blocks = (g.rows + norm_rows<NT>() - 1) / norm_rows<NT>();
         return launch_dependent(k_rmsnorm_fwd<FMT, NT, VPT>, dim3((unsigned)blocks), norm_threads<NT>(), 0, st, g);
@@ -485,11 +517,13 @@ int norm_fwd(const NormFwdArgs &g, cudaStream_t st)
 template <int FMT>
 int norm_bwd(NormBwdArgs &g, float *dw, int accumulate, cudaStream_t st)
 {
-    return norm_shape(g.cols, [&](auto nt, auto vpt) {
+    return norm_shape<true>(g.cols, [&](auto nt, auto vpt) {
         constexpr int NT = decltype(nt)::v, VPT = decltype(vpt)::v, kCtas = norm_ctas<NT, VPT>();
         constexpr int kRing = 220 * 1024 / kCtas - 2048;    // an SM's shared memory, shared by its CTAs
-        const int row = g.cols * (g.dsum ? 5 : 3);
+        constexpr int kRows = norm_rows<NT>();
+        const int row = g.cols * (g.dsum ? 5 : 3) * kRows;
         g.stages = std::min(kNormStages, kRing / row);
+        const size_t smem = std::max<size_t>((size_t)g.stages * row, NT == 32 ? (size_t)g.cols * kRows * sizeof(float) : 0);
         static bool attr_done[64] = {};
         int dev = 0;
         cudaGetDevice(&dev);
@@ -498,8 +532,8 @@ int norm_bwd(NormBwdArgs &g, float *dw, int accumulate, cudaStream_t st)
                 return (int)FP8_ERR_CUDA;
             attr_done[dev & 63] = true;
         }
-        const int64_t grid = std::min<int64_t>(g.rows, (int64_t)sm_count() * kCtas);
-        const int rc = launch_dependent(k_rmsnorm_bwd<FMT, NT, VPT>, dim3((unsigned)grid), NT, (size_t)g.stages * row, st, g);
+        const int64_t grid = std::min<int64_t>((g.rows + kRows - 1) / kRows, (int64_t)sm_count() * kCtas);
+        const int rc = launch_dependent(k_rmsnorm_bwd<FMT, NT, VPT>, dim3((unsigned)grid), norm_threads<NT>(), smem, st, g);
         if (rc != FP8_OK) return rc;
         return launch_dependent(k_column_sums, dim3((unsigned)(g.cols / 32)), 1024, 0, st, static_cast<const float *>(g.part), (int)grid, g.cols,
                                 dw, accumulate, g.status);
@@ -534,7 +568,7 @@ int launch_rmsnorm_fwd_ckpt(const void *x, int64_t rows, int64_t cols, int64_t l
 
 size_t rmsnorm_workspace_bytes(int64_t cols)
 {
-    const int ctas = norm_shape(cols, [](auto nt, auto vpt) { return norm_ctas<decltype(nt)::v, decltype(vpt)::v>(); });
+    const int ctas = norm_shape<true>(cols, [](auto nt, auto vpt) { return norm_ctas<decltype(nt)::v, decltype(vpt)::v>(); });
     return (size_t)sm_count() * ctas * (size_t)cols * sizeof(float);
 }
 
@@ -576,9 +610,13 @@ int launch_swiglu_fwd_ckpt(const void *gu, int64_t rows, int64_t F, int fmt, voi
 int launch_swiglu_bwd_ckpt(const void *c, const float *cs, const void *dh, int64_t rows, int64_t F, int fmt, void *dgu, int *status,
                            cudaStream_t st)
 {
+    int log_rows = 3;       // rows of a CTA; it takes 4096 columns over them
+    while (log_rows > 0 && F > (int64_t)512 << (3 - log_rows)) --log_rows;
+    const int64_t cols = (int64_t)512 << (3 - log_rows);
     return launch_dependent(fmt == FP8_E5M2 ? k_swiglu_bwd_ckpt<FP8_E5M2> : k_swiglu_bwd_ckpt<FP8_E4M3>,
-                            dim3((unsigned)((rows + 7) / 8), (unsigned)((F + 511) / 512)), 256, 0, st, static_cast<const uint8_t *>(c), cs,
-                            static_cast<const uint16_t *>(dh), rows, F, static_cast<uint16_t *>(dgu), status);
+                            dim3((unsigned)((rows + (1 << log_rows) - 1) >> log_rows), (unsigned)((F + cols - 1) / cols)), 256, 0, st,
+                            static_cast<const uint8_t *>(c), cs, static_cast<const uint16_t *>(dh), rows, F, log_rows,
+                            static_cast<uint16_t *>(dgu), status);
 }
 
 }  // namespace fp8fg

@@ -917,8 +917,9 @@ namespace {
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// A single tile of rows saves nothing by packing them.
-bool packs(int64_t tokens) { return tokens > kTile; }
+// Whether the forward packs its rows first: not where the whole product lasts
+// about as long as the packing kernel (5 us), or all rows fit one tile.
+bool packs(int64_t tokens, int64_t vocab, int64_t dim) { return tokens > kTile && tokens * vocab * dim > (int64_t)10000000000; }
 
 // Up to 128 tokens, one CTA's tiles hold them all, and a pair's would be half
 // empty: W streams past at 128 x BN tiles by single CTAs (64 x 128000 x 4096:
@@ -953,7 +954,7 @@ struct XentPlan {
         auto take = [&](int64_t n) { const int64_t p = at; at += up(n, 256); return p; };
         count = take(16);
         map = take(rows * 4);
-        xp = backward || packs(tokens) ? take(rows * dim * 2) : 0;
+        xp = backward || packs(tokens, vocab, dim) ? take(rows * dim * 2) : 0;
         if (!backward) {
             // long units write less; 16 of them a group keep the groups' shares even
             per_unit = 8;
@@ -1066,7 +1067,7 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
     int rc;
     const void *xp = x;
     int64_t ldxp = ldx, xrows = tokens;
-    if (packs(tokens)) {
+    if (packs(tokens, vocab, dim)) {
         if ((rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, loss, lse, nullptr, 0, false, status, st)) != FP8_OK) return rc;
         xp = ws + p.xp;
         ldxp = dim;

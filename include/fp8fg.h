@@ -602,8 +602,8 @@ FP8FG_API int fp8_swiglu_bwd_quant(const void *gu, const void *dh, int64_t rows,
  *   rstd = (sum_c h^2 / cols + eps)^(-1/2),  y = RN_bf16(h * rstd * w)
  * in FP32, and c, cs = the quantization of h.
  *   x, res, y, sum: BF16 [rows][ld...]; res and sum both NULL or both set.
- *   sum may be x or res, and y any of them (each element is read before it is
- *   written).  w: BF16 [cols].  rstd: FP32 [rows].
+ *   sum may be x or res, and so may y where sum is not (each element is read
+ *   before it is written).  w: BF16 [cols].  rstd: FP32 [rows].
  *   cols % 128 == 0, cols <= 16384, eps > 0; BF16 pointers and c 16-byte
  *   aligned, leading dimensions >= cols and multiples of 8.
  * A chunk of h holding Inf/NaN records FP8_ERR_NONFINITE (its codes are
@@ -678,7 +678,8 @@ FP8FG_API size_t fp8_linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, 
  * Products of BF16 values summed in FP32; loss is formed without the cancellation
  * that this difference has when the target carries the sum.
  *   x: BF16 [tokens][ldx], w: BF16 [vocab][ldw], dim % 8 == 0, 16-byte aligned,
- *   leading dimensions >= dim and multiples of 8; tokens, vocab, dim < 2^28.
+ *   leading dimensions >= dim and multiples of 8; tokens, vocab, dim < 2^28, the
+ *   product of any two < 2^46.
  *   target: DEVICE int32[tokens].  A token with a negative target does not count:
  *   loss = lse = 0, whatever its row of x holds.  One >= vocab records
  *   FP8_ERR_INVALID_ARG and does not count either.
@@ -699,7 +700,8 @@ FP8FG_API int fp8_linear_xent_fwd(const void *x, int64_t tokens, int64_t dim, in
  * element (operands and results below 2^-126 count as zero there); else every row
  * is written.  Tokens that do not count get dx = 0 and add nothing to dw, whatever
  * their rows of x, dloss and dlse hold.
- * dx [tokens][lddx], dw [vocab][lddw]: 16-byte aligned rows of at least dim.
+ * dx [tokens][lddx], dw [vocab][lddw]: 16-byte aligned rows of at least dim.  dx
+ * may be x.
  * The results are the same in every run. */
 FP8FG_API int fp8_linear_xent_bwd(const void *x, int64_t tokens, int64_t dim, int64_t ldx, const void *w,
                                   int64_t vocab, int64_t ldw, const int32_t *target, float scale, const float *loss,

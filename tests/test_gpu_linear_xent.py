@@ -60,7 +60,7 @@ def forward(x, w, t, scale=1.0, ws=None):
 
 
 SIZES = [(1, 1, 8), (1, 257, 64), (2, 7, 8), (3, 5003, 72), (127, 256, 128), (128, 255, 200), (129, 1000, 64), (255, 513, 136),
-         (256, 256, 256), (257, 1025, 64), (300, 2000, 512), (513, 300, 1024), (1000, 9001, 320), (5, 40000, 1024), (4, 10007, 1032), (2, 31, 4096), (1, 70001, 8)]
+         (256, 256, 256), (257, 1025, 64), (300, 2000, 512), (513, 300, 1024), (1000, 9001, 320), (5, 40000, 1024), (4, 10007, 1032), (2, 31, 4096), (1, 70001, 8), (4, 300, 8192), (70, 400, 6152)]
 
 
 @pytest.mark.parametrize("T,V,D", SIZES)
@@ -287,6 +287,18 @@ def test_runs_repeat_and_graphs_replay():
     step()
     assert all(torch.equal(a, b) for a, b in zip(got, (loss, lse, dx, dw)))
     assert fg.device_status() == fg.OK
+
+
+def test_gradient_in_place():
+    """dx may be x: every row of it has been copied before any is written."""
+    for T in (100, 700):
+        x, w, t = make(T, 1000, 128, 0.3, seed=16)
+        dl = torch.rand(T, device="cuda")
+        loss, lse = forward(x, w, t)
+        dx, dw = backward(x, w, t, loss, lse, dl, None)
+        ws, again = fg.new_linear_xent_workspace(T, 1000, 128), torch.empty_like(w)
+        fg.linear_xent_bwd(x, w, t, loss, lse, dl, x, again, ws)
+        assert torch.equal(x, dx) and torch.equal(again, dw) and fg.device_status() == fg.OK
 
 
 def test_on_another_stream():

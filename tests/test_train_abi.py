@@ -93,7 +93,7 @@ def xent(lib, back, x=P, T=4, D=64, ldx=64, w=P, V=10, ldw=64, t=P, scale=1.0, l
 
 
 @pytest.mark.parametrize("bad,status", [
-    ({"D": 63}, fg.ERR_SHAPE), ({"T": -1}, fg.ERR_SHAPE), ({"V": 0}, fg.ERR_SHAPE), ({"D": 0}, fg.ERR_SHAPE), ({"T": 1 << 28}, fg.ERR_SHAPE),
+    ({"D": 63}, fg.ERR_SHAPE), ({"T": -1}, fg.ERR_SHAPE), ({"V": 0}, fg.ERR_SHAPE), ({"D": 0}, fg.ERR_SHAPE), ({"T": 1 << 28}, fg.ERR_SHAPE), ({"T": 1 << 24, "V": 1 << 22}, fg.ERR_SHAPE),
     ({"scale": 0.0}, fg.ERR_INVALID_ARG), ({"scale": -1.0}, fg.ERR_INVALID_ARG), ({"scale": float("inf")}, fg.ERR_INVALID_ARG),
     ({"x": None}, fg.ERR_INVALID_ARG), ({"w": P + 2}, fg.ERR_ALIGNMENT), ({"ldx": 56}, fg.ERR_SHAPE), ({"ldw": 65}, fg.ERR_ALIGNMENT),
     ({"t": None}, fg.ERR_INVALID_ARG), ({"t": P + 1}, fg.ERR_ALIGNMENT), ({"loss": None}, fg.ERR_INVALID_ARG), ({"lse": P + 2}, fg.ERR_ALIGNMENT),
