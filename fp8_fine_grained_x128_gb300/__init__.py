@@ -203,11 +203,11 @@ def _on_device(t, name, dtypes):
         raise TypeError(f"{name}: dtype {t.dtype}, expected one of {tuple(str(d) for d in dtypes)}")
 
 
-def _buf(t, name, dtypes, numel, optional=False):
+def _buf(t, name, dtypes, numel, optional=False, dev=None):
     """Device pointer of an array the library reads or writes as `numel`
-    contiguous elements."""
-    if t.__class__ is _Tensor and -1 != t.get_device() == _cuda_device() and t.dtype in dtypes and t.is_contiguous() and \
-            t.numel() >= numel:
+    contiguous elements (dev: the current device, where the caller has looked)."""
+    if t.__class__ is _Tensor and -1 != t.get_device() == (_cuda_device() if dev is None else dev) and \
+            t.dtype in dtypes and t.is_contiguous() and t.numel() >= numel:
         return t.data_ptr()
     if t is None:
         if optional:
@@ -223,9 +223,10 @@ def _buf(t, name, dtypes, numel, optional=False):
     return t.data_ptr()
 
 
-def _mat(t, name, dtypes):
+def _mat(t, name, dtypes, dev=None):
     """(pointer, rows, cols, leading dimension) of a row-major 2-D view."""
-    _on_device(t, name, dtypes)
+    if t.__class__ is not _Tensor or dev is None or t.get_device() != dev or t.dtype not in dtypes:
+        _on_device(t, name, dtypes)
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: expected a 2-D tensor, got shape {tuple(shape)}")
@@ -257,10 +258,10 @@ def _gran_scales(gran, rows, cols):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, dev=None):
     if stream is None:
         if _raw_stream is not None:   # without the Stream object: 0.1 instead of 3 us a call
-            return _raw_stream(_cuda_device())
+            return _raw_stream(_cuda_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -776,18 +777,25 @@ def swiglu_bwd_quant(gu, dh, fmt, q, s, qT, sT, stream=None):
 
 # ------------------------------------------------------------------ activations kept in 8 bits
 
-def _like(t, name, dtypes, R, C, optional=False):
+def _like(t, name, dtypes, R, C, dev, optional=False):
     """(pointer, leading dimension) of a row-major [R, C] matrix."""
     if t is None and optional:
         return None, 0
-    p, r, c, ld = _mat(t, name, dtypes)
-    if (r, c) != (R, C):
+    p, r, c, ld = _mat(t, name, dtypes, dev)
+    if r != R or c != C:
         raise ValueError(f"{name}: shape {(r, c)}, expected {(R, C)}")
     return p, ld
 
 
-def _workspace(t, n):
-    return _buf(t, "workspace", (torch.uint8,), n)
+_U8 = (torch.uint8,)
+
+
+def _current():
+    """The current device, looked up once a call; None without a GPU (the checks of the tensors then say so)."""
+    try:
+        return _cuda_device()
+    except RuntimeError:
+        return None
 
 
 def _new_bytes(n, device):
@@ -797,49 +805,61 @@ def _new_bytes(n, device):
 def rmsnorm_fwd_ckpt(x, w, eps, fmt, y, c, cs, rstd, res=None, sum=None, stream=None):
     """``y`` <- RMSNorm of ``x`` (or of ``sum`` <- x + ``res``) with weight ``w`` [C]; its input is kept as codes ``c``
     [R, C] and scales ``cs`` [C/128, R] for rmsnorm_bwd_ckpt, with ``rstd`` [R]."""
-    L = lib()
-    px, R, C, ldx = _mat(x, "x", _BF16)
-    if (res is None) != (sum is None):
-        raise ValueError("res, sum: give both or neither")
-    (pr, ldr), (ps, lds) = _like(res, "res", _BF16, R, C, True), _like(sum, "sum", _BF16, R, C, True)
-    py, ldy = _like(y, "y", _BF16, R, C)
-    _check("fp8_rmsnorm_fwd_ckpt", L.fp8_rmsnorm_fwd_ckpt(
-        px, R, C, ldx, pr, ldr, _buf(w, "w", _BF16, C), eps, fmt, py, ldy, ps, lds, _buf(c, "c", _CODES, R * C),
-        _buf(cs, "cs", _F32, (C // 128) * R), _buf(rstd, "rstd", _F32, R), _stream(stream)))
+    L, dev = lib(), _current()
+    px, R, C, ldx = _mat(x, "x", _BF16, dev)
+    pr = ps = None
+    ldr = lds = 0
+    if res is not None or sum is not None:
+        if res is None or sum is None:
+            raise ValueError("res, sum: give both or neither")
+        (pr, ldr), (ps, lds) = _like(res, "res", _BF16, R, C, dev), _like(sum, "sum", _BF16, R, C, dev)
+    py, ldy = _like(y, "y", _BF16, R, C, dev)
+    rc = L.fp8_rmsnorm_fwd_ckpt(
+        px, R, C, ldx, pr, ldr, _buf(w, "w", _BF16, C, False, dev), eps, fmt, py, ldy, ps, lds,
+        _buf(c, "c", _CODES, R * C, False, dev), _buf(cs, "cs", _F32, (C // 128) * R, False, dev),
+        _buf(rstd, "rstd", _F32, R, False, dev), _stream(stream, dev))
+    _check("fp8_rmsnorm_fwd_ckpt", rc)
 
 
 def new_rmsnorm_workspace(cols, device="cuda") -> torch.Tensor:
     """A workspace of rmsnorm_bwd_ckpt for rows of ``cols`` columns (any number of rows)."""
-    return _new_bytes(_sized("fp8_rmsnorm_workspace_bytes", int(cols)), device)
+    return _new_bytes(_sized("fp8_rmsnorm_workspace_bytes", None, int(cols)), device)
 
 
 def rmsnorm_bwd_ckpt(c, cs, rstd, w, dy, fmt, dx, dw, workspace, dsum=None, accumulate=False, stream=None):
     """``dx`` [R, C] <- gradient of rmsnorm_fwd_ckpt's input from its codes (plus ``dsum``, the gradient that reaches the
     sum by other ways); ``dw`` [C] FP32 <- (or, accumulate, +=) the weight's."""
-    L = lib()
-    pdy, R, C, lddy = _mat(dy, "dy", _BF16)
-    (pds, ldds), (pdx, lddx) = _like(dsum, "dsum", _BF16, R, C, True), _like(dx, "dx", _BF16, R, C)
-    _check("fp8_rmsnorm_bwd_ckpt", L.fp8_rmsnorm_bwd_ckpt(
-        _buf(c, "c", _CODES, R * C), _buf(cs, "cs", _F32, (C // 128) * R), _buf(rstd, "rstd", _F32, R), fmt, R, C,
-        _buf(w, "w", _BF16, C), pdy, lddy, pds, ldds, pdx, lddx, _buf(dw, "dw", _F32, C), int(accumulate),
-        _workspace(workspace, _sized("fp8_rmsnorm_workspace_bytes", C)), _stream(stream)))
+    L, dev = lib(), _current()
+    pdy, R, C, lddy = _mat(dy, "dy", _BF16, dev)
+    (pds, ldds), (pdx, lddx) = _like(dsum, "dsum", _BF16, R, C, dev, True), _like(dx, "dx", _BF16, R, C, dev)
+    rc = L.fp8_rmsnorm_bwd_ckpt(
+        _buf(c, "c", _CODES, R * C, False, dev), _buf(cs, "cs", _F32, (C // 128) * R, False, dev),
+        _buf(rstd, "rstd", _F32, R, False, dev), fmt, R, C, _buf(w, "w", _BF16, C, False, dev), pdy, lddy, pds, ldds, pdx,
+        lddx, _buf(dw, "dw", _F32, C, False, dev), accumulate,
+        _buf(workspace, "workspace", _U8, _sized("fp8_rmsnorm_workspace_bytes", dev, C), False, dev), _stream(stream, dev))
+    _check("fp8_rmsnorm_bwd_ckpt", rc)
 
 
 def swiglu_fwd_ckpt(gu, fmt, h, c, cs, stream=None):
     """swiglu_fwd that also keeps ``gu`` [R, 2F] as codes ``c`` [R, 2F] and scales ``cs`` [2F/128, R]."""
-    L = lib()
-    pg, R, F = _gu(gu)
-    args = (_buf(h, "h", _BF16, R * F), _buf(c, "c", _CODES, R * 2 * F), _buf(cs, "cs", _F32, (2 * F // 128) * R))
-    _check("fp8_swiglu_fwd_ckpt", L.fp8_swiglu_fwd_ckpt(pg, R, F, fmt, *args, _stream(stream)))
+    L, dev = lib(), _current()
+    R, F2 = _shape(gu, "gu", 2)
+    n = R * F2
+    rc = L.fp8_swiglu_fwd_ckpt(_buf(gu, "gu", _BF16, n, False, dev), R, F2 // 2, fmt, _buf(h, "h", _BF16, n // 2, False, dev),
+                               _buf(c, "c", _CODES, n, False, dev), _buf(cs, "cs", _F32, (F2 // 128) * R, False, dev),
+                               _stream(stream, dev))
+    _check("fp8_swiglu_fwd_ckpt", rc)
 
 
 def swiglu_bwd_ckpt(c, cs, dh, fmt, dgu, stream=None):
     """``dgu`` [R, 2F] <- gradient of swiglu_fwd_ckpt from the codes it kept and ``dh`` [R, F]."""
-    L = lib()
+    L, dev = lib(), _current()
     R, F = _shape(dh, "dh", 2)
-    args = (_buf(c, "c", _CODES, R * 2 * F), _buf(cs, "cs", _F32, (2 * F // 128) * R), _buf(dh, "dh", _BF16, R * F))
-    _check("fp8_swiglu_bwd_ckpt", L.fp8_swiglu_bwd_ckpt(*args, R, F, fmt, _buf(dgu, "dgu", _BF16, R * 2 * F),
-                                                        _stream(stream)))
+    n = R * F
+    rc = L.fp8_swiglu_bwd_ckpt(_buf(c, "c", _CODES, 2 * n, False, dev), _buf(cs, "cs", _F32, (2 * F // 128) * R, False, dev),
+                               _buf(dh, "dh", _BF16, n, False, dev), R, F, fmt, _buf(dgu, "dgu", _BF16, 2 * n, False, dev),
+                               _stream(stream, dev))
+    _check("fp8_swiglu_bwd_ckpt", rc)
 
 
 # ------------------------------------------------------------------ the two ends of a step
@@ -847,79 +867,82 @@ def swiglu_bwd_ckpt(c, cs, dh, fmt, dgu, stream=None):
 _sizes = {}
 
 
-def _sized(name, *args):
-    """A workspace size of the library on the current device, looked up once."""
-    key = (name, _cuda_device(), *args)
-    if key not in _sizes:
+def _sized(name, dev, *args):
+    """A workspace size of the library on the current device (dev, where the caller has looked), looked up once."""
+    key = (name, _cuda_device() if dev is None else dev, args)
+    n = _sizes.get(key)
+    if n is None:
         if len(_sizes) >= 4096:     # a program of many lengths
             _sizes.clear()
-        _sizes[key] = int(getattr(lib(), name)(*args))
-    return _sizes[key]
+        n = _sizes[key] = int(getattr(lib(), name)(*args))
+    return n
 
 
 def embedding_fwd(ids, w, out, scale=1.0, stream=None):
     """``out`` [T, D] <- scale * ``w`` [V, D] at ``ids`` [T] int32; a negative id is padding (zeros)."""
-    L = lib()
-    pw, V, D, ldw = _mat(w, "w", _BF16)
+    L, dev = lib(), _current()
+    pw, V, D, ldw = _mat(w, "w", _BF16, dev)
     T, = _shape(ids, "ids", 1)
-    po, ldo = _like(out, "out", _BF16, T, D)
-    _check("fp8_embedding_fwd", L.fp8_embedding_fwd(_buf(ids, "ids", _I32, T), T, pw, V, D, ldw, scale, po, ldo,
-                                                    _stream(stream)))
+    po, ldo = _like(out, "out", _BF16, T, D, dev)
+    rc = L.fp8_embedding_fwd(_buf(ids, "ids", _I32, T, False, dev), T, pw, V, D, ldw, scale, po, ldo, _stream(stream, dev))
+    _check("fp8_embedding_fwd", rc)
 
 
 def new_embedding_workspace(tokens, vocab, dim, device="cuda") -> torch.Tensor:
     """A workspace of embedding_bwd for calls of up to these sizes."""
-    return _new_bytes(_sized("fp8_embedding_workspace_bytes", int(tokens), int(vocab), int(dim)), device)
+    return _new_bytes(_sized("fp8_embedding_workspace_bytes", None, int(tokens), int(vocab), int(dim)), device)
 
 
 def embedding_bwd(ids, dout, dw, workspace, scale=1.0, accumulate=False, stream=None):
     """``dw`` [V, D] (FP32 or BF16) <- scale * the sums of ``dout`` [T, D] over the tokens of each id, zeros where there
     are none; accumulate (FP32): added to dw."""
-    L = lib()
-    pd, T, D, ldd = _mat(dout, "dout", _BF16)
-    pw, V, Dw, ldw = _mat(dw, "dw", _OUT)
+    L, dev = lib(), _current()
+    pd, T, D, ldd = _mat(dout, "dout", _BF16, dev)
+    pw, V, Dw, ldw = _mat(dw, "dw", _OUT, dev)
     if Dw != D:
         raise ValueError(f"dw: shape {(V, Dw)}, expected [vocab][{D}]")
-    ws = _workspace(workspace, _sized("fp8_embedding_workspace_bytes", T, V, D))
-    _check("fp8_embedding_bwd", L.fp8_embedding_bwd(_buf(ids, "ids", _I32, T), T, pd, ldd, V, D, scale, pw,
-                                                    OUT_F32 if dw.dtype == torch.float32 else OUT_BF16, ldw,
-                                                    int(accumulate), ws, _stream(stream)))
+    ws = _buf(workspace, "workspace", _U8, _sized("fp8_embedding_workspace_bytes", dev, T, V, D), False, dev)
+    rc = L.fp8_embedding_bwd(_buf(ids, "ids", _I32, T, False, dev), T, pd, ldd, V, D, scale, pw,
+                             OUT_F32 if dw.dtype == torch.float32 else OUT_BF16, ldw, accumulate, ws, _stream(stream, dev))
+    _check("fp8_embedding_bwd", rc)
 
 
 def new_linear_xent_workspace(tokens, vocab, dim, backward=True, device="cuda") -> torch.Tensor:
     """A workspace for calls of linear_xent_fwd and (backward) linear_xent_bwd of these sizes."""
     sizes = int(tokens), int(vocab), int(dim)
-    n = max(_sized("fp8_linear_xent_workspace_bytes", *sizes, b) for b in range(2 if backward else 1))
+    n = max(_sized("fp8_linear_xent_workspace_bytes", None, *sizes, b) for b in range(2 if backward else 1))
     return _new_bytes(n, device)
 
 
-def _xent(x, w, target, loss, lse, workspace, backward):
-    px, T, D, ldx = _mat(x, "x", _BF16)
-    pw, V, Dw, ldw = _mat(w, "w", _BF16)
+def _xent(x, w, target, loss, lse, workspace, backward, dev):
+    px, T, D, ldx = _mat(x, "x", _BF16, dev)
+    pw, V, Dw, ldw = _mat(w, "w", _BF16, dev)
     if Dw != D:
         raise ValueError(f"w: shape {(V, Dw)}, expected [vocab][{D}]")
-    args = (px, T, D, ldx, pw, V, ldw, _buf(target, "target", _I32, T))
-    pl, pz = _buf(loss, "loss", _F32, T), _buf(lse, "lse", _F32, T)
-    return args, pl, pz, _workspace(workspace, _sized("fp8_linear_xent_workspace_bytes", T, V, D, backward))
+    return (px, T, D, ldx, pw, V, ldw, _buf(target, "target", _I32, T, False, dev),
+            _buf(loss, "loss", _F32, T, False, dev), _buf(lse, "lse", _F32, T, False, dev),
+            _buf(workspace, "workspace", _U8, _sized("fp8_linear_xent_workspace_bytes", dev, T, V, D, backward), False, dev))
 
 
 def linear_xent_fwd(x, w, target, loss, lse, workspace, scale=1.0, stream=None):
     """``loss`` and ``lse`` [T] FP32 <- softmax cross entropy of the logits scale * ``x`` [T, D] . ``w`` [V, D]^T with
     ``target`` [T] int32, and the logarithm of their sum of exponentials; a negative target does not count (0)."""
-    L = lib()
-    args, pl, pz, ws = _xent(x, w, target, loss, lse, workspace, 0)
-    _check("fp8_linear_xent_fwd", L.fp8_linear_xent_fwd(*args, scale, pl, pz, ws, _stream(stream)))
+    L, dev = lib(), _current()
+    px, T, D, ldx, pw, V, ldw, pt, pl, pz, ws = _xent(x, w, target, loss, lse, workspace, 0, dev)
+    rc = L.fp8_linear_xent_fwd(px, T, D, ldx, pw, V, ldw, pt, scale, pl, pz, ws, _stream(stream, dev))
+    _check("fp8_linear_xent_fwd", rc)
 
 
 def linear_xent_bwd(x, w, target, loss, lse, dloss, dx, dw, workspace, dlse=None, scale=1.0, accumulate=False,
                     stream=None):
     """``dx`` [T, D] BF16 and ``dw`` [V, D] (BF16, or FP32, then also added to: accumulate) <- gradients of
     linear_xent_fwd for those of its outputs, ``dloss`` and ``dlse`` [T]."""
-    L = lib()
-    args, pl, pz, ws = _xent(x, w, target, loss, lse, workspace, 1)
-    T, D, V = args[1], args[2], args[5]
-    pdx, lddx = _like(dx, "dx", _BF16, T, D)
-    pdw, lddw = _like(dw, "dw", _OUT, V, D)
-    _check("fp8_linear_xent_bwd", L.fp8_linear_xent_bwd(
-        *args, scale, pl, pz, _buf(dloss, "dloss", _F32, T), _buf(dlse, "dlse", _F32, T, True), pdx, lddx, pdw,
-        OUT_F32 if dw.dtype == torch.float32 else OUT_BF16, lddw, int(accumulate), ws, _stream(stream)))
+    L, dev = lib(), _current()
+    px, T, D, ldx, pw, V, ldw, pt, pl, pz, ws = _xent(x, w, target, loss, lse, workspace, 1, dev)
+    pdx, lddx = _like(dx, "dx", _BF16, T, D, dev)
+    pdw, lddw = _like(dw, "dw", _OUT, V, D, dev)
+    rc = L.fp8_linear_xent_bwd(
+        px, T, D, ldx, pw, V, ldw, pt, scale, pl, pz, _buf(dloss, "dloss", _F32, T, False, dev),
+        _buf(dlse, "dlse", _F32, T, True, dev), pdx, lddx, pdw, OUT_F32 if dw.dtype == torch.float32 else OUT_BF16, lddw,
+        accumulate, ws, _stream(stream, dev))
+    _check("fp8_linear_xent_bwd", rc)
