@@ -55,18 +55,28 @@ __global__ void __launch_bounds__(256) k_embedding_fwd(const int32_t *__restrict
 __device__ __forceinline__ int sort_key(int32_t id, int vocab) { return id < 0 || id >= vocab ? vocab : id; }
 
 // Both sorts are stable radix sorts by digits of 9 bits.  A warp ranks 32 * K
-// consecutive keys, 32 at a time: lanes of equal digits find one another by a
-// match, and the warp's counter of that digit holds how many came before.
+// consecutive keys, 32 at a time: lanes of equal digits find one another by ballots
+// of the digits' bits (many keys; the sort of 32768: 20 -> 17 us) or a match (two
+// a thread), and the warp's counter of that digit holds how many came before.
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 
-template <int K, typename N>
+template <int K, bool BALLOTS, typename N>
 __device__ __forceinline__ void rank_keys(const int (&key)[K], int shift, N *counter, int (&rank)[K])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int d = key[k] < 0 ? kDigits : (key[k] >> shift) & (kDigits - 1);
-        const unsigned same = __match_any_sync(0xffffffffu, d);
+        unsigned same = 0xffffffffu;
+        if (BALLOTS) {
+#pragma unroll
+            for (int b = 0; b <= kDigitBits; ++b) {
+                const unsigned set = __ballot_sync(0xffffffffu, d >> b & 1);
+                same &= d >> b & 1 ? set : ~set;
+            }
+        } else {
+            same = __match_any_sync(0xffffffffu, d);
+        }
         const int had = d < kDigits ? counter[d] : 0;
         rank[k] = had + __popc(same & ((1u << lane) - 1));
         __syncwarp();
@@ -128,7 +138,7 @@ __device__ __forceinline__ void sort_cluster(ClusterSort<K> &m, const int32_t *_
         int *tot = m.tot[p & 1];
         for (int i = t; i < kClusterWarps * kDigits / 2; i += kClusterThreads) reinterpret_cast<int *>(m.cnt)[i] = 0;
         __syncthreads();
-        rank_keys<K>(key, shift, m.cnt[warp], rank);
+        rank_keys<K, CLUSTER>(key, shift, m.cnt[warp], rank);
         __syncthreads();
         int n = 0;
         if (t < kDigits) {      // a thread per digit: exclusive over the warps
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t *__re
             before[h] += b < (int)blockIdx.x ? c[b] : 0;
         }
     }
-    rank_keys<kSortKeys>(key, shift, n[warp], rank);
+    rank_keys<kSortKeys, true>(key, shift, n[warp], rank);
     int start = total[0] + total[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
