@@ -32,7 +32,7 @@
 // k_xent is a persistent kernel of CTA pairs (cta_group::2): a pair computes
 // 256 x 256 tiles, each CTA holding 128 rows of A and 128 columns of B of every
 // 64-deep stage, so that an SM fetches 32 KB where a CTA alone would fetch 48 KB
-// for its half of the tile.  Warp 0 copies (TMA, 5 to 8 stages), one thread of the
+// for its half of the tile.  Warp 0 copies (TMA, 3 to 7 stages), one thread of the
 // even CTA's warp 1 issues the MMAs, warps 2..9 drain one of two accumulators
 // while the next tile fills the other.  Few tokens take tiles of single CTAs.
 #include <limits.h>
@@ -66,7 +66,7 @@ struct Form {
     static constexpr int kM = PAIR ? 256 : 128, kOwnN = PAIR ? BN / 2 : BN;
     static constexpr int kA = 128 * kBK * 2, kB = kOwnN * kBK * 2, kStage = kA + kB;
     static constexpr int kStaging = kEpiWarps * BOXES * kBox;
-    static constexpr int kMostStages = (226 * 1024 - 1024 - kStaging) / kStage, kStages = kMostStages < 8 ? kMostStages : 8;
+    static constexpr int kStages = (226 * 1024 - 1024 - kStaging) / kStage;
     static constexpr int kBars = 2 * kStages + 2 * 2 + 1;
     static constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
@@ -395,6 +395,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_commit_group();
         };
 
+        auto settle = [](uint32_t (&v)[32]) {       // loaded values are not used before the wait for them
+#pragma unroll
+            for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+        };
+
         // GRAD of single CTAs: the first box to row row0, the second to its lower terms' row
         auto send_terms = [&](int col, int row0) {
             fence_proxy_async_smem();
@@ -444,10 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t r[kQ][32];
                     auto load = [&](uint32_t (&to)[32], int q) {
                         tc_ld_32x32b_x32(tm_lane + (tc & 1) * BN + half * kCols + q * 32, to);
-                    };
-                    auto settle = [](uint32_t (&v)[32]) {       // not used before the wait
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
                     };
 #pragma unroll
                     for (int q = 0; q < kQ; ++q) load(r[q], q);
@@ -499,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t r[32];
                         tc_ld_32x32b_x32(from + q * 32, r);
                         tc_wait_ld();
+                        settle(r);
                         const int col = col0 + q * 32, at = target - col;
                         const int lim = token >= 0 ? a.vn - col : 0;
                         uint32_t low[PAIR ? 1 : 32];
@@ -533,12 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < kQ; ++q) tc_ld_32x32b_x32(from + q * 32, r[q]);
                     tc_wait_ld();
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q)
+                    for (int q = 0; q < kQ; ++q) {
+                        settle(r[q]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            asm volatile("" : "+r"(r[q][i]));       // not used before the wait
+                        for (int i = 0; i < 32; ++i)
                             if (t.k0 == t.k1) r[q][i] = 0;          // no K: the accumulator was not written
-                        }
+                    }
                     release();
                     const bool f32 = !t.dw || a.dw_f32, add = t.dw ? a.dw_add : a.dx_add;
                     const CUtensorMap *map = &maps.m[t.dw ? 5 : 2];
@@ -922,8 +924,8 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 bool packs(int64_t tokens, int64_t vocab, int64_t dim) { return tokens > kTile && tokens * vocab * dim > (int64_t)10000000000; }
 
 // Up to 128 tokens, one CTA's tiles hold them all, and a pair's would be half
-// empty: W streams past at 128 x BN tiles by single CTAs (64 x 128000 x 4096:
-// 100 us a pass over half of W in pairs' tiles, HBM's floor is 78).
+// empty: W streams past at 128 x BN tiles by single CTAs (64 x 128000 x 4096 forward:
+// 175 us in pairs' tiles, 168 so, HBM's floor is 157).
 bool single(int64_t tokens) { return tokens <= 128; }
 
 // Whether k_xent_few takes the forward: its x has to fit, twice an SM.

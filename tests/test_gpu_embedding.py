@@ -140,3 +140,25 @@ def test_no_tokens_or_words():
     out = torch.ones((2, 64), dtype=torch.bfloat16, device="cuda")
     fg.embedding_fwd(torch.full((2,), -1, dtype=torch.int32, device="cuda"), rows, out)     # nothing but padding, no words
     assert not out.any() and fg.device_status() == fg.OK
+
+
+@pytest.mark.parametrize("T", [500, 5000, 70000])
+def test_offsets_beyond_32_bits_full_size(T):
+    """A table of more than 2^31 elements, ids at both ends and scattered."""
+    V, D = 1100000, 2048
+    g = torch.Generator(device="cuda").manual_seed(8)
+    ids = torch.randint(V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    ids[:4] = torch.tensor([V - 1, 0, V - 1, V - 2], dtype=torch.int32)
+    w = torch.empty((V, D), dtype=torch.bfloat16, device="cuda")
+    w.view(torch.int16).copy_((torch.arange(V, device="cuda") % 16384).to(torch.int16)[:, None].expand(V, D))
+    out = torch.empty((T, D), dtype=torch.bfloat16, device="cuda")
+    fg.embedding_fwd(ids, w, out)
+    assert torch.equal(out.view(torch.int16), (ids % 16384).to(torch.int16)[:, None].expand(T, D))
+    del w
+    dout = torch.randint(-4, 5, (T, D), generator=g, device="cuda").bfloat16()
+    dw = torch.full((V, D), 3.0, device="cuda")
+    fg.embedding_bwd(ids, dout, dw, fg.new_embedding_workspace(T, V, D))
+    uniq, inv = torch.unique(ids, return_inverse=True)
+    want = torch.zeros((uniq.numel(), D), device="cuda").index_add_(0, inv, dout.float())
+    assert torch.equal(dw[uniq.long()], want)
+    assert int((dw != 0).any(1).sum()) <= uniq.numel() and fg.device_status() == fg.OK

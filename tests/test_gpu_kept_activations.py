@@ -205,3 +205,34 @@ def test_nonfinite_is_recorded():
         assert fg.device_status() == fg.ERR_NONFINITE
         fg.swiglu_fwd_ckpt(x, fg.E4M3, torch.empty((5, 128), dtype=torch.bfloat16, device="cuda"), c, cs)
         assert fg.device_status() == fg.ERR_NONFINITE
+
+
+def test_offsets_beyond_32_bits_full_size():
+    """More than 2^31 elements: the last rows are as those of a small call."""
+    R, F = 90000, 14336
+    gu = torch.empty((R, 2 * F), dtype=torch.bfloat16, device="cuda").normal_()
+    h, c, cs = torch.empty((R, F), dtype=torch.bfloat16, device="cuda"), torch.empty((R, 2 * F), dtype=torch.uint8, device="cuda"), torch.empty((2 * F // 128, R), device="cuda")
+    fg.swiglu_fwd_ckpt(gu, fg.E4M3, h, c, cs)
+    dgu = torch.empty_like(gu)
+    fg.swiglu_bwd_ckpt(c, cs, h, fg.E4M3, dgu)
+    n = 300
+    last = gu[-n:].contiguous()
+    h2, c2, cs2, d2 = torch.empty((n, F), dtype=torch.bfloat16, device="cuda"), torch.empty((n, 2 * F), dtype=torch.uint8, device="cuda"), torch.empty((2 * F // 128, n), device="cuda"), torch.empty_like(last)
+    fg.swiglu_fwd_ckpt(last, fg.E4M3, h2, c2, cs2)
+    fg.swiglu_bwd_ckpt(c2, cs2, h2, fg.E4M3, d2)
+    assert torch.equal(h[-n:], h2) and torch.equal(c[-n:], c2) and torch.equal(cs[:, -n:], cs2) and torch.equal(dgu[-n:], d2)
+    del h, c, cs, dgu
+    R, C = 140000, 16384
+    x = gu.view(-1)[:R * C].view(R, C)
+    w, ws = torch.randn(C, device="cuda").bfloat16(), fg.new_rmsnorm_workspace(C)
+
+    def both(x):
+        R = x.shape[0]
+        y, c, cs, r = torch.empty_like(x), torch.empty((R, C), dtype=torch.uint8, device="cuda"), torch.empty((C // 128, R), device="cuda"), torch.empty(R, device="cuda")
+        fg.rmsnorm_fwd_ckpt(x, w, 1e-5, fg.E4M3, y, c, cs, r)
+        dx, dw = torch.empty_like(x), torch.empty(C, device="cuda")
+        fg.rmsnorm_bwd_ckpt(c, cs, r, w, y, fg.E4M3, dx, dw, ws)
+        return y, c, r, dx
+
+    big, small = both(x), both(x[-n:].contiguous())
+    assert all(torch.equal(a[-n:], b) for a, b in zip(big, small)) and fg.device_status() == fg.OK

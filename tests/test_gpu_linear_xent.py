@@ -325,3 +325,30 @@ def test_no_tokens():
     assert bool((dw == 1).all())
     fg.linear_xent_bwd(x, w, t, e, e, e, x, dw, ws)
     assert not dw.any()
+
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_offsets_beyond_32_bits_full_size(T):
+    """W and dw of more than 2^31 elements: targets at both ends, checked on slices of the vocabulary."""
+    V, D = 270000, 8192
+    g = torch.Generator(device="cuda").manual_seed(17)
+    w = torch.empty((V, D), dtype=torch.bfloat16, device="cuda").normal_(generator=g).mul_(D ** -0.5)
+    x = torch.randn((T, D), generator=g, device="cuda").bfloat16()
+    t = torch.randint(V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    t[0], t[1] = V - 1, 0
+    x[0] += 20 * w[V - 1]
+    loss, lse = forward(x, w, t)
+    z = torch.cat([x.double() @ w[v:v + 30000].double().T for v in range(0, V, 30000)], 1)
+    want = torch.logsumexp(z, 1)
+    at = z.gather(1, t.long()[:, None])[:, 0]
+    off = (D / 16 + 16) * 2.0 ** -23 * float((x.double().abs() @ w[:2000].double().abs().T).max()) * 1.5 + sum_error(V, z)
+    assert float((lse - want).abs().max()) <= off and float((loss - (want - at)).abs().max()) <= 2 * off
+    dl = torch.ones(T, device="cuda")
+    dx, dw = backward(x, w, t, loss, lse, dl, None)
+    p = torch.exp(z - want[:, None])
+    p[torch.arange(T, device="cuda"), t.long()] -= 1
+    ref = sum(p[:, v:v + 30000] @ w[v:v + 30000].double() for v in range(0, V, 30000))
+    assert float((dx.double() - ref).norm()) <= 2 * HALF * float(ref.norm())
+    for v in (0, V // 2, V - 500):
+        ref = p[:, v:v + 500].T @ x.double()
+        assert float((dw[v:v + 500].double() - ref).norm()) <= 2 * HALF * float(ref.norm())
