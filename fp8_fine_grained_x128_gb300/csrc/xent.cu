@@ -20,10 +20,11 @@
 // of up to 8 tiles and writes 8 bytes a row and half unit, 1/32 of a BF16 logit row
 // and less; k_xent_join adds them in order.
 // Backward: for a piece of the vocabulary, g is rounded to BF16 (the tensor
-// cores' operand type; it costs each of the products up to 2^-8 a term, random
-// over the terms, beside the same rounding of the BF16 results; up to 128 tokens
-// it keeps a second term) and kept in the workspace, [tokens][piece]; dx is summed
-// over the pieces in FP32.
+// cores' operand type) and kept in the workspace, [tokens][piece]; dx is summed
+// over the pieces in FP32.  A token's g is mostly its target's entry, whose
+// rounding would reach all of the token's dx and all that it adds to dw.  So each
+// row is taken relative to that entry, which is then +-1: dx gets it back in FP32,
+// and dw from a copy of x times it, rounded to BF16.
 //
 // Tokens that do not count are left out from the start: k_xent_pack copies the
 // counted rows of x together, so neither the work nor the results see the
@@ -38,8 +39,6 @@
 #include <limits.h>
 
 #include <algorithm>
-
-#include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -94,18 +93,12 @@ struct XentArgs {
     int64_t rows;               // rows of the packed buffers
     // GRAD
     const float *loss, *lse, *dloss, *dlse;
+    const float *norm;          // [rows]: what the row of g is relative to
     // SUMS
-    int low;                    // kLow where g has second terms, else 0
     int dx_add;                 // dx's parts (FP32, [splits][rows][dim]) are added to
     int dw_f32, dw_add;
     int *status;
 };
-
-// Up to 128 tokens (GRAD by single CTAs) g keeps a second term, what its BF16
-// rounding leaves, as the rows from kLow on: the products are bound by memory there,
-// dx's tile of 256 rows has room for them, and few tokens' roundings do not average
-// out.  x lies twice in its buffer, at rows 0 and kLow, as dw's K runs over both.
-constexpr int kLow = 128;
 
 // The units of a pair (or single CTA), in the same order for every role: tiles
 // in columns [nt0, nt1) of row mt, K blocks [k0, k1).  Where a unit lies takes
@@ -139,9 +132,9 @@ struct Walk {
     // units lasts, and the rest of dw's go round all pairs.
     int rem, extra;
     __device__ __forceinline__ Walk(const XentArgs &a, int rows, int mine_, int step_)
-        : mine(mine_), step(step_), p(rows ? rows + a.low : 0, MODE == XENT_SUMS ? a.dim : a.vn, MODE == XENT_SUMS ? a.vn : a.dim, kM, BN,
+        : mine(mine_), step(step_), p(rows, MODE == XENT_SUMS ? a.dim : a.vn, MODE == XENT_SUMS ? a.vn : a.dim, kM, BN,
                                       MODE == XENT_LOSS ? a.per_unit : 1, MODE == XENT_SUMS ? a.splits : 1, a.band),
-          w(MODE == XENT_SUMS ? a.vn : 0, a.dim, rows ? rows + a.low : 0, kM, BN, 1, 1, a.band)
+          w(MODE == XENT_SUMS ? a.vn : 0, a.dim, rows, kM, BN, 1, 1, a.band)
     {
         rem = p.units % step;
         extra = rem == 0 ? 0 : min(p.per_split / max(w.nkb, kTileCost), w.units / (step - rem));
@@ -187,6 +180,12 @@ struct Walk {
 // Tensor maps: A, B and the result, of dx and then of dw for SUMS.
 template <int MODE>
 struct Maps { CUtensorMap m[MODE == XENT_SUMS ? 6 : 3]; };
+
+// g at the target, of a token with this loss.
+__device__ __forceinline__ float target_entry(float scale, float loss, float gl, float gz)
+{
+    return scale * (gl * expm1f(-loss) + gz * expf(-loss));
+}
 
 // 8 FP32 values to 16 bytes of BF16.
 __device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
@@ -400,16 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
         };
 
-        // GRAD of single CTAs: the first box to row row0, the second to its lower terms' row
-        auto send_terms = [&](int col, int row0) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane != 0) return;
-            tma_store_2d(&maps.m[2], staging, col, row0);
-            tma_store_2d(&maps.m[2], staging + (BOXES > 1 ? kBox : 0), col, row0 + kLow);
-            bulk_commit_group();
-        };
-
         int at_mt = -1;
         int token = -1, target = -1;                        // of this lane's row, LOSS and GRAD
         float lse2 = 0.0f, coef = 0.0f, at_target = 0.0f;   // GRAD
@@ -421,10 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 token = row < rows ? (a.map ? a.map[row] : row) : -1;
                 target = token >= 0 ? a.target[token] - a.v0 : -1;
                 if (MODE == XENT_GRAD && token >= 0) {
-                    const float lse = a.lse[token], loss = a.loss[token], gl = a.dloss[token], gz = a.dlse ? a.dlse[token] : 0.0f;
-                    lse2 = lse * kLog2e;
-                    coef = a.scale * (gl + gz);
-                    at_target = a.scale * (gl * expm1f(-loss) + gz * expf(-loss));
+                    const float gl = a.dloss[token], gz = a.dlse ? a.dlse[token] : 0.0f, by = a.norm[row];
+                    lse2 = a.lse[token] * kLog2e;
+                    coef = a.scale * (gl + gz) / by;
+                    at_target = target_entry(a.scale, a.loss[token], gl, gz) / by;
                 }
             }
             float top = -INFINITY, sum = 0.0f;              // LOSS
@@ -503,30 +492,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         settle(r);
                         const int col = col0 + q * 32, at = target - col;
                         const int lim = token >= 0 ? a.vn - col : 0;
-                        uint32_t low[PAIR ? 1 : 32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             float g = coef * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -lse2));
                             if (i == at) g = at_target;
                             g = i < lim ? g : 0.0f;
                             r[i] = __float_as_uint(g);
-                            if (!PAIR) low[PAIR ? 0 : i] = __float_as_uint(g - __bfloat162float(__float2bfloat16_rn(g)));
                         }
-                        if constexpr (PAIR) {
-                            const int in = q & (2 * BOXES - 1);     // quarter of the boxes
-                            if (in == 0) free_boxes();
-                            stage(r, in, false);
-                            if (in == 2 * BOXES - 1 || q == kQ - 1) {
-                                if (q == kQ - 1) release();
-                                send(&maps.m[2], in / 2 + 1, col - 32 * in, row0, INT_MAX, INT_MAX, false, false);
-                            }
-                        } else {        // two terms: one box each
-                            static_assert(PAIR || BOXES == 2, "a box for each term");
-                            if ((q & 1) == 0) free_boxes();
-                            stage(r, q & 1, false);
-                            stage(low, 2 + (q & 1), false);
+                        const int in = q & (2 * BOXES - 1);     // quarter of the boxes
+                        if (in == 0) free_boxes();
+                        stage(r, in, false);
+                        if (in == 2 * BOXES - 1 || q == kQ - 1) {
                             if (q == kQ - 1) release();
-                            if (q & 1) send_terms(col - 32, row0);
+                            send(&maps.m[2], in / 2 + 1, col - 32 * in, row0, INT_MAX, INT_MAX, false, false);
                         }
                     }
                 } else {
@@ -696,19 +674,32 @@ struct PackArgs {
     int tokens, vocab, dim;
     uint16_t *xp;               // [rows][dim]
     int64_t rows;
-    int twice;                  // up to kLow tokens: x at rows 0 and kLow
     int32_t *map;
     int *count;
     float *loss, *lse;          // forward: zeroed where a token does not count
     uint16_t *dx;               // backward: the same
     int64_t lddx;
+    const float *losses, *dloss, *dlse;     // backward
+    float scale;
+    float *norm;                // [rows]: the size of g at the target
+    uint16_t *xn;               // [rows][dim]: x times it
     int *status;
 };
+
+__device__ __forceinline__ uint4 times8(uint4 v, float by)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = bf16x2_rn(bf16_lo(w[k]) * by, bf16_hi(w[k]) * by);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
 
 __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
 {
     __shared__ int warp_n[8];
     __shared__ int32_t src[256];
+    __shared__ float by[256];
     dependents_launch();
     dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -752,7 +743,13 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
         }
         if (in) {
             src[before] = t;
-            if (dbg_span(at + before, 1, g.rows, g.status)) g.map[at + before] = t;
+            const bool fits = dbg_span(at + before, 1, g.rows, g.status);
+            if (fits) g.map[at + before] = t;
+            if (g.norm) {
+                const float n = fabsf(target_entry(g.scale, g.losses[t], g.dloss[t], g.dlse ? g.dlse[t] : 0.0f));
+                by[before] = n >= 0x1p-100f && n <= 0x1p100f ? n : 1.0f;    // else the row stays as it is
+                if (fits) g.norm[at + before] = by[before];
+            }
         } else if (mine && g.loss) {
             if (dbg_span(t, 1, g.tokens, g.status)) g.loss[t] = g.lse[t] = 0.0f;
         }
@@ -766,9 +763,9 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int v = v0 + 32 * i;
-                    if (v >= nv || !dbg_cell(at + r + (g.twice ? kLow : 0), v * 8, 8, g.rows, g.dim, g.status)) continue;
+                    if (v >= nv || !dbg_cell(at + r, v * 8, 8, g.rows, g.dim, g.status)) continue;
                     *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r) * g.dim + v * 8) = x[i];
-                    if (g.twice) *reinterpret_cast<uint4 *>(g.xp + (int64_t)(at + r + kLow) * g.dim + v * 8) = x[i];
+                    if (g.xn) *reinterpret_cast<uint4 *>(g.xn + (int64_t)(at + r) * g.dim + v * 8) = times8(x[i], by[r]);
                 }
             }
         }
@@ -781,13 +778,13 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
         at += total;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *g.count = all;
-    const int end = g.twice ? kTile : (all + kTile - 1) / kTile * kTile;
-    for (int r = all + blockIdx.x * 8 + warp; r < end; r += gridDim.x * 8) {
-        if (g.twice && r >= kLow && r < kLow + all) continue;
+    const int end = (all + kTile - 1) / kTile * kTile;
+    for (int r = all + blockIdx.x * 8 + warp; r < end; r += gridDim.x * 8)
         for (int v = lane; v < nv; v += 32)
-            if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status))
+            if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status)) {
                 *reinterpret_cast<uint4 *>(g.xp + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
-    }
+                if (g.xn) *reinterpret_cast<uint4 *>(g.xn + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
+            }
 }
 
 // ---------------------------------------------------------------------------
@@ -885,11 +882,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_xent_join(JoinArgs g)
     }
 }
 
-// Backward, last step: the parts of dx's K added in order, rounded to BF16, each
-// row where its token is.
+// Backward, last step: the parts of dx's K added in order, times what their row is
+// relative to, rounded to BF16, each row where its token is.
 constexpr int kSumThreads = 128;
 
-__global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, int splits, int low, int64_t rows, const int *count, const int32_t *map, int dim,
+__global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, int splits, int64_t rows, const int *count, const int32_t *map,
+                                                    const float *norm, int dim,
                                                     uint16_t *dx, int64_t lddx, int tokens, int *status)
 {
     dependents_launch();
@@ -901,13 +899,16 @@ __global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, 
         const int col = (int)(i - row * nv) * 8;
         float v[8] = {};
 #pragma unroll 8
-        for (int s = 0; s < (low ? 2 * splits : splits); ++s) {     // the second terms' first: they are the smaller
-            const float4 *p = reinterpret_cast<const float4 *>(acc + (s < splits ? s * rows + row + low : (s - splits) * rows + row) * dim + col);
+        for (int s = 0; s < splits; ++s) {
+            const float4 *p = reinterpret_cast<const float4 *>(acc + (s * rows + row) * dim + col);
             const float4 x = p[0], y = p[1];
             v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
             v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
         }
         const int64_t at = (int64_t)map[row] * lddx + col;
+        const float by = norm[row];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= by;
         if (dbg_span(at, 8, (int64_t)(tokens - 1) * lddx + dim, status))
             *reinterpret_cast<uint4 *>(dx + at) = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
     }
@@ -943,7 +944,7 @@ struct XentPlan {
     int per_unit, parts;            // forward: tiles of a unit, maxima and sums of a row
     int64_t piece;                  // backward: vocabulary of a piece
     int splits;                     // backward: parts of dx's K
-    int64_t count, map, xp, part, g, acc, bytes;    // byte offsets
+    int64_t count, map, xp, xn, norm, part, g, acc, bytes;      // byte offsets
     XentPlan(int64_t tokens, int64_t vocab, int64_t dim, bool backward)
     {
         const bool one = single(tokens);
@@ -973,6 +974,8 @@ struct XentPlan {
             const int64_t nd = (dim + kTile - 1) / kTile, kv = piece / kBK, kt = std::max<int64_t>(kTileCost, (tokens + kBK - 1) / kBK);
             const int64_t share = (mt * nd * kv + piece / kTile * nd * kt) / std::max(1, sm_count() / 2);
             splits = (int)std::max<int64_t>(1, std::min((kv + share) / (share + 1), kv / 8));
+            xn = take(rows * dim * 2);
+            norm = take(rows * 4);
             g = take(rows * piece * 2);
             acc = take((int64_t)splits * rows * dim * 4);
         }
@@ -1029,10 +1032,9 @@ bool map_out(CUtensorMap *m, void *p, bool f32, int64_t cols, int64_t rows, int6
                        (uint64_t)ld * (f32 ? 4 : 2), f32 ? 32 : 64, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
-int pack(const XentPlan &p, uint8_t *ws, const int32_t *target, const void *x, int64_t ldx, int64_t tokens, int64_t vocab, int64_t dim, float *loss,
-         float *lse, void *dx, int64_t lddx, bool twice, int *status, cudaStream_t st)
+int pack(const XentPlan &p, uint8_t *ws, PackArgs &g, const int32_t *target, const void *x, int64_t ldx, int64_t tokens, int64_t vocab, int64_t dim,
+         int *status, cudaStream_t st)
 {
-    PackArgs g{};
     g.target = target;
     g.x = static_cast<const uint16_t *>(x);
     g.ldx = ldx;
@@ -1041,13 +1043,8 @@ int pack(const XentPlan &p, uint8_t *ws, const int32_t *target, const void *x, i
     g.dim = (int)dim;
     g.xp = reinterpret_cast<uint16_t *>(ws + p.xp);
     g.rows = p.rows;
-    g.twice = twice;
     g.map = reinterpret_cast<int32_t *>(ws + p.map);
     g.count = reinterpret_cast<int *>(ws + p.count);
-    g.loss = loss;
-    g.lse = lse;
-    g.dx = static_cast<uint16_t *>(dx);
-    g.lddx = lddx;
     g.status = status;
     const int64_t grid = std::min<int64_t>((tokens + 7) / 8, (int64_t)sm_count() * 4);
     return launch_dependent(k_xent_pack, dim3((unsigned)grid), 256, 0, st, g);
@@ -1070,7 +1067,10 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
     const void *xp = x;
     int64_t ldxp = ldx, xrows = tokens;
     if (packs(tokens, vocab, dim)) {
-        if ((rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, loss, lse, nullptr, 0, false, status, st)) != FP8_OK) return rc;
+        PackArgs g{};
+        g.loss = loss;
+        g.lse = lse;
+        if ((rc = pack(p, ws, g, target, x, ldx, tokens, vocab, dim, status, st)) != FP8_OK) return rc;
         xp = ws + p.xp;
         ldxp = dim;
         xrows = p.rows;
@@ -1128,7 +1128,16 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
 {
     const XentPlan p(tokens, vocab, dim, true);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    int rc = pack(p, ws, target, x, ldx, tokens, vocab, dim, nullptr, nullptr, dx, lddx, single(tokens), status, st);
+    PackArgs pk{};
+    pk.dx = static_cast<uint16_t *>(dx);
+    pk.lddx = lddx;
+    pk.losses = loss;
+    pk.dloss = dloss;
+    pk.dlse = dlse;
+    pk.scale = scale;
+    pk.norm = reinterpret_cast<float *>(ws + p.norm);
+    pk.xn = reinterpret_cast<uint16_t *>(ws + p.xn);
+    int rc = pack(p, ws, pk, target, x, ldx, tokens, vocab, dim, status, st);
     if (rc != FP8_OK) return rc;
     XentArgs a{};
     a.count = reinterpret_cast<int *>(ws + p.count);
@@ -1145,6 +1154,7 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.lse = lse;
     a.dloss = dloss;
     a.dlse = dlse;
+    a.norm = pk.norm;
     a.status = status;
     void *xp = ws + p.xp, *g = ws + p.g, *acc = ws + p.acc;
     a.dw_f32 = dw_dtype == FP8_OUT_F32;
@@ -1154,26 +1164,24 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     if (!map_k(&grad.m[0], xp, dim, p.rows, dim) || !map_k(&grad.m[1], w, dim, vocab, ldw) ||
         !map_out(&grad.m[2], g, false, p.piece, p.rows, p.piece) || !map_k(&sums.m[0], g, p.piece, p.rows, p.piece) ||
         !map_mn(&sums.m[1], w, dim, vocab, ldw) || !map_out(&sums.m[2], acc, true, dim, p.splits * p.rows, dim) ||
-        !map_mn(&sums.m[3], g, p.piece, p.rows, p.piece) || !map_mn(&sums.m[4], xp, dim, p.rows, dim) ||
+        !map_mn(&sums.m[3], g, p.piece, p.rows, p.piece) || !map_mn(&sums.m[4], pk.xn, dim, p.rows, dim) ||
         !map_out(&sums.m[5], dw, a.dw_f32, dim, vocab, lddw))
         return FP8_ERR_CUDA;
     for (int64_t v = 0; v < vocab; v += p.piece) {
         a.v0 = (int)v;
         a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
-        a.low = 0;
         a.band = 16;
         rc = !single(tokens) ? run<XENT_GRAD, true, 256, 1>(grad, a, st)
              : p.bn == 256   ? run<XENT_GRAD, false, 256, 2>(grad, a, st)
-                             : run<XENT_GRAD, false, 128, 2>(grad, a, st);
+                             : run<XENT_GRAD, false, 128, 1>(grad, a, st);
         if (rc != FP8_OK) return rc;
-        a.low = single(tokens) ? kLow : 0;
         a.band = 8;
         a.dx_add = v > 0;
         rc = tokens <= kShallow ? run<XENT_SUMS, true, 256, 2>(sums, a, st) : run<XENT_SUMS, true, 256, 1>(sums, a, st);
         if (rc != FP8_OK) return rc;
     }
     const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + kSumThreads - 1) / kSumThreads, (int64_t)sm_count() * 16);
-    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), kSumThreads, 0, st, static_cast<const float *>(acc), p.splits, a.low, p.rows, a.count, a.map,
+    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), kSumThreads, 0, st, static_cast<const float *>(acc), p.splits, p.rows, a.count, a.map, a.norm,
                             a.dim, static_cast<uint16_t *>(dx), lddx, a.tokens, status);
 }
 

@@ -693,8 +693,10 @@ FP8FG_API int fp8_linear_xent_fwd(const void *x, int64_t tokens, int64_t dim, in
 /* Its gradient.  With gl = dloss[t], gz = dlse[t] (dlse NULL: 0), p_v = exp(z_v - lse):
  *   g[t][v] = scale * ((gl + gz) p_v - gl [v = target[t]])
  *   dx = g w (BF16),   dw (+)= g^T x (BF16 or FP32; dw_dtype)
- * p_target - 1 is taken from loss, as expm1(-loss).  g is rounded to BF16 (the
- * operands of the two products), everything else is FP32 up to the results.
+ * p_target - 1 is taken from loss, as expm1(-loss).  The operands of the two
+ * products are BF16: each token's g relative to its entry at the target (which is
+ * then +-1), and for dw x times that entry; everything else is FP32 up to the
+ * results.
  * loss, lse: as fp8_linear_xent_fwd left them for the same x, w, target, scale.
  * accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): added to dw in one addition an
  * element (operands and results below 2^-126 count as zero there); else every row
