@@ -662,8 +662,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_xent_few(const uint16_t *__r
 }
 
 // ---------------------------------------------------------------------------
-// The counted tokens' rows of x, one behind another, zeros up to the next
-// multiple of 256, and the token of each.  Every CTA takes a range of tokens and
+// The counted tokens' rows of x, one behind another, and the token of each.  Every CTA takes a range of tokens and
 // counts the ones before it by itself.  Rows of the outputs that belong to
 // tokens left out are zeroed here.
 // ---------------------------------------------------------------------------
@@ -778,13 +777,12 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
         at += total;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *g.count = all;
-    const int end = (all + kTile - 1) / kTile * kTile;
+    // dw's last K block reads on: zeros there.  (What lies behind xp's rows only makes rows that nobody looks at.)
+    const int end = g.xn ? (all + kBK - 1) / kBK * kBK : 0;
     for (int r = all + blockIdx.x * 8 + warp; r < end; r += gridDim.x * 8)
         for (int v = lane; v < nv; v += 32)
-            if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status)) {
-                *reinterpret_cast<uint4 *>(g.xp + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
-                if (g.xn) *reinterpret_cast<uint4 *>(g.xn + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
-            }
+            if (dbg_cell(r, v * 8, 8, g.rows, g.dim, g.status))
+                *reinterpret_cast<uint4 *>(g.xn + (int64_t)r * g.dim + v * 8) = make_uint4(0, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -1046,7 +1044,7 @@ int pack(const XentPlan &p, uint8_t *ws, PackArgs &g, const int32_t *target, con
     g.map = reinterpret_cast<int32_t *>(ws + p.map);
     g.count = reinterpret_cast<int *>(ws + p.count);
     g.status = status;
-    const int64_t grid = std::min<int64_t>((tokens + 7) / 8, (int64_t)sm_count() * 4);
+    const int64_t grid = std::min<int64_t>(std::max<int64_t>((tokens + 7) / 8, kBK / 8), (int64_t)sm_count() * 4);
     return launch_dependent(k_xent_pack, dim3((unsigned)grid), 256, 0, st, g);
 }
 
