@@ -745,8 +745,11 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
             const bool fits = dbg_span(at + before, 1, g.rows, g.status);
             if (fits) g.map[at + before] = t;
             if (g.norm) {
-                const float n = fabsf(target_entry(g.scale, g.losses[t], g.dloss[t], g.dlse ? g.dlse[t] : 0.0f));
-                by[before] = n >= 0x1p-100f && n <= 0x1p100f ? n : 1.0f;    // else the row stays as it is
+                const float loss = g.losses[t], gl = g.dloss[t], gz = g.dlse ? g.dlse[t] : 0.0f;
+                const float n = fabsf(target_entry(g.scale, loss, gl, gz)), c = fabsf(g.scale * (gl + gz));
+                // the row stays as it is where that entry, or the others relative to it, are beyond all measure
+                const bool relative = n >= 0x1p-100f && n <= 0x1p100f && c <= n * 0x1p120f && c * -expm1f(-loss) <= n * 0x1p60f;
+                by[before] = relative ? n : 1.0f;
                 if (fits) g.norm[at + before] = by[before];
             }
         } else if (mine && g.loss) {

@@ -212,6 +212,31 @@ def test_gradients(T, V, D, ignored, scale, pad, zloss, kind):
         assert float((dx.double() - want_dx).norm()) <= (2 * HALF + off) * float(want_dx.norm())
 
 
+@pytest.mark.parametrize("gl,gz", [(0.0, 2.0 ** 30), (0.0, 1.0), (-(2.0 ** -90), 2.0 ** 30), (2.0 ** 30, 0.0)])
+@pytest.mark.parametrize("at", [-89.4, -60.0, 89.4, 60.0])
+def test_entries_far_from_the_targets(gl, gz, at):
+    """A target at 1e-39 (or at 1 but for 1e-39) of the probability: its entry and the others' are far apart, and no
+    quotient of them may leave the range of FP32.  Every term is off by at most two roundings to BF16, those of p's
+    exponent (2^-15 of it at 93) and the result's; probabilities below 2^-126 may count as zero, V of them in the loss."""
+    T, V, D = 5, 40, 64
+    u = torch.linspace(0.5, 1.0, D, device="cuda").bfloat16()
+    w = torch.zeros((V, D), device="cuda")
+    w[3] = (at + math.log(V)) / float(u.double() @ u.double()) * u.float()
+    w[7, 5] = w[9, 6] = 0.25
+    w, x, t = w.bfloat16(), u.repeat(T, 1), torch.full((T,), 3, dtype=torch.int32, device="cuda")
+    loss, lse = forward(x, w, t)
+    dx, dw = backward(x, w, t, loss, lse, torch.full((T,), gl, device="cuda"), torch.full((T,), gz, device="cuda"),
+                      dw=torch.empty((V, D), device="cuda"))
+    z, _, want_loss = exact(x, w, t, 1.0)
+    p = torch.softmax(z, 1)
+    G = (gl + gz) * p
+    G[:, 3] = (gl * torch.expm1(-want_loss) + gz * torch.exp(-want_loss))
+    for have, want, terms in ((dx, G @ w.double(), G.abs() @ w.double().abs()), (dw, G.T @ x.double(), G.abs().T @ x.double().abs())):
+        assert bool(torch.isfinite(have).all())
+        flush = (abs(gl) + abs(gz)) * V * 2.0 ** -126 * V * float(w.double().abs().max())
+        assert bool(((have.double() - want).abs() <= 4 * HALF * terms + flush + 2.0 ** -126).all())
+
+
 def test_gradient_against_differences():
     """The directional derivative of the forward in 64 bits along the kernel's own gradients."""
     T, V, D = 48, 333, 64
