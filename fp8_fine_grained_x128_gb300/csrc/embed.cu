@@ -642,7 +642,8 @@ struct EmbedLayout {    // byte offsets in the workspace
         const int64_t warps = (int64_t)sm_count() * kSumWarps, segs = (dim + 255) / 256;
         piece = (int)std::max<int64_t>(8, up((tokens * segs + warps - 1) / warps, 8));
         pieces = (int)((tokens + piece - 1) / piece);
-        const int64_t most = std::min((tokens + 7) / 8, warps / segs + 1);   // of fewer tokens too
+        // pieces * dim of this call and of every smaller one: there are at most warps / segs + 1 pieces, and dim <= 256 segs
+        const int64_t most = std::min((tokens + 7) / 8 * dim, warps * 256 + dim);
         int64_t at = 0;
         auto take = [&](int64_t n) { const int64_t p = at; at += up(n, 16); return p; };
         for (int i = 0; i < 2; ++i) {
@@ -650,7 +651,7 @@ struct EmbedLayout {    // byte offsets in the workspace
             vals[i] = take(tokens * 4);
         }
         counts = take(tokens <= kClusterMost ? 0 : (int64_t)passes * kDigits * blocks * 4);
-        part = take(most * 2 * dim * 4);
+        part = take(most * 2 * 4);
         bytes = at;
     }
 };

@@ -938,7 +938,12 @@ bool few(int64_t tokens, int64_t dim) { return tokens <= kFewTokens && (tokens >
 // stage (64 x 64000 x 4096: dw 131 -> 117 us; 8192 tokens: 1% slower).
 constexpr int64_t kShallow = 512;
 
-// Sizes that follow from those of the call alone.
+// Elements of g that the workspace holds (224 MB), unless a tile's columns take more
+// (8192 x 128000 x 4096 backward: 15.9 ms, with 192 MB 16.0, with 256 MB 15.8).
+constexpr int64_t kGradMost = (int64_t)112 << 20;
+
+// Sizes that follow from those of the call alone.  What is taken of the workspace
+// does not shrink when a size grows, so it serves all smaller calls too.
 struct XentPlan {
     int64_t rows;                   // of the packed buffers
     int bn;                         // columns of a tile over the vocabulary
@@ -965,10 +970,12 @@ struct XentPlan {
             while (per_unit > 1 && mt * ((nt + per_unit - 1) / per_unit) < 16 * groups) per_unit /= 2;
             parts = (int)((nt + per_unit - 1) / per_unit) * 2;
             if (few(tokens, dim)) parts = (int)std::min<int64_t>((vocab + kFewRows * 8 - 1) / (kFewRows * 8), (int64_t)sm_count() * 2);
-            part = take((int64_t)parts * rows * 8);
+            // parts * mt: below 64 groups where units are shorter than 8 tiles
+            const int64_t most = std::min(2 * mt * ((vocab + 127) / 128), std::max<int64_t>(32 * sm_count(), mt * ((vocab + 2047) / 2048)));
+            part = take(2 * most * kTile * 8);
         } else {
-            // pieces of equal length whose gradient takes up to 256 MB
-            const int64_t most = std::max<int64_t>(kTile, ((int64_t)128 << 20) / rows / kTile * kTile);
+            // pieces of equal length
+            const int64_t most = std::max<int64_t>(kTile, kGradMost / rows / kTile * kTile);
             const int64_t pieces = (up(vocab, kTile) + most - 1) / most;
             piece = up((vocab + pieces - 1) / pieces, kTile);
             // dx's K is split until a part lasts no longer than a pair's share of dx and dw
@@ -977,8 +984,9 @@ struct XentPlan {
             splits = (int)std::max<int64_t>(1, std::min((kv + share) / (share + 1), kv / 8));
             xn = take(rows * dim * 2);
             norm = take(rows * 4);
-            g = take(rows * piece * 2);
-            acc = take((int64_t)splits * rows * dim * 4);
+            g = take(std::min(rows * up(vocab, kTile), std::max(rows * kTile, kGradMost)) * 2);
+            // splits: at most groups / (mt * nd) + 1, and kv / 8
+            acc = take(std::min(std::max<int64_t>(1, up(vocab, kTile) / (8 * kBK)) * rows * dim, sm_count() / 2 * kTile * kTile + rows * dim) * 4);
         }
         bytes = at;
     }

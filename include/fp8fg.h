@@ -668,8 +668,9 @@ FP8FG_API int fp8_embedding_bwd(const int32_t *ids, int64_t tokens, const void *
                                 void *workspace, void *stream);
 
 /* Bytes of the caller-owned workspace of fp8_linear_xent_fwd (backward = 0) or
- * fp8_linear_xent_bwd (1) on the current device (any content; calls sharing one
- * must not overlap on the GPU; the two calls of a step may share the larger). */
+ * fp8_linear_xent_bwd (1) on the current device, for calls of up to these sizes (any
+ * content; calls sharing one must not overlap on the GPU; the two calls of a step
+ * may share the larger). */
 FP8FG_API size_t fp8_linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim, int backward);
 
 /* Softmax cross entropy of a linear head, without keeping the logits.  With

@@ -111,8 +111,9 @@ def test_padding_holds_anything_and_bad_ids_are_recorded():
     assert fg.device_status() == fg.ERR_INVALID_ARG and bool((out[bad >= V] == 0).all())
 
 
-def test_captured():
-    T, V, D = 4000, 3001, 128
+@pytest.mark.parametrize("T", [300, 4000, 70000])
+def test_captured(T):
+    V, D = 3001, 128
     ids, dout = words(T, V, "zipf", 6), torch.randn((T, D), device="cuda").bfloat16()
     ws, dw = fg.new_embedding_workspace(T, V, D), torch.empty((V, D), device="cuda")
     fg.embedding_bwd(ids, dout, dw, ws)
@@ -125,6 +126,16 @@ def test_captured():
     got = dw.clone()
     fg.embedding_bwd(ids, dout, dw, ws)
     assert torch.equal(got, dw) and fg.device_status() == fg.OK
+
+
+def test_one_workspace_for_calls_of_many_sizes():
+    ws = fg.new_embedding_workspace(70000, 5000, 1032)
+    for T, V, D in ((70000, 5000, 8), (70000, 17, 1032), (1, 1, 1032), (3000, 5000, 512), (69999, 4999, 1024)):
+        ids, dout = words(T, V, "zipf", 6), torch.randn((T, D), device="cuda").bfloat16()
+        a, b = torch.empty((V, D), device="cuda"), torch.empty((V, D), device="cuda")
+        fg.embedding_bwd(ids, dout, a, ws)
+        fg.embedding_bwd(ids, dout, b, fg.new_embedding_workspace(T, V, D))
+        assert torch.equal(a, b) and fg.device_status() == fg.OK
 
 
 def test_no_tokens_or_words():

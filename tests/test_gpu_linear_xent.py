@@ -316,6 +316,18 @@ def test_runs_repeat_and_graphs_replay():
     assert fg.device_status() == fg.OK
 
 
+def test_one_workspace_for_calls_of_many_sizes():
+    ws = fg.new_linear_xent_workspace(1000, 5000, 520)
+    for T, V, D in ((1000, 5000, 64), (1000, 300, 520), (2, 5000, 520), (100, 4999, 512), (257, 700, 136)):
+        x, w, t = make(T, V, D, 0.2, seed=T)
+        own = forward(x, w, t)
+        shared = forward(x, w, t, ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(own, shared))
+        dl = torch.rand(T, device="cuda")
+        for a, b in zip(backward(x, w, t, *own, dl, None), backward(x, w, t, *own, dl, None, ws=ws)):
+            assert torch.equal(a, b)
+
+
 def test_gradient_in_place():
     """dx may be x: every row of it has been copied before any is written."""
     for T in (100, 700):

@@ -1,6 +1,7 @@
 """Refusals of the embedding, norm, SwiGLU-checkpoint and cross-entropy entry points: the documented status before
 anything touches the GPU (runs without one)."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -119,6 +120,16 @@ def test_workspace_sizes(lib):
     assert 0 < small < 8192 * 128000 * 2 // 16              # far below the logits
     assert lib.fp8_linear_xent_workspace_bytes(8192, 128000, 4096, 1) < 8192 * 128000 * 2 // 4
     assert lib.fp8_embedding_workspace_bytes(100, 10, 12) == 0 and lib.fp8_rmsnorm_workspace_bytes(1 << 20) == 0
+
+
+@pytest.mark.parametrize("bytes_of", [lambda L, *s: L.fp8_embedding_workspace_bytes(*s), lambda L, *s: L.fp8_linear_xent_workspace_bytes(*s, 0),
+                                      lambda L, *s: L.fp8_linear_xent_workspace_bytes(*s, 1)], ids=["embedding", "loss", "loss_gradient"])
+def test_workspaces_serve_smaller_calls(lib, bytes_of):
+    r = random.Random(1)
+    for _ in range(20000):
+        T, V, D = int(2 ** r.uniform(0, 22)), int(2 ** r.uniform(0, 18)), 8 * int(2 ** r.uniform(0, 11))
+        t, v, d = r.choice([r.randint(1, T), T]), r.choice([r.randint(1, V), V]), r.choice([8 * r.randint(1, D // 8), D])
+        assert bytes_of(lib, t, v, d) <= bytes_of(lib, T, V, D), (t, v, d, T, V, D)
 
 
 def test_binding_refuses_host_tensors():
