@@ -844,6 +844,8 @@ def swiglu_fwd_ckpt(gu, fmt, h, c, cs, stream=None):
     """swiglu_fwd that also keeps ``gu`` [R, 2F] as codes ``c`` [R, 2F] and scales ``cs`` [2F/128, R]."""
     L, dev = lib(), _current()
     R, F2 = _shape(gu, "gu", 2)
+    if F2 % 2:
+        raise ValueError(f"gu: {F2} columns, expected gate and up side by side")
     n = R * F2
     rc = L.fp8_swiglu_fwd_ckpt(_buf(gu, "gu", _BF16, n, False, dev), R, F2 // 2, fmt, _buf(h, "h", _BF16, n // 2, False, dev),
                                _buf(c, "c", _CODES, n, False, dev), _buf(cs, "cs", _F32, (F2 // 128) * R, False, dev),
@@ -908,7 +910,7 @@ def embedding_bwd(ids, dout, dw, workspace, scale=1.0, accumulate=False, stream=
 
 
 def new_linear_xent_workspace(tokens, vocab, dim, backward=True, device="cuda") -> torch.Tensor:
-    """A workspace for calls of linear_xent_fwd and (backward) linear_xent_bwd of these sizes."""
+    """A workspace for calls of linear_xent_fwd and (backward) linear_xent_bwd of up to these sizes."""
     sizes = int(tokens), int(vocab), int(dim)
     n = max(_sized("fp8_linear_xent_workspace_bytes", None, *sizes, b) for b in range(2 if backward else 1))
     return _new_bytes(n, device)

@@ -207,6 +207,49 @@ def test_nonfinite_is_recorded():
         assert fg.device_status() == fg.ERR_NONFINITE
 
 
+def test_columns_that_are_no_pair_are_refused():
+    gu, h = torch.zeros((2, 257), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        fg.swiglu_fwd_ckpt(gu, fg.E4M3, h, torch.zeros((2, 257), dtype=torch.uint8, device="cuda"), torch.zeros((2, 2), device="cuda"))
+
+
+@pytest.mark.parametrize("R,C", [(5, 512), (900, 2048)])
+def test_captured_on_another_stream(R, C):
+    """Norm and SwiGLU, forward and backward, as one graph of their own stream, replayed with other inputs."""
+    x, res, w = inputs(R, C, 31)
+    x2, res2, _ = inputs(R, C, 32)
+    side, F = torch.cuda.Stream(), C // 2
+    bf = lambda cols: torch.empty((R, cols), dtype=torch.bfloat16, device="cuda")
+    y, total, h, dgu, dx, c, cs = bf(C), bf(C), bf(F), bf(C), bf(C), torch.empty((R, C), dtype=torch.uint8, device="cuda"), torch.empty((C // 128, R), device="cuda")
+    c2, cs2, rstd, dw, ws = torch.empty_like(c), torch.empty_like(cs), torch.empty(R, device="cuda"), torch.zeros(C, device="cuda"), fg.new_rmsnorm_workspace(C)
+
+    def step():
+        fg.rmsnorm_fwd_ckpt(x, w, 1e-5, fg.E4M3, y, c, cs, rstd, res=res, sum=total)
+        fg.swiglu_fwd_ckpt(y, fg.E5M2, h, c2, cs2)
+        fg.swiglu_bwd_ckpt(c2, cs2, h, fg.E5M2, dgu)
+        fg.rmsnorm_bwd_ckpt(c, cs, rstd, w, dgu, fg.E4M3, dx, dw, ws, dsum=total)
+        return [a.clone() for a in (y, total, h, dgu, dx, dw, c, c2)]
+
+    want = []
+    for a, b in ((x, res), (x2, res2)):
+        x, res = a, b
+        want.append(step())
+    first = inputs(R, C, 31)
+    x, res = (a.clone() for a in first[:2])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = step()
+    for (a, b), ref in zip((first[:2], (x2, res2)), want):
+        x.copy_(a)
+        res.copy_(b)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, n) for m, n in zip(got, ref)) and fg.device_status() == fg.OK
+
+
 def test_offsets_beyond_32_bits_full_size():
     """More than 2^31 elements: the last rows are as those of a small call."""
     R, F = 90000, 14336
