@@ -1055,9 +1055,12 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// An arrival that hands over no memory, for the barrier of either CTA: what the
+// caller has read (tensor memory, after tcgen05.wait::ld) is in its registers.
+// (With release semantics it would wait for the caller's stores to global memory.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // 2-D tiled load into this CTA's shared memory, its bytes counted on a barrier

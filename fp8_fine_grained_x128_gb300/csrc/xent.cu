@@ -80,8 +80,6 @@ constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 struct XentArgs {
     const int *count;           // counted tokens (nullptr: all `tokens` rows)
-    const int32_t *map;         // packed row -> token (nullptr: the same)
-    const int32_t *target;
     int tokens, vocab, dim;
     int v0, vn;                 // this piece's vocabulary: columns [v0, v0 + vn)
     int per_unit;               // LOSS: tiles of a unit
@@ -89,11 +87,11 @@ struct XentArgs {
     int band;                   // M tiles of a raster band
     float scale;
     // LOSS
+    const int32_t *target;      // of every row
     float2 *part;               // [unit][half][rows]: maximum (times scale log2 e), sum of 2^(. - maximum)
     int64_t rows;               // rows of the packed buffers
     // GRAD
-    const float *loss, *lse, *dloss, *dlse;
-    const float *norm;          // [rows]: what the row of g is relative to
+    const float4 *info;         // [rows]: lse log2 e, factor of p, entry at the target; the target as an int
     // SUMS
     int dx_add;                 // dx's parts (FP32, [splits][rows][dim]) are added to
     int dw_f32, dw_add;
@@ -170,7 +168,8 @@ struct Walk {
                 const int nkb = t.dw ? w.nkb : p.nkb, per_split = t.dw ? w.per_split : p.per_split;
                 t.k0 = min(nkb, t.split * per_split);
                 t.k1 = min(nkb, t.k0 + per_split);
-                body(t);
+                // the row of tiles after this one, where it is known
+                body(t, k + 1 < todo ? __shfl_sync(0xffffffffu, m, k + 1) : -1);
             }
             if (todo < 32) break;
         }
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------ TMA producer
         uint32_t it = 0;
         bool ok = true;
-        walk.each(ok, [&](const Unit &t) {
+        walk.each(ok, [&](const Unit &t, int) {
             const int m = t.mt * F::kM + rank * 128, blocks = (t.nt1 - t.nt0) * (t.k1 - t.k0);
             if (lane == 0) {
                 int nt = t.nt0, kb = t.k0;
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             uint32_t it = 0, tc = 0;
             bool ok = true;
-            walk.each(ok, [&](const Unit &t) {
+            walk.each(ok, [&](const Unit &t, int) {
                 if (lane == 0) {
                     const uint32_t idesc = kSums && t.dw ? idesc_bf16(F::kM, BN, true, true) : idesc_bf16(F::kM, BN, false, kSums);
                     const int parts = (t.nt1 - t.nt0) * chunks;     // of the unit, an accumulator each
@@ -362,60 +361,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         // A result leaves through this warp's staging: boxes of 32 rows of 128 bytes,
         // 16-byte chunks swizzled as the copies expect them (neither side meets a bank
-        // twice), BOXES of them before they are sent.  stage: 32 values of this lane's
-        // row to columns 32 q of the boxes; send: `boxes` of them to row row0, columns
-        // col and on.  What reaches over the matrix's edge is not written; a box beyond
-        // it is not sent.
-        auto free_boxes = [&] {
-            if (lane == 0) bulk_wait_read_all();
+        // twice), filled in turn.  stage: 32 values of this lane's row to one half (BF16)
+        // of a box or all of it; send: box b to row row0, columns x and on.  What reaches
+        // over the matrix's edge is not written; a box beyond it is not sent.
+        auto free_box = [&] {       // the box sent BOXES boxes ago has been read
+            if (lane == 0) bulk_wait_read<(BOXES > 1 ? BOXES - 1 : 0)>();
             __syncwarp();
         };
-        auto stage = [&](const uint32_t (&r)[32], int q, bool f32) {
-            uint8_t *to = staging + (f32 ? q : q >> 1) * kBox + lane * 128;
+        auto stage = [&](const uint32_t (&r)[32], int b, int half_box, bool f32) {
+            uint8_t *to = staging + b * kBox + lane * 128;
             if (f32) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     *reinterpret_cast<uint4 *>(to + ((j ^ (lane & 7)) << 4)) = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(to + (((j + 4 * (q & 1)) ^ (lane & 7)) << 4)) = bf16x8(r + 8 * j);
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(to + (((j + 4 * half_box) ^ (lane & 7)) << 4)) = bf16x8(r + 8 * j);
             }
         };
-        auto send = [&](const CUtensorMap *to, int boxes, int col, int row0, int cols, int rows_end, bool f32, bool add) {
+        auto send = [&](const CUtensorMap *to, int b, int x, int row0, int cols, int rows_end, bool add) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane != 0 || row0 >= rows_end) return;
-            for (int b = 0; b < boxes; ++b) {
-                const int x = col + b * (f32 ? 32 : 64);
-                if (x >= cols) break;
+            if (lane != 0) return;
+            if (row0 < rows_end && x < cols) {
                 if (add) tma_reduce_add_2d(to, staging + b * kBox, x, row0);
                 else tma_store_2d(to, staging + b * kBox, x, row0);
             }
-            bulk_commit_group();
+            bulk_commit_group();    // an empty group too: free_box counts them
         };
+        constexpr int kBoxes = BOXES > 0 ? BOXES : 1;
 
         auto settle = [](uint32_t (&v)[32]) {       // loaded values are not used before the wait for them
 #pragma unroll
             for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
         };
 
-        int at_mt = -1;
-        int token = -1, target = -1;                        // of this lane's row, LOSS and GRAD
-        float lse2 = 0.0f, coef = 0.0f, at_target = 0.0f;   // GRAD
+        // What this lane has to know of its row (LOSS: the target), fetched a tile ahead
+        // where the rows of tiles change.
+        auto fetch = [&](int mt) {
+            const int row = mt * F::kM + rank * 128 + lq * 32 + lane;
+            float4 i = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
+            if constexpr (MODE == XENT_GRAD) {
+                if (row < rows) i = a.info[row];
+            } else if constexpr (MODE == XENT_LOSS) {
+                if (row < rows) i.w = __int_as_float(a.target[row]);
+            }
+            return i;
+        };
+        int at_mt = -1, ahead_mt = -1;
+        float4 info, ahead;
         const float c = a.scale * kLog2e;
-        walk.each(ok, [&](const Unit &t) {
+        walk.each(ok, [&](const Unit &t, int next_mt) {
             const int row0 = t.mt * F::kM + rank * 128 + lq * 32, row = row0 + lane;
-            if (MODE <= XENT_GRAD && t.mt != at_mt) {
+            if (MODE <= XENT_GRAD) {
+                if (t.mt != at_mt) info = t.mt == ahead_mt ? ahead : fetch(t.mt);
                 at_mt = t.mt;
-                token = row < rows ? (a.map ? a.map[row] : row) : -1;
-                target = token >= 0 ? a.target[token] - a.v0 : -1;
-                if (MODE == XENT_GRAD && token >= 0) {
-                    const float gl = a.dloss[token], gz = a.dlse ? a.dlse[token] : 0.0f, by = a.norm[row];
-                    lse2 = a.lse[token] * kLog2e;
-                    coef = a.scale * (gl + gz) / by;
-                    at_target = target_entry(a.scale, a.loss[token], gl, gz) / by;
+                if (next_mt >= 0 && next_mt != at_mt) {
+                    ahead = fetch(next_mt);
+                    ahead_mt = next_mt;
                 }
             }
+            const int target = __float_as_int(info.w) - a.v0;
             float top = -INFINITY, sum = 0.0f;              // LOSS
             for (int nt = t.nt0; nt < t.nt1; ++nt, ++tc) {
                 auto full_accumulator = [&] {
@@ -491,21 +497,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_wait_ld();
                         settle(r);
                         const int col = col0 + q * 32, at = target - col;
-                        const int lim = token >= 0 ? a.vn - col : 0;
+                        const int lim = row < rows ? a.vn - col : 0;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            float g = coef * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -lse2));
-                            if (i == at) g = at_target;
+                            float g = info.y * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -info.x));
+                            if (i == at) g = info.z;
                             g = i < lim ? g : 0.0f;
                             r[i] = __float_as_uint(g);
                         }
-                        const int in = q & (2 * BOXES - 1);     // quarter of the boxes
-                        if (in == 0) free_boxes();
-                        stage(r, in, false);
-                        if (in == 2 * BOXES - 1 || q == kQ - 1) {
-                            if (q == kQ - 1) release();
-                            send(&maps.m[2], in / 2 + 1, col - 32 * in, row0, INT_MAX, INT_MAX, false, false);
-                        }
+                        const int box = q / 2 % kBoxes;
+                        if (q % 2 == 0) free_box();
+                        stage(r, box, q % 2, false);
+                        if (q == kQ - 1) release();
+                        if (q % 2 == 1) send(&maps.m[2], box, col - 32, row0, INT_MAX, INT_MAX, false);
                     }
                 } else {
                     uint32_t r[kQ][32];
@@ -526,18 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (f32) {
 #pragma unroll
                         for (int q = 0; q < kQ; ++q) {
-                            const int in = q % BOXES;
-                            if (in == 0) free_boxes();
-                            stage(r[q], in, true);
-                            if (in == BOXES - 1) send(map, BOXES, col0 + 32 * (q - in), to, a.dim, end, true, add);
+                            free_box();
+                            stage(r[q], q % kBoxes, 0, true);
+                            send(map, q % kBoxes, col0 + 32 * q, to, a.dim, end, add);
                         }
                     } else {
 #pragma unroll
                         for (int q = 0; q < kQ; ++q) {
-                            const int in = q % (2 * BOXES);
-                            if (in == 0) free_boxes();
-                            stage(r[q], in, false);
-                            if (in == 2 * BOXES - 1 || q == kQ - 1) send(map, in / 2 + 1, col0 + 32 * (q - in), to, a.dim, end, false, false);
+                            const int box = q / 2 % kBoxes;
+                            if (q % 2 == 0) free_box();
+                            stage(r[q], box, q % 2, false);
+                            if (q % 2 == 1) send(map, box, col0 + 32 * (q - 1), to, a.dim, end, false);
                         }
                     }
                 }
@@ -678,9 +681,11 @@ struct PackArgs {
     float *loss, *lse;          // forward: zeroed where a token does not count
     uint16_t *dx;               // backward: the same
     int64_t lddx;
-    const float *losses, *dloss, *dlse;     // backward
+    const float *losses, *lses, *dloss, *dlse;      // backward
     float scale;
-    float *norm;                // [rows]: the size of g at the target
+    int32_t *row_target;        // forward: [rows], the target of each row
+    float *norm;                // backward: [rows], the size of g at the target,
+    float4 *info;               // and what its gradient is made of
     uint16_t *xn;               // [rows][dim]: x times it
     int *status;
 };
@@ -744,13 +749,17 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
             src[before] = t;
             const bool fits = dbg_span(at + before, 1, g.rows, g.status);
             if (fits) g.map[at + before] = t;
+            if (fits && g.row_target) g.row_target[at + before] = g.target[t];
             if (g.norm) {
                 const float loss = g.losses[t], gl = g.dloss[t], gz = g.dlse ? g.dlse[t] : 0.0f;
-                const float n = fabsf(target_entry(g.scale, loss, gl, gz)), c = fabsf(g.scale * (gl + gz));
+                const float entry = target_entry(g.scale, loss, gl, gz), factor = g.scale * (gl + gz), n = fabsf(entry), c = fabsf(factor);
                 // the row stays as it is where that entry, or the others relative to it, are beyond all measure
                 const bool relative = n >= 0x1p-100f && n <= 0x1p100f && c <= n * 0x1p120f && c * -expm1f(-loss) <= n * 0x1p60f;
                 by[before] = relative ? n : 1.0f;
-                if (fits) g.norm[at + before] = by[before];
+                if (fits) {
+                    g.norm[at + before] = by[before];
+                    g.info[at + before] = make_float4(g.lses[t] * kLog2e, factor / by[before], entry / by[before], __int_as_float(g.target[t]));
+                }
             }
         } else if (mine && g.loss) {
             if (dbg_span(t, 1, g.tokens, g.status)) g.loss[t] = g.lse[t] = 0.0f;
@@ -950,7 +959,7 @@ struct XentPlan {
     int per_unit, parts;            // forward: tiles of a unit, maxima and sums of a row
     int64_t piece;                  // backward: vocabulary of a piece
     int splits;                     // backward: parts of dx's K
-    int64_t count, map, xp, xn, norm, part, g, acc, bytes;      // byte offsets
+    int64_t count, map, target, xp, xn, norm, info, part, g, acc, bytes;    // byte offsets
     XentPlan(int64_t tokens, int64_t vocab, int64_t dim, bool backward)
     {
         const bool one = single(tokens);
@@ -963,6 +972,7 @@ struct XentPlan {
         auto take = [&](int64_t n) { const int64_t p = at; at += up(n, 256); return p; };
         count = take(16);
         map = take(rows * 4);
+        target = take(rows * 4);
         xp = backward || packs(tokens, vocab, dim) ? take(rows * dim * 2) : 0;
         if (!backward) {
             // long units write less; 16 of them a group keep the groups' shares even
@@ -984,6 +994,7 @@ struct XentPlan {
             splits = (int)std::max<int64_t>(1, std::min((kv + share) / (share + 1), kv / 8));
             xn = take(rows * dim * 2);
             norm = take(rows * 4);
+            info = take(rows * 16);
             g = take(std::min(rows * up(vocab, kTile), std::max(rows * kTile, kGradMost)) * 2);
             // splits: at most groups / (mt * nd) + 1, and kv / 8
             acc = take(std::min(std::max<int64_t>(1, up(vocab, kTile) / (8 * kBK)) * rows * dim, sm_count() / 2 * kTile * kTile + rows * dim) * 4);
@@ -1075,16 +1086,20 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
     int rc;
     const void *xp = x;
     int64_t ldxp = ldx, xrows = tokens;
+    const int32_t *map = nullptr;
+    a.target = target;
     if (packs(tokens, vocab, dim)) {
         PackArgs g{};
         g.loss = loss;
         g.lse = lse;
+        g.row_target = reinterpret_cast<int32_t *>(ws + p.target);
         if ((rc = pack(p, ws, g, target, x, ldx, tokens, vocab, dim, status, st)) != FP8_OK) return rc;
         xp = ws + p.xp;
         ldxp = dim;
         xrows = p.rows;
         a.count = reinterpret_cast<int *>(ws + p.count);
-        a.map = reinterpret_cast<int32_t *>(ws + p.map);
+        map = reinterpret_cast<int32_t *>(ws + p.map);
+        a.target = g.row_target;
     }
     a.part = reinterpret_cast<float2 *>(ws + p.part);
     a.rows = p.rows;
@@ -1096,7 +1111,6 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
         Maps<XENT_LOSS> maps;
         if (!map_k(&maps.m[0], xp, dim, xrows, ldxp) || !map_k(&maps.m[1], w, dim, vocab, ldw)) return FP8_ERR_CUDA;
         maps.m[2] = maps.m[0];      // there is no matrix to write
-        a.target = target;
         a.tokens = (int)tokens;
         a.vocab = a.vn = (int)vocab;
         a.dim = (int)dim;
@@ -1115,7 +1129,7 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
     j.parts = p.parts;
     j.rows = p.rows;
     j.count = a.count;
-    j.map = a.map;
+    j.map = map;
     j.target = target;
     j.x = static_cast<const uint16_t *>(xp);
     j.w = static_cast<const uint16_t *>(w);
@@ -1141,17 +1155,18 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     pk.dx = static_cast<uint16_t *>(dx);
     pk.lddx = lddx;
     pk.losses = loss;
+    pk.lses = lse;
     pk.dloss = dloss;
     pk.dlse = dlse;
     pk.scale = scale;
     pk.norm = reinterpret_cast<float *>(ws + p.norm);
+    pk.info = reinterpret_cast<float4 *>(ws + p.info);
     pk.xn = reinterpret_cast<uint16_t *>(ws + p.xn);
     int rc = pack(p, ws, pk, target, x, ldx, tokens, vocab, dim, status, st);
     if (rc != FP8_OK) return rc;
     XentArgs a{};
     a.count = reinterpret_cast<int *>(ws + p.count);
-    a.map = reinterpret_cast<int32_t *>(ws + p.map);
-    a.target = target;
+    a.info = pk.info;
     a.tokens = (int)tokens;
     a.vocab = (int)vocab;
     a.dim = (int)dim;
@@ -1159,11 +1174,6 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.per_unit = 1;
     a.scale = scale;
     a.rows = p.rows;
-    a.loss = loss;
-    a.lse = lse;
-    a.dloss = dloss;
-    a.dlse = dlse;
-    a.norm = pk.norm;
     a.status = status;
     void *xp = ws + p.xp, *g = ws + p.g, *acc = ws + p.acc;
     a.dw_f32 = dw_dtype == FP8_OUT_F32;
@@ -1190,7 +1200,7 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
         if (rc != FP8_OK) return rc;
     }
     const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + kSumThreads - 1) / kSumThreads, (int64_t)sm_count() * 16);
-    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), kSumThreads, 0, st, static_cast<const float *>(acc), p.splits, p.rows, a.count, a.map, a.norm,
+    return launch_dependent(k_xent_dx_join, dim3((unsigned)blocks), kSumThreads, 0, st, static_cast<const float *>(acc), p.splits, p.rows, a.count, pk.map, pk.norm,
                             a.dim, static_cast<uint16_t *>(dx), lddx, a.tokens, status);
 }
 
