@@ -885,6 +885,14 @@ __device__ __forceinline__ void tc_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[3
         : "r"(taddr));
 }
 
+// The largest of three.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Packed FP32 pair arithmetic (two IEEE binary32 lanes, each rounded to
 // nearest like the scalar instruction).
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi)

@@ -141,14 +141,6 @@ __device__ __forceinline__ bool elect_one()
     return e != 0;
 }
 
-// The largest of three.
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // 4-D tiled bulk tensor load (columns, row in page, head, page).
 __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap *map, uint64_t *bar, int x, int y,
                                             int z, int w)

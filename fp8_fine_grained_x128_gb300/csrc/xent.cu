@@ -438,83 +438,111 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 if (!(ok = full_accumulator())) return;
-                const uint32_t from = tm_lane + (tc & 1) * BN + half * kCols;
                 const int col0 = nt * BN + half * kCols;    // in the piece, or of dx / dw
-                if constexpr (MODE == XENT_LOSS) {
-                    uint32_t r[kQ][32];
-                    auto load = [&](uint32_t (&to)[32], int q) {
-                        tc_ld_32x32b_x32(tm_lane + (tc & 1) * BN + half * kCols + q * 32, to);
-                    };
-#pragma unroll
-                    for (int q = 0; q < kQ; ++q) load(r[q], q);
+                auto load = [&](uint32_t (&to)[32], int q) { tc_ld_32x32b_x32(tm_lane + (tc & 1) * BN + half * kCols + q * 32, to); };
+                // f(v, q) for every 32 columns, the next ones on their way meanwhile
+                auto each_32 = [&](auto &&f) {
+                    uint32_t v[2][32];
+                    load(v[0], 0);
                     tc_wait_ld();
+                    settle(v[0]);
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q) settle(r[q]);
-                    release();
-                    for (int i = 1; i < chunks; ++i) {
-                        ++tc;
-                        if (!(ok = full_accumulator())) return;
-#pragma unroll
-                        for (int q = 0; q < kQ; ++q) {
-                            uint32_t v[32];
-                            load(v, q);
+                    for (int q = 0; q < kQ; ++q) {
+                        if (q + 1 < kQ) load(v[(q + 1) & 1], q + 1);
+                        f(v[q & 1], q);
+                        if (q + 1 < kQ) {
                             tc_wait_ld();
-                            settle(v);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[q][e] = __float_as_uint(__uint_as_float(r[q][e]) + __uint_as_float(v[e]));
+                            settle(v[(q + 1) & 1]);
+                            if (q + 2 == kQ) release();
                         }
-                        release();
                     }
-                    const int lim = a.vn - col0, at = target - col0;
-                    if (lim < kCols || (at >= 0 && at < kCols)) {   // beyond the vocabulary; the target is left out of the sum
-#pragma unroll
-                        for (int q = 0; q < kQ; ++q)
+                };
+                if constexpr (MODE == XENT_LOSS) {
+                    auto take = [&](uint32_t (&v)[32], int q) {
+                        const int lim = a.vn - (col0 + q * 32), at = target - (col0 + q * 32);
+                        if (lim < 32 || (unsigned)at < 32u) {       // beyond the vocabulary; the target is left out of the sum
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (q * 32 + i >= lim || q * 32 + i == at) r[q][i] = __float_as_uint(-INFINITY);
-                    }
-                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s[4] = {};
+                                if (i >= lim || i == at) v[i] = __float_as_uint(-INFINITY);
+                        }
+                        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q)
+                        for (int i = 0; i < 32; i += 2) m[i / 2 & 3] = max3(m[i / 2 & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                        const float high = max3(m[0], m[1], fmaxf(m[2], m[3])) * c;
+                        if (high > top) {
+                            sum *= ex2_approx_ftz(top - high);
+                            top = high;
+                        }
+                        const float off = top == -INFINITY ? 0.0f : -top;
+                        const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(off, off);
+                        uint64_t s[2] = {};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], __uint_as_float(r[q][i]));
-                    const float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-                    if (high > top) {
-                        sum *= ex2_approx_ftz(top - high);
-                        top = high;
-                    }
-                    const float off = top == -INFINITY ? 0.0f : -top;
+                        for (int i = 0; i < 32; i += 2) {
+                            float x, y;
+                            f2_unpack(f2_fma_bits(v[i], v[i + 1], c2, off2), x, y);
+                            s[i / 2 & 1] = f2_add(s[i / 2 & 1], f2_pack(ex2_approx_ftz(x), ex2_approx_ftz(y)));
+                        }
+                        float s0, s1;
+                        f2_unpack(f2_add(s[0], s[1]), s0, s1);
+                        sum += s0 + s1;
+                        asm volatile("" : "+f"(sum), "+f"(top));    // done before the wait for the next ones
+                    };
+                    if (chunks == 1) {
+                        each_32(take);
+                    } else {
+                        uint32_t r[kQ][32];
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[i & 3] += ex2_approx_ftz(fmaf(__uint_as_float(r[q][i]), c, off));
-                    sum += (s[0] + s[1]) + (s[2] + s[3]);
-                } else if constexpr (MODE == XENT_GRAD) {
-#pragma unroll 1
-                    for (int q = 0; q < kQ; ++q) {
-                        uint32_t r[32];
-                        tc_ld_32x32b_x32(from + q * 32, r);
+                        for (int q = 0; q < kQ; ++q) load(r[q], q);
                         tc_wait_ld();
-                        settle(r);
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q) settle(r[q]);
+                        release();
+                        for (int i = 1; i < chunks; ++i) {
+                            ++tc;
+                            if (!(ok = full_accumulator())) return;
+#pragma unroll
+                            for (int q = 0; q < kQ; ++q) {
+                                uint32_t v[32];
+                                load(v, q);
+                                tc_wait_ld();
+                                settle(v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) r[q][e] = __float_as_uint(__uint_as_float(r[q][e]) + __uint_as_float(v[e]));
+                            }
+                            release();
+                        }
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q) take(r[q], q);
+                    }
+                } else if constexpr (MODE == XENT_GRAD) {
+                    const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(-info.x, -info.x), by2 = f2_pack(info.y, info.y);
+                    each_32([&](uint32_t (&r)[32], int q) {
                         const int col = col0 + q * 32, at = target - col;
                         const int lim = row < rows ? a.vn - col : 0;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            float g = info.y * ex2_approx_ftz(fmaf(__uint_as_float(r[i]), c, -info.x));
-                            if (i == at) g = info.z;
-                            g = i < lim ? g : 0.0f;
-                            r[i] = __float_as_uint(g);
+                        for (int i = 0; i < 32; i += 2) {
+                            float x, y;
+                            f2_unpack(f2_fma_bits(r[i], r[i + 1], c2, off2), x, y);
+                            f2_unpack(f2_mul_bits(__float_as_uint(ex2_approx_ftz(x)), __float_as_uint(ex2_approx_ftz(y)), by2), x, y);
+                            r[i] = __float_as_uint(x);
+                            r[i + 1] = __float_as_uint(y);
+                        }
+                        if (lim < 32 || (unsigned)at < 32u) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                if (i == at) r[i] = __float_as_uint(info.z);
+                                if (i >= lim) r[i] = 0;
+                            }
                         }
                         const int box = q / 2 % kBoxes;
                         if (q % 2 == 0) free_box();
                         stage(r, box, q % 2, false);
-                        if (q == kQ - 1) release();
                         if (q % 2 == 1) send(&maps.m[2], box, col - 32, row0, INT_MAX, INT_MAX, false);
-                    }
+                    });
                 } else {
                     uint32_t r[kQ][32];
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q) tc_ld_32x32b_x32(from + q * 32, r[q]);
+                    for (int q = 0; q < kQ; ++q) load(r[q], q);
                     tc_wait_ld();
 #pragma unroll
                     for (int q = 0; q < kQ; ++q) {
