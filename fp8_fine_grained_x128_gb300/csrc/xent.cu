@@ -68,7 +68,7 @@ struct Form {
     static constexpr int kStages = (226 * 1024 - 1024 - kStaging) / kStage;
     static constexpr int kBars = 2 * kStages + 2 * 2 + 1;
     static constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBars * 8 + 16;
-    static_assert(kSmem <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
+    static_assert(kSmem + 1024 <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
 };
 
 // The tensor cores' sums lean towards zero, by up to a last place for every 16 of K
@@ -137,41 +137,79 @@ struct Walk {
         rem = p.units % step;
         extra = rem == 0 ? 0 : min(p.per_split / max(w.nkb, kTileCost), w.units / (step - rem));
     }
+    // The pair's unit i; whether there is one.
+    __device__ __forceinline__ bool unit(int i, Unit &t) const
+    {
+        const int j = i - (p.units / step + (mine < rem));      // beyond this pair's units of p
+        const bool dw = MODE == XENT_SUMS && j >= 0;
+        int64_t u = mine + (int64_t)i * step;
+        if (dw) {
+            const int ahead = mine >= rem ? extra : 0;
+            u = j < ahead ? (int64_t)j * (step - rem) + mine - rem : (int64_t)extra * (step - rem) + (int64_t)(j - ahead) * step + mine;
+        }
+        const Grid &g = dw ? w : p;
+        if (u >= g.units) return false;
+        const int flat = g.num_mt * g.num_ng;
+        t.split = (int)u / flat;
+        tile_coords_raster((int)u - t.split * flat, g.num_mt, g.num_ng, g.band, t.mt, t.nt0);
+        t.nt0 *= p.per;
+        t.dw = dw;
+        t.k0 = min(g.nkb, t.split * g.per_split);
+        t.k1 = min(g.nkb, t.k0 + g.per_split);
+        return true;
+    }
+    // body(unit, row of tiles of the next one where that is known), by the whole warp
     template <typename Body>
     __device__ __forceinline__ void each(bool &ok, Body &&body) const
     {
-        const int lane = threadIdx.x & 31, first = p.units / step + (mine < rem);    // units of p that are this pair's
+        const int lane = threadIdx.x & 31;
         for (int base = 0; ok; base += 32) {
-            const int i = base + lane, j = i - first;
-            const bool dw = MODE == XENT_SUMS && j >= 0;
-            int64_t u = mine + (int64_t)i * step;
-            if (dw) {
-                const int ahead = mine >= rem ? extra : 0;
-                u = j < ahead ? (int64_t)j * (step - rem) + mine - rem : (int64_t)extra * (step - rem) + (int64_t)(j - ahead) * step + mine;
-            }
-            const Grid &g = dw ? w : p;
-            const bool valid = u < g.units;
-            int of = 0, m = 0, n = 0;
-            if (valid) {
-                const int flat = g.num_mt * g.num_ng;
-                of = (int)u / flat;
-                tile_coords_raster((int)u - of * flat, g.num_mt, g.num_ng, g.band, m, n);
-            }
-            const int todo = __popc(__ballot_sync(0xffffffffu, valid));     // the valid ones are the first
+            Unit mine_{};
+            const int todo = __popc(__ballot_sync(0xffffffffu, unit(base + lane, mine_)));      // the valid ones are the first
             for (int k = 0; k < todo && ok; ++k) {
-                Unit t;
-                t.dw = MODE == XENT_SUMS ? __shfl_sync(0xffffffffu, (int)dw, k) : 0;
-                t.mt = __shfl_sync(0xffffffffu, m, k);
-                t.nt0 = __shfl_sync(0xffffffffu, n, k) * p.per;
+                auto from = [&](int v, int i) { return __shfl_sync(0xffffffffu, v, i); };
+                Unit t{};
+                t.mt = from(mine_.mt, k);
+                t.nt0 = from(mine_.nt0, k);
+                if (MODE == XENT_SUMS) {
+                    t.dw = from(mine_.dw, k);
+                    t.k0 = from(mine_.k0, k);
+                    t.k1 = from(mine_.k1, k);
+                    t.split = from(mine_.split, k);
+                }
                 t.nt1 = min(t.dw ? w.num_nt : p.num_nt, t.nt0 + p.per);
-                t.split = __shfl_sync(0xffffffffu, of, k);
-                const int nkb = t.dw ? w.nkb : p.nkb, per_split = t.dw ? w.per_split : p.per_split;
-                t.k0 = min(nkb, t.split * per_split);
-                t.k1 = min(nkb, t.k0 + per_split);
-                // the row of tiles after this one, where it is known
-                body(t, k + 1 < todo ? __shfl_sync(0xffffffffu, m, k + 1) : -1);
+                body(t, MODE <= XENT_GRAD && k + 1 < todo ? from(mine_.mt, k + 1) : -1);
             }
             if (todo < 32) break;
+        }
+    }
+    // body(unit) by lane 0 alone, until it returns false: the warp does not meet
+    // between the units (700 cycles a unit, which a pair's tensor cores would wait)
+    template <typename Body>
+    __device__ __forceinline__ bool each_alone(int4 *list, Body &&body) const
+    {
+        const int lane = threadIdx.x & 31;
+        for (int base = 0;; base += 32) {
+            Unit t{};
+            const bool valid = unit(base + lane, t);
+            list[lane] = make_int4(t.mt, t.nt0, t.k0, t.k1 << 1 | t.dw);
+            const int todo = __popc(__ballot_sync(0xffffffffu, valid));
+            __syncwarp();
+            bool ok = true;
+            if (lane == 0) {
+                for (int k = 0; k < todo && ok; ++k) {
+                    const int4 i = list[k];
+                    t.mt = i.x;
+                    t.nt0 = i.y;
+                    t.k0 = i.z;
+                    t.k1 = i.w >> 1;
+                    t.dw = i.w & 1;
+                    t.nt1 = min(t.dw ? w.num_nt : p.num_nt, t.nt0 + p.per);
+                    ok = body(t);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok || todo < 32) return ok;
         }
     }
 };
@@ -203,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kSums = MODE == XENT_SUMS;
     constexpr int kStages = F::kStages;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ int4 units[2][32];       // of the copying and of the issuing warp
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * F::kStage + F::kStaging);
     uint64_t *empty = full + kStages;
@@ -251,15 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         uint32_t it = 0;
-        bool ok = true;
-        walk.each(ok, [&](const Unit &t, int) {
-            const int m = t.mt * F::kM + rank * 128, blocks = (t.nt1 - t.nt0) * (t.k1 - t.k0);
-            if (lane == 0) {
-                int nt = t.nt0, kb = t.k0;
-                for (int i = 0; i < blocks; ++i) {
-                    const uint32_t n_it = it + i;
-                    const int s = n_it % kStages, n = nt * BN + rank * F::kOwnN;
-                    if (!thread_wait(smem_u32(&empty[s]), ((n_it / kStages) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
+        const bool ok = walk.each_alone(units[0], [&](const Unit &t) {
+            const int m = t.mt * F::kM + rank * 128;
+            for (int nt = t.nt0; nt < t.nt1; ++nt) {
+                const int n = nt * BN + rank * F::kOwnN;
+                for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!thread_wait(smem_u32(&empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, a.status)) return false;
                     // what lies outside a matrix is filled with zeros and counts its bytes all the same
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * F::kStage);
                     const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
@@ -284,22 +321,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < F::kOwnN; j += 128) load(sb + j * 128, &maps.m[1], kb * kBK, a.v0 + n + j);
                     }
-                    if (++kb == t.k1) {
-                        kb = t.k0;
-                        ++nt;
-                    }
                 }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (ok) it += blocks;
+            return true;
         });
         // the next kernel may be set up (k_xent_join reads this call's inputs before it waits: so not before this one has)
         dependents_launch();
         // the copies in flight land (the even CTA's barrier counts both CTAs'),
         // and the last stages' releases arrive, before the pair may leave
         if (lane == 0) {
-            const uint32_t first = it > (uint32_t)kStages ? it - kStages : 0, end = ok ? it : it + kStages;
-            for (uint32_t j = first; j < end; ++j) {
+            for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j) {
                 if (rank == 0) mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1, nullptr);
                 if (ok) mbar_wait_bounded(&empty[j % kStages], (j / kStages) & 1, abort_flag);
             }
@@ -312,38 +343,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (rank == 0) {
             uint32_t it = 0, tc = 0;
-            bool ok = true;
-            walk.each(ok, [&](const Unit &t, int) {
-                if (lane == 0) {
-                    const uint32_t idesc = kSums && t.dw ? idesc_bf16(F::kM, BN, true, true) : idesc_bf16(F::kM, BN, false, kSums);
-                    const int parts = (t.nt1 - t.nt0) * chunks;     // of the unit, an accumulator each
-                    for (int i = 0; i < parts && ok; ++i, ++tc) {
-                        const int c0 = chunks == 1 ? t.k0 : i % chunks * kChunk, c1 = chunks == 1 ? t.k1 : min(t.k1, c0 + kChunk);
-                        const uint32_t buf = tc & 1;
-                        if (!thread_wait(smem_u32(&tempty[buf]), ((tc >> 1) & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
+            walk.each_alone(units[1], [&](const Unit &t) {
+                const uint32_t idesc = kSums && t.dw ? idesc_bf16(F::kM, BN, true, true) : idesc_bf16(F::kM, BN, false, kSums);
+                const int parts = (t.nt1 - t.nt0) * chunks;     // of the unit, an accumulator each
+                for (int i = 0; i < parts; ++i, ++tc) {
+                    const int c0 = chunks == 1 ? t.k0 : i % chunks * kChunk, c1 = chunks == 1 ? t.k1 : min(t.k1, c0 + kChunk);
+                    const uint32_t buf = tc & 1;
+                    if (!thread_wait(smem_u32(&tempty[buf]), ((tc >> 1) & 1) ^ 1, abort_flag, a.status)) return false;
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + buf * BN;
+                    for (int kb = c0; kb < c1; ++kb, ++it) {
+                        const int s = it % kStages;
+                        if (!thread_wait(smem_u32(&full[s]), (it / kStages) & 1, abort_flag, a.status)) return false;
                         tc_fence_after();
-                        const uint32_t d = tmem_base + buf * BN;
-                        for (int kb = c0; kb < c1; ++kb, ++it) {
-                            const int s = it % kStages;
-                            if (!thread_wait(smem_u32(&full[s]), (it / kStages) & 1, abort_flag, a.status)) { ok = false; break; }
-                            tc_fence_after();
-                            const uint32_t sa = smem_u32(smem + s * F::kStage), sb = sa + F::kA;
-                            // 16 of K: 32 bytes along a row, or two 1024-byte swizzle atoms of rows
-                            const uint64_t ad = kSums && t.dw ? sdesc_mnmajor_sw128(sa, 8192, 1024) : sdesc_kmajor_sw128(sa);
-                            const uint64_t bd = kSums ? sdesc_mnmajor_sw128(sb, 8192, 1024) : sdesc_kmajor_sw128(sb);
-                            const uint64_t a_step = (kSums && t.dw ? 2048 : 32) >> 4, b_step = (kSums ? 2048 : 32) >> 4;
+                        const uint32_t sa = smem_u32(smem + s * F::kStage), sb = sa + F::kA;
+                        // 16 of K: 32 bytes along a row, or two 1024-byte swizzle atoms of rows
+                        const uint64_t ad = kSums && t.dw ? sdesc_mnmajor_sw128(sa, 8192, 1024) : sdesc_kmajor_sw128(sa);
+                        const uint64_t bd = kSums ? sdesc_mnmajor_sw128(sb, 8192, 1024) : sdesc_kmajor_sw128(sb);
+                        const uint64_t a_step = (kSums && t.dw ? 2048 : 32) >> 4, b_step = (kSums ? 2048 : 32) >> 4;
 #pragma unroll
-                            for (int k = 0; k < kBK / 16; ++k) {
-                                const uint32_t more = kb > c0 || k > 0;
-                                if (PAIR) tc_mma_f16_pair(d, ad + k * a_step, bd + k * b_step, idesc, more);
-                                else tc_mma_f16(d, ad + k * a_step, bd + k * b_step, idesc, more);
-                            }
-                            commit(&empty[s]);
+                        for (int k = 0; k < kBK / 16; ++k) {
+                            const uint32_t more = kb > c0 || k > 0;
+                            if (PAIR) tc_mma_f16_pair(d, ad + k * a_step, bd + k * b_step, idesc, more);
+                            else tc_mma_f16(d, ad + k * a_step, bd + k * b_step, idesc, more);
                         }
-                        if (ok) commit(&tfull[buf]);
+                        commit(&empty[s]);
                     }
+                    commit(&tfull[buf]);
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                return true;
             });
             if (lane == 0) commit(mma_done);
         }
