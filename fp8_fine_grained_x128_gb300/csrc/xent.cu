@@ -486,62 +486,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 if constexpr (MODE == XENT_LOSS) {
-                    auto take = [&](uint32_t (&v)[32], int q) {
-                        const int lim = a.vn - (col0 + q * 32), at = target - (col0 + q * 32);
-                        if (lim < 32 || (unsigned)at < 32u) {       // beyond the vocabulary; the target is left out of the sum
+                    uint32_t r[kQ][32];
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q) load(r[q], q);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q) settle(r[q]);
+                    release();
+                    for (int i = 1; i < chunks; ++i) {
+                        ++tc;
+                        if (!(ok = full_accumulator())) return;
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q) {
+                            uint32_t v[32];
+                            load(v, q);
+                            tc_wait_ld();
+                            settle(v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[q][e] = __float_as_uint(__uint_as_float(r[q][e]) + __uint_as_float(v[e]));
+                        }
+                        release();
+                    }
+                    const int lim = a.vn - col0, at = target - col0;
+                    if (lim < kCols || (unsigned)at < (unsigned)kCols) {    // beyond the vocabulary; the target is left out of the sum
+#pragma unroll
+                        for (int q = 0; q < kQ; ++q)
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (i >= lim || i == at) v[i] = __float_as_uint(-INFINITY);
-                        }
-                        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                                if (q * 32 + i >= lim || q * 32 + i == at) r[q][i] = __float_as_uint(-INFINITY);
+                    }
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) m[i / 2 & 3] = max3(m[i / 2 & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                        const float high = max3(m[0], m[1], fmaxf(m[2], m[3])) * c;
-                        if (high > top) {
-                            sum *= ex2_approx_ftz(top - high);
-                            top = high;
-                        }
-                        const float off = top == -INFINITY ? 0.0f : -top;
-                        const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(off, off);
-                        uint64_t s[2] = {};
+                    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) m[i / 2 & 3] = max3(m[i / 2 & 3], __uint_as_float(r[q][i]), __uint_as_float(r[q][i + 1]));
+                    const float high = max3(m[0], m[1], fmaxf(m[2], m[3])) * c;
+                    if (high > top) {
+                        sum *= ex2_approx_ftz(top - high);
+                        top = high;
+                    }
+                    const float off = top == -INFINITY ? 0.0f : -top;
+                    const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(off, off);
+                    uint64_t s[4] = {};
+#pragma unroll
+                    for (int q = 0; q < kQ; ++q)
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             float x, y;
-                            f2_unpack(f2_fma_bits(v[i], v[i + 1], c2, off2), x, y);
-                            s[i / 2 & 1] = f2_add(s[i / 2 & 1], f2_pack(ex2_approx_ftz(x), ex2_approx_ftz(y)));
+                            f2_unpack(f2_fma_bits(r[q][i], r[q][i + 1], c2, off2), x, y);
+                            s[i / 2 & 3] = f2_add(s[i / 2 & 3], f2_pack(ex2_approx_ftz(x), ex2_approx_ftz(y)));
                         }
-                        float s0, s1;
-                        f2_unpack(f2_add(s[0], s[1]), s0, s1);
-                        sum += s0 + s1;
-                        asm volatile("" : "+f"(sum), "+f"(top));    // done before the wait for the next ones
-                    };
-                    if (chunks == 1) {
-                        each_32(take);
-                    } else {
-                        uint32_t r[kQ][32];
-#pragma unroll
-                        for (int q = 0; q < kQ; ++q) load(r[q], q);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int q = 0; q < kQ; ++q) settle(r[q]);
-                        release();
-                        for (int i = 1; i < chunks; ++i) {
-                            ++tc;
-                            if (!(ok = full_accumulator())) return;
-#pragma unroll
-                            for (int q = 0; q < kQ; ++q) {
-                                uint32_t v[32];
-                                load(v, q);
-                                tc_wait_ld();
-                                settle(v);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) r[q][e] = __float_as_uint(__uint_as_float(r[q][e]) + __uint_as_float(v[e]));
-                            }
-                            release();
-                        }
-#pragma unroll
-                        for (int q = 0; q < kQ; ++q) take(r[q], q);
-                    }
+                    float s0, s1;
+                    f2_unpack(f2_add(f2_add(s[0], s[1]), f2_add(s[2], s[3])), s0, s1);
+                    sum += s0 + s1;
                 } else if constexpr (MODE == XENT_GRAD) {
                     const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(-info.x, -info.x), by2 = f2_pack(info.y, info.y);
                     each_32([&](uint32_t (&r)[32], int q) {
