@@ -1004,6 +1004,17 @@ constexpr int64_t kShallow = 512;
 // (8192 x 128000 x 4096 backward: 15.9 ms, with 192 MB 16.0, with 256 MB 15.8).
 constexpr int64_t kGradMost = (int64_t)112 << 20;
 
+// Tiles of a unit, `per` or more.  Short rows' products (8 cycles a tile and column of
+// x) last less than a tile's epilogue (2100 cycles, and 1600 for a unit), and longer
+// units are worth a less even share (4096 x 32000 x 256 forward: 84 us by single
+// tiles, 64 by four; from dim 600 on nothing changes).
+int longer_units(int per, int64_t mt, int64_t nt, int64_t groups, int64_t dim)
+{
+    auto cycles = [&](int64_t n) { return (mt * ((nt + n - 1) / n) + groups - 1) / groups * std::max(n * 8 * dim, n * 2100 + 1600); };
+    while (per < 8 && cycles(2 * per) * 33 < cycles(per) * 32) per *= 2;
+    return per;
+}
+
 // Sizes that follow from those of the call alone.  What is taken of the workspace
 // does not shrink when a size grows, so it serves all smaller calls too.
 struct XentPlan {
@@ -1031,6 +1042,7 @@ struct XentPlan {
             // long units write less; 16 of them a group keep the groups' shares even
             per_unit = 8;
             while (per_unit > 1 && mt * ((nt + per_unit - 1) / per_unit) < 16 * groups) per_unit /= 2;
+            per_unit = longer_units(per_unit, mt, nt, groups, dim);
             parts = (int)((nt + per_unit - 1) / per_unit) * 2;
             if (few(tokens, dim)) parts = (int)std::min<int64_t>((vocab + kFewRows * 8 - 1) / (kFewRows * 8), (int64_t)sm_count() * 2);
             // parts * mt: below 64 groups where units are shorter than 8 tiles
@@ -1224,7 +1236,6 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.vocab = (int)vocab;
     a.dim = (int)dim;
     a.splits = p.splits;
-    a.per_unit = 1;
     a.scale = scale;
     a.rows = p.rows;
     a.status = status;
