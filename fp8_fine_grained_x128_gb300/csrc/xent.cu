@@ -33,7 +33,7 @@
 // k_xent is a persistent kernel of CTA pairs (cta_group::2): a pair computes
 // 256 x 256 tiles, each CTA holding 128 rows of A and 128 columns of B of every
 // 64-deep stage, so that an SM fetches 32 KB where a CTA alone would fetch 48 KB
-// for its half of the tile.  Warp 0 copies (TMA, 3 to 7 stages), one thread of the
+// for its half of the tile.  Warp 0 copies (TMA, 4 to 7 stages), one thread of the
 // even CTA's warp 1 issues the MMAs, warps 2..9 drain one of two accumulators
 // while the next tile fills the other.  Few tokens take tiles of single CTAs.
 #include <limits.h>
@@ -58,13 +58,13 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kBox = 4096;              // staging for one copy: 32 rows of 128 bytes
 
 // PAIR: 256 x BN tiles by two CTAs, of 128 rows and BN / 2 columns each; else
-// 128 x BN tiles by one.  BOXES of staging for every epilogue warp (LOSS has no
+// 128 x BN tiles by one.  A box of staging for every epilogue warp (LOSS has no
 // matrix to write); the rest of the shared memory is stages.
-template <int MODE, bool PAIR, int BN, int BOXES>
+template <int MODE, bool PAIR, int BN>
 struct Form {
     static constexpr int kM = PAIR ? 256 : 128, kOwnN = PAIR ? BN / 2 : BN;
     static constexpr int kA = 128 * kBK * 2, kB = kOwnN * kBK * 2, kStage = kA + kB;
-    static constexpr int kStaging = kEpiWarps * BOXES * kBox;
+    static constexpr int kStaging = MODE == XENT_LOSS ? 0 : kEpiWarps * kBox;
     static constexpr int kStages = (226 * 1024 - 1024 - kStaging) / kStage;
     static constexpr int kBars = 2 * kStages + 2 * 2 + 1;
     static constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBars * 8 + 16;
@@ -233,11 +233,11 @@ __device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
 
 }  // namespace
 
-template <int MODE, bool PAIR, int BN, int BOXES>
+template <int MODE, bool PAIR, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_xent(const __grid_constant__ Maps<MODE> maps, const XentArgs a)
 {
-    using F = Form<MODE, PAIR, BN, BOXES>;
+    using F = Form<MODE, PAIR, BN>;
     constexpr bool kSums = MODE == XENT_SUMS;
     constexpr int kStages = F::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -383,21 +383,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = (warp - kEpiWarp0) >> 2;       // and its columns
         const uint32_t tm_lane = tmem_base + ((uint32_t)(lq * 32) << 16);
         constexpr int kCols = BN / 2, kQ = kCols / 32;  // of this warp
-        uint8_t *staging = smem + kStages * F::kStage + (warp - kEpiWarp0) * BOXES * kBox;
+        uint8_t *staging = smem + kStages * F::kStage + (warp - kEpiWarp0) * kBox;
         uint32_t tc = 0;
         bool ok = true;
 
-        // A result leaves through this warp's staging: boxes of 32 rows of 128 bytes,
-        // 16-byte chunks swizzled as the copies expect them (neither side meets a bank
-        // twice), filled in turn.  stage: 32 values of this lane's row to one half (BF16)
-        // of a box or all of it; send: box b to row row0, columns x and on.  What reaches
-        // over the matrix's edge is not written; a box beyond it is not sent.
-        auto free_box = [&] {       // the box sent BOXES boxes ago has been read
-            if (lane == 0) bulk_wait_read<(BOXES > 1 ? BOXES - 1 : 0)>();
+        // A result leaves through this warp's staging, a box of 32 rows of 128 bytes (a
+        // second one is worth less than the stage that it costs: 64 x 128000 x 4096
+        // backward 624 us, 642 with two), 16-byte chunks swizzled as the copies expect
+        // them (neither side meets a bank twice).  stage: 32 values of this lane's row to
+        // one half (BF16) of the box or all of it; send: the box to row row0, columns x
+        // and on.  What reaches over the matrix's edge is not written; a box beyond it is
+        // not sent.
+        auto free_box = [&] {
+            if (lane == 0) bulk_wait_read_all();
             __syncwarp();
         };
-        auto stage = [&](const uint32_t (&r)[32], int b, int half_box, bool f32) {
-            uint8_t *to = staging + b * kBox + lane * 128;
+        auto stage = [&](const uint32_t (&r)[32], int half_box, bool f32) {
+            uint8_t *to = staging + lane * 128;
             if (f32) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -407,17 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(to + (((j + 4 * half_box) ^ (lane & 7)) << 4)) = bf16x8(r + 8 * j);
             }
         };
-        auto send = [&](const CUtensorMap *to, int b, int x, int row0, int cols, int rows_end, bool add) {
+        auto send = [&](const CUtensorMap *to, int x, int row0, int cols, int rows_end, bool add) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane != 0) return;
-            if (row0 < rows_end && x < cols) {
-                if (add) tma_reduce_add_2d(to, staging + b * kBox, x, row0);
-                else tma_store_2d(to, staging + b * kBox, x, row0);
-            }
-            bulk_commit_group();    // an empty group too: free_box counts them
+            if (lane != 0 || row0 >= rows_end || x >= cols) return;
+            if (add) tma_reduce_add_2d(to, staging, x, row0);
+            else tma_store_2d(to, staging, x, row0);
+            bulk_commit_group();
         };
-        constexpr int kBoxes = BOXES > 0 ? BOXES : 1;
 
         auto settle = [](uint32_t (&v)[32]) {       // loaded values are not used before the wait for them
 #pragma unroll
@@ -559,10 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (i >= lim) r[i] = 0;
                             }
                         }
-                        const int box = q / 2 % kBoxes;
                         if (q % 2 == 0) free_box();
-                        stage(r, box, q % 2, false);
-                        if (q % 2 == 1) send(&maps.m[2], box, col - 32, row0, INT_MAX, INT_MAX, false);
+                        stage(r, q % 2, false);
+                        if (q % 2 == 1) send(&maps.m[2], col - 32, row0, INT_MAX, INT_MAX, false);
                     });
                 } else {
                     uint32_t r[kQ][32];
@@ -584,16 +582,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int q = 0; q < kQ; ++q) {
                             free_box();
-                            stage(r[q], q % kBoxes, 0, true);
-                            send(map, q % kBoxes, col0 + 32 * q, to, a.dim, end, add);
+                            stage(r[q], 0, true);
+                            send(map, col0 + 32 * q, to, a.dim, end, add);
                         }
                     } else {
 #pragma unroll
                         for (int q = 0; q < kQ; ++q) {
-                            const int box = q / 2 % kBoxes;
                             if (q % 2 == 0) free_box();
-                            stage(r[q], box, q % 2, false);
-                            if (q % 2 == 1) send(map, box, col0 + 32 * (q - 1), to, a.dim, end, false);
+                            stage(r[q], q % 2, false);
+                            if (q % 2 == 1) send(map, col0 + 32 * (q - 1), to, a.dim, end, false);
                         }
                     }
                 }
@@ -995,11 +992,6 @@ bool single(int64_t tokens) { return tokens <= 128; }
 // Whether k_xent_few takes the forward: its x has to fit, twice an SM.
 bool few(int64_t tokens, int64_t dim) { return tokens <= kFewTokens && (tokens > 2 ? 4 : tokens) * dim * 4 <= kFewSmem; }
 
-// Up to so many tokens (dw's K), a tile of dw takes longer to write than to
-// compute, and a second box of staging an epilogue warp is worth more than a sixth
-// stage (64 x 64000 x 4096: dw 131 -> 117 us; 8192 tokens: 1% slower).
-constexpr int64_t kShallow = 512;
-
 // Elements of g that the workspace holds (224 MB), unless a tile's columns take more
 // (8192 x 128000 x 4096 backward: 15.9 ms, with 192 MB 16.0, with 256 MB 15.8).
 constexpr int64_t kGradMost = (int64_t)112 << 20;
@@ -1068,19 +1060,19 @@ struct XentPlan {
     }
 };
 
-template <int MODE, bool PAIR, int BN, int BOXES>
+template <int MODE, bool PAIR, int BN>
 int run(const Maps<MODE> &maps, const XentArgs &a, cudaStream_t st)
 {
-    using F = Form<MODE, PAIR, BN, BOXES>;
+    using F = Form<MODE, PAIR, BN>;
     static bool attr_done[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!attr_done[dev & 63]) {
-        if (cudaFuncSetAttribute(k_xent<MODE, PAIR, BN, BOXES>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess) return FP8_ERR_CUDA;
+        if (cudaFuncSetAttribute(k_xent<MODE, PAIR, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess) return FP8_ERR_CUDA;
         attr_done[dev & 63] = true;
     }
     const int sms = sm_count();
-    return launch_dependent_cluster(k_xent<MODE, PAIR, BN, BOXES>, dim3((unsigned)(PAIR ? sms / 2 * 2 : sms)), PAIR ? 2 : 1, kThreads, F::kSmem, st, maps,
+    return launch_dependent_cluster(k_xent<MODE, PAIR, BN>, dim3((unsigned)(PAIR ? sms / 2 * 2 : sms)), PAIR ? 2 : 1, kThreads, F::kSmem, st, maps,
                                     a);
 }
 
@@ -1184,9 +1176,9 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.band = 16;
         a.scale = scale;
         a.status = status;
-        rc = !single(tokens) ? run<XENT_LOSS, true, 256, 0>(maps, a, st)
-             : p.bn == 256   ? run<XENT_LOSS, false, 256, 0>(maps, a, st)
-                             : run<XENT_LOSS, false, 128, 0>(maps, a, st);
+        rc = !single(tokens) ? run<XENT_LOSS, true, 256>(maps, a, st)
+             : p.bn == 256   ? run<XENT_LOSS, false, 256>(maps, a, st)
+                             : run<XENT_LOSS, false, 128>(maps, a, st);
     }
     if (rc != FP8_OK) return rc;
     JoinArgs j{};
@@ -1254,13 +1246,13 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.v0 = (int)v;
         a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
         a.band = 16;
-        rc = !single(tokens) ? run<XENT_GRAD, true, 256, 1>(grad, a, st)
-             : p.bn == 256   ? run<XENT_GRAD, false, 256, 2>(grad, a, st)
-                             : run<XENT_GRAD, false, 128, 1>(grad, a, st);
+        rc = !single(tokens) ? run<XENT_GRAD, true, 256>(grad, a, st)
+             : p.bn == 256   ? run<XENT_GRAD, false, 256>(grad, a, st)
+                             : run<XENT_GRAD, false, 128>(grad, a, st);
         if (rc != FP8_OK) return rc;
         a.band = 8;
         a.dx_add = v > 0;
-        rc = tokens <= kShallow ? run<XENT_SUMS, true, 256, 2>(sums, a, st) : run<XENT_SUMS, true, 256, 1>(sums, a, st);
+        rc = run<XENT_SUMS, true, 256>(sums, a, st);
         if (rc != FP8_OK) return rc;
     }
     const int64_t blocks = std::min<int64_t>((tokens * (dim / 8) + kSumThreads - 1) / kSumThreads, (int64_t)sm_count() * 16);
