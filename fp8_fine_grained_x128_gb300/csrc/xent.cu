@@ -39,6 +39,7 @@
 #include <limits.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -715,6 +716,197 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_xent_few(const uint16_t *__r
 }
 
 // ---------------------------------------------------------------------------
+// Backward of up to 4 tokens, W read and dw written once (k_xent reads W twice:
+// 1 x 128000 x 4096 616 us, 350 here; 1 x 1151 x 440 21 and 6) and everything in FP32.  A team of warps,
+// 8 columns a thread, takes R rows of W at a time: their logits by a reduction over
+// the team (halving the values with every exchange, so that each lane ends with one),
+// g by each warp for itself, then g x to dw and g w to the thread's sums of dx.  The
+// CTAs' sums of dx are added in order by k_xent_few_dx.
+// ---------------------------------------------------------------------------
+constexpr int kFewGradThreads = 512, kFewGradDim = 8 * kFewGradThreads;
+
+enum { DW_F32 = 0, DW_ADD = 1, DW_BF16 = 2 };
+
+struct FewGradArgs {
+    const uint16_t *x, *w;
+    int64_t ldx, ldw, lddw;
+    const int32_t *target;
+    const float *loss, *lse, *dloss, *dlse;
+    int tokens, vocab, dim;
+    float scale;
+    void *dw;
+    float *part;            // [CTA][T][dim]: sums of dx
+    int team_warps, teams;
+    int *status;
+};
+
+template <int T, int OUT>
+__global__ void __launch_bounds__(kFewGradThreads, 1) k_xent_few_grad(const FewGradArgs a)
+{
+    constexpr int R = kFewRows, N = R * T, kLanes = 32 / N;     // N values, kLanes lanes each
+    extern __shared__ float dxs[];          // [team][T][columns]
+    __shared__ float sums[2][kFewGradThreads / 32][N];
+    dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / a.team_warps, first_warp = team * a.team_warps;
+    const int col = (threadIdx.x - first_warp * 32) * 8, cols = a.team_warps * 256;
+    const bool in = col < a.dim;
+    auto counts = [&](int t) { return t < a.tokens && a.target[t] >= 0 && a.target[t] < a.vocab; };
+    if (blockIdx.x == 0 && (int)threadIdx.x < a.tokens && a.target[threadIdx.x] >= a.vocab) set_status(a.status, FP8_ERR_INVALID_ARG);
+    uint64_t x[T][4], dx[T][4] = {};
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const uint4 q = in && counts(t) ? *reinterpret_cast<const uint4 *>(a.x + t * a.ldx + col) : make_uint4(0, 0, 0, 0);
+        x[t][0] = p2_bf16x2(q.x);
+        x[t][1] = p2_bf16x2(q.y);
+        x[t][2] = p2_bf16x2(q.z);
+        x[t][3] = p2_bf16x2(q.w);
+    }
+    // this lane's value: of row `row` and token `token`
+    const int value = lane / kLanes, row = value / T, token = value % T;
+    const float c = a.scale * kLog2e;
+    const bool counted = counts(token);
+    int target = -1;
+    float lse2 = 0.0f, factor = 0.0f, entry = 0.0f;
+    if (counted) {
+        const float gl = a.dloss[token], gz = a.dlse ? a.dlse[token] : 0.0f;
+        target = a.target[token];
+        lse2 = a.lse[token] * kLog2e;
+        factor = a.scale * (gl + gz);
+        entry = target_entry(a.scale, a.loss[token], gl, gz);
+    }
+    const int groups = (a.vocab + R - 1) / R, step = gridDim.x * a.teams;
+    auto fetch = [&](int group, uint4 (&to)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t v = (int64_t)group * R + r;
+            to[r] = in && v < a.vocab ? ldg_stream(a.w + v * a.ldw + col) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    uint4 q[R];
+    int group = blockIdx.x * a.teams + team;
+    fetch(group, q);
+    for (int k = 0; group < groups; group += step, k ^= 1) {
+        uint4 next[R];
+        fetch(group + step, next);
+        float z[N];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint64_t w[4] = {p2_bf16x2(q[r].x), p2_bf16x2(q[r].y), p2_bf16x2(q[r].z), p2_bf16x2(q[r].w)};
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                uint64_t acc = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc = p2_fma(w[e], x[t][e], acc);
+                float lo, hi;
+                f2_unpack(acc, lo, hi);
+                z[r * T + t] = lo + hi;
+            }
+        }
+#pragma unroll
+        for (int o = 16, n = N / 2; o > 0; o >>= 1, n >>= 1) {
+            if (n > 0) {
+                const bool upper = lane & o;
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float keep = upper ? z[i + n] : z[i], give = upper ? z[i] : z[i + n];
+                    z[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            } else {
+                z[0] += __shfl_xor_sync(0xffffffffu, z[0], o);
+            }
+        }
+        float logit = z[0];
+        if (a.team_warps > 1) {
+            if (lane % kLanes == 0) sums[k][warp][value] = logit;
+            named_bar_sync(1 + team, a.team_warps * 32);
+            logit = 0.0f;
+            for (int i = 0; i < a.team_warps; ++i) logit += sums[k][first_warp + i][value];
+        }
+        const int v0 = group * R, v = v0 + row;
+        float g = factor * ex2_approx_ftz(fmaf(logit, c, -lse2));
+        if (v == target) g = entry;
+        if (!counted || v >= a.vocab) g = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint64_t w[4] = {p2_bf16x2(q[r].x), p2_bf16x2(q[r].y), p2_bf16x2(q[r].z), p2_bf16x2(q[r].w)};
+            uint64_t out[4] = {};
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const float gt = __shfl_sync(0xffffffffu, g, (r * T + t) * kLanes);
+                const uint64_t g2 = f2_pack(gt, gt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    out[e] = p2_fma(g2, x[t][e], out[e]);
+                    dx[t][e] = p2_fma(g2, w[e], dx[t][e]);
+                }
+            }
+            const int64_t at = (int64_t)(v0 + r) * a.lddw + col;
+            if (!in || v0 + r >= a.vocab || !dbg_span(at, 8, (int64_t)(a.vocab - 1) * a.lddw + a.dim, a.status)) continue;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f2_unpack(out[e], f[2 * e], f[2 * e + 1]);
+            if (OUT == DW_BF16) {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dw) + at) =
+                    make_uint4(bf16x2_rn(f[0], f[1]), bf16x2_rn(f[2], f[3]), bf16x2_rn(f[4], f[5]), bf16x2_rn(f[6], f[7]));
+            } else {
+                float *to = static_cast<float *>(a.dw) + at;
+#pragma unroll
+                for (int h = 0; h < 8; h += 4) {
+                    if (OUT == DW_ADD)
+                        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + h), "f"(f[h]), "f"(f[h + 1]),
+                                     "f"(f[h + 2]), "f"(f[h + 3])
+                                     : "memory");
+                    else
+                        *reinterpret_cast<float4 *>(to + h) = make_float4(f[h], f[h + 1], f[h + 2], f[h + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) q[r] = next[r];
+    }
+    dependents_launch();
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            f2_unpack(dx[t][e], lo, hi);
+            *reinterpret_cast<float2 *>(&dxs[(team * T + t) * cols + col + 2 * e]) = make_float2(lo, hi);
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < T * cols; i += blockDim.x) {
+        const int t = i / cols, at = i - t * cols;
+        float sum = 0.0f;
+        for (int m = 0; m < a.teams; ++m) sum += dxs[(m * T + t) * cols + at];
+        if (at < a.dim && dbg_cell(blockIdx.x * T + t, at, 1, (int64_t)gridDim.x * T, a.dim, a.status))
+            a.part[((int64_t)blockIdx.x * T + t) * a.dim + at] = sum;
+    }
+}
+
+// dx: a CTA for 32 columns of a token, a warp for every eighth of the parts.
+__global__ void __launch_bounds__(256) k_xent_few_dx(const float *__restrict__ part, int parts, int T, const int32_t *__restrict__ target, int vocab,
+                                                  int dim, uint16_t *__restrict__ dx, int64_t lddx, int tokens, int *status)
+{
+    __shared__ float sums[8][32];
+    dependents_launch();
+    dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.y, col = blockIdx.x * 32 + lane;
+    float sum = 0.0f;
+    if (col < dim) {
+#pragma unroll 10
+        for (int i = warp; i < parts; i += 8) sum += part[((int64_t)i * T + t) * dim + col];
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0 || col >= dim) return;
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += sums[i][lane];
+    if (target[t] < 0 || target[t] >= vocab) sum = 0.0f;       // whatever W holds
+    if (dbg_span(t * lddx + col, 1, (tokens - 1) * lddx + dim, status)) dx[t * lddx + col] = (uint16_t)bf16x2_rn(sum, 0.0f);
+}
+
+// ---------------------------------------------------------------------------
 // The counted tokens' rows of x, one behind another, and the token of each.  Every CTA takes a range of tokens and
 // counts the ones before it by itself.  Rows of the outputs that belong to
 // tokens left out are zeroed here.
@@ -992,6 +1184,12 @@ bool single(int64_t tokens) { return tokens <= 128; }
 // Whether k_xent_few takes the forward: its x has to fit, twice an SM.
 bool few(int64_t tokens, int64_t dim) { return tokens <= kFewTokens && (tokens > 2 ? 4 : tokens) * dim * 4 <= kFewSmem; }
 
+// Whether k_xent_few_grad takes the backward, and the CTAs that it may have.  With 3
+// or 4 tokens and one team an SM nothing hides a team's exchanges (4 x 128000 x 4096:
+// 696 us, k_xent 617; x 2048, two teams: 339 and 322, but 3 x 3456 x 1672 21 and 32).
+bool few_grad(int64_t tokens, int64_t dim) { return tokens <= 2 ? dim <= kFewGradDim : tokens <= kFewTokens && dim <= kFewGradDim / 2; }
+int64_t few_grad_ctas(int64_t vocab) { return std::min<int64_t>(sm_count(), (vocab + kFewRows - 1) / kFewRows); }
+
 // Elements of g that the workspace holds (224 MB), unless a tile's columns take more
 // (8192 x 128000 x 4096 backward: 15.9 ms, with 192 MB 16.0, with 256 MB 15.8).
 constexpr int64_t kGradMost = (int64_t)112 << 20;
@@ -1056,9 +1254,30 @@ struct XentPlan {
             // splits: at most groups / (mt * nd) + 1, and kv / 8
             acc = take(std::min(std::max<int64_t>(1, up(vocab, kTile) / (8 * kBK)) * rows * dim, sm_count() / 2 * kTile * kTile + rows * dim) * 4);
         }
-        bytes = at;
+        bytes = backward ? std::max(at, xp + few_grad_ctas(vocab) * kFewTokens * dim * 4) : at;      // k_xent_few_grad's part lies at xp
     }
 };
+
+template <int T, int OUT>
+int run_few_grad(FewGradArgs &a, void *dx, int64_t lddx, cudaStream_t st)
+{
+    a.team_warps = (a.dim + 255) / 256;
+    a.teams = kFewGradThreads / 32 / a.team_warps;
+    const int threads = a.teams * a.team_warps * 32;
+    const int64_t groups = (a.vocab + kFewRows - 1) / kFewRows, ctas = std::min((groups + a.teams - 1) / a.teams, few_grad_ctas(a.vocab));
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!attr_done[dev & 63]) {
+        if (cudaFuncSetAttribute(k_xent_few_grad<T, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewGradThreads * 8 * T * 4) != cudaSuccess)
+            return FP8_ERR_CUDA;
+        attr_done[dev & 63] = true;
+    }
+    const int rc = launch_dependent(k_xent_few_grad<T, OUT>, dim3((unsigned)ctas), threads, (size_t)threads * 8 * T * 4, st, a);
+    if (rc != FP8_OK) return rc;
+    return launch_dependent(k_xent_few_dx, dim3((unsigned)((a.dim + 31) / 32), (unsigned)a.tokens), 256, 0, st, a.part, (int)ctas, T, a.target,
+                            a.vocab, a.dim, static_cast<uint16_t *>(dx), lddx, a.tokens, a.status);
+}
 
 template <int MODE, bool PAIR, int BN>
 int run(const Maps<MODE> &maps, const XentArgs &a, cudaStream_t st)
@@ -1208,6 +1427,35 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
 {
     const XentPlan p(tokens, vocab, dim, true);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (few_grad(tokens, dim)) {
+        FewGradArgs a{};
+        a.x = static_cast<const uint16_t *>(x);
+        a.w = static_cast<const uint16_t *>(w);
+        a.ldx = ldx;
+        a.ldw = ldw;
+        a.lddw = lddw;
+        a.target = target;
+        a.loss = loss;
+        a.lse = lse;
+        a.dloss = dloss;
+        a.dlse = dlse;
+        a.tokens = (int)tokens;
+        a.vocab = (int)vocab;
+        a.dim = (int)dim;
+        a.scale = scale;
+        a.dw = dw;
+        a.part = reinterpret_cast<float *>(ws + p.xp);
+        a.status = status;
+        auto with = [&](auto t) {
+            constexpr int T = decltype(t)::value;
+            return dw_dtype != FP8_OUT_F32 ? run_few_grad<T, DW_BF16>(a, dx, lddx, st)
+                   : accumulate            ? run_few_grad<T, DW_ADD>(a, dx, lddx, st)
+                                           : run_few_grad<T, DW_F32>(a, dx, lddx, st);
+        };
+        return tokens == 1   ? with(std::integral_constant<int, 1>{})
+               : tokens == 2 ? with(std::integral_constant<int, 2>{})
+                             : with(std::integral_constant<int, 4>{});
+    }
     PackArgs pk{};
     pk.dx = static_cast<uint16_t *>(dx);
     pk.lddx = lddx;

@@ -61,7 +61,8 @@ def forward(x, w, t, scale=1.0, ws=None):
 
 
 SIZES = [(1, 1, 8), (1, 257, 64), (2, 7, 8), (3, 5003, 72), (127, 256, 128), (128, 255, 200), (129, 1000, 64), (255, 513, 136),
-         (256, 256, 256), (257, 1025, 64), (300, 2000, 512), (513, 300, 1024), (1000, 9001, 320), (5, 40000, 1024), (4, 10007, 1032), (2, 31, 4096), (1, 70001, 8), (4, 300, 8192), (70, 400, 6152)]
+         (256, 256, 256), (257, 1025, 64), (300, 2000, 512), (513, 300, 1024), (1000, 9001, 320), (5, 40000, 1024), (4, 10007, 1032), (2, 31, 4096), (1, 70001, 8), (4, 300, 8192), (70, 400, 6152),
+         (1, 5001, 3992), (2, 3001, 264), (3, 2002, 4096)]
 
 
 @pytest.mark.parametrize("T,V,D", SIZES)
@@ -90,7 +91,7 @@ def test_small_losses_keep_their_digits():
     assert bool(((loss - want).abs() <= want * tol)[normal].all())
 
 
-@pytest.mark.parametrize("T", [40, 700])
+@pytest.mark.parametrize("T", [4, 40, 700])
 def test_rows_that_do_not_count_hold_anything(T):
     x, w, t = make(T, 900, 128, 0.5, seed=5)
     dl, dz = torch.rand(T, device="cuda"), torch.rand(T, device="cuda")
@@ -134,7 +135,7 @@ def test_no_token_counts():
 
 
 def test_target_out_of_range_is_recorded_and_left_out():
-    for T in (30, 300):
+    for T in (4, 30, 300):
         x, w, t = make(T, 100, 64, seed=8)
         ref = t.clone()
         ref[[2, T - 1]] = -1
