@@ -1179,7 +1179,14 @@ bool packs(int64_t tokens, int64_t vocab, int64_t dim) { return tokens > kTile &
 // Up to 128 tokens, one CTA's tiles hold them all, and a pair's would be half
 // empty: W streams past at 128 x BN tiles by single CTAs (64 x 128000 x 4096 forward:
 // 175 us in pairs' tiles, 168 so, HBM's floor is 157).
-bool single(int64_t tokens) { return tokens <= 128; }
+// So do products that 128 x 128 tiles lay out over the SMs at once, whose length is a
+// tile's (783 x 2512 x 304 forward: 10.0 us in pairs' tiles, 8.6 so; 170 x 1594 x 2040
+// 19.0 and 16.8), unless W is most of what they read, which a pair fetches once for
+// 256 rows (256 x 9000 x 1024: 12.8 and 13.8).
+bool single(int64_t tokens, int64_t vocab)
+{
+    return tokens <= 128 || (vocab <= 16 * tokens && (tokens + 127) / 128 * ((vocab + 127) / 128) <= sm_count());
+}
 
 // Whether k_xent_few takes the forward: its x has to fit, twice an SM.
 bool few(int64_t tokens, int64_t dim) { return tokens <= kFewTokens && (tokens > 2 ? 4 : tokens) * dim * 4 <= kFewSmem; }
@@ -1216,7 +1223,7 @@ struct XentPlan {
     int64_t count, map, target, xp, xn, norm, info, part, g, acc, bytes;    // byte offsets
     XentPlan(int64_t tokens, int64_t vocab, int64_t dim, bool backward)
     {
-        const bool one = single(tokens);
+        const bool one = single(tokens, vocab);
         rows = up(tokens, kTile);
         const int64_t mt = rows / kTile, groups = std::max(1, one ? sm_count() : sm_count() / 2);
         // narrower tiles where the wider ones would leave CTAs without any
@@ -1395,7 +1402,7 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.band = 16;
         a.scale = scale;
         a.status = status;
-        rc = !single(tokens) ? run<XENT_LOSS, true, 256>(maps, a, st)
+        rc = !single(tokens, vocab) ? run<XENT_LOSS, true, 256>(maps, a, st)
              : p.bn == 256   ? run<XENT_LOSS, false, 256>(maps, a, st)
                              : run<XENT_LOSS, false, 128>(maps, a, st);
     }
@@ -1494,7 +1501,7 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.v0 = (int)v;
         a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
         a.band = 16;
-        rc = !single(tokens) ? run<XENT_GRAD, true, 256>(grad, a, st)
+        rc = !single(tokens, vocab) ? run<XENT_GRAD, true, 256>(grad, a, st)
              : p.bn == 256   ? run<XENT_GRAD, false, 256>(grad, a, st)
                              : run<XENT_GRAD, false, 128>(grad, a, st);
         if (rc != FP8_OK) return rc;

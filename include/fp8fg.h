@@ -695,10 +695,10 @@ FP8FG_API int fp8_linear_xent_fwd(const void *x, int64_t tokens, int64_t dim, in
  *   g[t][v] = scale * ((gl + gz) p_v - gl [v = target[t]])
  *   dx = g w (BF16),   dw (+)= g^T x (BF16 or FP32; dw_dtype)
  * p_target - 1 is taken from loss, as expm1(-loss).  The operands of the two
- * products are BF16 (calls of up to 4 tokens may take FP32): each token's g relative to its entry at the target (which is
- * then +-1), and for dw x times that entry; or g and x as they are where that entry
- * is below 2^-100, above 2^100 or less than 2^-60 of another.  Everything else is
- * FP32 up to the results.
+ * products are BF16 (FP32 in some calls of up to 4 tokens): each token's g relative
+ * to its entry at the target (which is then +-1), and for dw x times that entry; or g
+ * and x as they are where that entry is below 2^-100, above 2^100 or less than 2^-60
+ * of another.  Everything else is FP32 up to the results.
  * loss, lse: as fp8_linear_xent_fwd left them for the same x, w, target, scale.
  * accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): added to dw in one addition an
  * element (operands and results below 2^-126 count as zero there); else every row
