@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(256) k_embedding_joins(EmbedSumArgs g)
 // Backward of few tokens in one launch: every CTA sorts all of them for itself
 // (2 keys a thread, in its shared memory) and then sums 32 columns: 4 lanes take
 // a piece of 8 sorted tokens, and the runs that reach over pieces are added up
-// from shared memory.  Three launches of the form above took 16 us at 1000 x 1024.
+// from shared memory (1000 x 1024: 10 us, three launches of the form above 16).
 // ---------------------------------------------------------------------------
 constexpr int kSmallKeys = 2, kSmallMost = kSmallKeys * kClusterThreads, kSmallPieces = kSmallMost / 8;
 
