@@ -87,6 +87,7 @@ struct XentArgs {
     int per_unit;               // LOSS: tiles of a unit
     int splits;                 // dx: parts of K
     int band;                   // M tiles of a raster band
+    int box;                    // single CTAs: rows of x that are fetched for a tile (the others' results are not used)
     float scale;
     // LOSS
     const int32_t *target;      // of every row
@@ -299,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
                     const int s = it % kStages;
                     if (!thread_wait(smem_u32(&empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, a.status)) return false;
-                    // what lies outside a matrix is filled with zeros and counts its bytes all the same
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * F::kStage);
+                    // what of a copy lies outside its matrix is filled with zeros and counts its bytes all the same
+                    const int bytes = PAIR || kSums ? (PAIR ? 2 : 1) * F::kStage : a.box * (kBK * 2) + F::kB;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
                     const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : 0;
                     uint8_t *sa = smem + s * F::kStage, *sb = sa + F::kA;
                     auto load = [&](uint8_t *to, const CUtensorMap *map, int x, int y) {
@@ -1329,10 +1331,15 @@ int run_few(const void *x, int64_t ldx, const void *w, int64_t ldw, const int32_
                             static_cast<const uint16_t *>(w), ldw, target, (int)tokens, (int)vocab, (int)dim, scale, part, p.rows, status);
 }
 
-// K-major operand: rows of K, 128 of them a box; MN-major: rows along K, boxes of 64 columns.
-bool map_k(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t ld)
+// Rows of x in a copy: up to 128 tokens all that there are, since a copy that lies
+// mostly outside its matrix is slow (14 x 67014 x 1896 forward: 84 us with 128 rows, 52
+// with 16; from 128 tokens on smaller copies gain nothing).
+int x_box(int64_t tokens) { return (int)std::min<int64_t>(128, up(tokens, 8)); }
+
+// K-major operand: rows of K, `box` of them a copy; MN-major: rows along K, boxes of 64 columns.
+bool map_k(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t ld, int box = 128)
 {
-    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, kBK, 128,
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, (uint64_t)cols, (uint64_t)rows, (uint64_t)ld * 2, kBK, (uint32_t)box,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 bool map_mn(CUtensorMap *m, const void *p, int64_t cols, int64_t rows, int64_t ld)
@@ -1404,7 +1411,8 @@ int launch_linear_xent_fwd(const void *x, int64_t ldx, const void *w, int64_t ld
                            : run_few<4>(x, ldx, w, ldw, target, tokens, vocab, dim, scale, a.part, p, status, st);
     } else {
         Maps<XENT_LOSS> maps;
-        if (!map_k(&maps.m[0], xp, dim, xrows, ldxp) || !map_k(&maps.m[1], w, dim, vocab, ldw)) return FP8_ERR_CUDA;
+        a.box = x_box(tokens);
+        if (!map_k(&maps.m[0], xp, dim, xrows, ldxp, a.box) || !map_k(&maps.m[1], w, dim, vocab, ldw)) return FP8_ERR_CUDA;
         maps.m[2] = maps.m[0];      // there is no matrix to write
         a.tokens = (int)tokens;
         a.vocab = a.vn = (int)vocab;
@@ -1503,7 +1511,8 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.dw_add = accumulate;
     Maps<XENT_GRAD> grad;
     Maps<XENT_SUMS> sums;
-    if (!map_k(&grad.m[0], xp, dim, p.rows, dim) || !map_k(&grad.m[1], w, dim, vocab, ldw) ||
+    a.box = x_box(tokens);
+    if (!map_k(&grad.m[0], xp, dim, p.rows, dim, a.box) || !map_k(&grad.m[1], w, dim, vocab, ldw) ||
         !map_out(&grad.m[2], g, false, p.piece, p.rows, p.piece) || !map_k(&sums.m[0], g, p.piece, p.rows, p.piece) ||
         !map_mn(&sums.m[1], w, dim, vocab, ldw) || !map_out(&sums.m[2], acc, true, dim, p.splits * p.rows, dim) ||
         !map_mn(&sums.m[3], g, p.piece, p.rows, p.piece) || !map_mn(&sums.m[4], pk.xn, dim, p.rows, dim) ||
