@@ -329,6 +329,35 @@ def test_one_workspace_for_calls_of_many_sizes():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,V,D", [(1, 3000, 640), (4, 2000, 264), (2, 900, 4096), (30, 3000, 328), (200, 1500, 256)])
+def test_small_calls_replay(T, V, D):
+    """The forms for few tokens and few tiles, captured and replayed with other inputs, two calls behind one another."""
+    x, w, t = make(T, V, D, seed=T)
+    x2, w2, t2 = (a.contiguous() for a in make(T, V, D, 0.5, seed=T + 1))
+    x, w, dl = x.contiguous(), w.contiguous(), torch.rand(T, device="cuda")
+    ws, loss, lse = fg.new_linear_xent_workspace(T, V, D), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dx, dw = torch.empty_like(x), torch.zeros((V, D), device="cuda")
+
+    def step():
+        for _ in range(2):
+            fg.linear_xent_fwd(x, w, t, loss, lse, ws)
+            fg.linear_xent_bwd(x, w, t, loss, lse, dl, dx, dw, ws, accumulate=True)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for a, b in ((x, x2), (w, w2), (t, t2)):
+        a.copy_(b)
+    dw.zero_()
+    graph.replay()
+    got = [a.clone() for a in (loss, lse, dx, dw)]
+    dw.zero_()
+    step()
+    assert all(torch.equal(a, b) for a, b in zip(got, (loss, lse, dx, dw))) and fg.device_status() == fg.OK
+
+
 def test_gradient_in_place():
     """dx may be x: every row of it has been copied before any is written."""
     for T in (100, 700):
@@ -367,10 +396,9 @@ def test_no_tokens():
     assert not dw.any()
 
 
-@pytest.mark.parametrize("T", [3, 40, 300])
-def test_offsets_beyond_32_bits_full_size(T):
+@pytest.mark.parametrize("T,V,D", [(3, 270000, 8192), (40, 270000, 8192), (300, 270000, 8192), (2, 540000, 4096)])
+def test_offsets_beyond_32_bits_full_size(T, V, D):
     """W and dw of more than 2^31 elements: targets at both ends, checked on slices of the vocabulary."""
-    V, D = 270000, 8192
     g = torch.Generator(device="cuda").manual_seed(17)
     w = torch.empty((V, D), dtype=torch.bfloat16, device="cuda").normal_(generator=g).mul_(D ** -0.5)
     x = torch.randn((T, D), generator=g, device="cuda").bfloat16()
