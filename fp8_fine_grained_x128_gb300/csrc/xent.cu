@@ -29,7 +29,8 @@
 //
 // Tokens that do not count are left out from the start: k_xent_pack copies the
 // counted rows of x together, so neither the work nor the results see the
-// others, whatever they hold.
+// others, whatever they hold.  (Up to 128 tokens, and small forwards, keep their
+// rows: the others' are independent of them, or zeros.)
 //
 // k_xent is a persistent kernel of CTA pairs (cta_group::2): a pair computes
 // 256 x 256 tiles, each CTA holding 128 rows of A and 128 columns of B of every
@@ -89,12 +90,17 @@ struct XentArgs {
     int band;                   // M tiles of a raster band
     int box;                    // single CTAs: rows of x that are fetched for a tile (the others' results are not used)
     float scale;
+    const int32_t *target;      // LOSS: of every row; GRAD: of every token
     // LOSS
-    const int32_t *target;      // of every row
     float2 *part;               // [unit][half][rows]: maximum (times scale log2 e), sum of 2^(. - maximum)
     int64_t rows;               // rows of the packed buffers
     // GRAD
-    const float4 *info;         // [rows]: lse log2 e, factor of p, entry at the target; the target as an int
+    const float4 *info;         // [rows]: see row_info; nullptr: the rows are the tokens and not packed, and made of
+    const float *loss, *lse, *dloss, *dlse;
+    const uint16_t *x;          // then also: x, and where it goes, times norm, in this launch (xn nullptr: it has already)
+    int64_t ldx;
+    uint16_t *xn;
+    float *norm;
     // SUMS
     int dx_add;                 // dx's parts (FP32, [splits][rows][dim]) are added to
     int dw_f32, dw_add;
@@ -225,6 +231,27 @@ struct Maps { CUtensorMap m[MODE == XENT_SUMS ? 6 : 3]; };
 __device__ __forceinline__ float target_entry(float scale, float loss, float gl, float gz)
 {
     return scale * (gl * expm1f(-loss) + gz * expf(-loss));
+}
+
+// What a row of g is made of: lse log2 e, the factor of p, the entry at the target, the
+// target as an int; relative to `by`, the size of that entry.
+__device__ __forceinline__ float4 row_info(float scale, float loss, float lse, float gl, float gz, int target, float &by)
+{
+    const float entry = target_entry(scale, loss, gl, gz), factor = scale * (gl + gz), n = fabsf(entry), c = fabsf(factor);
+    // the row stays as it is where that entry, or the others relative to it, are beyond all measure
+    const bool relative = n >= 0x1p-100f && n <= 0x1p100f && c <= n * 0x1p120f && c * -expm1f(-loss) <= n * 0x1p60f;
+    by = relative ? n : 1.0f;
+    return make_float4(lse * kLog2e, factor / by, entry / by, __int_as_float(target));
+}
+
+// 8 BF16 values, times `by`.
+__device__ __forceinline__ uint4 times8(uint4 v, float by)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = bf16x2_rn(bf16_lo(w[k]) * by, bf16_hi(w[k]) * by);
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // 8 FP32 values to 16 bytes of BF16.
@@ -433,12 +460,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = mt * F::kM + rank * 128 + lq * 32 + lane;
             float4 i = make_float4(0.0f, 0.0f, 0.0f, __int_as_float(-1));
             if constexpr (MODE == XENT_GRAD) {
-                if (row < rows) i = a.info[row];
+                if (row < rows && a.info) {
+                    i = a.info[row];
+                } else if (row < rows) {
+                    const int target = a.target[row];
+                    float by;
+                    if (target >= 0 && target < a.vocab)
+                        i = row_info(a.scale, a.loss[row], a.lse[row], a.dloss[row], a.dlse ? a.dlse[row] : 0.0f, target, by);
+                }
             } else if constexpr (MODE == XENT_LOSS) {
                 if (row < rows) i.w = __int_as_float(a.target[row]);
             }
             return i;
         };
+        // Up to 128 tokens: what k_xent_pack does of the work else, while the first tiles come.  Tokens that do
+        // not count keep their rows, of zeros (norm 0).
+        if (MODE == XENT_GRAD && !PAIR && a.xn) {
+            const int e = warp - kEpiWarp0, nv = a.dim / 8;
+            for (int r = blockIdx.x; r < (rows + kBK - 1) / kBK * kBK; r += gridDim.x) {
+                const int target = r < rows ? a.target[r] : -1;
+                const bool counts = target >= 0 && target < a.vocab;
+                float by = 0.0f;
+                if (counts) row_info(a.scale, a.loss[r], a.lse[r], a.dloss[r], a.dlse ? a.dlse[r] : 0.0f, target, by);
+                if (e == 0 && lane == 0 && r < rows) {
+                    if (target >= a.vocab) set_status(a.status, FP8_ERR_INVALID_ARG);
+                    if (dbg_span(r, 1, a.rows, a.status)) a.norm[r] = by;
+                }
+                for (int v = e * 32 + lane; v < nv; v += kEpiWarps * 32) {
+                    const uint4 q = counts ? times8(ldg_stream(a.x + r * a.ldx + v * 8), by) : make_uint4(0, 0, 0, 0);
+                    if (dbg_cell(r, v * 8, 8, a.rows, a.dim, a.status)) *reinterpret_cast<uint4 *>(a.xn + (int64_t)r * a.dim + v * 8) = q;
+                }
+            }
+        }
         int at_mt = -1, ahead_mt = -1;
         float4 info, ahead;
         const float c = a.scale * kLog2e;
@@ -546,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t c2 = f2_pack(c, c), off2 = f2_pack(-info.x, -info.x), by2 = f2_pack(info.y, info.y);
                     each_32([&](uint32_t (&r)[32], int q) {
                         const int col = col0 + q * 32, at = target - col;
-                        const int lim = row < rows ? a.vn - col : 0;
+                        const int lim = __float_as_int(info.w) >= 0 ? a.vn - col : 0;
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             float x, y;
@@ -935,15 +988,6 @@ struct PackArgs {
     int *status;
 };
 
-__device__ __forceinline__ uint4 times8(uint4 v, float by)
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = bf16x2_rn(bf16_lo(w[k]) * by, bf16_hi(w[k]) * by);
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
 {
     __shared__ int warp_n[8];
@@ -996,14 +1040,10 @@ __global__ void __launch_bounds__(256) k_xent_pack(PackArgs g)
             if (fits) g.map[at + before] = t;
             if (fits && g.row_target) g.row_target[at + before] = g.target[t];
             if (g.norm) {
-                const float loss = g.losses[t], gl = g.dloss[t], gz = g.dlse ? g.dlse[t] : 0.0f;
-                const float entry = target_entry(g.scale, loss, gl, gz), factor = g.scale * (gl + gz), n = fabsf(entry), c = fabsf(factor);
-                // the row stays as it is where that entry, or the others relative to it, are beyond all measure
-                const bool relative = n >= 0x1p-100f && n <= 0x1p100f && c <= n * 0x1p120f && c * -expm1f(-loss) <= n * 0x1p60f;
-                by[before] = relative ? n : 1.0f;
+                const float4 info = row_info(g.scale, g.losses[t], g.lses[t], g.dloss[t], g.dlse ? g.dlse[t] : 0.0f, g.target[t], by[before]);
                 if (fits) {
                     g.norm[at + before] = by[before];
-                    g.info[at + before] = make_float4(g.lses[t] * kLog2e, factor / by[before], entry / by[before], __int_as_float(g.target[t]));
+                    g.info[at + before] = info;
                 }
             }
         } else if (mine && g.loss) {
@@ -1150,7 +1190,7 @@ __global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, 
     dependents_launch();
     dependency_wait();
     const int nv = dim / 8;
-    const int64_t items = (int64_t)*count * nv;
+    const int64_t items = (int64_t)(count ? *count : tokens) * nv;
     // whole warps go round, for the exchange
     for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; (i & ~(int64_t)31) < items * LANES; i += (int64_t)gridDim.x * kSumThreads) {
         const bool valid = i < items * LANES;
@@ -1171,10 +1211,10 @@ __global__ void __launch_bounds__(kSumThreads) k_xent_dx_join(const float *acc, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
         if (!valid || i % LANES != 0) continue;
-        const int64_t at = (int64_t)map[row] * lddx + col;
+        const int64_t at = (map ? map[row] : row) * lddx + col;
         const float by = norm[row];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= by;
+        for (int e = 0; e < 8; ++e) v[e] = by == 0.0f ? 0.0f : v[e] * by;      // 0: does not count, whatever W holds
         if (dbg_span(at, 8, (int64_t)(tokens - 1) * lddx + dim, status))
             *reinterpret_cast<uint4 *>(dx + at) = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
     }
@@ -1494,11 +1534,24 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     pk.norm = reinterpret_cast<float *>(ws + p.norm);
     pk.info = reinterpret_cast<float4 *>(ws + p.info);
     pk.xn = reinterpret_cast<uint16_t *>(ws + p.xn);
-    int rc = pack(p, ws, pk, target, x, ldx, tokens, vocab, dim, status, st);
-    if (rc != FP8_OK) return rc;
+    int rc = FP8_OK;
     XentArgs a{};
-    a.count = reinterpret_cast<int *>(ws + p.count);
-    a.info = pk.info;
+    const bool packed = tokens > 128;       // else the first launch does it (100 x 8000 x 256: 18 us, 21 with a packing launch)
+    if (packed) {
+        if ((rc = pack(p, ws, pk, target, x, ldx, tokens, vocab, dim, status, st)) != FP8_OK) return rc;
+        a.count = reinterpret_cast<int *>(ws + p.count);
+        a.info = pk.info;
+    } else {
+        a.target = target;
+        a.loss = loss;
+        a.lse = lse;
+        a.dloss = dloss;
+        a.dlse = dlse;
+        a.x = static_cast<const uint16_t *>(x);
+        a.ldx = ldx;
+        a.xn = pk.xn;
+        a.norm = pk.norm;
+    }
     a.tokens = (int)tokens;
     a.vocab = (int)vocab;
     a.dim = (int)dim;
@@ -1506,13 +1559,14 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
     a.scale = scale;
     a.rows = p.rows;
     a.status = status;
-    void *xp = ws + p.xp, *g = ws + p.g, *acc = ws + p.acc;
+    const void *xp = packed ? ws + p.xp : x;
+    void *g = ws + p.g, *acc = ws + p.acc;
     a.dw_f32 = dw_dtype == FP8_OUT_F32;
     a.dw_add = accumulate;
     Maps<XENT_GRAD> grad;
     Maps<XENT_SUMS> sums;
     a.box = x_box(tokens);
-    if (!map_k(&grad.m[0], xp, dim, p.rows, dim, a.box) || !map_k(&grad.m[1], w, dim, vocab, ldw) ||
+    if (!map_k(&grad.m[0], xp, dim, packed ? p.rows : tokens, packed ? dim : ldx, a.box) || !map_k(&grad.m[1], w, dim, vocab, ldw) ||
         !map_out(&grad.m[2], g, false, p.piece, p.rows, p.piece) || !map_k(&sums.m[0], g, p.piece, p.rows, p.piece) ||
         !map_mn(&sums.m[1], w, dim, vocab, ldw) || !map_out(&sums.m[2], acc, true, dim, p.splits * p.rows, dim) ||
         !map_mn(&sums.m[3], g, p.piece, p.rows, p.piece) || !map_mn(&sums.m[4], pk.xn, dim, p.rows, dim) ||
@@ -1526,6 +1580,7 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
              : p.bn == 256   ? run<XENT_GRAD, false, 256>(grad, a, st)
                              : run<XENT_GRAD, false, 128>(grad, a, st);
         if (rc != FP8_OK) return rc;
+        a.xn = nullptr;
         a.band = 8;
         a.dx_add = v > 0;
         rc = run<XENT_SUMS, true, 256>(sums, a, st);
