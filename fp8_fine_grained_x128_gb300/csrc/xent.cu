@@ -1143,7 +1143,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_xent_join(JoinArgs g)
     }
     __syncthreads();
     M = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    const float off = M == -INFINITY ? 0.0f : M;    // -inf: no other logit, or all of them -inf (or NaN)
+    const float off = M == -INFINITY ? 0.0f : M;    // -inf: no other logit, or all of them -inf (or NaN); S is 0 then (or NaN)
     if (counts)
 #pragma unroll 4
         for (int u = threadIdx.x; u < g.parts; u += kJoinThreads) {
@@ -1160,8 +1160,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_xent_join(JoinArgs g)
         S = (sums[0] + sums[1]) + (sums[2] + sums[3]);
         const float zt = ((dots[0] + dots[1]) + (dots[2] + dots[3])) * g.scale, yt = zt * kLog2e;
         if (yt >= M) {          // the target leads: log(1 + the rest relative to it)
-            l = log1pf(S * exp2f(off - yt));
-            z = zt + l;
+            l = log1pf(S * exp2f(M - yt));      // 0 times 0 where there is no rest, however small yt; NaN where there is nothing at all
+            z = S == 0.0f ? zt : zt + l;
         } else {
             const float s = logf(S + exp2f(yt - M));
             l = (M - yt) * kLn2 + s;

@@ -686,7 +686,8 @@ FP8FG_API size_t fp8_linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, 
  *   FP8_ERR_INVALID_ARG and does not count either.
  *   loss, lse: FP32 [tokens].  scale > 0.  vocab or dim 0: FP8_ERR_SHAPE where
  *   there are tokens.
- * A counted row whose logits hold NaN or +Inf gives NaN, for itself alone. */
+ * A counted row whose logits hold NaN or +Inf gives NaN, for itself alone; one whose
+ * logits are all -Inf lse = -Inf and a loss of NaN. */
 FP8FG_API int fp8_linear_xent_fwd(const void *x, int64_t tokens, int64_t dim, int64_t ldx, const void *w,
                                   int64_t vocab, int64_t ldw, const int32_t *target, float scale, float *loss,
                                   float *lse, void *workspace, void *stream);

@@ -1,0 +1,58 @@
+"""Linear cross entropy where nothing but the target is left of a row's logits."""
+import math
+
+import pytest
+import torch
+
+import fp8_fine_grained_x128_gb300 as fg
+
+pytestmark = pytest.mark.gpu
+
+HALF = 2.0 ** -8      # half a step of BF16, relative
+
+
+def forward(x, w, t, scale=1.0):
+    T = x.shape[0]
+    loss, lse = torch.full((T,), 7.0, device="cuda"), torch.full((T,), 7.0, device="cuda")
+    fg.linear_xent_fwd(x, w, t, loss, lse, fg.new_linear_xent_workspace(T, w.shape[0], x.shape[1]), scale=scale)
+    assert fg.device_status() == fg.OK
+    return loss, lse
+
+
+# tokens: the one-pass forms (1, 4), single CTAs' tiles (5, 100), pairs' (300)
+@pytest.mark.parametrize("T", [1, 4, 5, 100, 300])
+@pytest.mark.parametrize("z", [-1000.0, -100.0, -60.0, 0.0, 60.0, 100.0])
+def test_one_word(T, z):
+    """A vocabulary of one word: its probability is 1, its loss 0 and lse its logit, however far that is from 0.  Sums of
+    64 equal multiples of 1/64 are exact in FP32; the gradient of a row is dlse alone."""
+    D = 64
+    x, w = torch.ones((T, D), dtype=torch.bfloat16, device="cuda"), torch.full((1, D), z / D, dtype=torch.bfloat16, device="cuda")
+    t = torch.zeros(T, dtype=torch.int32, device="cuda")
+    loss, lse = forward(x, w, t)
+    assert bool((loss == 0).all()) and bool((lse == z).all())
+    dl, dz = torch.rand(T, device="cuda") + 0.5, torch.rand(T, device="cuda") + 0.5
+    dx, dw = torch.full_like(x, 3.0), torch.full((1, D), 3.0, device="cuda")
+    fg.linear_xent_bwd(x, w, t, loss, lse, dl, dx, dw, fg.new_linear_xent_workspace(T, 1, D), dlse=dz)
+    assert fg.device_status() == fg.OK
+    want = dz.double()[:, None] * w.double()
+    assert bool(((dx.double() - want).abs() <= HALF * (1 + HALF) * want.abs()).all())      # the result's rounding
+    size = float(dz.double().sum())     # a sum of x times dlse, rounded to BF16 each, in steps of 16
+    assert bool(((dw.double() - size).abs() <= (HALF + (T / 16 + 16) * 2.0 ** -23) * size).all())
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 100, 300])
+@pytest.mark.parametrize("z", [-1000.0, -100.0, 60.0])
+def test_the_other_words_ruled_out(T, z):
+    """Logits of -Inf for every word but the target."""
+    V, D = 5, 64
+    x = torch.ones((T, D), dtype=torch.bfloat16, device="cuda")
+    w = torch.full((V, D), -math.inf, dtype=torch.bfloat16, device="cuda")
+    w[2] = z / D
+    loss, lse = forward(x, w, torch.full((T,), 2, dtype=torch.int32, device="cuda"))
+    assert bool((loss == 0).all()) and bool((lse == z).all())
+    # the target ruled out, one other word left; then no word at all: the logarithm of 0, and a loss that is not a number
+    loss, lse = forward(x, w, torch.full((T,), 3, dtype=torch.int32, device="cuda"))
+    assert bool((loss == math.inf).all()) and bool(((lse - z).abs() <= 2.0 ** -22 * abs(z)).all())
+    w[2] = -math.inf
+    loss, lse = forward(x, w, torch.full((T,), 2, dtype=torch.int32, device="cuda"))
+    assert bool((lse == -math.inf).all()) and bool(torch.isnan(loss).all())
