@@ -720,7 +720,7 @@ static int xent_checks(int64_t tokens, int64_t vocab, int64_t dim, float scale)
     if (tokens >= kMost || vocab >= kMost || dim >= kMost) return FP8_ERR_SHAPE;
     constexpr int64_t kTiles = (int64_t)1 << 46;    // 2^30 tiles of 256 x 256 in any of the products
     if (tokens * vocab >= kTiles || tokens * dim >= kTiles || vocab * dim >= kTiles) return FP8_ERR_SHAPE;
-    if (!(scale > 0.0f) || scale > 3.0e38f) return FP8_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || scale > 0x1p127f) return FP8_ERR_INVALID_ARG;     // scale log2 e is a finite number
     return FP8_OK;
 }
 

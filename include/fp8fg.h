@@ -684,7 +684,7 @@ FP8FG_API size_t fp8_linear_xent_workspace_bytes(int64_t tokens, int64_t vocab, 
  *   target: DEVICE int32[tokens].  A token with a negative target does not count:
  *   loss = lse = 0, whatever its row of x holds.  One >= vocab records
  *   FP8_ERR_INVALID_ARG and does not count either.
- *   loss, lse: FP32 [tokens].  scale > 0.  vocab or dim 0: FP8_ERR_SHAPE where
+ *   loss, lse: FP32 [tokens].  0 < scale <= 2^127.  vocab or dim 0: FP8_ERR_SHAPE where
  *   there are tokens.
  * A counted row whose logits hold NaN or +Inf gives NaN, for itself alone; one whose
  * logits are all -Inf lse = -Inf and a loss of NaN. */
