@@ -75,9 +75,15 @@ struct Form {
 };
 
 // The tensor cores' sums lean towards zero, by up to a last place for every 16 of K
-// (1.1e-6 of the loss at dim 4096): the forward sums 2048 of K at a time, and adds
-// those to nearest.
+// (1.1e-6 of the loss at dim 4096; in one sum over 65536 tokens, 1.8e-4 of dw): LOSS and
+// SUMS take 2048 of K at a time, and add those to nearest.  (GRAD's K is dim, 2e-5 of a
+// logit at 8192: less than g's rounding to BF16 shows.)  SUMS without a longer K is
+// compiled apart (100 x 8000 x 256 backward 18.7 us, 19.1 with the code for longer ones;
+// 64 x 128000 x 4096, where dx's parts are long, 605 us in one sum and 608 in pieces).
 constexpr int kChunk = 2048 / kBK;
+
+// Sums of a tile whose K is `blocks` blocks; one, of nothing, where there are none.
+__device__ __forceinline__ int chunks_of(int blocks) { return max(1, (blocks + kChunk - 1) / kChunk); }
 
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
@@ -263,7 +269,8 @@ __device__ __forceinline__ uint4 bf16x8(const uint32_t *r)
 
 }  // namespace
 
-template <int MODE, bool PAIR, int BN>
+// LONG: SUMS of which some K is longer than kChunk.
+template <int MODE, bool PAIR, int BN, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
     k_xent(const __grid_constant__ Maps<MODE> maps, const XentArgs a)
 {
@@ -313,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
     dependency_wait();
     const int rows = a.count ? *a.count : a.tokens;
-    // accumulators of a tile of LOSS, one for every kChunk blocks of K
-    const int chunks = MODE == XENT_LOSS ? max(1, ((a.dim + kBK - 1) / kBK + kChunk - 1) / kChunk) : 1;
+    // accumulators of a tile, one for every kChunk blocks of K: of LOSS here, of SUMS by the unit
+    const int loss_chunks = MODE == XENT_LOSS ? chunks_of((a.dim + kBK - 1) / kBK) : 1;
     const Walk<MODE, PAIR, BN> walk(a, rows, PAIR ? blockIdx.x >> 1 : blockIdx.x, PAIR ? gridDim.x >> 1 : gridDim.x);
 
     if (warp == 0) {
@@ -376,9 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t it = 0, tc = 0;
             walk.each_alone(units[1], [&](const Unit &t) {
                 const uint32_t idesc = kSums && t.dw ? idesc_bf16(F::kM, BN, true, true) : idesc_bf16(F::kM, BN, false, kSums);
+                const int chunks = kSums ? (LONG ? chunks_of(t.k1 - t.k0) : 1) : loss_chunks;
                 const int parts = (t.nt1 - t.nt0) * chunks;     // of the unit, an accumulator each
                 for (int i = 0; i < parts; ++i, ++tc) {
-                    const int c0 = chunks == 1 ? t.k0 : i % chunks * kChunk, c1 = chunks == 1 ? t.k1 : min(t.k1, c0 + kChunk);
+                    const int c0 = chunks == 1 ? t.k0 : t.k0 + i % chunks * kChunk, c1 = chunks == 1 ? t.k1 : min(t.k1, c0 + kChunk);
                     const uint32_t buf = tc & 1;
                     if (!thread_wait(smem_u32(&tempty[buf]), ((tc >> 1) & 1) ^ 1, abort_flag, a.status)) return false;
                     tc_fence_after();
@@ -449,9 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_commit_group();
         };
 
-        auto settle = [](uint32_t (&v)[32]) {       // loaded values are not used before the wait for them
+        auto settle = [](auto &v) {     // loaded values are not used before the wait for them
 #pragma unroll
-            for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+            for (uint32_t &e : v) asm volatile("" : "+r"(e));
         };
 
         // What this lane has to know of its row (LOSS: the target), fetched a tile ahead
@@ -541,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
-                if constexpr (MODE == XENT_LOSS) {
-                    uint32_t r[kQ][32];
+                // all columns in one go, of the sum of `chunks` accumulators
+                auto load_all = [&](uint32_t (&r)[kQ][32], int chunks) {
 #pragma unroll
                     for (int q = 0; q < kQ; ++q) load(r[q], q);
                     tc_wait_ld();
@@ -551,18 +559,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     release();
                     for (int i = 1; i < chunks; ++i) {
                         ++tc;
-                        if (!(ok = full_accumulator())) return;
+                        if (!full_accumulator()) return false;
 #pragma unroll
-                        for (int q = 0; q < kQ; ++q) {
-                            uint32_t v[32];
-                            load(v, q);
+                        for (int h = 0; h < 2 * kQ; ++h) {      // by 16: 32 more registers are not there
+                            uint32_t v[16];
+                            tc_ld_32x32b_x16(tm_lane + (tc & 1) * BN + half * kCols + h * 16, v);
                             tc_wait_ld();
                             settle(v);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) r[q][e] = __float_as_uint(__uint_as_float(r[q][e]) + __uint_as_float(v[e]));
+                            for (int e = 0; e < 16; ++e) {
+                                uint32_t &to = r[h / 2][h % 2 * 16 + e];
+                                to = __float_as_uint(__uint_as_float(to) + __uint_as_float(v[e]));
+                            }
                         }
                         release();
                     }
+                    return true;
+                };
+                if constexpr (MODE == XENT_LOSS) {
+                    uint32_t r[kQ][32];
+                    if (!(ok = load_all(r, loss_chunks))) return;
                     const int lim = a.vn - col0, at = target - col0;
                     if (lim < kCols || (unsigned)at < (unsigned)kCols) {    // beyond the vocabulary; the target is left out of the sum
 #pragma unroll
@@ -621,17 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     });
                 } else {
                     uint32_t r[kQ][32];
+                    if (!(ok = load_all(r, LONG ? chunks_of(t.k1 - t.k0) : 1))) return;
+                    if (t.k0 == t.k1) {         // no K: the accumulator was not written
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q) load(r[q], q);
-                    tc_wait_ld();
+                        for (int q = 0; q < kQ; ++q)
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q) {
-                        settle(r[q]);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (t.k0 == t.k1) r[q][i] = 0;          // no K: the accumulator was not written
+                            for (int i = 0; i < 32; ++i) r[q][i] = 0;
                     }
-                    release();
                     const bool f32 = !t.dw || a.dw_f32, add = t.dw ? a.dw_add : a.dx_add;
                     const CUtensorMap *map = &maps.m[t.dw ? 5 : 2];
                     const int to = t.dw ? a.v0 + row0 : (int)(t.split * a.rows) + row0, end = t.dw ? a.vocab : INT_MAX;
@@ -1340,7 +1352,7 @@ int run_few_grad(FewGradArgs &a, void *dx, int64_t lddx, cudaStream_t st)
                             a.vocab, a.dim, static_cast<uint16_t *>(dx), lddx, a.tokens, a.status);
 }
 
-template <int MODE, bool PAIR, int BN>
+template <int MODE, bool PAIR, int BN, bool LONG = false>
 int run(const Maps<MODE> &maps, const XentArgs &a, cudaStream_t st)
 {
     using F = Form<MODE, PAIR, BN>;
@@ -1348,11 +1360,11 @@ int run(const Maps<MODE> &maps, const XentArgs &a, cudaStream_t st)
     int dev = 0;
     cudaGetDevice(&dev);
     if (!attr_done[dev & 63]) {
-        if (cudaFuncSetAttribute(k_xent<MODE, PAIR, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess) return FP8_ERR_CUDA;
+        if (cudaFuncSetAttribute(k_xent<MODE, PAIR, BN, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem) != cudaSuccess) return FP8_ERR_CUDA;
         attr_done[dev & 63] = true;
     }
     const int sms = sm_count();
-    return launch_dependent_cluster(k_xent<MODE, PAIR, BN>, dim3((unsigned)(PAIR ? sms / 2 * 2 : sms)), PAIR ? 2 : 1, kThreads, F::kSmem, st, maps,
+    return launch_dependent_cluster(k_xent<MODE, PAIR, BN, LONG>, dim3((unsigned)(PAIR ? sms / 2 * 2 : sms)), PAIR ? 2 : 1, kThreads, F::kSmem, st, maps,
                                     a);
 }
 
@@ -1572,6 +1584,8 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
         !map_mn(&sums.m[3], g, p.piece, p.rows, p.piece) || !map_mn(&sums.m[4], pk.xn, dim, p.rows, dim) ||
         !map_out(&sums.m[5], dw, a.dw_f32, dim, vocab, lddw))
         return FP8_ERR_CUDA;
+    // blocks of K in a unit of SUMS: tokens for dw, a part of the piece for dx
+    const int64_t longest = std::max((tokens + kBK - 1) / kBK, (p.piece / kBK + p.splits - 1) / p.splits);
     for (int64_t v = 0; v < vocab; v += p.piece) {
         a.v0 = (int)v;
         a.vn = (int)std::min<int64_t>(p.piece, vocab - v);
@@ -1583,7 +1597,7 @@ int launch_linear_xent_bwd(const void *x, int64_t ldx, const void *w, int64_t ld
         a.xn = nullptr;
         a.band = 8;
         a.dx_add = v > 0;
-        rc = run<XENT_SUMS, true, 256>(sums, a, st);
+        rc = longest > kChunk ? run<XENT_SUMS, true, 256, true>(sums, a, st) : run<XENT_SUMS, true, 256, false>(sums, a, st);
         if (rc != FP8_OK) return rc;
     }
     // many parts means few columns: eight threads each (61 x 20674 x 192: 6 us, by one 13)

@@ -1,4 +1,4 @@
-"""Linear cross entropy where nothing but the target is left of a row's logits."""
+"""Linear cross entropy where nothing but the target is left of a row's logits, and sums over many tokens."""
 import math
 
 import pytest
@@ -56,3 +56,23 @@ def test_the_other_words_ruled_out(T, z):
     w[2] = -math.inf
     loss, lse = forward(x, w, torch.full((T,), 2, dtype=torch.int32, device="cuda"))
     assert bool((lse == -math.inf).all()) and bool(torch.isnan(loss).all())
+
+
+@pytest.mark.parametrize("T", [2048, 16384, 65536])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_sums_over_many_tokens_do_not_lean(T, accumulate):
+    """dw of words of equal probability 2^-8 and dlse = 1: sums of x / 256, whose terms are exact BF16 values of one sign
+    (of several sizes: equal ones' sums would be exact in FP32).  2048 tokens in steps of 16, each off by at most a last
+    place; the parts added to nearest."""
+    V, D = 256, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.exp2(-10 * torch.rand((T, D), generator=g, device="cuda")).bfloat16()
+    w = torch.zeros((V, D), dtype=torch.bfloat16, device="cuda")
+    t = torch.randint(V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    loss, lse = forward(x, w, t)
+    dx, dw = torch.empty_like(x), torch.zeros((V, D), device="cuda")
+    fg.linear_xent_bwd(x, w, t, loss, lse, torch.zeros(T, device="cuda"), dx, dw, fg.new_linear_xent_workspace(T, V, D),
+                       dlse=torch.ones(T, device="cuda"), accumulate=accumulate)
+    assert fg.device_status() == fg.OK
+    want = x.double().sum(0) / V
+    assert float(((dw.double() - want) / want).abs().max()) <= 128 * 2.0 ** -23 + (T / 2048) * 2.0 ** -24 + 2.0 ** -23
