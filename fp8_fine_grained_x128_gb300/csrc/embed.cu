@@ -259,9 +259,16 @@ __global__ void __launch_bounds__(kClusterThreads) k_sort_cluster(const int32_t 
                     });
 }
 
-// More tokens: through memory, a kernel that counts and one a digit.
+// More tokens: through memory, a kernel that counts, then one a digit that places the keys,
+// and before it one that adds the counts up where there are many: every placing CTA doing
+// so for itself costs the square of the tokens, but spares a launch (D 8, two digits:
+// 114689 tokens 51 us, with the launches 59; 150001 61 and 65; 170001 84 and 66; 2^24
+// 225 ms and 1.8).
 constexpr int kSortThreads = 256, kSortKeys = 8, kSortTile = kSortThreads * kSortKeys;   // keys of one CTA
 static_assert(kDigits == 2 * kSortThreads, "two digits a thread");
+constexpr int kScanBlocks = 76;     // more blocks' counts are added up by k_sort_scan
+// Counts of a digit lie this far from the next one's: not a power of two, whose loads would all meet in few banks of the L2.
+__host__ __device__ constexpr int count_stride(int blocks) { return blocks | 1; }
 
 // counts[digit][block] of the first digit; the other digits' are cleared.
 __global__ void __launch_bounds__(kSortThreads) k_sort_count(const int32_t *__restrict__ ids, int tokens, int vocab, int *__restrict__ counts,
@@ -281,17 +288,52 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(const int32_t *__re
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kDigits; i += kSortThreads) {
-        counts[(int64_t)i * gridDim.x + blockIdx.x] = n[i];
-        for (int p = 1; p < passes; ++p) counts[((int64_t)p * kDigits + i) * gridDim.x + blockIdx.x] = 0;
+        counts[(int64_t)i * count_stride(gridDim.x) + blockIdx.x] = n[i];
+        for (int p = 1; p < passes; ++p) counts[((int64_t)p * kDigits + i) * count_stride(gridDim.x) + blockIdx.x] = 0;
     }
 }
 
-// Places every key behind the equal digits before it.  Each CTA adds the counts
-// up for itself.  The next digit is counted for the block that a key goes to
-// (whole numbers: the atomics' order changes nothing).
+// A CTA for every digit: its counts become what the blocks before have of it, totals[digit]
+// what all have.
+__global__ void __launch_bounds__(kSortThreads) k_sort_scan(int *__restrict__ counts, int blocks, int *__restrict__ totals, int *status)
+{
+    constexpr int kWarps = kSortThreads / 32;
+    __shared__ int warp_sums[kWarps];
+    dependents_launch();
+    dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int *c = counts + (int64_t)blockIdx.x * count_stride(blocks);
+    int before = 0;
+    for (int b0 = 0; b0 < blocks; b0 += kSortThreads) {
+        const int b = b0 + threadIdx.x, n = b < blocks ? c[b] : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        __syncthreads();        // the round before has read its sums
+        if (lane == 31) warp_sums[warp] = sum;
+        __syncthreads();
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            sum += w < warp ? warp_sums[w] : 0;
+            all += warp_sums[w];
+        }
+        if (b < blocks) c[b] = before + sum - n;
+        before += all;
+    }
+    if (threadIdx.x == 0 && dbg_span(blockIdx.x, 1, kDigits, status)) totals[blockIdx.x] = before;
+}
+
+// Places every key behind the equal digits before it.  Without totals each CTA adds the
+// counts up for itself.  The next digit is counted for the block that a key goes to (whole
+// numbers: the atomics' order changes nothing).
 __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t *__restrict__ keys, const int32_t *__restrict__ vals, int tokens,
-                                                           int vocab, int shift, int *__restrict__ counts, int *__restrict__ next_counts,
-                                                           int32_t *__restrict__ keys_out, int32_t *__restrict__ vals_out, int *status)
+                                                           int vocab, int shift, const int *__restrict__ counts, const int *__restrict__ totals,
+                                                           int *__restrict__ next_counts, int32_t *__restrict__ keys_out,
+                                                           int32_t *__restrict__ vals_out, int *status)
 {
     constexpr int kWarps = kSortThreads / 32;
     __shared__ int n[kWarps][kDigits];
@@ -312,7 +354,12 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t *__re
     int before[2], total[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int *c = counts + (int64_t)(2 * threadIdx.x + h) * blocks;
+        const int *c = counts + (int64_t)(2 * threadIdx.x + h) * count_stride(blocks);
+        if (totals) {
+            before[h] = c[blockIdx.x];
+            total[h] = totals[2 * threadIdx.x + h];
+            continue;
+        }
         before[h] = total[h] = 0;
 #pragma unroll 8
         for (int b = 0; b < blocks; ++b) {
@@ -354,7 +401,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_place(const int32_t *__re
         if (next_counts) {      // one addition for the lanes of one digit and block: a frequent id has thousands
             const int d = (key[k] >> (shift + kDigitBits)) & (kDigits - 1), block = at / kSortTile;
             const unsigned same = __match_any_sync(0xffffffffu, at < 0 ? -1 : block << kDigitBits | d);
-            if (at >= 0 && lane == __ffs(same) - 1) atomicAdd(&next_counts[(int64_t)d * blocks + block], __popc(same));
+            if (at >= 0 && lane == __ffs(same) - 1) atomicAdd(&next_counts[(int64_t)d * count_stride(blocks) + block], __popc(same));
         }
     }
 }
@@ -631,7 +678,7 @@ namespace {
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 struct EmbedLayout {    // byte offsets in the workspace
-    int64_t keys[2], vals[2], counts, part, bytes;
+    int64_t keys[2], vals[2], counts, totals, part, bytes;
     int blocks, passes, piece, pieces;
     EmbedLayout(int64_t tokens, int64_t vocab, int64_t dim)
     {
@@ -650,7 +697,8 @@ struct EmbedLayout {    // byte offsets in the workspace
             keys[i] = take(tokens * 4);
             vals[i] = take(tokens * 4);
         }
-        counts = take(tokens <= kClusterMost ? 0 : (int64_t)passes * kDigits * blocks * 4);
+        counts = take(tokens <= kClusterMost ? 0 : (int64_t)passes * kDigits * count_stride(blocks) * 4);
+        totals = take(tokens <= kClusterMost ? 0 : kDigits * 4);
         part = take(most * 2 * 4);
         bytes = at;
     }
@@ -781,17 +829,20 @@ int launch_embedding_bwd(const int32_t *ids, int64_t tokens, const void *dout, i
         if ((rc = run_sort(ids, n, V, L.passes, c, keys[0], vals[0], status, st)) != FP8_OK) return rc;
     } else {
         if (!accumulate && (rc = clear()) != FP8_OK) return rc;
-        int *counts = reinterpret_cast<int *>(base + L.counts);
-        const int64_t stride = (int64_t)kDigits * L.blocks;
+        int *counts = reinterpret_cast<int *>(base + L.counts), *totals = reinterpret_cast<int *>(base + L.totals);
+        const int64_t stride = (int64_t)kDigits * count_stride(L.blocks);
         if ((rc = launch_dependent(k_sort_count, dim3((unsigned)L.blocks), kSortThreads, 0, st, ids, n, V, counts, L.passes, status)) != FP8_OK)
             return rc;
         for (int p = 0; p < L.passes; ++p) {
             const int from = (p + 1) & 1;
+            const bool scan = L.blocks > kScanBlocks;
+            const int32_t *in = p == 0 ? ids : keys[from], *in_vals = p == 0 ? nullptr : vals[from];
+            int *c = counts + p * stride, *next = p + 1 < L.passes ? c + stride : nullptr;
             sorted = p & 1;
-            if ((rc = launch_dependent(k_sort_place, dim3((unsigned)L.blocks), kSortThreads, 0, st, p == 0 ? ids : static_cast<const int32_t *>(keys[from]),
-                                       p == 0 ? static_cast<const int32_t *>(nullptr) : static_cast<const int32_t *>(vals[from]), n, V, p * kDigitBits,
-                                       counts + p * stride, p + 1 < L.passes ? counts + (p + 1) * stride : static_cast<int *>(nullptr), keys[sorted],
-                                       vals[sorted], status)) != FP8_OK)
+            if (scan && (rc = launch_dependent(k_sort_scan, dim3(kDigits), kSortThreads, 0, st, c, L.blocks, totals, status)) != FP8_OK) return rc;
+            if ((rc = launch_dependent(k_sort_place, dim3((unsigned)L.blocks), kSortThreads, 0, st, in, in_vals, n, V, p * kDigitBits,
+                                       static_cast<const int *>(c), static_cast<const int *>(scan ? totals : nullptr), next, keys[sorted], vals[sorted],
+                                       status)) != FP8_OK)
                 return rc;
         }
     }
