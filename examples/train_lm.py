@@ -36,24 +36,29 @@ def bf16(*shape):
 class Weight:
     """FP32 master, BF16 working copy, AdamW moments in FP8."""
 
-    def __init__(self, rows, cols, scale, g):
-        self.master = torch.randn((rows, cols), generator=g, device="cuda") * scale
-        n = rows * cols
+    decay = 0.01
+
+    def __init__(self, master):
+        self.master, n = master, master.numel()
         self.m, self.v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
         self.sm, self.sv = (torch.ones(n // 128, device="cuda") for _ in range(2))
-        self.grad, self.bf16 = f32(rows, cols), self.master.bfloat16()
+        self.grad, self.bf16 = f32(*master.shape), master.bfloat16()
 
     def update(self, lr, step):
-        h = fg.adamw_hparams(lr, 0.9, 0.95, 1e-8, 0.01, step)
+        h = fg.adamw_hparams(lr, 0.9, 0.95, 1e-8, self.decay, step)
         fg.adamw_step_fp8_states(self.master, self.grad.bfloat16(), self.m, self.sm, self.v, self.sv, h)
         self.bf16.copy_(self.master)
+
+
+def normal(rows, cols, scale, g):
+    return torch.randn((rows, cols), generator=g, device="cuda") * scale
 
 
 class Linear(Weight):
     """y = x W^T in FP8 (1x128 activations, 128x128 weight blocks); weight [out, in]."""
 
     def __init__(self, out, inp, g):
-        super().__init__(out, inp, inp ** -0.5, g)
+        super().__init__(normal(out, inp, inp ** -0.5, g))
         self.q, self.s = u8(out, inp), f32(out // 128, inp // 128)
         self.qT, self.sT = u8(inp, out), f32(inp // 128, out // 128)
 
@@ -74,12 +79,14 @@ class Linear(Weight):
         del self.xT, self.sxT
 
 
-class Norm:
+class Norm(Weight):
     """Residual add and RMSNorm; keeps the sum in 8 bits."""
 
+    decay = 0.0
+
     def __init__(self, dim):
-        self.w, self.grad = torch.ones(dim, dtype=torch.bfloat16, device="cuda"), f32(dim)
-        self.workspace = fg.new_rmsnorm_workspace(dim)
+        super().__init__(torch.ones(dim, device="cuda"))
+        self.w, self.workspace = self.bf16, fg.new_rmsnorm_workspace(dim)
 
     def forward(self, x, stream, y, total):
         R, C = x.shape
@@ -125,7 +132,7 @@ class Model:
 
     def __init__(self, vocab, dim, ffn, blocks, seed=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
-        self.table = Weight(vocab, dim, dim ** -0.5, g)
+        self.table = Weight(normal(vocab, dim, dim ** -0.5, g))
         self.blocks = [Block(dim, ffn, g) for _ in range(blocks)]
         self.norm, self.dim = Norm(dim), dim
 
@@ -158,7 +165,7 @@ class Model:
         fg.embedding_bwd(self.ids, d, self.table.grad, fg.new_embedding_workspace(T, V, self.dim), scale=self.dim ** 0.5, accumulate=True)
 
     def update(self, lr, step):
-        for w in [self.table] + [w for b in self.blocks for w in (b.up, b.down)]:
+        for w in [self.table, self.norm] + [w for b in self.blocks for w in (b.up, b.down, b.norm)]:
             w.update(lr, step)
 
 
