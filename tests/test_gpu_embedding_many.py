@@ -1,4 +1,4 @@
-"""The embedding's gradient over millions of tokens."""
+"""The embedding's gradient over millions of tokens, and on a stream of its own."""
 import pytest
 import torch
 
@@ -44,3 +44,24 @@ def test_time_grows_with_the_tokens():
         return min(times[1:])
 
     assert shortest(1 << 24) <= 32 * shortest(1 << 20)
+
+
+@pytest.mark.parametrize("T", [500, 5000, 70000])
+def test_on_another_stream(T):
+    V, D = 2000, 64
+    ids, dout = case(T, V, D, 1)
+
+    def step():
+        dw, out = torch.ones((V, D), device="cuda"), torch.empty_like(dout)
+        fg.embedding_bwd(ids, dout, dw, fg.new_embedding_workspace(T, V, D), accumulate=True)
+        fg.embedding_fwd(ids, dw.bfloat16(), out, scale=0.5)
+        return dw, out
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1000000)
+        got = step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and fg.device_status() == fg.OK

@@ -76,3 +76,26 @@ def test_sums_over_many_tokens_do_not_lean(T, accumulate):
     assert fg.device_status() == fg.OK
     want = x.double().sum(0) / V
     assert float(((dw.double() - want) / want).abs().max()) <= 128 * 2.0 ** -23 + (T / 2048) * 2.0 ** -24 + 2.0 ** -23
+
+
+@pytest.mark.parametrize("T,V,D", [(2, 900, 512), (70, 3000, 128), (300, 3000, 128)])
+def test_gradient_on_another_stream(T, V, D):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, w = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((T, D), (V, D)))
+    t = torch.randint(V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    dl = torch.rand(T, generator=g, device="cuda")
+
+    def step():
+        loss, lse = forward(x, w, t, D ** -0.5)
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        fg.linear_xent_bwd(x, w, t, loss, lse, dl, dx, dw, fg.new_linear_xent_workspace(T, V, D), scale=D ** -0.5)
+        return dx, dw
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1000000)      # the default stream would be past this call's inputs by then
+        got = step()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and fg.device_status() == fg.OK
