@@ -938,7 +938,8 @@ def linear_xent_fwd(x, w, target, loss, lse, workspace, scale=1.0, stream=None):
 def linear_xent_bwd(x, w, target, loss, lse, dloss, dx, dw, workspace, dlse=None, scale=1.0, accumulate=False,
                     stream=None):
     """``dx`` [T, D] BF16 and ``dw`` [V, D] (BF16, or FP32, then also added to: accumulate) <- gradients of
-    linear_xent_fwd for those of its outputs, ``dloss`` and ``dlse`` [T]."""
+    linear_xent_fwd for those of its outputs, ``dloss`` and ``dlse`` [T].  Sums in FP32; the products' operands are BF16,
+    the logits' gradient among them (each token's relative to its target's), but for some calls of up to 4 tokens."""
     L, dev = lib(), _current()
     px, T, D, ldx, pw, V, ldw, pt, pl, pz, ws = _xent(x, w, target, loss, lse, workspace, 1, dev)
     pdx, lddx = _like(dx, "dx", _BF16, T, D, dev)

@@ -6,7 +6,8 @@
 // their order; here the tokens are sorted by id, each id's in their order, and
 // every id's rows are summed in FP32 in that order: by one warp per 256 columns
 // where they lie in one piece of the sorted tokens, else piece by piece and then
-// over the pieces.  The order depends on the ids alone, so the results do too.
+// over the pieces.  The order depends on the ids, the sizes and the number of SMs
+// alone, so the results repeat.
 #include <algorithm>
 
 #include "common.cuh"

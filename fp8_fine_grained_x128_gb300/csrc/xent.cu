@@ -19,7 +19,7 @@
 //
 // Forward: the epilogue keeps, per row, a running maximum and sum over a unit
 // of up to 8 tiles and writes 8 bytes a row and half unit, 1/32 of a BF16 logit row
-// and less; k_xent_join adds them in order.
+// and less (1/16 with tiles of 128 columns); k_xent_join adds them in order.
 // Backward: for a piece of the vocabulary, g is rounded to BF16 (the tensor
 // cores' operand type) and kept in the workspace, [tokens][piece]; dx is summed
 // over the pieces in FP32.  A token's g is mostly its target's entry, whose

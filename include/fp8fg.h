@@ -651,12 +651,14 @@ FP8FG_API int fp8_swiglu_bwd_ckpt(const void *c, const float *cs, const void *dh
 FP8FG_API int fp8_embedding_fwd(const int32_t *ids, int64_t tokens, const void *w, int64_t vocab, int64_t dim,
                                 int64_t ldw, float scale, void *out, int64_t ldo, void *stream);
 
-/* Bytes of the caller-owned workspace of fp8_embedding_bwd for calls of up to
- * these sizes (any content; calls sharing one must not overlap on the GPU). */
+/* Bytes of the caller-owned workspace of fp8_embedding_bwd on the current device
+ * for calls of up to these sizes (any content; calls sharing one must not overlap
+ * on the GPU). */
 FP8FG_API size_t fp8_embedding_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
 
 /* dw[v] (+)= scale * sum over t with ids[t] = v of dout[t], summed in FP32 in an
- * order that the ids alone decide.  dw [vocab][lddw] FP32 or BF16 (dw_dtype);
+ * order that the ids, the sizes and the GPU's number of SMs decide: the same in
+ * every run.  dw [vocab][lddw] FP32 or BF16 (dw_dtype);
  * accumulate (FP32 only, else FP8_ERR_UNSUPPORTED): each sum is added to dw in one
  * addition (whose operands and result count as zero below 2^-126), rows without
  * tokens stay as they are; else every row of dw is written, zeros where
